@@ -82,6 +82,9 @@ typedef enum flce_status {
   FLCE_ERR_TIMEOUT = 7       /* device status: a bounded wait inside a kernel ran out */
 } flce_status;
 
+/* Element types of the tensors that may come in more than one. */
+typedef enum flce_dtype { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_F32 = 1 } flce_dtype;
+
 typedef enum flce_reduction {
   FLCE_REDUCTION_NONE = 0,
   FLCE_REDUCTION_MEAN = 1,
@@ -278,6 +281,47 @@ FLCE_API flce_status flce_backward_shard(const float* dloss, const void* H, cons
                                          int32_t reduction, void* dH_partial, float* dW_shard, void* workspace,
                                          size_t workspace_bytes, void* stream);
 
+/* ---- the norm in front of the head ------------------------------------------
+ * Residual add and root-mean-square norm, the last step before the LM head:
+ *   h = x + residual, rounded to the residual's type (h = x without a residual)
+ *   rstd_t = (mean_c h_{t,c}^2 + eps)^(-1/2),  y_{t,c} = h_{t,c} rstd_t w_c
+ * with sums in fp32 over the rounded h, the value every later reader of the
+ * residual stream sees.  Any of three outputs:
+ *   y        [T, Hd] bf16 or NULL   what flce_forward takes as H
+ *   q        [T, Hd] e4m3 or NULL   y in 8 bits, what flce_linear_fp8 takes, with
+ *   q_scale  [T, ceil(Hd/128)]      one E8M0 byte s per row and 128 channels: the value
+ *                                   of an element is q 2^(s - 127).  2^(s - 127) is the
+ *                                   smallest power of two, at least 2^-126, that brings
+ *                                   the block's largest |y| to 448 or less; q is rounded
+ *                                   once, from the fp32 y, to nearest even.  A NaN stays
+ *                                   NaN and does not count for its block's scale.
+ *   rstd     [T] fp32 or NULL       for the backward
+ * Inputs: x [T, Hd] (row stride ldx elements), residual [T, Hd] (ldr) or NULL, each
+ * bf16 or fp32 (flce_dtype), weight [Hd] bf16 or fp32.  h [T, Hd] (ldh, the
+ * residual's type) is written when a residual is given and must be NULL
+ * otherwise; it may be the residual itself (same pointer and stride) or, with
+ * equal types, x itself.
+ * Hd: a multiple of 16 up to 16384 (else FLCE_ERR_UNSUPPORTED).  Tensors 16-byte
+ * aligned, row strides whole multiples of 16 bytes. */
+FLCE_API flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const void* residual,
+                                       int32_t residual_dtype, int64_t ldr, const void* weight, int32_t weight_dtype,
+                                       int64_t T, int64_t Hd, float eps, void* h, int64_t ldh, void* y, float* rstd,
+                                       void* q, uint8_t* q_scale, void* stream);
+
+/* Its backward, for the gradient dy of y (bf16 or fp32) and, where h is read
+ * elsewhere too, the gradient dh of h itself (h's type, or NULL):
+ *   u = dy w,  dx = rstd (u - h rstd^2 mean_c(u h)) + dh,  dweight = sum_t dy h rstd
+ *   dx       [T, Hd] h's type, contiguous   the gradient of x and of the residual alike
+ *   dweight  [Hd] fp32                      summed in a fixed order
+ * h and rstd as flce_add_rms_norm wrote them (h = x there without a residual).
+ *   workspace, workspace_bytes  >= flce_add_rms_norm_backward_workspace_size(T, Hd) */
+FLCE_API size_t flce_add_rms_norm_backward_workspace_size(int64_t T, int64_t Hd);
+FLCE_API flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const void* h,
+                                                int32_t h_dtype, int64_t ldh, const void* weight,
+                                                int32_t weight_dtype, const float* rstd, const void* dh, int64_t lddh,
+                                                int64_t T, int64_t Hd, void* dx, float* dweight, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
 /* Synchronizes `stream`, then reads the device status word of the latest call
  * made with `workspace` into *out (an flce_status value). */
 FLCE_API flce_status flce_read_device_status(const void* workspace, void* stream, int32_t* out);
@@ -334,7 +378,10 @@ typedef enum flce_kernel_kind {
   FLCE_KERNEL_BWD_GATHER = 6,     /* the chunk's rows of H gathered through the row list */
   FLCE_KERNEL_BWD_SCATTER = 7,    /* not launched: the dH tiles write their rows straight to their tokens */
   FLCE_KERNEL_FWD_LIST = 8,       /* flce_forward_valid: the list of rows with a valid target */
-  FLCE_KERNEL_KINDS = 9
+  FLCE_KERNEL_ADD_RMS_NORM = 9,   /* residual add, norm, 8-bit output */
+  FLCE_KERNEL_NORM_BWD = 10,      /* dx and each block's share of dweight */
+  FLCE_KERNEL_NORM_DW = 11,       /* the shares' fixed-order sum */
+  FLCE_KERNEL_KINDS = 12
 } flce_kernel_kind;
 
 FLCE_API void flce_profile_enable(int32_t on);

@@ -34,3 +34,10 @@ from .binding import (  # noqa: F401
     linear_log_probs,
     load_library,
 )
+from .ops import (  # noqa: F401
+    AddRMSNorm,
+    add_rms_norm,
+    flce_add_rms_norm,
+    flce_add_rms_norm_backward,
+    flce_add_rms_norm_backward_workspace_size,
+)

@@ -22,13 +22,15 @@ STATUS_NAMES = {
     0: "FLCE_OK", 1: "FLCE_ERR_INVALID_ARG", 2: "FLCE_ERR_UNSUPPORTED", 3: "FLCE_ERR_ALIGNMENT",
     4: "FLCE_ERR_WORKSPACE", 5: "FLCE_ERR_CUDA", 6: "FLCE_ERR_TARGET_RANGE", 7: "FLCE_ERR_TIMEOUT",
 }
-KERNEL_KINDS = 9
+KERNEL_KINDS = 12
 ABI_VERSION = 2  # FLCE_ABI_VERSION of include/flce.h
 
 # Every symbol the header declares: name -> (restype, argtypes).
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
+_F32 = ctypes.c_float
+_SZ = ctypes.c_size_t
 SIGNATURES = {
     "flce_forward_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "flce_backward_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
@@ -51,6 +53,11 @@ SIGNATURES = {
     "flce_backward": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
     "flce_backward_logp": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _P, _P, ctypes.c_size_t,
                                   _P]),
+    "flce_add_rms_norm": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _P, _I32, _I64, _I64, _F32, _P, _I64, _P, _P, _P, _P,
+                                 _P]),
+    "flce_add_rms_norm_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "flce_add_rms_norm_backward": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _P, _I32, _P, _P, _I64, _I64, _I64, _P, _P,
+                                          _P, _SZ, _P]),
     "flce_read_device_status": (_I32, [_P, _P, ctypes.POINTER(_I32)]),
     "flce_selftest_wait_timeout": (_I32, [_P, ctypes.c_uint64, _P]),
     "flce_status_string": (ctypes.c_char_p, [_I32]),

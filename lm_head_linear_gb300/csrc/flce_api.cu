@@ -1,10 +1,5 @@
 // Host side of the C ABI declared in include/flce.h: argument checks, workspace
 // layout, TMA tensor maps, launch sequence and the optional per-kernel timing.
-#include <cuda.h>
-#include <cuda_runtime.h>
-#include <cudaTypedefs.h>
-#include <nvtx3/nvToolsExt.h>
-
 #include <algorithm>
 #include <atomic>
 #include <cstdarg>
@@ -14,11 +9,15 @@
 #include <vector>
 
 #include "flce.h"
+#include "flce_host.cuh"
 #include "flce_kernels.cuh"
 
-namespace {
-
 using namespace flce;
+using namespace flce::host;
+
+// ------------------------------------------------------------------ shared host pieces (flce_host.cuh)
+namespace flce {
+namespace host {
 
 thread_local char g_last_error[512] = "";
 
@@ -29,20 +28,6 @@ flce_status fail(flce_status st, const char* fmt, ...) {
   va_end(ap);
   return st;
 }
-
-#define CUDA_TRY(expr)                                                                            \
-  do {                                                                                            \
-    cudaError_t e_ = (expr);                                                                      \
-    if (e_ != cudaSuccess) return fail(FLCE_ERR_CUDA, "%s: %s", #expr, cudaGetErrorString(e_));  \
-  } while (0)
-
-constexpr size_t kHeaderBytes = 256;  // status word and spare scalars at the start of each workspace
-constexpr size_t kUnitCounterOff = 32;  // forward header: the logit kernel's work-unit counter (int32, zeroed per call)
-constexpr int kMaxSplit = 16;         // forward: vocab ranges per token block
-constexpr int64_t kDefaultChunk = 8192;
-constexpr int32_t kMaxShards = 64;    // vocab shards one combine call merges
-// T and V bound: tile coordinates (block * 128 + row) stay inside int32 with room to spare.
-constexpr int64_t kMaxRows = int64_t(1) << 30;
 
 std::atomic<uint64_t> g_timeout_ns{4000000000ull};
 std::atomic<bool> g_timeout_fixed{false};  // set by flce_set_wait_timeout_ns
@@ -58,22 +43,141 @@ uint64_t wait_limit_ns(int64_t k_max) {
   return std::max<uint64_t>(base, 16ull * static_cast<uint64_t>(std::max<int64_t>(k_max, 0)));
 }
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
 
-// The kernels read and write the per-token arrays with plain typed loads and
-// stores, so each pointer must carry its type's natural alignment (checked on the
-// host: a misaligned access would fault the device instead of returning an error).
-template <typename E>
-bool misaligned(const E* p) {
-  return (reinterpret_cast<uintptr_t>(p) % alignof(E)) != 0;
+flce_status get_encoder() {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) return fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  return FLCE_OK;
 }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+std::mutex g_prof_mu;
+bool g_prof_on = false;
+std::vector<LaunchRecord> g_records;
+std::vector<cudaEvent_t> g_event_pool;
+
+// An event from the pool, or a new one; nullptr if none can be created.
+static cudaEvent_t take_event() {
+  if (!g_event_pool.empty()) {
+    cudaEvent_t e = g_event_pool.back();
+    g_event_pool.pop_back();
+    return e;
+  }
+  cudaEvent_t e = nullptr;
+  if (cudaEventCreate(&e) != cudaSuccess) return nullptr;
+  return e;
+}
+
+KernelScope::KernelScope(int kind, cudaStream_t s, double flops, double bytes, const int32_t* rows_dev,
+                         int64_t index0, int64_t cap, double flops_per_row, double bytes_per_row)
+    : stream(s) {
+  nvtxRangePushA(flce_kernel_name(kind));
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  if (!g_prof_on) return;
+  on = true;
+  rec.kind = kind;
+  rec.flops = flops;
+  rec.bytes = bytes;
+  rec.rows_dev = rows_dev;
+  rec.index0 = index0;
+  rec.cap = cap;
+  rec.flops_per_row = flops_per_row;
+  rec.bytes_per_row = bytes_per_row;
+  rec.start = take_event();
+  rec.stop = take_event();
+  if (!rec.start || !rec.stop || cudaEventRecord(rec.start, s) != cudaSuccess) {
+    // no timing for this launch (the profile is an aid; the launch itself goes
+    // ahead, and the failed call's error is cleared so that it is not taken for
+    // the launch's)
+    (void)cudaGetLastError();
+    release_events();
+  }
+}
+
+KernelScope::~KernelScope() {
+  if (nvtx) nvtxRangePop();
+  if (on) {  // an error return before done(): the events go back to the pool
+    std::lock_guard<std::mutex> lk(g_prof_mu);
+    release_events();
+  }
+}
+
+void KernelScope::release_events() {
+  if (rec.start) g_event_pool.push_back(rec.start);
+  if (rec.stop) g_event_pool.push_back(rec.stop);
+  rec.start = rec.stop = nullptr;
+  on = false;
+}
+
+void KernelScope::done() {
+  if (nvtx) {
+    nvtxRangePop();
+    nvtx = false;
+  }
+  if (!on) return;
+  const bool ok = cudaEventRecord(rec.stop, stream) == cudaSuccess;
+  if (!ok) (void)cudaGetLastError();
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  if (ok) {
+    g_records.push_back(rec);
+    on = false;
+  } else {
+    release_events();
+  }
+}
+
+flce_status check_launch(const char* what) {
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(FLCE_ERR_CUDA, "launch of %s failed: %s", what, cudaGetErrorString(e));
+  return FLCE_OK;
+}
+
+flce_status current_device(int* slot, int* sms) {
+  struct Known {
+    bool init = false;
+    int sms = 0, major = 0, minor = 0;
+  };
+  static std::mutex mu;
+  static Known known[64];
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= 64) return fail(FLCE_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+  std::lock_guard<std::mutex> lk(mu);
+  Known& d = known[dev];
+  if (!d.init) {
+    CUDA_TRY(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
+    CUDA_TRY(cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev));
+    CUDA_TRY(cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev));
+    d.init = true;
+  }
+  if (!(d.major == 10 && d.minor == 3))
+    return fail(FLCE_ERR_UNSUPPORTED, "this library is built for sm_103a; device is sm_%d%d", d.major, d.minor);
+  *slot = dev;
+  *sms = d.sms;
+  return FLCE_OK;
+}
+
+}  // namespace host
+}  // namespace flce
+
+namespace {
+
+constexpr size_t kUnitCounterOff = 32;  // forward header: the logit kernel's work-unit counter (int32, zeroed per call)
+constexpr int kMaxSplit = 16;         // forward: vocab ranges per token block
+constexpr int64_t kDefaultChunk = 8192;
+constexpr int32_t kMaxShards = 64;    // vocab shards one combine call merges
 
 // ------------------------------------------------------------------ device info
 struct DeviceInfo {
-  bool init = false;
   int sms = 0;
-  int major = 0, minor = 0;
   bool attrs_set = false;
   int pairs[4] = {0, 0, 0, 0};  // co-resident CTA pairs (clusters of 2) per GEMM mode
 };
@@ -93,19 +197,12 @@ std::mutex g_dev_mu;
 DeviceInfo g_dev[64];
 
 flce_status device_info(DeviceInfo** out) {
-  int dev = 0;
-  CUDA_TRY(cudaGetDevice(&dev));
-  if (dev < 0 || dev >= 64) return fail(FLCE_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+  int dev = 0, sms = 0;
+  flce_status known = current_device(&dev, &sms);
+  if (known != FLCE_OK) return known;
   std::lock_guard<std::mutex> lk(g_dev_mu);
   DeviceInfo& d = g_dev[dev];
-  if (!d.init) {
-    CUDA_TRY(cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev));
-    CUDA_TRY(cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev));
-    CUDA_TRY(cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev));
-    d.init = true;
-  }
-  if (!(d.major == 10 && d.minor == 3))
-    return fail(FLCE_ERR_UNSUPPORTED, "this library is built for sm_103a; device is sm_%d%d", d.major, d.minor);
+  d.sms = sms;
   if (!d.attrs_set) {
     CUDA_TRY(cudaFuncSetAttribute(gemm_kernel<MODE_FWD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   smem_bytes_for(MODE_FWD)));
@@ -127,22 +224,6 @@ flce_status device_info(DeviceInfo** out) {
 }
 
 // ------------------------------------------------------------------ tensor maps
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-flce_status get_encoder() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  if (!g_encode) return fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  return FLCE_OK;
-}
-
 // 2-D map over a row-major matrix: `inner` contiguous elements per row,
 // `outer` rows, `pitch` bytes between rows; box {box_inner, box_outer};
 // 128-byte swizzle; out-of-range elements read as zero, stores are clipped.
@@ -178,104 +259,6 @@ flce_status make_panel_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint6
     return fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for panels {64, %llu, %llu} box rows %u",
                 static_cast<int>(r), static_cast<unsigned long long>(rows), static_cast<unsigned long long>(panels),
                 box_rows);
-  return FLCE_OK;
-}
-
-// ------------------------------------------------------------------ profiling
-struct LaunchRecord {
-  int kind;
-  cudaEvent_t start, stop;
-  double flops, bytes;
-  // Launches over the backward's row list add rows * (flops, bytes) per row, the
-  // rows read from the workspace when the records are collected.
-  const int32_t* rows_dev;
-  int64_t index0, cap;
-  double flops_per_row, bytes_per_row;
-};
-std::mutex g_prof_mu;
-bool g_prof_on = false;
-std::vector<LaunchRecord> g_records;
-std::vector<cudaEvent_t> g_event_pool;
-
-// An event from the pool, or a new one; nullptr if none can be created.
-cudaEvent_t take_event() {
-  if (!g_event_pool.empty()) {
-    cudaEvent_t e = g_event_pool.back();
-    g_event_pool.pop_back();
-    return e;
-  }
-  cudaEvent_t e = nullptr;
-  if (cudaEventCreate(&e) != cudaSuccess) return nullptr;
-  return e;
-}
-
-// Brackets one launch with an NVTX range named after the kernel (seen by any
-// attached profiler) and, while profiling is enabled, with events on its stream.
-struct KernelScope {
-  bool on = false;
-  bool nvtx = true;
-  LaunchRecord rec{};
-  cudaStream_t stream;
-  KernelScope(int kind, cudaStream_t s, double flops, double bytes, const int32_t* rows_dev = nullptr,
-              int64_t index0 = 0, int64_t cap = 0, double flops_per_row = 0.0, double bytes_per_row = 0.0)
-      : stream(s) {
-    nvtxRangePushA(flce_kernel_name(kind));
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    if (!g_prof_on) return;
-    on = true;
-    rec.kind = kind;
-    rec.flops = flops;
-    rec.bytes = bytes;
-    rec.rows_dev = rows_dev;
-    rec.index0 = index0;
-    rec.cap = cap;
-    rec.flops_per_row = flops_per_row;
-    rec.bytes_per_row = bytes_per_row;
-    rec.start = take_event();
-    rec.stop = take_event();
-    if (!rec.start || !rec.stop || cudaEventRecord(rec.start, s) != cudaSuccess) {
-      // no timing for this launch (the profile is an aid; the launch itself goes
-      // ahead, and the failed call's error is cleared so that it is not taken for
-      // the launch's)
-      (void)cudaGetLastError();
-      release_events();
-    }
-  }
-  ~KernelScope() {
-    if (nvtx) nvtxRangePop();
-    if (on) {  // an error return before done(): the events go back to the pool
-      std::lock_guard<std::mutex> lk(g_prof_mu);
-      release_events();
-    }
-  }
-  // Caller holds g_prof_mu.
-  void release_events() {
-    if (rec.start) g_event_pool.push_back(rec.start);
-    if (rec.stop) g_event_pool.push_back(rec.stop);
-    rec.start = rec.stop = nullptr;
-    on = false;
-  }
-  void done() {
-    if (nvtx) {
-      nvtxRangePop();
-      nvtx = false;
-    }
-    if (!on) return;
-    const bool ok = cudaEventRecord(rec.stop, stream) == cudaSuccess;
-    if (!ok) (void)cudaGetLastError();
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    if (ok) {
-      g_records.push_back(rec);
-      on = false;
-    } else {
-      release_events();
-    }
-  }
-};
-
-flce_status check_launch(const char* what) {
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return fail(FLCE_ERR_CUDA, "launch of %s failed: %s", what, cudaGetErrorString(e));
   return FLCE_OK;
 }
 
@@ -788,6 +771,9 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_KERNEL_BWD_GATHER: return "bwd_gather";
     case FLCE_KERNEL_BWD_SCATTER: return "bwd_scatter";
     case FLCE_KERNEL_FWD_LIST: return "fwd_list";
+    case FLCE_KERNEL_ADD_RMS_NORM: return "add_rms_norm";
+    case FLCE_KERNEL_NORM_BWD: return "norm_bwd";
+    case FLCE_KERNEL_NORM_DW: return "norm_dw";
     default: return "unknown";
   }
 }

@@ -1,0 +1,182 @@
+// Host side of the residual add + RMS norm entry points of include/flce.h.
+#include <algorithm>
+
+#include "flce_host.cuh"
+#include "norm_kernels.cuh"
+
+using namespace flce;
+using namespace flce::host;
+
+namespace {
+
+constexpr int64_t kMaxNormHd = 16384;   // a row stays in the registers of one CTA
+constexpr int64_t kMaxNormBlocks = 512; // CTAs of the backward: rows of its workspace
+
+bool known_dtype(int32_t d) { return d == FLCE_DTYPE_BF16 || d == FLCE_DTYPE_F32; }
+int64_t size_of(int32_t d) { return d == FLCE_DTYPE_F32 ? 4 : 2; }
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+bool bad_ld(int64_t ld, int64_t Hd, int32_t dtype) { return ld < Hd || (ld * size_of(dtype)) % 16 != 0; }
+
+// Vectors per thread and threads per row.  Few rows: one vector per thread, the
+// shortest chain from load to store.  Many: more per thread, so that a row needs
+// fewer warps and a warp has more loads in flight.
+struct Shape {
+  int nv, group, threads;
+};
+Shape pick_shape(int64_t T, int64_t Hd, int sms, int nv_many, int threads_many) {
+  const int nvec = static_cast<int>(Hd / norm::kVec);
+  int nv = 1;
+  if (T > sms) nv = nv_many;
+  while (cdiv(cdiv(nvec, nv), 32) * 32 > norm::max_threads(nv)) nv *= 2;
+  while (nv > 1 && (nv / 2) * 32 >= nvec) nv /= 2;  // a warp would leave whole steps idle
+  Shape s;
+  s.nv = nv;
+  s.group = static_cast<int>(cdiv(cdiv(nvec, nv), 32) * 32);
+  s.threads = T > sms ? std::max(s.group, threads_many / s.group * s.group) : s.group;
+  s.threads = std::min(s.threads, norm::max_threads(nv) / s.group * s.group);
+  return s;
+}
+
+template <typename TX, typename TR, int NV>
+void launch_fwd(const norm::FwdParams& p, const Shape& s, int64_t blocks, cudaStream_t st) {
+  norm::add_rms_norm_kernel<TX, TR, NV><<<static_cast<unsigned>(blocks), s.threads, 0, st>>>(p);
+}
+template <typename TX, typename TR>
+void launch_fwd_nv(const norm::FwdParams& p, const Shape& s, int64_t blocks, cudaStream_t st) {
+  if (s.nv == 1) launch_fwd<TX, TR, 1>(p, s, blocks, st);
+  else if (s.nv == 2) launch_fwd<TX, TR, 2>(p, s, blocks, st);
+  else if (s.nv == 4) launch_fwd<TX, TR, 4>(p, s, blocks, st);
+  else launch_fwd<TX, TR, 8>(p, s, blocks, st);
+}
+
+template <typename TY, typename TH>
+void launch_bwd_nv(const norm::BwdParams& p, const Shape& s, int64_t blocks, size_t smem, cudaStream_t st) {
+  const unsigned b = static_cast<unsigned>(blocks);
+  if (s.nv == 1) norm::norm_backward_kernel<TY, TH, 1><<<b, s.threads, smem, st>>>(p);
+  else if (s.nv == 2) norm::norm_backward_kernel<TY, TH, 2><<<b, s.threads, smem, st>>>(p);
+  else if (s.nv == 4) norm::norm_backward_kernel<TY, TH, 4><<<b, s.threads, smem, st>>>(p);
+  else norm::norm_backward_kernel<TY, TH, 8><<<b, s.threads, smem, st>>>(p);
+}
+
+flce_status check_sizes(int64_t T, int64_t Hd) {
+  if (T < 0 || T >= kMaxRows) return fail(FLCE_ERR_INVALID_ARG, "T = %lld out of range", (long long)T);
+  if (Hd < 1) return fail(FLCE_ERR_INVALID_ARG, "Hd = %lld out of range", (long long)Hd);
+  if (Hd % 16 != 0 || Hd > kMaxNormHd)
+    return fail(FLCE_ERR_UNSUPPORTED, "Hd = %lld is not a multiple of 16 up to %lld", (long long)Hd,
+                (long long)kMaxNormHd);
+  return FLCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const void* residual,
+                              int32_t residual_dtype, int64_t ldr, const void* weight, int32_t weight_dtype,
+                              int64_t T, int64_t Hd, float eps, void* h, int64_t ldh, void* y, float* rstd, void* q,
+                              uint8_t* q_scale, void* stream) {
+  flce_status st = check_sizes(T, Hd);
+  if (st != FLCE_OK) return st;
+  if (!known_dtype(x_dtype) || !known_dtype(weight_dtype) || (residual && !known_dtype(residual_dtype)))
+    return fail(FLCE_ERR_INVALID_ARG, "unknown element type");
+  if (!(eps >= 0.0f)) return fail(FLCE_ERR_INVALID_ARG, "eps must not be negative");
+  if (!weight || (T > 0 && !x)) return fail(FLCE_ERR_INVALID_ARG, "x or weight is NULL");
+  if ((residual != nullptr) != (h != nullptr) && T > 0)
+    return fail(FLCE_ERR_INVALID_ARG, "residual and h are given together or not at all");
+  if ((q != nullptr) != (q_scale != nullptr)) return fail(FLCE_ERR_INVALID_ARG, "q and q_scale are given together");
+  if (T > 0 && !y && !q) return fail(FLCE_ERR_INVALID_ARG, "neither y nor q is given");
+  if (bad_ld(ldx, Hd, x_dtype) || (residual && (bad_ld(ldr, Hd, residual_dtype) || bad_ld(ldh, Hd, residual_dtype))))
+    return fail(FLCE_ERR_ALIGNMENT, "row strides must be at least Hd and whole multiples of 16 bytes");
+  if (off16(x) || off16(residual) || off16(weight) || off16(h) || off16(y) || off16(q))
+    return fail(FLCE_ERR_ALIGNMENT, "x, residual, weight, h, y and q must be 16-byte aligned");
+  if (misaligned(rstd)) return fail(FLCE_ERR_ALIGNMENT, "rstd must be 4-byte aligned");
+  int dev = 0, sms = 0;
+  if ((st = current_device(&dev, &sms)) != FLCE_OK) return st;
+  if (T == 0) return FLCE_OK;
+  norm::FwdParams p{};
+  p.x = x, p.r = residual, p.w = weight, p.h = h;
+  p.y = static_cast<uint16_t*>(y), p.rstd = rstd, p.q = static_cast<uint8_t*>(q), p.qs = q_scale;
+  p.ldx = ldx, p.ldr = ldr, p.ldh = ldh, p.T = T, p.Hd = static_cast<int32_t>(Hd);
+  p.w_f32 = weight_dtype == FLCE_DTYPE_F32, p.eps = eps, p.inv_hd = 1.0f / static_cast<float>(Hd);
+  const Shape s = pick_shape(T, Hd, sms, 4, 256);
+  p.group = s.group;
+  const int64_t blocks = cdiv(T, s.threads / s.group);
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const double n = static_cast<double>(T) * Hd;
+  KernelScope ks(FLCE_KERNEL_ADD_RMS_NORM, cs, 8.0 * n,
+                 n * (size_of(x_dtype) + (residual ? 2.0 * size_of(residual_dtype) : 0.0) + (y ? 2.0 : 0.0) +
+                      (q ? 1.0 + 1.0 / 128 : 0.0)));
+  const bool xf = x_dtype == FLCE_DTYPE_F32, rf = residual ? residual_dtype == FLCE_DTYPE_F32 : xf;
+  if (xf && rf) launch_fwd_nv<float, float>(p, s, blocks, cs);
+  else if (xf) launch_fwd_nv<float, uint16_t>(p, s, blocks, cs);
+  else if (rf) launch_fwd_nv<uint16_t, float>(p, s, blocks, cs);
+  else launch_fwd_nv<uint16_t, uint16_t>(p, s, blocks, cs);
+  ks.done();
+  return check_launch("add_rms_norm");
+}
+
+size_t flce_add_rms_norm_backward_workspace_size(int64_t T, int64_t Hd) {
+  if (T < 0 || Hd < 1) return 0;
+  return kHeaderBytes + sizeof(float) * static_cast<size_t>(std::min<int64_t>(std::max<int64_t>(T, 1), kMaxNormBlocks)) *
+                            static_cast<size_t>(Hd);
+}
+
+flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const void* h, int32_t h_dtype,
+                                       int64_t ldh, const void* weight, int32_t weight_dtype, const float* rstd,
+                                       const void* dh, int64_t lddh, int64_t T, int64_t Hd, void* dx, float* dweight,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  flce_status st = check_sizes(T, Hd);
+  if (st != FLCE_OK) return st;
+  if (!known_dtype(dy_dtype) || !known_dtype(h_dtype) || !known_dtype(weight_dtype))
+    return fail(FLCE_ERR_INVALID_ARG, "unknown element type");
+  if (!weight || !dweight || (T > 0 && (!dy || !h || !rstd || !dx)))
+    return fail(FLCE_ERR_INVALID_ARG, "dy, h, weight, rstd, dx or dweight is NULL");
+  if (bad_ld(lddy, Hd, dy_dtype) || bad_ld(ldh, Hd, h_dtype) || (dh && bad_ld(lddh, Hd, h_dtype)))
+    return fail(FLCE_ERR_ALIGNMENT, "row strides must be at least Hd and whole multiples of 16 bytes");
+  if (off16(dy) || off16(h) || off16(weight) || off16(dh) || off16(dx))
+    return fail(FLCE_ERR_ALIGNMENT, "dy, h, weight, dh and dx must be 16-byte aligned");
+  if (misaligned(rstd) || misaligned(dweight)) return fail(FLCE_ERR_ALIGNMENT, "rstd and dweight must be 4-byte aligned");
+  if (!workspace) return fail(FLCE_ERR_WORKSPACE, "workspace is NULL");
+  if (workspace_bytes < flce_add_rms_norm_backward_workspace_size(T, Hd))
+    return fail(FLCE_ERR_WORKSPACE, "workspace of %zu bytes < %zu required", workspace_bytes,
+                flce_add_rms_norm_backward_workspace_size(T, Hd));
+  if (reinterpret_cast<uintptr_t>(workspace) & 255)
+    return fail(FLCE_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  int dev = 0, sms = 0;
+  if ((st = current_device(&dev, &sms)) != FLCE_OK) return st;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    CUDA_TRY(cudaMemsetAsync(workspace, 0, kHeaderBytes, cs));
+    CUDA_TRY(cudaMemsetAsync(dweight, 0, sizeof(float) * Hd, cs));
+    return FLCE_OK;
+  }
+  norm::BwdParams p{};
+  p.dy = dy, p.h = h, p.w = weight, p.rstd = rstd, p.dh = dh, p.dx = dx;
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
+  p.lddy = lddy, p.ldh = ldh, p.lddh = lddh, p.T = T, p.Hd = static_cast<int32_t>(Hd);
+  p.w_f32 = weight_dtype == FLCE_DTYPE_F32, p.inv_hd = 1.0f / static_cast<float>(Hd);
+  const Shape s = pick_shape(T, Hd, sms, 2, 256);
+  p.group = s.group;
+  const int groups = s.threads / s.group;
+  const size_t smem = groups > 1 ? sizeof(float) * static_cast<size_t>(groups) * Hd : 0;
+  const int64_t blocks = std::min<int64_t>(std::min<int64_t>(cdiv(T, groups), 3ll * sms), kMaxNormBlocks);
+  const double n = static_cast<double>(T) * Hd;
+  {
+    KernelScope ks(FLCE_KERNEL_NORM_BWD, cs, 10.0 * n,
+                   n * (size_of(dy_dtype) + (dh ? 3.0 : 2.0) * size_of(h_dtype)) + 4.0 * Hd);
+    const bool yf = dy_dtype == FLCE_DTYPE_F32, hf = h_dtype == FLCE_DTYPE_F32;
+    if (yf && hf) launch_bwd_nv<float, float>(p, s, blocks, smem, cs);
+    else if (yf) launch_bwd_nv<float, uint16_t>(p, s, blocks, smem, cs);
+    else if (hf) launch_bwd_nv<uint16_t, float>(p, s, blocks, smem, cs);
+    else launch_bwd_nv<uint16_t, uint16_t>(p, s, blocks, smem, cs);
+    ks.done();
+    if ((st = check_launch("norm_bwd")) != FLCE_OK) return st;
+  }
+  KernelScope ks(FLCE_KERNEL_NORM_DW, cs, 0.0, 4.0 * blocks * Hd + 4.0 * Hd);
+  norm::norm_dw_kernel<<<static_cast<unsigned>(cdiv(Hd, 32)), 32 * norm::kDwSlices, 0, cs>>>(
+      p.partial, static_cast<int>(blocks), p.Hd, dweight, static_cast<int32_t*>(workspace));
+  ks.done();
+  return check_launch("norm_dw");
+}
+
+}  // extern "C"

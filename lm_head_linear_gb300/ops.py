@@ -1,0 +1,157 @@
+"""The operators around the LM head: the norm in front of it.
+
+As in :mod:`.binding`: arguments are checked, outputs and workspaces allocated
+with torch (or taken from the caller), and the library's kernels do the work.
+These calls can be a few microseconds long on the GPU, so their Python side is
+kept short: pointers go to ctypes as plain integers.
+"""
+
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from .binding import _check, _out, load_library
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # flce_dtype
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream(stream, device) -> int:
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+
+
+def _rows(name: str, t: torch.Tensor, shape, device, dtypes=_DTYPES) -> int:
+    """Checks a [T, Hd] tensor with contiguous rows; returns its row stride in elements."""
+    if t.dtype not in dtypes or t.shape != shape or t.device != device or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a {' or '.join(map(str, dtypes))} tensor of shape {tuple(shape)} on {device} "
+                         f"with contiguous rows, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _vector(name: str, t: torch.Tensor, n: int, dtype, device):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _ws(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def _weight(weight: torch.Tensor, Hd: int, device) -> int:
+    if weight.dtype not in _DTYPES or weight.shape != (Hd,) or weight.device != device or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous bfloat16 or float32 tensor of {Hd} elements on {device}")
+    return _DTYPES[weight.dtype]
+
+
+def flce_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                      eps: float = 1e-6, normed: bool = True, fp8: bool = False, save_rstd: bool = False, stream=None,
+                      out: Optional[dict] = None):
+    """Run ``flce_add_rms_norm``; returns ``(y, h, rstd, q, q_scale)``.
+
+    ``h`` is x + residual in the residual's dtype (x itself without a residual);
+    ``y`` the bf16 norm (with ``normed``), ``q`` / ``q_scale`` its e4m3 form with a
+    float8_e8m0fnu scale per 128 channels (with ``fp8``), ``rstd`` with
+    ``save_rstd``; None where not asked for.  ``out`` may hold preallocated tensors
+    under those names (``h`` may be the residual).
+    """
+    if not x.is_cuda or x.dim() != 2:
+        raise ValueError("x must be a CUDA tensor [T, Hd]")
+    lib = load_library()
+    dev, shape = x.device, x.shape
+    T, Hd = shape
+    ldx = _rows("x", x, shape, dev)
+    w_dtype = _weight(weight, Hd, dev)
+    h, ldr, ldh, r_dtype = x, 0, 0, 0
+    if residual is not None:
+        ldr = _rows("residual", residual, shape, dev)
+        r_dtype = _DTYPES[residual.dtype]
+        h = (out or {}).get("h")
+        if h is None:
+            h = torch.empty(shape, dtype=residual.dtype, device=dev)
+        ldh = _rows("out['h']", h, shape, dev, (residual.dtype,))
+    y = _out(out, "y", shape, torch.bfloat16, dev) if normed else None
+    rstd = _out(out, "rstd", T, torch.float32, dev) if save_rstd else None
+    q = _out(out, "q", shape, torch.float8_e4m3fn, dev) if fp8 else None
+    qs = _out(out, "q_scale", (T, (Hd + 127) // 128), torch.float8_e8m0fnu, dev) if fp8 else None
+    _check(lib.flce_add_rms_norm(
+        x.data_ptr(), _DTYPES[x.dtype], ldx, residual.data_ptr() if residual is not None else None, r_dtype, ldr,
+        weight.data_ptr(), w_dtype, T, Hd, eps, h.data_ptr() if residual is not None else None, ldh,
+        y.data_ptr() if normed else None, rstd.data_ptr() if save_rstd else None, q.data_ptr() if fp8 else None,
+        qs.data_ptr() if fp8 else None, _stream(stream, dev)))
+    return y, h, rstd, q, qs
+
+
+def flce_add_rms_norm_backward_workspace_size(T: int, Hd: int) -> int:
+    return int(load_library().flce_add_rms_norm_backward_workspace_size(T, Hd))
+
+
+def flce_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                               dh: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                               stream=None, out: Optional[dict] = None):
+    """Run ``flce_add_rms_norm_backward``; returns ``(dx [T, Hd] in h's dtype, dweight [Hd] fp32, workspace)``.
+    ``dx`` is the gradient of x and of the residual; ``dh`` an upstream gradient on h.
+    ``out`` may hold preallocated ``dx`` and ``dweight`` tensors."""
+    if not h.is_cuda or h.dim() != 2:
+        raise ValueError("h must be a CUDA tensor [T, Hd]")
+    lib = load_library()
+    dev, shape = h.device, h.shape
+    T, Hd = shape
+    ldh = _rows("h", h, shape, dev)
+    lddy = _rows("dy", dy, shape, dev)
+    w_dtype = _weight(weight, Hd, dev)
+    _vector("rstd", rstd, T, torch.float32, dev)
+    lddh = _rows("dh", dh, shape, dev, (h.dtype,)) if dh is not None else 0
+    dx = _out(out, "dx", shape, h.dtype, dev)
+    dw = _out(out, "dweight", Hd, torch.float32, dev)
+    ws = _ws(lib.flce_add_rms_norm_backward_workspace_size(T, Hd), dev, workspace)
+    _check(lib.flce_add_rms_norm_backward(
+        dy.data_ptr(), _DTYPES[dy.dtype], lddy, h.data_ptr(), _DTYPES[h.dtype], ldh, weight.data_ptr(), w_dtype,
+        rstd.data_ptr(), dh.data_ptr() if dh is not None else None, lddh, T, Hd, dx.data_ptr(), dw.data_ptr(),
+        ws.data_ptr(), ws.numel(), _stream(stream, dev)))
+    return dx, dw, ws
+
+
+class AddRMSNorm(torch.autograd.Function):
+    """autograd wrapper of the norm: returns ``(y, h)``, both differentiable."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual=None, eps: float = 1e-6):
+        y, h, rstd, _, _ = flce_add_rms_norm(x, weight, residual, eps, save_rstd=True)
+        ctx.save_for_backward(h, weight, rstd)
+        ctx.x_dtype = x.dtype
+        ctx.has_residual = residual is not None
+        ctx.set_materialize_grads(False)
+        if residual is None:
+            h = x.view_as(x)  # an input returned as it is would lose its place in the graph
+        return y, h
+
+    @staticmethod
+    def backward(ctx, dy, dh):
+        h, weight, rstd = ctx.saved_tensors
+        if dy is None and dh is None:
+            return None, None, None, None
+        if dy is None:
+            dx, dw = dh, None
+        else:
+            dx, dw, _ = flce_add_rms_norm_backward(_dense_rows(dy), h, weight, rstd,
+                                                   dh=None if dh is None else _dense_rows(dh.to(h.dtype)))
+            dw = dw.to(weight.dtype)
+        return dx.to(ctx.x_dtype), dw, dx if ctx.has_residual else None, None
+
+
+def _dense_rows(t: torch.Tensor) -> torch.Tensor:
+    """A gradient as the kernels take it (expanded and transposed ones are copied)."""
+    return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] and t.data_ptr() % 16 == 0 and \
+        t.stride(0) * t.element_size() % 16 == 0 else t.contiguous()
+
+
+def add_rms_norm(x, weight, residual=None, eps: float = 1e-6):
+    """``(rms_norm(x + residual) * weight, x + residual)``, differentiable in every input."""
+    return AddRMSNorm.apply(x, weight, residual, eps)
