@@ -79,7 +79,8 @@ typedef enum flce_status {
   FLCE_ERR_WORKSPACE = 4,    /* workspace missing or smaller than required */
   FLCE_ERR_CUDA = 5,         /* a CUDA runtime / driver call failed; see flce_last_error() */
   FLCE_ERR_TARGET_RANGE = 6, /* device status: a target outside [0, V) and != ignore_index */
-  FLCE_ERR_TIMEOUT = 7       /* device status: a bounded wait inside a kernel ran out */
+  FLCE_ERR_TIMEOUT = 7,      /* device status: a bounded wait inside a kernel ran out */
+  FLCE_ERR_SEQUENCES = 8     /* device status: cu_seqlens decreases or leaves [0, T] */
 } flce_status;
 
 /* Element types of the tensors that may come in more than one. */
@@ -88,7 +89,8 @@ typedef enum flce_dtype { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_F32 = 1 } flce_dtype;
 typedef enum flce_reduction {
   FLCE_REDUCTION_NONE = 0,
   FLCE_REDUCTION_MEAN = 1,
-  FLCE_REDUCTION_SUM = 2
+  FLCE_REDUCTION_SUM = 2,
+  FLCE_REDUCTION_SEQUENCE_MEAN = 3 /* flce_policy_loss only */
 } flce_reduction;
 
 /* Bytes of workspace flce_forward() needs for these sizes (>= 256). */
@@ -322,6 +324,76 @@ FLCE_API flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype
                                                 int64_t T, int64_t Hd, void* dx, float* dweight, void* workspace,
                                                 size_t workspace_bytes, void* stream);
 
+/* ---- objectives on logp ------------------------------------------------------
+ * Both take the per-token log-probabilities that the forward returns and give
+ * the gradient that flce_backward_logp takes as dlogp: forward, loss, backward
+ * without a host step in between.  Tokens whose target is ignore_index do not
+ * count: whatever logp, old_logp, ref_logp or the advantages hold there (NaN
+ * and infinities included) has no effect, and their dlogp is 0.
+ *
+ * cu_seqlens [n + 1] int64 gives the packed sequences: sequence i is the tokens
+ * cu_seqlens[i] .. cu_seqlens[i + 1] - 1; empty ones are allowed, and a token in no
+ * sequence (before cu_seqlens[0], from cu_seqlens[n] on) is treated as ignored.  If it
+ * decreases or leaves [0, T] the device status is FLCE_ERR_SEQUENCES and the
+ * outputs mean nothing (no access leaves the arrays).
+ *
+ * Either of loss and dlogp may be NULL.  dloss is the gradient of the loss
+ * output ([1], or one per loss entry with NONE), NULL for ones. */
+
+/* Clipped policy loss with a KL term.  Per valid token, with
+ *   d = logp - old_logp clamped to [-20, 20],  rho = e^d,  A the advantage:
+ *   pg = -min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)
+ *        and, with dual_clip c > 1 and A < 0, at most -c A (dual_clip 0: no such limit)
+ *   e = ref_logp - logp;  kl = -e (K1), e^2 / 2 (K2), e^e - 1 - e (K3, e clamped like d)
+ *   L = pg + kl_coef kl
+ * loss = sum over valid tokens / n_valid (MEAN), the sum (SUM), one per token (NONE),
+ * or (SEQUENCE_MEAN) the mean over the sequences that have a valid token of each
+ * one's mean.  The gradient of pg is -A rho where rho is not clipped and d not
+ * clamped, else 0.  No valid token: loss and stats are 0.
+ *   logp, old_logp [T] fp32; ref_logp [T] fp32 or NULL (kl = 0; kl_coef must be 0)
+ *   advantages [T] fp32, or [n_seqs] with advantages_per_sequence
+ *   cu_seqlens [n_seqs + 1] or NULL (one stretch of T tokens); needed by
+ *              SEQUENCE_MEAN and advantages_per_sequence
+ *   dlogp   [T] fp32
+ *   stats   [4] fp32 or NULL: means over the valid tokens of kl, of "clipped"
+ *           (either way), of d and of rho
+ *   n_valid [1] int64 or NULL
+ *   workspace >= flce_policy_loss_workspace_size(T, n_seqs) */
+typedef enum flce_kl { FLCE_KL_K1 = 1, FLCE_KL_K2 = 2, FLCE_KL_K3 = 3 } flce_kl;
+FLCE_API size_t flce_policy_loss_workspace_size(int64_t T, int64_t n_seqs);
+FLCE_API flce_status flce_policy_loss(const float* dloss, const float* logp, const float* old_logp,
+                                      const float* ref_logp, const float* advantages,
+                                      int32_t advantages_per_sequence, const int64_t* targets,
+                                      const int64_t* cu_seqlens, int64_t n_seqs, int64_t T, int64_t ignore_index,
+                                      int32_t reduction, float clip_low, float clip_high, float dual_clip,
+                                      float kl_coef, int32_t kl_kind, float* loss, float* dlogp, float* stats,
+                                      int64_t* n_valid, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Preference loss on paired log ratios.  Sequence 2p is pair p's chosen answer,
+ * 2p + 1 the rejected one.  S_i = sum over sequence i's valid tokens of
+ * logp - ref_logp (of logp without ref_logp), divided by their number with
+ * length_normalize; 0 for a sequence without one.  D_p = S_{2p} - S_{2p+1},
+ * h = beta D - margin:
+ *   SIGMOID  (1 - label_smoothing) softplus(-h) + label_smoothing softplus(h)
+ *   HINGE    max(0, 1 - h)
+ *   IPO      (D - 1 / (2 beta))^2
+ * loss = the mean over all n_pairs pairs, the sum, or one per pair (NONE).
+ *   cu_seqlens [2 n_pairs + 1]
+ *   chosen_rewards, rejected_rewards [n_pairs] fp32 or NULL: beta S
+ *   workspace >= flce_preference_loss_workspace_size(n_pairs) */
+typedef enum flce_preference {
+  FLCE_PREFERENCE_SIGMOID = 0,
+  FLCE_PREFERENCE_HINGE = 1,
+  FLCE_PREFERENCE_IPO = 2
+} flce_preference;
+FLCE_API size_t flce_preference_loss_workspace_size(int64_t n_pairs);
+FLCE_API flce_status flce_preference_loss(const float* dloss, const float* logp, const float* ref_logp,
+                                          const int64_t* targets, const int64_t* cu_seqlens, int64_t n_pairs,
+                                          int64_t T, int64_t ignore_index, int32_t reduction, int32_t kind, float beta,
+                                          float label_smoothing, float margin, int32_t length_normalize, float* loss,
+                                          float* dlogp, float* chosen_rewards, float* rejected_rewards,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronizes `stream`, then reads the device status word of the latest call
  * made with `workspace` into *out (an flce_status value). */
 FLCE_API flce_status flce_read_device_status(const void* workspace, void* stream, int32_t* out);
@@ -381,7 +453,9 @@ typedef enum flce_kernel_kind {
   FLCE_KERNEL_ADD_RMS_NORM = 9,   /* residual add, norm, 8-bit output */
   FLCE_KERNEL_NORM_BWD = 10,      /* dx and each block's share of dweight */
   FLCE_KERNEL_NORM_DW = 11,       /* the shares' fixed-order sum */
-  FLCE_KERNEL_KINDS = 12
+  FLCE_KERNEL_POLICY_LOSS = 12,   /* flce_policy_loss, all launches of a call */
+  FLCE_KERNEL_PREFERENCE_LOSS = 13, /* flce_preference_loss, all launches of a call */
+  FLCE_KERNEL_KINDS = 14
 } flce_kernel_kind;
 
 FLCE_API void flce_profile_enable(int32_t on);

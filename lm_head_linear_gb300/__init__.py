@@ -36,8 +36,16 @@ from .binding import (  # noqa: F401
 )
 from .ops import (  # noqa: F401
     AddRMSNorm,
+    PolicyLoss,
+    PreferenceLoss,
     add_rms_norm,
     flce_add_rms_norm,
     flce_add_rms_norm_backward,
     flce_add_rms_norm_backward_workspace_size,
+    flce_policy_loss,
+    flce_policy_loss_workspace_size,
+    flce_preference_loss,
+    flce_preference_loss_workspace_size,
+    policy_loss,
+    preference_loss,
 )

@@ -21,8 +21,9 @@ REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
 STATUS_NAMES = {
     0: "FLCE_OK", 1: "FLCE_ERR_INVALID_ARG", 2: "FLCE_ERR_UNSUPPORTED", 3: "FLCE_ERR_ALIGNMENT",
     4: "FLCE_ERR_WORKSPACE", 5: "FLCE_ERR_CUDA", 6: "FLCE_ERR_TARGET_RANGE", 7: "FLCE_ERR_TIMEOUT",
+    8: "FLCE_ERR_SEQUENCES",
 }
-KERNEL_KINDS = 12
+KERNEL_KINDS = 14
 ABI_VERSION = 2  # FLCE_ABI_VERSION of include/flce.h
 
 # Every symbol the header declares: name -> (restype, argtypes).
@@ -58,6 +59,12 @@ SIGNATURES = {
     "flce_add_rms_norm_backward_workspace_size": (_SZ, [_I64, _I64]),
     "flce_add_rms_norm_backward": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _P, _I32, _P, _P, _I64, _I64, _I64, _P, _P,
                                           _P, _SZ, _P]),
+    "flce_policy_loss_workspace_size": (_SZ, [_I64, _I64]),
+    "flce_policy_loss": (_I32, [_P, _P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _I32, _F32, _F32, _F32, _F32, _I32,
+                                _P, _P, _P, _P, _P, _SZ, _P]),
+    "flce_preference_loss_workspace_size": (_SZ, [_I64]),
+    "flce_preference_loss": (_I32, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _I32, _F32, _F32, _F32, _I32, _P, _P,
+                                    _P, _P, _P, _SZ, _P]),
     "flce_read_device_status": (_I32, [_P, _P, ctypes.POINTER(_I32)]),
     "flce_selftest_wait_timeout": (_I32, [_P, ctypes.c_uint64, _P]),
     "flce_status_string": (ctypes.c_char_p, [_I32]),

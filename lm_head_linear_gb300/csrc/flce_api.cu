@@ -751,6 +751,7 @@ const char* flce_status_string(int32_t st) {
     case FLCE_ERR_CUDA: return "FLCE_ERR_CUDA";
     case FLCE_ERR_TARGET_RANGE: return "FLCE_ERR_TARGET_RANGE";
     case FLCE_ERR_TIMEOUT: return "FLCE_ERR_TIMEOUT";
+    case FLCE_ERR_SEQUENCES: return "FLCE_ERR_SEQUENCES";
     default: return "FLCE_ERR_UNKNOWN";
   }
 }
@@ -774,6 +775,8 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_KERNEL_ADD_RMS_NORM: return "add_rms_norm";
     case FLCE_KERNEL_NORM_BWD: return "norm_bwd";
     case FLCE_KERNEL_NORM_DW: return "norm_dw";
+    case FLCE_KERNEL_POLICY_LOSS: return "policy_loss";
+    case FLCE_KERNEL_PREFERENCE_LOSS: return "preference_loss";
     default: return "unknown";
   }
 }

@@ -1,4 +1,5 @@
-"""The operators around the LM head: the norm in front of it.
+"""The operators around the LM head: the norm in front of it, and the policy and
+preference losses on the log-probabilities it returns.
 
 As in :mod:`.binding`: arguments are checked, outputs and workspaces allocated
 with torch (or taken from the caller), and the library's kernels do the work.
@@ -12,7 +13,7 @@ from typing import Optional
 
 import torch
 
-from .binding import _check, _out, load_library
+from .binding import REDUCTIONS, _check, _out, load_library
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # flce_dtype
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -155,3 +156,167 @@ def _dense_rows(t: torch.Tensor) -> torch.Tensor:
 def add_rms_norm(x, weight, residual=None, eps: float = 1e-6):
     """``(rms_norm(x + residual) * weight, x + residual)``, differentiable in every input."""
     return AddRMSNorm.apply(x, weight, residual, eps)
+
+
+POLICY_REDUCTIONS = {"none": 0, "mean": 1, "sum": 2, "sequence_mean": 3}
+KL_KINDS = {"k1": 1, "k2": 2, "k3": 3}
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+
+
+def flce_policy_loss_workspace_size(T: int, n_seqs: int) -> int:
+    return int(load_library().flce_policy_loss_workspace_size(T, n_seqs))
+
+
+def flce_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: torch.Tensor, targets: torch.Tensor,
+                     ref_logp: Optional[torch.Tensor] = None, cu_seqlens: Optional[torch.Tensor] = None,
+                     per_sequence: bool = False, ignore_index: int = -100, reduction: str = "mean",
+                     clip_low: float = 0.2, clip_high: float = 0.2, dual_clip: float = 0.0, kl_coef: float = 0.0,
+                     kl: str = "k3", dloss: Optional[torch.Tensor] = None, forward: bool = True, grad: bool = True,
+                     workspace: Optional[torch.Tensor] = None, stream=None, out: Optional[dict] = None):
+    """Run ``flce_policy_loss``; returns ``(loss, dlogp, stats, n_valid, workspace)``.
+
+    ``loss`` is a 1-element fp32 tensor ([T] with reduction "none"; None without
+    ``forward``), ``dlogp`` the gradient on logp, already multiplied with ``dloss``
+    (None without ``grad``): pass it to :func:`flce_backward` as ``dlogp``.  ``stats``
+    holds the valid tokens' means of (kl, clipped, log ratio, ratio).  ``advantages``
+    is [T], or with ``per_sequence`` one per sequence of ``cu_seqlens``.  ``out`` may
+    hold preallocated ``loss``, ``dlogp``, ``stats`` and ``n_valid`` tensors.
+    """
+    if not logp.is_cuda or logp.dim() != 1:
+        raise ValueError("logp must be a CUDA tensor [T]")
+    lib = load_library()
+    dev, T = logp.device, logp.shape[0]
+    red = POLICY_REDUCTIONS[reduction]
+    n_seqs = 0
+    if cu_seqlens is not None:
+        n_seqs = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
+        if n_seqs < 0:
+            raise ValueError("cu_seqlens must be a tensor [n_seqs + 1]")
+        _vector("cu_seqlens", cu_seqlens, n_seqs + 1, torch.int64, dev)
+    _vector("logp", logp, T, torch.float32, dev)
+    _vector("old_logp", old_logp, T, torch.float32, dev)
+    _vector("advantages", advantages, n_seqs if per_sequence else T, torch.float32, dev)
+    _vector("targets", targets, T, torch.int64, dev)
+    if ref_logp is not None:
+        _vector("ref_logp", ref_logp, T, torch.float32, dev)
+    if dloss is not None:
+        dloss = dloss.reshape(-1)
+        _vector("dloss", dloss, T if red == 0 else 1, torch.float32, dev)
+    loss = _out(out, "loss", T if red == 0 else 1, torch.float32, dev) if forward else None
+    dlogp = _out(out, "dlogp", T, torch.float32, dev) if grad else None
+    stats = _out(out, "stats", 4, torch.float32, dev)
+    n_valid = _out(out, "n_valid", 1, torch.int64, dev)
+    ws = _ws(lib.flce_policy_loss_workspace_size(T, n_seqs), dev, workspace)
+    _check(lib.flce_policy_loss(
+        dloss.data_ptr() if dloss is not None else None, logp.data_ptr(), old_logp.data_ptr(),
+        ref_logp.data_ptr() if ref_logp is not None else None, advantages.data_ptr(), per_sequence, targets.data_ptr(),
+        cu_seqlens.data_ptr() if cu_seqlens is not None else None, n_seqs, T, ignore_index, red, clip_low, clip_high,
+        dual_clip, kl_coef, KL_KINDS[kl], loss.data_ptr() if forward else None, dlogp.data_ptr() if grad else None,
+        stats.data_ptr(), n_valid.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream, dev)))
+    return loss, dlogp, stats, n_valid, ws
+
+
+class PolicyLoss(torch.autograd.Function):
+    """autograd wrapper of the policy loss, differentiable in logp."""
+
+    @staticmethod
+    def forward(ctx, logp, old_logp, advantages, targets, ref_logp, cu_seqlens, kwargs):
+        logp = logp.contiguous()
+        loss, _, stats, _, ws = flce_policy_loss(logp, old_logp, advantages, targets, ref_logp=ref_logp,
+                                                 cu_seqlens=cu_seqlens, grad=False, **kwargs)
+        ctx.save_for_backward(logp, old_logp, advantages, targets, ref_logp, cu_seqlens)
+        ctx.kwargs = kwargs
+        ctx.mark_non_differentiable(stats)
+        return (loss if kwargs.get("reduction") == "none" else loss.reshape(())), stats
+
+    @staticmethod
+    def backward(ctx, dloss, _):
+        logp, old_logp, advantages, targets, ref_logp, cu_seqlens = ctx.saved_tensors
+        _, dlogp, _, _, _ = flce_policy_loss(logp, old_logp, advantages, targets, ref_logp=ref_logp,
+                                             cu_seqlens=cu_seqlens, dloss=dloss.contiguous(), forward=False,
+                                             **ctx.kwargs)
+        return dlogp, None, None, None, None, None, None
+
+
+def policy_loss(logp, old_logp, advantages, targets, ref_logp=None, cu_seqlens=None, **kwargs):
+    """Clipped policy loss with a KL term, differentiable in ``logp``; returns ``(loss, stats)``.
+    Keyword arguments as :func:`flce_policy_loss` (per_sequence, ignore_index, reduction, clip_low,
+    clip_high, dual_clip, kl_coef, kl)."""
+    return PolicyLoss.apply(logp, old_logp, advantages, targets, ref_logp, cu_seqlens, kwargs)
+
+
+def flce_preference_loss_workspace_size(n_pairs: int) -> int:
+    return int(load_library().flce_preference_loss_workspace_size(n_pairs))
+
+
+def flce_preference_loss(logp: torch.Tensor, targets: torch.Tensor, cu_seqlens: torch.Tensor,
+                         ref_logp: Optional[torch.Tensor] = None, ignore_index: int = -100, reduction: str = "mean",
+                         kind: str = "sigmoid", beta: float = 0.1, label_smoothing: float = 0.0, margin: float = 0.0,
+                         length_normalize: bool = False, dloss: Optional[torch.Tensor] = None, forward: bool = True,
+                         grad: bool = True, workspace: Optional[torch.Tensor] = None, stream=None,
+                         out: Optional[dict] = None):
+    """Run ``flce_preference_loss``; returns ``(loss, dlogp, chosen_rewards, rejected_rewards, workspace)``.
+
+    ``cu_seqlens`` [2 P + 1]: sequence 2p is pair p's chosen answer, 2p + 1 the rejected
+    one.  ``loss`` is a 1-element fp32 tensor ([P] with reduction "none"; None without
+    ``forward``), ``dlogp`` [T] the gradient on logp, already multiplied with ``dloss``
+    (None without ``grad``).  ``out`` may hold preallocated ``loss``, ``dlogp``, ``chosen``
+    and ``rejected`` tensors.
+    """
+    if not logp.is_cuda or logp.dim() != 1:
+        raise ValueError("logp must be a CUDA tensor [T]")
+    lib = load_library()
+    dev, T = logp.device, logp.shape[0]
+    red = REDUCTIONS[reduction]
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] % 2 == 0:
+        raise ValueError("cu_seqlens must be a tensor [2 n_pairs + 1]")
+    P = cu_seqlens.shape[0] // 2
+    _vector("cu_seqlens", cu_seqlens, 2 * P + 1, torch.int64, dev)
+    _vector("logp", logp, T, torch.float32, dev)
+    _vector("targets", targets, T, torch.int64, dev)
+    if ref_logp is not None:
+        _vector("ref_logp", ref_logp, T, torch.float32, dev)
+    if dloss is not None:
+        dloss = dloss.reshape(-1)
+        _vector("dloss", dloss, P if red == 0 else 1, torch.float32, dev)
+    loss = _out(out, "loss", P if red == 0 else 1, torch.float32, dev) if forward else None
+    dlogp = _out(out, "dlogp", T, torch.float32, dev) if grad else None
+    chosen = _out(out, "chosen", P, torch.float32, dev)
+    rejected = _out(out, "rejected", P, torch.float32, dev)
+    ws = _ws(lib.flce_preference_loss_workspace_size(P), dev, workspace)
+    _check(lib.flce_preference_loss(
+        dloss.data_ptr() if dloss is not None else None, logp.data_ptr(),
+        ref_logp.data_ptr() if ref_logp is not None else None, targets.data_ptr(), cu_seqlens.data_ptr(), P, T,
+        ignore_index, red, PREFERENCE_KINDS[kind], beta, label_smoothing, margin, length_normalize,
+        loss.data_ptr() if forward else None, dlogp.data_ptr() if grad else None, chosen.data_ptr(),
+        rejected.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream, dev)))
+    return loss, dlogp, chosen, rejected, ws
+
+
+class PreferenceLoss(torch.autograd.Function):
+    """autograd wrapper of the preference loss, differentiable in logp."""
+
+    @staticmethod
+    def forward(ctx, logp, targets, cu_seqlens, ref_logp, kwargs):
+        logp = logp.contiguous()
+        loss, _, chosen, rejected, _ = flce_preference_loss(logp, targets, cu_seqlens, ref_logp=ref_logp, grad=False,
+                                                            **kwargs)
+        ctx.save_for_backward(logp, targets, cu_seqlens, ref_logp)
+        ctx.kwargs = kwargs
+        ctx.mark_non_differentiable(chosen, rejected)
+        return (loss if kwargs.get("reduction") == "none" else loss.reshape(())), chosen, rejected
+
+    @staticmethod
+    def backward(ctx, dloss, _c, _r):
+        logp, targets, cu_seqlens, ref_logp = ctx.saved_tensors
+        _, dlogp, _, _, _ = flce_preference_loss(logp, targets, cu_seqlens, ref_logp=ref_logp,
+                                                 dloss=dloss.contiguous(), forward=False, **ctx.kwargs)
+        return dlogp, None, None, None, None
+
+
+def preference_loss(logp, targets, cu_seqlens, ref_logp=None, **kwargs):
+    """Preference loss on paired log ratios, differentiable in ``logp``; returns
+    ``(loss, chosen_rewards, rejected_rewards)``.  Keyword arguments as
+    :func:`flce_preference_loss` (ignore_index, reduction, kind, beta, label_smoothing, margin,
+    length_normalize)."""
+    return PreferenceLoss.apply(logp, targets, cu_seqlens, ref_logp, kwargs)
