@@ -324,6 +324,30 @@ FLCE_API flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype
                                                 int64_t T, int64_t Hd, void* dx, float* dweight, void* workspace,
                                                 size_t workspace_bytes, void* stream);
 
+/* ---- the head's product in 8 bits ---------------------------------------------
+ * For rollouts, and for scoring by a policy that is not trained: logits from e4m3
+ * operands with one power-of-two scale (an E8M0 byte s, worth 2^(s - 127); 255 is
+ * NaN) per block of 128 along K.
+ *
+ * flce_quantize_fp8 lays out a matrix: a [rows, K] bf16 or fp32 (row stride lda)
+ *   q        [rows, K] e4m3
+ *   q_scale  [ceil(rows / block_rows), ceil(K/128)], block_rows 128 for weights (128 x 128
+ *            blocks), 1 for activations; the scale rule is flce_add_rms_norm's. */
+FLCE_API flce_status flce_quantize_fp8(const void* a, int32_t a_dtype, int64_t lda, int64_t rows, int64_t K,
+                                       int32_t block_rows, void* q, uint8_t* q_scale, void* stream);
+
+/* y[t, v] = sum_b 2^(x_scale[t, b] + W_scale[v / 128, b] - 254) sum_{k in block b} x[t, k] W[v, k]
+ *   x [T, K] e4m3, x_scale [T, ceil(K/128)];  W [V, K] e4m3, W_scale [ceil(V/128), ceil(K/128)]
+ *   y [T, V] bf16 or fp32 (y_dtype), row stride ldy >= V elements
+ * fp32 accumulation over the whole of K, one rounding to bf16.  K: a multiple of 16
+ * (the last block may be short).  x and W 16-byte aligned and contiguous.
+ *   workspace, workspace_bytes  >= flce_linear_fp8_workspace_size(T, K, V); its status word
+ *                               reports FLCE_ERR_TIMEOUT */
+FLCE_API size_t flce_linear_fp8_workspace_size(int64_t T, int64_t K, int64_t V);
+FLCE_API flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W, const uint8_t* W_scale,
+                                     int64_t T, int64_t K, int64_t V, void* y, int32_t y_dtype, int64_t ldy,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- objectives on logp ------------------------------------------------------
  * Both take the per-token log-probabilities that the forward returns and give
  * the gradient that flce_backward_logp takes as dlogp: forward, loss, backward
@@ -455,7 +479,9 @@ typedef enum flce_kernel_kind {
   FLCE_KERNEL_NORM_DW = 11,       /* the shares' fixed-order sum */
   FLCE_KERNEL_POLICY_LOSS = 12,   /* flce_policy_loss, all launches of a call */
   FLCE_KERNEL_PREFERENCE_LOSS = 13, /* flce_preference_loss, all launches of a call */
-  FLCE_KERNEL_KINDS = 14
+  FLCE_KERNEL_QUANTIZE_FP8 = 14,  /* a matrix to e4m3 with block scales */
+  FLCE_KERNEL_LINEAR_FP8 = 15,    /* the 8-bit head product */
+  FLCE_KERNEL_KINDS = 16
 } flce_kernel_kind;
 
 FLCE_API void flce_profile_enable(int32_t on);

@@ -42,10 +42,13 @@ from .ops import (  # noqa: F401
     flce_add_rms_norm,
     flce_add_rms_norm_backward,
     flce_add_rms_norm_backward_workspace_size,
+    flce_linear_fp8,
+    flce_linear_fp8_workspace_size,
     flce_policy_loss,
     flce_policy_loss_workspace_size,
     flce_preference_loss,
     flce_preference_loss_workspace_size,
+    flce_quantize_fp8,
     policy_loss,
     preference_loss,
 )

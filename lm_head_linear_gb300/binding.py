@@ -23,7 +23,7 @@ STATUS_NAMES = {
     4: "FLCE_ERR_WORKSPACE", 5: "FLCE_ERR_CUDA", 6: "FLCE_ERR_TARGET_RANGE", 7: "FLCE_ERR_TIMEOUT",
     8: "FLCE_ERR_SEQUENCES",
 }
-KERNEL_KINDS = 14
+KERNEL_KINDS = 16
 ABI_VERSION = 2  # FLCE_ABI_VERSION of include/flce.h
 
 # Every symbol the header declares: name -> (restype, argtypes).
@@ -59,6 +59,9 @@ SIGNATURES = {
     "flce_add_rms_norm_backward_workspace_size": (_SZ, [_I64, _I64]),
     "flce_add_rms_norm_backward": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _P, _I32, _P, _P, _I64, _I64, _I64, _P, _P,
                                           _P, _SZ, _P]),
+    "flce_quantize_fp8": (_I32, [_P, _I32, _I64, _I64, _I64, _I32, _P, _P, _P]),
+    "flce_linear_fp8_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "flce_linear_fp8": (_I32, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _I32, _I64, _P, _SZ, _P]),
     "flce_policy_loss_workspace_size": (_SZ, [_I64, _I64]),
     "flce_policy_loss": (_I32, [_P, _P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _I32, _F32, _F32, _F32, _F32, _I32,
                                 _P, _P, _P, _P, _P, _SZ, _P]),

@@ -777,6 +777,8 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_KERNEL_NORM_DW: return "norm_dw";
     case FLCE_KERNEL_POLICY_LOSS: return "policy_loss";
     case FLCE_KERNEL_PREFERENCE_LOSS: return "preference_loss";
+    case FLCE_KERNEL_QUANTIZE_FP8: return "quantize_fp8";
+    case FLCE_KERNEL_LINEAR_FP8: return "linear_fp8";
     default: return "unknown";
   }
 }

@@ -24,7 +24,7 @@ struct Shape {
   int nv, group, threads;
 };
 Shape pick_shape(int64_t T, int64_t Hd, int sms, int nv_many, int threads_many) {
-  const int nvec = static_cast<int>(Hd / norm::kVec);
+  const int nvec = static_cast<int>(Hd / kVec);
   int nv = 1;
   if (T > sms) nv = nv_many;
   while (cdiv(cdiv(nvec, nv), 32) * 32 > norm::max_threads(nv)) nv *= 2;

@@ -1,0 +1,419 @@
+// 8-bit head product: Y = (X sx)(W sw)^T with e4m3 operands and one power-of-two
+// scale per 128 channels of a row of X and per 128 x 128 block of W.
+//
+//   Y[t, v] = sum_b sx[t, b] sw[v / 128, b] sum_{k in block b} X[t, k] W[v, k]
+//
+// The scales are E8M0 bytes, which the tensor cores apply themselves
+// (kind::mxf8f6f4 with block scaling): the products of a block are scaled on
+// their way into the fp32 accumulator, and no partial sum leaves TMEM before the
+// whole K loop is done.
+//
+// Orientation: the vocabulary is the M side (256 rows per SM pair, 128 per CTA)
+// and the tokens are the N side (up to 224 per tile).  A decoding step of a few
+// tokens then runs narrow tiles (N = 32) over wide W tiles, bound by reading W;
+// a prompt runs 256 x 224 tiles.  In the accumulator a lane is a vocabulary row,
+// so a warp's store of one token's logits is contiguous.
+//
+// A CTA has 10 warps: the TMA producer, the MMA issuer (even CTA of the pair),
+// four epilogue warps and four scale warps.  The scale bytes come from their plain
+// row-major arrays: a scale warp loads, for the 32 TMEM lanes it may write, the
+// words of four consecutive K blocks and stores them to TMEM, four blocks a stage.
+// 224, not 256, tokens per tile: two accumulators (448 columns) and four stages
+// of scales (64 columns) fill the 512 columns of TMEM.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "ptx.cuh"
+#include "vec8.cuh"
+
+namespace flce {
+namespace fp8 {
+
+constexpr int kBlockK = 128;                  // bytes of a K block: one swizzled 128-byte row, one scale
+constexpr int kRowsCta = 128;                 // vocabulary rows of one CTA: one row block of W's scales
+constexpr int kABytes = kRowsCta * kBlockK;   // 16 KB
+constexpr int kMaxN = 224;
+constexpr int kMaxStages = 12;
+constexpr int kScaleStages = 4;
+constexpr int kScaleCols = 16;                // columns of a scale stage: A's at +0 (4), B's at +8 (8)
+constexpr int kScaleBase = 2 * kMaxN;         // 448
+constexpr int kEpiWarps = 4;
+constexpr int kScaleWarps = 4;
+constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSmemTail = 512;
+constexpr int kSmemLimit = 232448;
+constexpr int kStatusTimeout = 7;
+constexpr uint64_t kDrainNs = 2000000000ull;
+constexpr uint64_t kSettleNs = 200000ull;
+static_assert(kScaleBase + kScaleStages * kScaleCols <= static_cast<int>(kTmemCols), "TMEM columns");
+
+struct Params {
+  CUtensorMap tmW;   // [V, K] bytes, box 128 x 128 rows
+  CUtensorMap tmX;   // [T, K] bytes, box 128 x N / 2 rows
+  const uint8_t* sx; // [T, kb]
+  const uint8_t* sw; // [ceil(V / 128), kb]
+  void* y;
+  int64_t ldy;
+  int32_t* status;
+  uint64_t timeout_ns;
+  int32_t T, K, V;
+  int32_t kb;        // K blocks
+  int32_t n;         // tokens per tile (a multiple of 32 up to kMaxN)
+  int32_t n_tiles, units;
+  int32_t stages, stage_bytes;
+  int32_t y_f32;
+};
+
+// full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], scale_full[4], scale_empty[4], drain
+struct Smem {
+  uint8_t* stages;
+  uint64_t* bars;
+  uint32_t* tmem_slot;
+  volatile int* abort_flag;
+  __device__ __forceinline__ uint32_t bar(int i) const { return ptx::smem_u32(bars + i); }
+  __device__ __forceinline__ uint32_t full(int i) const { return bar(i); }
+  __device__ __forceinline__ uint32_t empty(int i) const { return bar(kMaxStages + i); }
+  __device__ __forceinline__ uint32_t acc_full(int i) const { return bar(2 * kMaxStages + i); }
+  __device__ __forceinline__ uint32_t acc_empty(int i) const { return bar(2 * kMaxStages + 2 + i); }
+  __device__ __forceinline__ uint32_t scale_full(int i) const { return bar(2 * kMaxStages + 4 + i); }
+  __device__ __forceinline__ uint32_t scale_empty(int i) const { return bar(2 * kMaxStages + 4 + kScaleStages + i); }
+  __device__ __forceinline__ uint32_t drain() const { return bar(2 * kMaxStages + 4 + 2 * kScaleStages); }
+};
+constexpr int kBars = 2 * kMaxStages + 4 + 2 * kScaleStages + 1;
+static_assert(kBars * 8 + 8 <= kSmemTail, "smem tail");
+
+__device__ __forceinline__ void give_up(const Params& p, const Smem& s) {
+  *s.abort_flag = 1;
+  atomicCAS(p.status, 0, kStatusTimeout);
+}
+
+// A ring position: slot and the phase bit its barriers are at.
+struct Slot {
+  int i = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++i == n) i = 0, phase ^= 1u;
+  }
+};
+
+// Unit u: tokens of tile u % n_tiles (fastest: the units in flight share W's rows
+// and the tokens stay in L2), vocabulary pair u / n_tiles.
+struct Unit {
+  int m, t0;
+};
+__device__ __forceinline__ Unit unit_of(const Params& p, int u) {
+  Unit r;
+  r.m = u / p.n_tiles;
+  r.t0 = (u - r.m * p.n_tiles) * p.n;
+  return r;
+}
+
+// Both CTAs: this CTA's 128 rows of W and its half of the tokens.
+__device__ __forceinline__ void producer(const Params& p, const Smem& s, uint32_t rank, int u0, int du) {
+  Slot at;
+  uint32_t used = 0;
+  bool ok = true;
+  const uint32_t tx = 2u * static_cast<uint32_t>(p.stage_bytes);
+  for (int u = u0; u < p.units && ok; u += du) {
+    const Unit un = unit_of(p, u);
+    const int row = (2 * un.m + static_cast<int>(rank)) * kRowsCta;
+    const int tok = un.t0 + static_cast<int>(rank) * (p.n / 2);
+    for (int kb = 0; kb < p.kb; ++kb) {
+      if (!ptx::wait_bounded_cluster(s.empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
+        give_up(p, s);
+        ok = false;
+        break;
+      }
+      if (rank == 0) ptx::mbar_arrive_expect_tx(s.full(at.i), tx);
+      const uint32_t full = ptx::mapa(s.full(at.i), 0);
+      const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes);
+      ptx::tma_load_2d_pair(a, &p.tmW, kb * kBlockK, row, full);
+      ptx::tma_load_2d_pair(a + kABytes, &p.tmX, kb * kBlockK, tok, full);
+      used |= 1u << at.i;
+      at.next(p.stages);
+    }
+  }
+  // the even CTA's barriers count both CTAs' loads: none is in flight once their
+  // last armed phase has completed
+  if (rank == 0)
+    for (int i = 0; i < p.stages; ++i)
+      if (used & (1u << i)) ptx::wait_bounded(s.full(i), i < at.i ? at.phase : at.phase ^ 1u, kDrainNs, nullptr);
+}
+
+// Even CTA only.
+__device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, uint32_t tmem, int u0, int du) {
+  Slot at, sc, acc;
+  bool ok = true;
+  const uint32_t idesc0 = ptx::idesc_mxf8(2 * kRowsCta, static_cast<uint32_t>(p.n), 0);
+  for (int u = u0; u < p.units && ok; u += du) {
+    ok = ptx::wait_bounded_cluster(s.acc_empty(acc.i), acc.phase ^ 1u, p.timeout_ns, s.abort_flag);
+    if (!ok) break;
+    ptx::tc_fence_after();
+    const uint32_t d = tmem + acc.i * kMaxN;
+    for (int kb = 0; kb < p.kb; ++kb) {
+      if ((kb & 3) == 0) {
+        ok = ptx::wait_bounded_cluster(s.scale_full(sc.i), sc.phase, p.timeout_ns, s.abort_flag);
+        if (!ok) break;
+      }
+      ok = ptx::wait_bounded(s.full(at.i), at.phase, p.timeout_ns, s.abort_flag);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes);
+      const uint32_t sf = static_cast<uint32_t>(kb & 3);
+      const uint32_t idesc = idesc0 | (sf << 4) | (sf << 29);
+      const uint32_t sfa = tmem + kScaleBase + sc.i * kScaleCols;
+#pragma unroll
+      for (int k = 0; k < kBlockK / 32; ++k)
+        ptx::mma_mxf8_pair(d, ptx::smem_desc_sw128(a + k * 32, 16, 1024),
+                           ptx::smem_desc_sw128(a + kABytes + k * 32, 16, 1024), idesc, sfa, sfa + 8,
+                           (kb | k) != 0 ? 1u : 0u);
+      ptx::mma_commit_pair(s.empty(at.i), 0x3);
+      at.next(p.stages);
+      if ((kb & 3) == 3 || kb == p.kb - 1) {
+        ptx::mma_commit_pair(s.scale_empty(sc.i), 0x3);
+        sc.next(kScaleStages);
+      }
+    }
+    if (!ok) break;
+    ptx::mma_commit_pair(s.acc_full(acc.i), 0x3);
+    acc.next(2);
+  }
+  if (!ok) give_up(p, s);
+  // every MMA issued so far is done before TMEM is freed
+  ptx::mma_commit_pair(s.drain(), 0x1);
+  ptx::wait_bounded(s.drain(), 0, kDrainNs, nullptr);
+}
+
+// The E8M0 bytes of K blocks 4 g .. 4 g + 3 of one row as a word (127, scale 1, past the end).
+__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int g, int kb, bool words) {
+  if (words) return __ldg(reinterpret_cast<const uint32_t*>(row) + g);
+  uint32_t w = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    w |= static_cast<uint32_t>(4 * g + j < kb ? __ldg(row + 4 * g + j) : 127) << (8 * j);
+  return w;
+}
+
+// Each of the four warps writes the same words to its own quarter of the lanes:
+// row r of A (or B) is lane r % 32, column r / 32, in every quarter.
+__device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, uint32_t tmem, uint32_t rank, int warp,
+                                             int lane, int u0, int du) {
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const bool words_x = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 3) == 0;
+  const bool words_w = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sw) & 3) == 0;
+  const int groups = (p.kb + 3) / 4;
+  const int row_blocks = (p.V + kRowsCta - 1) / kRowsCta;
+  Slot at;
+  for (int u = u0; u < p.units; u += du) {
+    const Unit un = unit_of(p, u);
+    const int rb = 2 * un.m + static_cast<int>(rank);
+    const uint8_t* wrow = p.sw + static_cast<int64_t>(rb < row_blocks ? rb : 0) * p.kb;
+    for (int g = 0; g < groups; ++g) {
+      const uint32_t a = scale_word(wrow, g, p.kb, words_w);
+      uint32_t b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int t = un.t0 + 32 * j + lane;
+        b[j] = 32 * j < p.n && t < p.T ? scale_word(p.sx + static_cast<int64_t>(t) * p.kb, g, p.kb, words_x) : 0x7f7f7f7fu;
+      }
+      if (!ptx::wait_bounded_cluster(s.scale_empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
+        give_up(p, s);
+        return;
+      }
+      ptx::tc_fence_after();
+      __syncwarp();
+      const uint32_t col = tmem + lanes + kScaleBase + at.i * kScaleCols;
+      ptx::tmem_st4(col, a, a, a, a);
+      ptx::tmem_st8(col + 8, b);
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(s.scale_full(at.i), 0));
+      at.next(kScaleStages);
+    }
+  }
+}
+
+// Lane = vocabulary row, column = token: one store per token, contiguous over the warp.
+template <bool F32>
+__device__ __forceinline__ void epilogue(const Params& p, const Smem& s, uint32_t tmem, uint32_t rank, int warp,
+                                         int lane, int u0, int du) {
+  const int q = warp & 3;
+  Slot acc;
+  for (int u = u0; u < p.units; u += du) {
+    const Unit un = unit_of(p, u);
+    const int v = (2 * un.m + static_cast<int>(rank)) * kRowsCta + q * 32 + lane;
+    if (!ptx::wait_bounded_cluster(s.acc_full(acc.i), acc.phase, p.timeout_ns, s.abort_flag)) {
+      give_up(p, s);
+      return;
+    }
+    __syncwarp();
+    ptx::tc_fence_after();
+    const uint32_t col = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.i * kMaxN;
+#pragma unroll 1
+    for (int c = 0; c < p.n; c += 32) {
+      uint32_t r[32];
+      ptx::tmem_ld32(col + c, r);
+      ptx::tmem_wait_ld32(r);
+      const int t0 = un.t0 + c;
+      if (v < p.V) {
+        const int64_t at = static_cast<int64_t>(t0) * p.ldy + v;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (t0 + j < p.T) {
+            if constexpr (F32)
+              static_cast<float*>(p.y)[at + j * p.ldy] = __uint_as_float(r[j]);
+            else
+              static_cast<__nv_bfloat16*>(p.y)[at + j * p.ldy] = __float2bfloat16_rn(__uint_as_float(r[j]));
+          }
+        }
+      }
+    }
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(s.acc_empty(acc.i), 0));
+    acc.next(2);
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_fp8_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem s;
+  s.stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* tail = s.stages + p.stages * p.stage_bytes;
+  s.bars = reinterpret_cast<uint64_t*>(tail);
+  s.tmem_slot = reinterpret_cast<uint32_t*>(tail + kBars * 8);
+  s.abort_flag = reinterpret_cast<volatile int*>(tail + kBars * 8 + 4);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int u0 = static_cast<int>(blockIdx.x >> 1), du = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      ptx::mbar_init(s.full(i), 1);
+      ptx::mbar_init(s.empty(i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(s.acc_full(i), 1);
+      ptx::mbar_init(s.acc_empty(i), 2 * kEpiWarps);
+    }
+    for (int i = 0; i < kScaleStages; ++i) {
+      ptx::mbar_init(s.scale_full(i), 2 * kScaleWarps);
+      ptx::mbar_init(s.scale_empty(i), 1);
+    }
+    ptx::mbar_init(s.drain(), 1);
+    *s.abort_flag = 0;
+    ptx::fence_barrier_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&p.tmW);
+    ptx::prefetch_tmap(&p.tmX);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(s.tmem_slot), kTmemCols);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *s.tmem_slot;
+
+  if (warp == 0) {
+    if (ptx::elect_one()) producer(p, s, rank, u0, du);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0 && ptx::elect_one()) mma_issuer(p, s, tmem, u0, du);
+    __syncwarp();
+  } else if (warp < 2 + kEpiWarps) {
+    if (p.y_f32)
+      epilogue<true>(p, s, tmem, rank, warp, lane, u0, du);
+    else
+      epilogue<false>(p, s, tmem, rank, warp, lane, u0, du);
+    __syncwarp();
+  } else {
+    scale_writer(p, s, tmem, rank, warp, lane, u0, du);
+    __syncwarp();
+  }
+
+  // After an abort the odd CTA's loads may not have been consumed: give a TMA write
+  // still in flight time to land before shared memory is released.
+  if (warp == 0 && *s.abort_flag) {
+    const uint64_t t0 = ptx::globaltimer();
+    while (ptx::globaltimer() - t0 < kSettleNs) {
+    }
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ quantising a matrix
+// a [R, K] -> e4m3 values and one E8M0 byte per block of `rows` x 128, rows = 1 or 128
+// (the scale rule of the norm's 8-bit output).  One CTA per 128 x 128 block: 16
+// threads across a row, 16 rows at a time.
+constexpr int kQuantThreads = 256;
+
+template <typename E, bool SQUARE>
+__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const E* a, int64_t lda, int64_t R, int K, uint8_t* q,
+                                                                 uint8_t* qs) {
+  constexpr int kSteps = 128 / (kQuantThreads / 16);
+  __shared__ float red[kQuantThreads / 32];
+  const int nb = (K + 127) / 128;
+  const int64_t rb = blockIdx.x / nb;
+  const int kb = static_cast<int>(blockIdx.x - rb * nb);
+  const int c = kb * 128 + (threadIdx.x & 15) * kVec;
+  const int64_t r0 = rb * 128 + (threadIdx.x >> 4);
+  float v[kSteps][kVec];
+  float m[kSteps];
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int64_t r = r0 + i * (kQuantThreads / 16);
+    m[i] = 0.0f;
+    if (r < R && c < K) {
+      unpack8<E>(load8(a + r * lda + c), v[i]);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) m[i] = fmaxf(m[i], fabsf(v[i][j]));
+    }
+    amax = fmaxf(amax, m[i]);
+  }
+  if constexpr (SQUARE) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+    __syncthreads();
+    amax = red[0];
+#pragma unroll
+    for (int i = 1; i < kQuantThreads / 32; ++i) amax = fmaxf(amax, red[i]);
+    if (threadIdx.x == 0) qs[rb * nb + kb] = static_cast<uint8_t>(e8m0_of(amax));
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int64_t r = r0 + i * (kQuantThreads / 16);
+    float top = amax;
+    if constexpr (!SQUARE) {
+      top = m[i];
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    }
+    if (r < R && c < K) {
+      const uint32_t e = e8m0_of(top);
+      *reinterpret_cast<uint2*>(q + r * K + c) = to_e4m3x8(v[i], inv_scale(e));
+      if (!SQUARE && (threadIdx.x & 15) == 0) qs[r * nb + kb] = static_cast<uint8_t>(e);
+    }
+  }
+}
+
+}  // namespace fp8
+}  // namespace flce

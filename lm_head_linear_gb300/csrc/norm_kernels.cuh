@@ -13,80 +13,16 @@
 #pragma once
 
 #include <cstdint>
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include "ptx.cuh"
+#include "vec8.cuh"
 
 namespace flce {
 namespace norm {
 
-constexpr int kVec = 8;            // channels per thread and step: one 16-byte bf16 load
-constexpr int kBlockVecs = 16;     // 16 threads x 8 channels: one block of 128
-
 // Threads per CTA for a thread that holds NV vectors (its row values live in
 // registers: 8 NV floats, plus the raw loads).
 __host__ __device__ constexpr int max_threads(int nv) { return nv <= 2 ? 1024 : (nv <= 4 ? 512 : 256); }
-
-// ------------------------------------------------------------------ 8-channel loads and stores
-struct Raw8 {
-  uint4 a, b;  // bf16: a only
-};
-
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
-// Loads that must see this kernel's own aliasing stores as ordered (h may be the
-// residual itself): plain loads.
-__device__ __forceinline__ uint4 ldg_plain(const void* p) { return *static_cast<const uint4*>(p); }
-
-template <typename E>
-__device__ __forceinline__ Raw8 load8(const E* p) {
-  Raw8 r;
-  r.a = ldg_plain(p);
-  if constexpr (sizeof(E) == 4) r.b = ldg_plain(p + 4);
-  return r;
-}
-
-template <typename E>
-__device__ __forceinline__ void unpack8(const Raw8& r, float (&v)[kVec]) {
-  if constexpr (sizeof(E) == 4) {
-    v[0] = __uint_as_float(r.a.x), v[1] = __uint_as_float(r.a.y), v[2] = __uint_as_float(r.a.z);
-    v[3] = __uint_as_float(r.a.w), v[4] = __uint_as_float(r.b.x), v[5] = __uint_as_float(r.b.y);
-    v[6] = __uint_as_float(r.b.z), v[7] = __uint_as_float(r.b.w);
-  } else {
-    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-}
-
-template <typename E>
-__device__ __forceinline__ Raw8 pack8(const float (&v)[kVec]) {
-  Raw8 r;
-  if constexpr (sizeof(E) == 4) {
-    r.a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-    r.b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
-  } else {
-    r.a = make_uint4(ptx::pack_bf16x2(v[0], v[1]), ptx::pack_bf16x2(v[2], v[3]), ptx::pack_bf16x2(v[4], v[5]),
-                     ptx::pack_bf16x2(v[6], v[7]));
-  }
-  return r;
-}
-
-template <typename E>
-__device__ __forceinline__ void store8(E* p, const Raw8& r) {
-  *reinterpret_cast<uint4*>(p) = r.a;
-  if constexpr (sizeof(E) == 4) *reinterpret_cast<uint4*>(p + 4) = r.b;
-}
 
 // Eight weights, bf16 or fp32 (read by every row: they stay in L1).
 __device__ __forceinline__ void load_weight8(const void* w, bool w_f32, int c, float (&v)[kVec]) {
@@ -100,27 +36,6 @@ __device__ __forceinline__ void load_weight8(const void* w, bool w_f32, int c, f
     r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c));
     unpack8<uint16_t>(r, v);
   }
-}
-
-// ------------------------------------------------------------------ e4m3 with a power-of-two scale
-// E8M0 byte of the smallest 2^e with amax / 2^e <= 448 = 1.75 * 2^8, e >= -126.
-// From amax's own exponent and mantissa (amax is finite and not negative).
-__device__ __forceinline__ uint32_t e8m0_of(float amax) {
-  const uint32_t bits = __float_as_uint(amax);
-  const int e = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return static_cast<uint32_t>(max(e, 1));
-}
-
-// 2^-(e - 127) for an e8m0_of() byte (1 .. 248): exact.
-__device__ __forceinline__ float inv_scale(uint32_t e8m0) { return __uint_as_float((254u - e8m0) << 23); }
-
-// Eight floats to e4m3, round to nearest even, |v| > 448 to 448, NaN kept.
-__device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[kVec], float inv) {
-  uint16_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(v[2 * i + 1] * inv), "f"(v[2 * i] * inv));
-  return make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16));
 }
 
 // ------------------------------------------------------------------ reductions

@@ -1,5 +1,6 @@
-"""The operators around the LM head: the norm in front of it, and the policy and
-preference losses on the log-probabilities it returns.
+"""The operators around the LM head: the norm in front of it, its
+product in 8 bits, and the policy and preference losses on the log-probabilities
+it returns.
 
 As in :mod:`.binding`: arguments are checked, outputs and workspaces allocated
 with torch (or taken from the caller), and the library's kernels do the work.
@@ -156,6 +157,66 @@ def _dense_rows(t: torch.Tensor) -> torch.Tensor:
 def add_rms_norm(x, weight, residual=None, eps: float = 1e-6):
     """``(rms_norm(x + residual) * weight, x + residual)``, differentiable in every input."""
     return AddRMSNorm.apply(x, weight, residual, eps)
+
+
+# Scales are E8M0 bytes: torch's float8_e8m0fnu, or the bytes as uint8.
+_SCALES = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _blocks(name: str, q: torch.Tensor, scale: torch.Tensor, block_rows: int, device):
+    if q.dtype != torch.float8_e4m3fn or q.dim() != 2 or q.device != device or not q.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float8_e4m3fn matrix on {device}")
+    want = ((q.shape[0] + block_rows - 1) // block_rows, (q.shape[1] + 127) // 128)
+    if scale.dtype not in _SCALES or scale.shape != want or scale.device != device or not scale.is_contiguous():
+        raise ValueError(f"{name}'s scales must be a contiguous float8_e8m0fnu or uint8 tensor of shape {want} on {device}, "
+                         f"got {scale.dtype} {tuple(scale.shape)} on {scale.device}")
+
+
+def flce_quantize_fp8(a: torch.Tensor, block_rows: int = 128, stream=None, out: Optional[dict] = None):
+    """Run ``flce_quantize_fp8``; returns ``(q float8_e4m3fn [rows, K], q_scale float8_e8m0fnu)``: one scale
+    per ``block_rows`` x 128 block, 128 for weights, 1 for activations.  ``out`` may hold preallocated
+    ``q`` and ``q_scale`` tensors."""
+    if not a.is_cuda or a.dim() != 2:
+        raise ValueError("a must be a CUDA matrix")
+    dev, (rows, K) = a.device, a.shape
+    lda = _rows("a", a, a.shape, dev)
+    q = _out(out, "q", (rows, K), torch.float8_e4m3fn, dev)
+    qs = _out(out, "q_scale", ((rows + block_rows - 1) // max(block_rows, 1), (K + 127) // 128), torch.float8_e8m0fnu, dev)
+    _check(load_library().flce_quantize_fp8(a.data_ptr(), _DTYPES[a.dtype], lda, rows, K, block_rows, q.data_ptr(),
+                                            qs.data_ptr(), _stream(stream, dev)))
+    return q, qs
+
+
+def flce_linear_fp8_workspace_size(T: int, K: int, V: int) -> int:
+    return int(load_library().flce_linear_fp8_workspace_size(T, K, V))
+
+
+def flce_linear_fp8(x: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, W_scale: torch.Tensor,
+                    dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None, stream=None,
+                    out: Optional[dict] = None):
+    """Run ``flce_linear_fp8``; returns ``(y [T, V], workspace)`` in ``dtype`` (bfloat16 or float32).
+
+    ``x`` [T, K] and ``W`` [V, K] are float8_e4m3fn with one E8M0 scale per row and 128
+    channels (``x_scale`` [T, ceil(K/128)]) and per 128 x 128 block (``W_scale``): what
+    :func:`flce_add_rms_norm` and :func:`flce_quantize_fp8` write.  ``out`` may hold a
+    preallocated ``y``, whose rows may be longer than V.
+    """
+    if not x.is_cuda or x.dim() != 2 or W.dim() != 2 or W.shape[1] != x.shape[1]:
+        raise ValueError("x [T, K] and W [V, K] must be CUDA matrices of equal K")
+    lib = load_library()
+    dev, (T, K), V = x.device, x.shape, W.shape[0]
+    _blocks("x", x, x_scale, 1, dev)
+    _blocks("W", W, W_scale, 128, dev)
+    if dtype not in _DTYPES:
+        raise ValueError("dtype must be bfloat16 or float32")
+    y = (out or {}).get("y")
+    if y is None:
+        y = torch.empty((T, V), dtype=dtype, device=dev)
+    ldy = _rows("out['y']", y, torch.Size((T, V)), dev, (dtype,))
+    ws = _ws(256, dev, workspace)
+    _check(lib.flce_linear_fp8(x.data_ptr(), x_scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(), T, K, V, y.data_ptr(),
+                               _DTYPES[dtype], ldy, ws.data_ptr(), ws.numel(), _stream(stream, dev)))
+    return y, ws
 
 
 POLICY_REDUCTIONS = {"none": 0, "mean": 1, "sum": 2, "sequence_mean": 3}
