@@ -1,6 +1,7 @@
 // Host side of the policy and preference losses of include/flce.h.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "flce_host.cuh"
 #include "loss_kernels.cuh"
@@ -43,6 +44,61 @@ PairLayout pair_layout(int64_t P) {
   off = align_up(off + sizeof(int32_t) * std::max<int64_t>(P, 1), 256);
   L.total = off;
   return L;
+}
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+// CTAs of the largest cluster these kernels may use on a device: 16 where the
+// device schedules it (queried once), else the portable 8.
+flce_status largest_cluster(int dev, int* ctas) {
+  static std::mutex mu;
+  static int known[64] = {};
+  std::lock_guard<std::mutex> lk(mu);
+  if (known[dev] == 0) {
+    const void* kernels[] = {reinterpret_cast<const void*>(loss::policy_cluster_kernel<1>),
+                             reinterpret_cast<const void*>(loss::policy_cluster_kernel<2>),
+                             reinterpret_cast<const void*>(loss::policy_cluster_kernel<4>),
+                             reinterpret_cast<const void*>(loss::preference_kernel<true>)};
+    int most = loss::kClusterCtas;
+    for (const void* k : kernels) {
+      CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+      cudaLaunchAttribute at{};
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = loss::kClusterCtas, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(loss::kClusterCtas);
+      cfg.blockDim = dim3(loss::kClusterThreads);
+      cfg.attrs = &at, cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        most = 8;
+      }
+    }
+    known[dev] = most;
+  }
+  *ctas = known[dev];
+  return FLCE_OK;
+}
+
+template <typename P>
+flce_status launch_cluster(void (*kernel)(P), const P& p, int64_t grid, int ctas, int threads, cudaStream_t s) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(ctas), at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
+  return FLCE_OK;
+}
+
+int pow2_up(int64_t v, int most) {
+  int r = 1;
+  while (r < v && r < most) r *= 2;
+  return r;
 }
 
 flce_status check_workspace(const void* ws, size_t bytes, size_t need) {
@@ -108,14 +164,29 @@ flce_status flce_policy_loss(const float* dloss, const float* logp, const float*
   p.block_sum = reinterpret_cast<double*>(ws + L.sum_off);
   p.block_count = reinterpret_cast<int32_t*>(ws + L.count_off);
   p.seq_count = reinterpret_cast<int32_t*>(ws + L.seq_off);
-  p.blocks = static_cast<int32_t>(L.blocks);
-  CUDA_TRY(cudaMemsetAsync(ws, 0, kHeaderBytes, s));
-  if (reduction == FLCE_REDUCTION_SEQUENCE_MEAN)
-    CUDA_TRY(cudaMemsetAsync(p.seq_count, 0, sizeof(int32_t) * std::max<int64_t>(n_seqs, 1), s));
+  p.vec = !(off16(logp) || off16(old_logp) || off16(ref_logp) || (!advantages_per_sequence && off16(advantages)) ||
+            off16(targets) || off16(dlogp) ||
+            (reduction == FLCE_REDUCTION_NONE && (off16(loss) || off16(dloss))));
+  int most = 0;
+  if ((st = largest_cluster(dev, &most)) != FLCE_OK) return st;
   KernelScope ks(FLCE_KERNEL_POLICY_LOSS, s, 20.0 * T, T * (12.0 + (ref_logp ? 4.0 : 0.0) + 8.0 + (dlogp ? 4.0 : 0.0)));
-  loss::policy_count_kernel<<<p.blocks, loss::kPolicyThreads, 0, s>>>(p);
-  loss::policy_main_kernel<<<p.blocks, loss::kPolicyThreads, 0, s>>>(p);
-  loss::policy_reduce_kernel<<<1, loss::kPolicyThreads, 0, s>>>(p);
+  constexpr int64_t kCtaTokens = loss::kClusterThreads * loss::kGroup;
+  if (T <= most * kCtaTokens * 4) {
+    p.blocks = pow2_up(cdiv(T, kCtaTokens), most);
+    const int64_t groups = cdiv(T, kCtaTokens * p.blocks);
+    st = groups <= 1   ? launch_cluster(loss::policy_cluster_kernel<1>, p, p.blocks, p.blocks, loss::kClusterThreads, s)
+         : groups == 2 ? launch_cluster(loss::policy_cluster_kernel<2>, p, p.blocks, p.blocks, loss::kClusterThreads, s)
+                       : launch_cluster(loss::policy_cluster_kernel<4>, p, p.blocks, p.blocks, loss::kClusterThreads, s);
+    if (st != FLCE_OK) return st;
+  } else {
+    p.blocks = static_cast<int32_t>(L.blocks);
+    CUDA_TRY(cudaMemsetAsync(ws, 0, kHeaderBytes, s));
+    if (reduction == FLCE_REDUCTION_SEQUENCE_MEAN)
+      CUDA_TRY(cudaMemsetAsync(p.seq_count, 0, sizeof(int32_t) * std::max<int64_t>(n_seqs, 1), s));
+    loss::policy_count_kernel<<<p.blocks, loss::kPolicyThreads, 0, s>>>(p);
+    loss::policy_main_kernel<<<p.blocks, loss::kPolicyThreads, 0, s>>>(p);
+    loss::policy_reduce_kernel<<<1, loss::kPolicyThreads, 0, s>>>(p);
+  }
   ks.done();
   return check_launch("policy_loss");
 }
@@ -174,8 +245,20 @@ flce_status flce_preference_loss(const float* dloss, const float* logp, const fl
   p.pair_loss = reinterpret_cast<double*>(ws + L.loss_off);
   p.pair_bad = reinterpret_cast<int32_t*>(ws + L.bad_off);
   KernelScope ks(FLCE_KERNEL_PREFERENCE_LOSS, s, 4.0 * T, T * (12.0 + (ref_logp ? 4.0 : 0.0) + (dlogp ? 4.0 : 0.0)));
-  loss::preference_kernel<<<p.P, loss::kPairThreads, 0, s>>>(p);
-  loss::preference_reduce_kernel<<<1, loss::kPairThreads, 0, s>>>(p);
+  p.vec = !(off16(logp) || off16(ref_logp) || off16(targets) || off16(dlogp));
+  int most = 0;
+  if ((st = largest_cluster(dev, &most)) != FLCE_OK) return st;
+  const int64_t mean = cdiv(T, n_pairs);
+  if (cdiv(n_pairs, most) * std::max<int64_t>(mean, 512) <= 8192) {
+    p.ctas = pow2_up(n_pairs, most);
+    st = launch_cluster(loss::preference_kernel<true>, p, p.ctas, p.ctas, loss::kPairThreads, s);
+  } else {
+    // enough CTAs to fill the device, of at least 2048 tokens each
+    p.ctas = pow2_up(std::min<int64_t>(mean / 2048, 2 * sms / n_pairs), 8);
+    st = launch_cluster(loss::preference_kernel<false>, p, n_pairs * p.ctas, p.ctas, loss::kPairThreads, s);
+    if (st == FLCE_OK) loss::preference_reduce_kernel<<<1, loss::kReduceThreads, 0, s>>>(p);
+  }
+  if (st != FLCE_OK) return st;
   ks.done();
   return check_launch("preference_loss");
 }

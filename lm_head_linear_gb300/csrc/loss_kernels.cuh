@@ -13,6 +13,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "ptx.cuh"
+
 namespace flce {
 namespace loss {
 
@@ -67,7 +69,8 @@ struct PolicyParams {
   int32_t* seq_count;    // [S] valid tokens of each sequence (SEQUENCE_MEAN)
   int32_t* block_count;  // [blocks]
   double* block_sum;     // [blocks][5]
-  int32_t blocks;
+  int32_t blocks;        // CTAs of the launches over token blocks, or of the one cluster
+  int32_t vec;           // every per-token array is 16-byte aligned
 };
 
 struct PolicyTerm {
@@ -224,6 +227,304 @@ __global__ void __launch_bounds__(kPolicyThreads) policy_reduce_kernel(const Pol
   if (p.n_valid) *p.n_valid = n;
 }
 
+// ------------------------------------------------------------------ policy loss in one launch
+// Up to kClusterCtas * 512 * 16 tokens: one cluster of CTAs.  A token's loss and
+// gradient do not depend on how many tokens count; only the common weight does.
+// So every thread reads its tokens once and keeps the unscaled gradients in
+// registers while the counts go round the cluster through distributed shared
+// memory (or, per sequence, through integer atomics in the workspace), and scales
+// and stores them after one cluster barrier.  No second launch, no second reading.
+constexpr int kClusterCtas = 16;
+constexpr int kClusterThreads = 512;
+constexpr int kGroup = 4;            // consecutive tokens of a thread and step
+constexpr int kCuShared = 4096;      // sequence offsets kept in shared memory
+
+__device__ __forceinline__ float4 load4(const float* p, int64_t t, int n, bool vec) {
+  if (vec) return __ldg(reinterpret_cast<const float4*>(p + t));
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (n > 0) v.x = __ldg(p + t);
+  if (n > 1) v.y = __ldg(p + t + 1);
+  if (n > 2) v.z = __ldg(p + t + 2);
+  if (n > 3) v.w = __ldg(p + t + 3);
+  return v;
+}
+
+__device__ __forceinline__ void store4(float* p, int64_t t, int n, bool vec, const float (&v)[kGroup]) {
+  if (vec) {
+    *reinterpret_cast<float4*>(p + t) = make_float4(v[0], v[1], v[2], v[3]);
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j)
+    if (j < n) p[t + j] = v[j];
+}
+
+// Bit j: token t + j counts by its target.
+__device__ __forceinline__ uint32_t valid4(const int64_t* y, int64_t ignore, int64_t t, int n, bool vec) {
+  if (vec) {
+    const longlong2 a = __ldg(reinterpret_cast<const longlong2*>(y + t));
+    const longlong2 b = __ldg(reinterpret_cast<const longlong2*>(y + t + 2));
+    return (a.x != ignore ? 1u : 0u) | (a.y != ignore ? 2u : 0u) | (b.x != ignore ? 4u : 0u) | (b.y != ignore ? 8u : 0u);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j)
+    if (j < n && __ldg(y + t + j) != ignore) m |= 1u << j;
+  return m;
+}
+
+__device__ __forceinline__ float lane4(const float4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
+
+__device__ __forceinline__ float warp_total(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// The two halves of the cluster barrier; every thread of the warp together.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The offsets of the sequences: from shared memory where they fit, else from global.
+struct Offsets {
+  const int32_t* sh;
+  const int64_t* cu;
+  int n;       // sequences
+  __device__ __forceinline__ int64_t at(int i) const { return sh ? sh[i] : __ldg(cu + i); }
+  // as find_sequence()
+  __device__ __forceinline__ int find(int64_t t) const {
+    int lo = 0, hi = n + 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (at(mid) > t) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo > n ? -1 : lo - 1;
+  }
+  // the sequence of token t + 1 .. from the one of an earlier token
+  __device__ __forceinline__ int step(int s, int64_t t) const {
+    if (s < 0) return find(t);
+    while (s < n && at(s + 1) <= t) ++s;
+    return s < n ? s : -1;
+  }
+};
+
+template <int NG>
+__global__ void __launch_bounds__(kClusterThreads) policy_cluster_kernel(const PolicyParams p) {
+  constexpr int kWarps = kClusterThreads / 32;
+  __shared__ int32_t cu_sh[kCuShared];
+  __shared__ float warp_sum[kWarps][kSums];
+  __shared__ int warp_n[kWarps];
+  __shared__ int cta_n[kClusterCtas];              // written by the cluster's CTAs
+  __shared__ double cta_sum[kClusterCtas][kSums];  // CTA 0's: written by all
+  __shared__ int total;
+  const int rank = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ctas = p.blocks;
+  const bool seq_mean = p.reduction == kSequenceMean;
+  const bool by_seq = seq_mean || p.adv_per_seq;
+
+  if (seq_mean)
+    for (int i = rank * kClusterThreads + tid; i < p.S; i += ctas * kClusterThreads) p.seq_count[i] = 0;
+  Offsets off{by_seq && p.S < kCuShared ? cu_sh : nullptr, p.cu, p.S};
+  bool bad = false;
+  if (p.cu) {
+    // every CTA reads what it keeps; otherwise the CTAs share the check
+    const int first = off.sh ? tid : rank * kClusterThreads + tid;
+    const int step = off.sh ? kClusterThreads : ctas * kClusterThreads;
+    for (int i = first; i <= p.S; i += step) {
+      const int64_t a = i ? p.cu[i - 1] : 0, b = p.cu[i];
+      bad = bad || b < a || b > p.T;
+      if (off.sh) cu_sh[i] = static_cast<int32_t>(min(max(b, int64_t(0)), int64_t(p.T)));
+    }
+  }
+  const int64_t first_tok = p.cu ? p.cu[0] : 0, end_tok = p.cu ? p.cu[p.S] : p.T;
+  bad = __syncthreads_or(bad);
+  if (rank == 0 && tid == 0) *p.status = 0;
+  cluster_arrive();  // zeroed counts, and: every CTA of the cluster is running
+
+  float grad[NG][kGroup], val[NG][kGroup];
+  uint32_t mask[NG];
+  int seq0[NG];
+  float sum[kSums] = {};
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+    const int64_t t = static_cast<int64_t>(kGroup) * ((static_cast<int64_t>(k) * ctas + rank) * kClusterThreads + tid);
+    const int left = static_cast<int>(min(max(p.T - t, int64_t(0)), int64_t(kGroup)));
+    const bool vec = p.vec && left == kGroup;
+    mask[k] = 0;
+    seq0[k] = -1;
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) grad[k][j] = val[k][j] = 0.0f;
+    if (left > 0) {
+      uint32_t m = valid4(p.targets, p.ignore_index, t, left, vec);
+      const float4 lp = load4(p.logp, t, left, vec), old = load4(p.old_logp, t, left, vec);
+      float4 ref = make_float4(0.0f, 0.0f, 0.0f, 0.0f), adv = ref;
+      if (p.ref) ref = load4(p.ref, t, left, vec);
+      if (!p.adv_per_seq) adv = load4(p.adv, t, left, vec);
+      if (p.cu) {
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+          if (t + j < first_tok || t + j >= end_tok) m &= ~(1u << j);
+      }
+      int s = -1;
+      if (by_seq && m) {
+        s = seq0[k] = off.find(t + __ffs(m) - 1);
+        if (s < 0) m = 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        if (!(m >> j & 1u)) continue;
+        float A = lane4(adv, j);
+        if (by_seq) {
+          s = off.step(s, t + j);
+          if (s < 0) {  // only where cu is not in order
+            m &= ~(1u << j);
+            continue;
+          }
+          if (p.adv_per_seq) A = __ldg(p.adv + s);
+        }
+        const PolicyTerm o = policy_token(p, lane4(lp, j), lane4(old, j), lane4(ref, j), A);
+        grad[k][j] = o.grad;
+        val[k][j] = o.loss;
+        sum[0] += o.loss, sum[1] += o.kl, sum[2] += o.cut, sum[3] += o.d, sum[4] += o.rho;
+        ++n;
+      }
+      mask[k] = m;
+    }
+  }
+
+  cluster_wait();
+  if (seq_mean) {
+    // valid tokens of each sequence: one atomic for a warp whose tokens lie in one
+    // sequence, else one for each run of a thread's tokens
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      const int64_t t = static_cast<int64_t>(kGroup) * ((static_cast<int64_t>(k) * ctas + rank) * kClusterThreads + tid);
+      int s = seq0[k], run = 0, last = s;
+      bool one = true;
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j)
+        if (mask[k] >> j & 1u) {
+          s = off.step(s, t + j);
+          one = one && s == seq0[k];
+          last = s;
+        }
+      const unsigned has = __ballot_sync(0xffffffffu, mask[k] != 0);
+      if (has == 0) continue;
+      const int lead = __shfl_sync(0xffffffffu, seq0[k], __ffs(has) - 1);
+      const bool same = mask[k] == 0 || (one && seq0[k] == lead);
+      if (__all_sync(0xffffffffu, same)) {
+        const int c = __reduce_add_sync(0xffffffffu, __popc(mask[k]));
+        if (lane == 0) atomicAdd(p.seq_count + lead, c);
+      } else if (mask[k]) {
+        s = last = seq0[k];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j)
+          if (mask[k] >> j & 1u) {
+            s = off.step(s, t + j);
+            if (s != last) {
+              atomicAdd(p.seq_count + last, run);
+              run = 0, last = s;
+            }
+            ++run;
+          }
+        atomicAdd(p.seq_count + last, run);
+      }
+    }
+    cluster_arrive();
+    cluster_wait();
+    // sequences with a valid token, counted by every CTA
+    int c = 0;
+    for (int i = tid; i < p.S; i += kClusterThreads) c += __ldcg(p.seq_count + i) > 0;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) warp_n[warp] = c;
+    __syncthreads();
+    if (tid == 0) {
+      int a = 0;
+      for (int i = 0; i < kWarps; ++i) a += warp_n[i];
+      total = a;
+    }
+    __syncthreads();
+    const float scale = 1.0f / fmaxf(static_cast<float>(total), 1.0f);
+    sum[0] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+      const int64_t t = static_cast<int64_t>(kGroup) * ((static_cast<int64_t>(k) * ctas + rank) * kClusterThreads + tid);
+      int s = seq0[k];
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j)
+        if (mask[k] >> j & 1u) {
+          s = off.step(s, t + j);
+          const float w = scale / static_cast<float>(__ldcg(p.seq_count + s));
+          grad[k][j] *= w;
+          sum[0] = fmaf(val[k][j], w, sum[0]);
+        }
+    }
+  }
+
+  // this CTA's sums: fp32 in a warp, 64 bits across warps; one thread per sum pushes them
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) {
+    const float v = warp_total(sum[i]);
+    if (lane == 0) warp_sum[warp][i] = v;
+  }
+  n = __reduce_add_sync(0xffffffffu, n);
+  __syncthreads();  // warp_n may still be read above
+  if (lane == 0) warp_n[warp] = n;
+  __syncthreads();
+  if (tid < kSums) {
+    double v = 0.0;
+    for (int i = 0; i < kWarps; ++i) v += static_cast<double>(warp_sum[i][tid]);
+    const uint32_t to = ptx::mapa(ptx::smem_u32(&cta_sum[rank][tid]), 0);
+    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(v) : "memory");
+  } else if (tid >= 32 && tid < 32 + ctas) {
+    int a = 0;
+    for (int i = 0; i < kWarps; ++i) a += warp_n[i];
+    ptx::st_shared_cluster_u32(ptx::mapa(ptx::smem_u32(&cta_n[rank]), tid - 32), static_cast<uint32_t>(a));
+  }
+  cluster_arrive();
+  cluster_wait();
+
+  int valid = 0;
+  for (int i = 0; i < ctas; ++i) valid += cta_n[i];
+  const float scale = p.reduction == kMean ? 1.0f / fmaxf(static_cast<float>(valid), 1.0f) : 1.0f;
+  const float up = p.dloss && p.reduction != kNone ? p.dloss[0] : 1.0f;
+#pragma unroll
+  for (int k = 0; k < NG; ++k) {
+    const int64_t t = static_cast<int64_t>(kGroup) * ((static_cast<int64_t>(k) * ctas + rank) * kClusterThreads + tid);
+    const int left = static_cast<int>(min(max(p.T - t, int64_t(0)), int64_t(kGroup)));
+    if (left <= 0) continue;
+    const bool vec = p.vec && left == kGroup;
+    if (p.dlogp) {
+      float4 u = make_float4(up, up, up, up);
+      if (p.reduction == kNone && p.dloss) u = load4(p.dloss, t, left, vec);
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) grad[k][j] = mask[k] >> j & 1u ? grad[k][j] * scale * lane4(u, j) : 0.0f;
+      store4(p.dlogp, t, left, vec, grad[k]);
+    }
+    if (p.loss && p.reduction == kNone) store4(p.loss, t, left, vec, val[k]);
+  }
+  if (rank == 0 && tid < kSums) {
+    double v = 0.0;
+    for (int i = 0; i < ctas; ++i) v += cta_sum[i][tid];
+    const double inv = valid > 0 ? 1.0 / static_cast<double>(valid) : 0.0;
+    if (tid == 0) {
+      if (p.loss && p.reduction != kNone) p.loss[0] = static_cast<float>(p.reduction == kMean ? v * inv : v);
+      if (p.n_valid) *p.n_valid = valid;
+    } else if (p.stats) {
+      p.stats[tid - 1] = static_cast<float>(v * inv);
+    }
+  }
+  if (bad && tid == 0) atomicCAS(p.status, 0, kStatusSequences);
+}
+
 // ------------------------------------------------------------------ preference loss
 struct PreferenceParams {
   const float* dloss;    // [1] or [P] (NONE), nullptr: ones
@@ -243,6 +544,8 @@ struct PreferenceParams {
   int32_t* status;
   int32_t* pair_bad;     // [P]
   double* pair_loss;     // [P]
+  int32_t ctas;          // CTAs of a cluster
+  int32_t vec;           // every per-token array is 16-byte aligned
 };
 
 __device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
@@ -264,71 +567,178 @@ __device__ __forceinline__ void pair_loss(const PreferenceParams& p, float D, fl
   }
 }
 
-constexpr int kPairThreads = 256;
+constexpr int kPairThreads = 512;    // 256 for the chosen answer, 256 for the rejected one
+constexpr int kSide = kPairThreads / 2;
+constexpr int kSideWarps = kSide / 32;
+constexpr int kKept = 8;             // steps whose mask bits a thread keeps for the second pass
+constexpr int kPairCtas = 16;
 
-// One block per pair: the sums of both sequences, the pair's loss, then the
-// gradient, which is one number per sequence.
+// Both answers of a pair at once, one per half of the CTA.  One reading gives the
+// sums; the gradient is one number per sequence, so the second pass only stores
+// (the mask bits of the first 8 x 1024 tokens stay in a register).
+//   SOLO   one cluster holds every pair, CTA r takes pairs r, r + CTAs, ...; the
+//          scalar loss is summed through distributed shared memory: one launch.
+//   else   one cluster per pair, whose CTAs share the pair's tokens and exchange
+//          their sums; preference_reduce_kernel adds the pairs' losses.
+template <bool SOLO>
 __global__ void __launch_bounds__(kPairThreads) preference_kernel(const PreferenceParams p) {
-  __shared__ double sh[kPairThreads / 32];
-  __shared__ int sh_n[kPairThreads / 32];
+  __shared__ float warp_s[kPairThreads / 32];
+  __shared__ int warp_n[kPairThreads / 32];
+  __shared__ double cta_s[2][kPairCtas];  // by CTA of the cluster: sums of the two answers; SOLO: [0] the losses
+  __shared__ int cta_n[2][kPairCtas];     // counts; SOLO: [0] malformed pairs
   __shared__ float slope_of[2];
-  const int pair = blockIdx.x;
-  int64_t at[3];
-  bool bad = false;
-  for (int i = 0; i < 3; ++i) {
-    const int64_t v = p.cu[2 * static_cast<int64_t>(pair) + i];
-    at[i] = min(max(v, int64_t(0)), p.T);  // no access outside [0, T) whatever cu holds
-    bad = bad || v != at[i];
-  }
-  bad = bad || at[1] < at[0] || at[2] < at[1];
-  double S[2];
-  int n[2];
-  for (int side = 0; side < 2; ++side) {
-    float s = 0.0f;
-    int c = 0;
-    for (int64_t t = at[side] + threadIdx.x; t < at[side + 1]; t += kPairThreads)
-      if (p.targets[t] != p.ignore_index) {
-        s += p.ref ? p.logp[t] - p.ref[t] : p.logp[t];
-        ++c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int side = tid / kSide, i = tid - side * kSide;
+  const int ctas = p.ctas;                // of a cluster
+  const int rank = blockIdx.x % ctas;
+  const int share = SOLO ? 1 : ctas;      // CTAs working on one pair
+  const int part = SOLO ? 0 : rank;
+  cluster_arrive();  // matched by the wait before the first access to another CTA
+  bool arrived = true;
+  double loss_sum = 0.0;
+  int bad_sum = 0;
+  for (int pair = SOLO ? rank : blockIdx.x / ctas; pair < p.P; pair += SOLO ? ctas : p.P) {
+    int64_t at[3];
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const int64_t v = p.cu[2 * static_cast<int64_t>(pair) + k];
+      at[k] = min(max(v, int64_t(0)), p.T);  // no access outside [0, T) whatever cu holds
+      bad = bad || v != at[k];
+    }
+    bad = bad || at[1] < at[0] || at[2] < at[1];
+    const int64_t lo = side ? at[1] : at[0], hi = side ? at[2] : at[1];
+    const int64_t g0 = lo & ~int64_t(kGroup - 1);
+    const int64_t stride = static_cast<int64_t>(kGroup) * kSide * share;
+    float sum = 0.0f;
+    int n = 0, step = 0;
+    uint32_t kept = 0;
+    for (int64_t t = g0 + static_cast<int64_t>(kGroup) * (part * kSide + i); t < hi; t += stride, ++step) {
+      const int left = static_cast<int>(min(p.T - t, int64_t(kGroup)));
+      const bool vec = p.vec && left == kGroup;
+      uint32_t m = valid4(p.targets, p.ignore_index, t, left, vec);
+      const float4 lp = load4(p.logp, t, left, vec);
+      float4 ref = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (p.ref) ref = load4(p.ref, t, left, vec);
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) {
+        if (t + j < lo || t + j >= hi) m &= ~(1u << j);
+        if (m >> j & 1u) sum += lane4(lp, j) - lane4(ref, j);
       }
-    S[side] = block_sum<double, kPairThreads>(static_cast<double>(s), sh);
-    n[side] = block_sum<int, kPairThreads>(c, sh_n);
+      n += __popc(m);
+      if (step < kKept) kept |= m << (4 * step);
+    }
+    const float ws = warp_total(sum);
+    const int wn = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) warp_s[warp] = ws, warp_n[warp] = wn;
+    __syncthreads();
+    if (warp == 0) {
+      // lanes 0 .. 7: the chosen answer's warps, 8 .. 15 the rejected one's
+      double S = lane < 2 * kSideWarps ? static_cast<double>(warp_s[lane]) : 0.0;
+      int c = lane < 2 * kSideWarps ? warp_n[lane] : 0;
+#pragma unroll
+      for (int d = kSideWarps / 2; d > 0; d >>= 1) {
+        S += __shfl_xor_sync(0xffffffffu, S, d);
+        c += __shfl_xor_sync(0xffffffffu, c, d);
+      }
+      double S0 = __shfl_sync(0xffffffffu, S, 0), S1 = __shfl_sync(0xffffffffu, S, kSideWarps);
+      int c0 = __shfl_sync(0xffffffffu, c, 0), c1 = __shfl_sync(0xffffffffu, c, kSideWarps);
+      if (!SOLO && ctas > 1) {
+        cluster_wait();
+        arrived = false;
+        if (lane < ctas) {
+          asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(ptx::mapa(ptx::smem_u32(&cta_s[0][rank]), lane)), "d"(S0)
+                       : "memory");
+          asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(ptx::mapa(ptx::smem_u32(&cta_s[1][rank]), lane)), "d"(S1)
+                       : "memory");
+          ptx::st_shared_cluster_u32(ptx::mapa(ptx::smem_u32(&cta_n[0][rank]), lane), static_cast<uint32_t>(c0));
+          ptx::st_shared_cluster_u32(ptx::mapa(ptx::smem_u32(&cta_n[1][rank]), lane), static_cast<uint32_t>(c1));
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        S0 = S1 = 0.0, c0 = c1 = 0;
+        for (int r = 0; r < ctas; ++r) S0 += cta_s[0][r], S1 += cta_s[1][r], c0 += cta_n[0][r], c1 += cta_n[1][r];
+      }
+      if (lane == 0) {
+        if (p.normalize) S0 /= max(c0, 1), S1 /= max(c1, 1);
+        float value, slope;
+        pair_loss(p, static_cast<float>(S0 - S1), &value, &slope);
+        const float up = p.dloss ? p.dloss[p.reduction == kNone ? pair : 0] : 1.0f;
+        slope *= p.reduction == kMean ? up / static_cast<float>(p.P) : up;
+        slope_of[0] = p.normalize ? slope / static_cast<float>(max(c0, 1)) : slope;
+        slope_of[1] = p.normalize ? -slope / static_cast<float>(max(c1, 1)) : -slope;
+        if (part == 0) {
+          if (p.chosen) p.chosen[pair] = static_cast<float>(p.beta * S0);
+          if (p.rejected) p.rejected[pair] = static_cast<float>(p.beta * S1);
+          if (p.loss && p.reduction == kNone) p.loss[pair] = value;
+          if (!SOLO) p.pair_loss[pair] = value, p.pair_bad[pair] = bad;
+        }
+        loss_sum += value;
+        bad_sum += bad;
+      }
+    } else if (!SOLO && ctas > 1) {
+      cluster_wait();
+      arrived = false;
+      cluster_arrive();
+      cluster_wait();
+    }
+    __syncthreads();
+    if (p.dlogp) {
+      const float g = slope_of[side];
+      step = 0;
+      for (int64_t t = g0 + static_cast<int64_t>(kGroup) * (part * kSide + i); t < hi; t += stride, ++step) {
+        const int left = static_cast<int>(min(p.T - t, int64_t(kGroup)));
+        const bool vec = p.vec && left == kGroup;
+        const uint32_t m = step < kKept ? kept >> (4 * step) : valid4(p.targets, p.ignore_index, t, left, vec);
+        float v[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) v[j] = m >> j & 1u ? g : 0.0f;
+        if (t >= lo && t + kGroup <= hi) {
+          store4(p.dlogp, t, kGroup, p.vec, v);
+        } else {  // the first and last group hold tokens of other sequences
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j)
+            if (t + j >= lo && t + j < hi) p.dlogp[t + j] = v[j];
+        }
+      }
+      // tokens of no sequence: before the first and after the last
+      if (pair == 0)
+        for (int64_t t = part * kPairThreads + tid; t < at[0]; t += share * kPairThreads) p.dlogp[t] = 0.0f;
+      if (pair == p.P - 1)
+        for (int64_t t = at[2] + part * kPairThreads + tid; t < p.T; t += share * kPairThreads) p.dlogp[t] = 0.0f;
+    }
   }
-  if (threadIdx.x == 0) {
-    for (int side = 0; side < 2; ++side)
-      if (p.normalize) S[side] /= max(n[side], 1);
-    float value, slope;
-    pair_loss(p, static_cast<float>(S[0] - S[1]), &value, &slope);
-    const float up = p.dloss ? p.dloss[p.reduction == kNone ? pair : 0] : 1.0f;
-    slope *= p.reduction == kMean ? up / static_cast<float>(p.P) : up;
-    slope_of[0] = p.normalize ? slope / max(n[0], 1) : slope;
-    slope_of[1] = p.normalize ? -slope / max(n[1], 1) : -slope;
-    if (p.chosen) p.chosen[pair] = static_cast<float>(p.beta * S[0]);
-    if (p.rejected) p.rejected[pair] = static_cast<float>(p.beta * S[1]);
-    if (p.loss && p.reduction == kNone) p.loss[pair] = value;
-    p.pair_loss[pair] = value;
-    p.pair_bad[pair] = bad;
+  if (arrived) cluster_wait();
+  if constexpr (SOLO) {
+    if (tid == 0) {
+      asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(ptx::mapa(ptx::smem_u32(&cta_s[0][rank]), 0)), "d"(loss_sum)
+                   : "memory");
+      ptx::st_shared_cluster_u32(ptx::mapa(ptx::smem_u32(&cta_n[0][rank]), 0), static_cast<uint32_t>(bad_sum));
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (rank == 0 && tid == 0) {
+      double s = 0.0;
+      int b = 0;
+      for (int r = 0; r < ctas; ++r) s += cta_s[0][r], b += cta_n[0][r];
+      if (p.loss && p.reduction != kNone) p.loss[0] = static_cast<float>(p.reduction == kMean ? s / p.P : s);
+      *p.status = b ? kStatusSequences : 0;
+    }
   }
-  __syncthreads();
-  if (!p.dlogp) return;
-  for (int side = 0; side < 2; ++side)
-    for (int64_t t = at[side] + threadIdx.x; t < at[side + 1]; t += kPairThreads)
-      p.dlogp[t] = p.targets[t] != p.ignore_index ? slope_of[side] : 0.0f;
-  // tokens of no sequence: before the first and after the last
-  if (pair == 0)
-    for (int64_t t = threadIdx.x; t < at[0]; t += kPairThreads) p.dlogp[t] = 0.0f;
-  if (pair == p.P - 1)
-    for (int64_t t = at[2] + threadIdx.x; t < p.T; t += kPairThreads) p.dlogp[t] = 0.0f;
 }
 
-__global__ void __launch_bounds__(kPairThreads) preference_reduce_kernel(const PreferenceParams p) {
-  __shared__ double sh[kPairThreads / 32];
-  __shared__ int sh_n[kPairThreads / 32];
+constexpr int kReduceThreads = 256;
+
+__global__ void __launch_bounds__(kReduceThreads) preference_reduce_kernel(const PreferenceParams p) {
+  __shared__ double sh[kReduceThreads / 32];
+  __shared__ int sh_n[kReduceThreads / 32];
   double s = 0.0;
   int bad = 0;
-  for (int i = threadIdx.x; i < p.P; i += kPairThreads) s += p.pair_loss[i], bad += p.pair_bad[i];
-  s = block_sum<double, kPairThreads>(s, sh);
-  bad = block_sum<int, kPairThreads>(bad, sh_n);
+  for (int i = threadIdx.x; i < p.P; i += kReduceThreads) s += p.pair_loss[i], bad += p.pair_bad[i];
+  s = block_sum<double, kReduceThreads>(s, sh);
+  bad = block_sum<int, kReduceThreads>(bad, sh_n);
   if (threadIdx.x != 0) return;
   if (p.loss && p.reduction != kNone) p.loss[0] = static_cast<float>(p.reduction == kMean ? s / p.P : s);
   *p.status = bad ? kStatusSequences : 0;
