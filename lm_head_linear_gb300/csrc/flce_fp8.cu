@@ -13,18 +13,19 @@ namespace {
 
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
-// [rows, K] bytes, box 128 bytes x box_rows, 128-byte swizzle; out of range reads as zero.
-flce_status byte_map(CUtensorMap* m, const void* ptr, int64_t K, int64_t rows, int box_rows) {
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
-  cuuint32_t box[2] = {fp8::kBlockK, static_cast<cuuint32_t>(box_rows)};
+// A row-major matrix of `rows` x `inner` elements, rows `pitch` bytes apart; out of
+// range reads as zero, stores are clipped.
+flce_status matrix_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* ptr,
+                       int64_t inner, int64_t rows, int64_t pitch, int box_inner, int box_rows) {
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t step[2] = {1, 1};
-  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, step,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = g_encode(m, type, 2, const_cast<void*>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
-    return fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for {%lld, %lld} bytes, box rows %d",
-                static_cast<int>(r), (long long)K, (long long)rows, box_rows);
+    return fail(FLCE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for {%lld, %lld} pitch %lld box {%d, %d}",
+                static_cast<int>(r), (long long)inner, (long long)rows, (long long)pitch, box_inner, box_rows);
   return FLCE_OK;
 }
 
@@ -117,8 +118,10 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   if ((st = get_encoder()) != FLCE_OK) return st;
   if ((st = resident_pairs(dev, sms, &pairs)) != FLCE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CUDA_TRY(cudaMemsetAsync(workspace, 0, kHeaderBytes, s));
-  if (T == 0) return FLCE_OK;
+  if (T == 0) {
+    CUDA_TRY(cudaMemsetAsync(workspace, 0, kHeaderBytes, s));
+    return FLCE_OK;
+  }
   fp8::Params p;
   std::memset(&p, 0, sizeof(p));
   // Token tiles of equal width: as few as hold T, each rounded up to 32 tokens.
@@ -129,17 +132,27 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   if (units >= (int64_t(1) << 31) - 1024) return fail(FLCE_ERR_INVALID_ARG, "T x V is too large");
   p.units = static_cast<int32_t>(units);
   p.stage_bytes = fp8::kABytes + p.n / 2 * fp8::kBlockK;
-  p.stages = std::min((fp8::kSmemLimit - 1024 - fp8::kSmemTail) / p.stage_bytes, fp8::kMaxStages);
-  if ((st = byte_map(&p.tmW, W, K, V, fp8::kRowsCta)) != FLCE_OK) return st;
-  if ((st = byte_map(&p.tmX, x, K, T, p.n / 2)) != FLCE_OK) return st;
+  p.stages = std::min((fp8::kSmemLimit - 1024 - fp8::kStagingBytes - fp8::kSmemTail) / p.stage_bytes, fp8::kMaxStages);
+  const int64_t es = y_dtype == FLCE_DTYPE_F32 ? 4 : 2;
+  p.y_tma = !off16(y) && (ldy * es) % 16 == 0;
+  if ((st = matrix_map(&p.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, W, K, V, K, fp8::kBlockK,
+                       p.n_tiles == 1 ? 32 : fp8::kRowsCta)) != FLCE_OK)
+    return st;
+  if ((st = matrix_map(&p.tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, x, K, T, K, fp8::kBlockK,
+                       p.n / 2)) != FLCE_OK)
+    return st;
+  if (p.y_tma && (st = matrix_map(&p.tmY, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                  CU_TENSOR_MAP_SWIZZLE_NONE, y, V, T, ldy * es, 32, 32)) != FLCE_OK)
+    return st;
   p.sx = x_scale, p.sw = W_scale, p.y = y, p.ldy = ldy;
   p.status = static_cast<int32_t*>(workspace);
   p.timeout_ns = wait_limit_ns(K);
   p.T = static_cast<int32_t>(T), p.K = static_cast<int32_t>(K), p.V = static_cast<int32_t>(V);
   p.kb = static_cast<int32_t>(cdiv(K, fp8::kBlockK));
   p.y_f32 = y_dtype == FLCE_DTYPE_F32;
-  const int grid = 2 * static_cast<int>(std::min<int64_t>(pairs, units));
-  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + fp8::kSmemTail;
+  const int64_t shares = p.n_tiles == 1 ? cdiv(V, fp8::kGranule) : units;  // a pair takes at least one
+  const int grid = 2 * static_cast<int>(std::min<int64_t>(pairs, shares));
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + fp8::kStagingBytes + fp8::kSmemTail;
   KernelScope ks(FLCE_KERNEL_LINEAR_FP8, s, 2.0 * T * K * V,
                  1.0 * T * K + 1.0 * V * K + (p.y_f32 ? 4.0 : 2.0) * T * V);
   fp8::linear_fp8_kernel<<<grid, fp8::kThreads, smem, s>>>(p);

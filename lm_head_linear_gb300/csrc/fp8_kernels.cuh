@@ -45,6 +45,8 @@ constexpr int kEpiWarps = 4;
 constexpr int kScaleWarps = 4;
 constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
 constexpr uint32_t kTmemCols = 512;
+constexpr int kStagingWarp = 2 * 32 * 32 * 4;  // two 32 x 32 boxes of up to 4 bytes for each epilogue warp
+constexpr int kStagingBytes = kEpiWarps * kStagingWarp;
 constexpr int kSmemTail = 512;
 constexpr int kSmemLimit = 232448;
 constexpr int kStatusTimeout = 7;
@@ -53,8 +55,9 @@ constexpr uint64_t kSettleNs = 200000ull;
 static_assert(kScaleBase + kScaleStages * kScaleCols <= static_cast<int>(kTmemCols), "TMEM columns");
 
 struct Params {
-  CUtensorMap tmW;   // [V, K] bytes, box 128 x 128 rows
+  CUtensorMap tmW;   // [V, K] bytes, box 128 x 128 rows (one token tile: x 32 rows)
   CUtensorMap tmX;   // [T, K] bytes, box 128 x N / 2 rows
+  CUtensorMap tmY;   // [T, V] logits, box 32 vocabulary rows x 32 tokens (y_tma)
   const uint8_t* sx; // [T, kb]
   const uint8_t* sw; // [ceil(V / 128), kb]
   void* y;
@@ -67,11 +70,13 @@ struct Params {
   int32_t n_tiles, units;
   int32_t stages, stage_bytes;
   int32_t y_f32;
+  int32_t y_tma;     // y's rows start on 16-byte boundaries: stored by TMA, else by plain stores
 };
 
 // full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], scale_full[4], scale_empty[4], drain
 struct Smem {
   uint8_t* stages;
+  uint8_t* staging;
   uint64_t* bars;
   uint32_t* tmem_slot;
   volatile int* abort_flag;
@@ -101,28 +106,69 @@ struct Slot {
   }
 };
 
-// Unit u: tokens of tile u % n_tiles (fastest: the units in flight share W's rows
-// and the tokens stay in L2), vocabulary pair u / n_tiles.
+// The tiles of one pair.  Several token tiles: tiles of 256 rows, tokens fastest
+// (the pairs in flight share W's rows and the tokens stay in L2), strided over the
+// pairs.  One token tile (decoding, bound by reading W): every pair takes an equal
+// share of W in granules of 64 rows, in tiles of up to four; 485 tiles of 256 rows over
+// 76 pairs would leave 9 % of them idle in the last round.
 struct Unit {
-  int m, t0;
+  int row;    // this CTA's first row of W
+  int boxes;  // 32-row boxes this CTA holds (4: a full tile)
+  int t0;
 };
-__device__ __forceinline__ Unit unit_of(const Params& p, int u) {
+struct Work {
+  int first, count, step;  // tile indexes
+  int g0, g1;              // granules (one token tile)
+};
+constexpr int kGranule = 64;
+
+__device__ __forceinline__ Work work_of(const Params& p) {
+  const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+  Work w{pair, p.units, pairs, 0, 0};
+  if (p.n_tiles == 1) {
+    const int64_t total = (static_cast<int64_t>(p.V) + kGranule - 1) / kGranule;
+    w.g0 = static_cast<int>(total * pair / pairs);
+    w.g1 = static_cast<int>(total * (pair + 1) / pairs);
+    w.first = 0, w.step = 1, w.count = (w.g1 - w.g0 + 3) / 4;
+  }
+  return w;
+}
+
+__device__ __forceinline__ Unit unit_of(const Params& p, const Work& w, int u, uint32_t rank) {
   Unit r;
-  r.m = u / p.n_tiles;
-  r.t0 = (u - r.m * p.n_tiles) * p.n;
+  if (p.n_tiles == 1) {
+    const int g = w.g0 + 4 * u;
+    r.boxes = min(4, w.g1 - g);
+    r.row = g * kGranule + static_cast<int>(rank) * 32 * r.boxes;
+    r.t0 = 0;
+  } else {
+    const int m = u / p.n_tiles;
+    r.boxes = 4;
+    r.row = (2 * m + static_cast<int>(rank)) * kRowsCta;
+    r.t0 = (u - m * p.n_tiles) * p.n;
+  }
   return r;
 }
 
+// An arrival on a barrier of the even CTA that passes no generic memory on (what it
+// orders is TMEM, through tcgen05.wait and the tcgen05 fences): relaxed, since a
+// release would first wait for the thread's own loads and stores in flight
+// (1 x 2048 x 124,160: 67.8 us with release, 50.2 us relaxed).
+__device__ __forceinline__ void arrive_even(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(ptx::mapa(bar, 0)) : "memory");
+}
+
 // Both CTAs: this CTA's 128 rows of W and its half of the tokens.
-__device__ __forceinline__ void producer(const Params& p, const Smem& s, uint32_t rank, int u0, int du) {
+__device__ __forceinline__ void producer(const Params& p, const Smem& s, const Work& w, uint32_t rank) {
   Slot at;
   uint32_t used = 0;
   bool ok = true;
-  const uint32_t tx = 2u * static_cast<uint32_t>(p.stage_bytes);
-  for (int u = u0; u < p.units && ok; u += du) {
-    const Unit un = unit_of(p, u);
-    const int row = (2 * un.m + static_cast<int>(rank)) * kRowsCta;
+  const bool small = p.n_tiles == 1;
+  const int b_bytes = p.stage_bytes - kABytes;
+  for (int u = w.first; u < w.count && ok; u += w.step) {
+    const Unit un = unit_of(p, w, u, rank);
     const int tok = un.t0 + static_cast<int>(rank) * (p.n / 2);
+    const uint32_t tx = 2u * static_cast<uint32_t>(un.boxes * 32 * kBlockK + b_bytes);
     for (int kb = 0; kb < p.kb; ++kb) {
       if (!ptx::wait_bounded_cluster(s.empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
         give_up(p, s);
@@ -132,7 +178,12 @@ __device__ __forceinline__ void producer(const Params& p, const Smem& s, uint32_
       if (rank == 0) ptx::mbar_arrive_expect_tx(s.full(at.i), tx);
       const uint32_t full = ptx::mapa(s.full(at.i), 0);
       const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes);
-      ptx::tma_load_2d_pair(a, &p.tmW, kb * kBlockK, row, full);
+      if (small) {
+        for (int b = 0; b < un.boxes; ++b)
+          ptx::tma_load_2d_pair(a + b * 32 * kBlockK, &p.tmW, kb * kBlockK, un.row + 32 * b, full);
+      } else {
+        ptx::tma_load_2d_pair(a, &p.tmW, kb * kBlockK, un.row, full);
+      }
       ptx::tma_load_2d_pair(a + kABytes, &p.tmX, kb * kBlockK, tok, full);
       used |= 1u << at.i;
       at.next(p.stages);
@@ -146,11 +197,11 @@ __device__ __forceinline__ void producer(const Params& p, const Smem& s, uint32_
 }
 
 // Even CTA only.
-__device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, uint32_t tmem, int u0, int du) {
+__device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const Work& w, uint32_t tmem) {
   Slot at, sc, acc;
   bool ok = true;
   const uint32_t idesc0 = ptx::idesc_mxf8(2 * kRowsCta, static_cast<uint32_t>(p.n), 0);
-  for (int u = u0; u < p.units && ok; u += du) {
+  for (int u = w.first; u < w.count && ok; u += w.step) {
     ok = ptx::wait_bounded_cluster(s.acc_empty(acc.i), acc.phase ^ 1u, p.timeout_ns, s.abort_flag);
     if (!ok) break;
     ptx::tc_fence_after();
@@ -199,86 +250,141 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int g, int kb
   return w;
 }
 
+// The words of one scale stage: this CTA's rows 32 j .. and the tile's tokens
+// 32 j + lane, K blocks 4 g .. 4 g + 3.
+struct ScaleWords {
+  uint32_t a[4], b[8];
+};
+
 // Each of the four warps writes the same words to its own quarter of the lanes:
-// row r of A (or B) is lane r % 32, column r / 32, in every quarter.
-__device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, uint32_t tmem, uint32_t rank, int warp,
-                                             int lane, int u0, int du) {
+// row r of A (or B) is lane r % 32, column r / 32, in every quarter.  The words of
+// the next stage are loaded before this one's TMEM stage is waited for, so a
+// load's latency does not stand between two stages.
+__device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, const Work& w, uint32_t tmem,
+                                             uint32_t rank, int warp, int lane) {
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   const bool words_x = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 3) == 0;
   const bool words_w = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sw) & 3) == 0;
   const int groups = (p.kb + 3) / 4;
-  const int row_blocks = (p.V + kRowsCta - 1) / kRowsCta;
-  Slot at;
-  for (int u = u0; u < p.units; u += du) {
-    const Unit un = unit_of(p, u);
-    const int rb = 2 * un.m + static_cast<int>(rank);
-    const uint8_t* wrow = p.sw + static_cast<int64_t>(rb < row_blocks ? rb : 0) * p.kb;
-    for (int g = 0; g < groups; ++g) {
-      const uint32_t a = scale_word(wrow, g, p.kb, words_w);
-      uint32_t b[8];
+  const int last_block = (p.V + kRowsCta - 1) / kRowsCta - 1;
+  const auto load = [&](int u, int g) {
+    ScaleWords r;
+    const Unit un = unit_of(p, w, u, rank);
+    // four 32-row columns touch at most two of W's row blocks
+    const int b0 = min(un.row / kRowsCta, last_block), b1 = min((un.row + 96) / kRowsCta, last_block);
+    const uint32_t w0 = scale_word(p.sw + static_cast<int64_t>(b0) * p.kb, g, p.kb, words_w);
+    const uint32_t w1 = b1 == b0 ? w0 : scale_word(p.sw + static_cast<int64_t>(b1) * p.kb, g, p.kb, words_w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int t = un.t0 + 32 * j + lane;
-        b[j] = 32 * j < p.n && t < p.T ? scale_word(p.sx + static_cast<int64_t>(t) * p.kb, g, p.kb, words_x) : 0x7f7f7f7fu;
-      }
-      if (!ptx::wait_bounded_cluster(s.scale_empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
-        give_up(p, s);
-        return;
-      }
-      ptx::tc_fence_after();
-      __syncwarp();
-      const uint32_t col = tmem + lanes + kScaleBase + at.i * kScaleCols;
-      ptx::tmem_st4(col, a, a, a, a);
-      ptx::tmem_st8(col + 8, b);
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(s.scale_full(at.i), 0));
-      at.next(kScaleStages);
+    for (int j = 0; j < 4; ++j) r.a[j] = (un.row + 32 * j) / kRowsCta <= b0 ? w0 : w1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int t = un.t0 + 32 * j + lane;
+      r.b[j] = 32 * j < p.n && t < p.T ? scale_word(p.sx + static_cast<int64_t>(t) * p.kb, g, p.kb, words_x) : 0x7f7f7f7fu;
     }
+    return r;
+  };
+  Slot at;
+  int u = w.first, g = 0;
+  if (u >= w.count) return;
+  ScaleWords now = load(u, g);
+  while (true) {
+    if (++g == groups) g = 0, u += w.step;
+    const bool more = u < w.count;
+    ScaleWords next;
+    if (more) next = load(u, g);
+    if (!ptx::wait_bounded_cluster(s.scale_empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
+      give_up(p, s);
+      return;
+    }
+    ptx::tc_fence_after();
+    __syncwarp();
+    const uint32_t col = tmem + lanes + kScaleBase + at.i * kScaleCols;
+    ptx::tmem_st4(col, now.a[0], now.a[1], now.a[2], now.a[3]);
+    ptx::tmem_st8(col + 8, now.b);
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_even(s.scale_full(at.i));
+    at.next(kScaleStages);
+    if (!more) return;
+    now = next;
   }
 }
 
-// Lane = vocabulary row, column = token: one store per token, contiguous over the warp.
-template <bool F32>
-__device__ __forceinline__ void epilogue(const Params& p, const Smem& s, uint32_t tmem, uint32_t rank, int warp,
-                                         int lane, int u0, int du) {
+// A warp's 32 rows x 32 tokens at a time.  In TMEM a lane is a vocabulary row and a
+// column a token; the staging buffer holds them token by token (32 lanes write one
+// token's 32 consecutive logits: no bank conflict), and one TMA store puts the box
+// into y, clipped at T and V.  Plain stores from the registers took 500 us more of
+// the 1.75 ms at 8192 x 2048 x 124,160: 64-byte pieces, one instruction each.
+template <typename E>
+__device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const Work& w, uint32_t tmem, uint32_t rank,
+                                         int warp, int lane) {
   const int q = warp & 3;
+  const uint32_t staging = ptx::smem_u32(s.staging) + q * kStagingWarp;
   Slot acc;
-  for (int u = u0; u < p.units; u += du) {
-    const Unit un = unit_of(p, u);
-    const int v = (2 * un.m + static_cast<int>(rank)) * kRowsCta + q * 32 + lane;
+  uint32_t box = 0;
+  for (int u = w.first; u < w.count; u += w.step) {
+    const Unit un = unit_of(p, w, u, rank);
     if (!ptx::wait_bounded_cluster(s.acc_full(acc.i), acc.phase, p.timeout_ns, s.abort_flag)) {
       give_up(p, s);
-      return;
+      break;
     }
     __syncwarp();
     ptx::tc_fence_after();
     const uint32_t col = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.i * kMaxN;
+    const int v0 = un.row + q * 32;
+    if (q < un.boxes && v0 < p.V) {
 #pragma unroll 1
-    for (int c = 0; c < p.n; c += 32) {
-      uint32_t r[32];
-      ptx::tmem_ld32(col + c, r);
-      ptx::tmem_wait_ld32(r);
-      const int t0 = un.t0 + c;
-      if (v < p.V) {
-        const int64_t at = static_cast<int64_t>(t0) * p.ldy + v;
+      for (int c = 0; c < p.n && un.t0 + c < p.T; c += 32) {
+        uint32_t r[32];
+        ptx::tmem_ld32(col + c, r);
+        const int t0 = un.t0 + c;
+        if (p.y_tma) {
+          const uint32_t buf = staging + (box & 1u) * (kStagingWarp / 2);
+          if (lane == 0) ptx::bulk_wait_read<1>();  // the store before last has read this buffer
+          __syncwarp();
+          ptx::tmem_wait_ld32(r);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (t0 + j < p.T) {
-            if constexpr (F32)
-              static_cast<float*>(p.y)[at + j * p.ldy] = __uint_as_float(r[j]);
+          for (int j = 0; j < 32; ++j) {
+            if constexpr (sizeof(E) == 4)
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + j * 128 + lane * 4), "r"(r[j]) : "memory");
             else
-              static_cast<__nv_bfloat16*>(p.y)[at + j * p.ldy] = __float2bfloat16_rn(__uint_as_float(r[j]));
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + j * 64 + lane * 2),
+                           "h"(__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j]))))
+                           : "memory");
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::tma_store_2d(&p.tmY, buf, v0, t0);
+            ptx::bulk_commit();
+          }
+          ++box;
+        } else {
+          ptx::tmem_wait_ld32(r);
+          const int v = v0 + lane;
+          if (v < p.V) {
+            E* y = static_cast<E*>(p.y) + static_cast<int64_t>(t0) * p.ldy + v;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (t0 + j < p.T) {
+                if constexpr (sizeof(E) == 4)
+                  y[j * p.ldy] = __uint_as_float(r[j]);
+                else
+                  y[j * p.ldy] = __float2bfloat16_rn(__uint_as_float(r[j]));
+              }
+            }
           }
         }
       }
     }
     ptx::tc_fence_before();
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(s.acc_empty(acc.i), 0));
+    if (lane == 0) arrive_even(s.acc_empty(acc.i));
     acc.next(2);
   }
+  if (lane == 0) ptx::bulk_wait<0>();  // shared memory stays until the stores have read it
+  __syncwarp();
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -286,15 +392,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   Smem s;
   s.stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* tail = s.stages + p.stages * p.stage_bytes;
+  s.staging = s.stages + p.stages * p.stage_bytes;
+  uint8_t* tail = s.staging + kStagingBytes;
   s.bars = reinterpret_cast<uint64_t*>(tail);
   s.tmem_slot = reinterpret_cast<uint32_t*>(tail + kBars * 8);
   s.abort_flag = reinterpret_cast<volatile int*>(tail + kBars * 8 + 4);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
-  const int u0 = static_cast<int>(blockIdx.x >> 1), du = static_cast<int>(gridDim.x >> 1);
+  const Work w = work_of(p);
 
+  // The status of this call.  The first CTA is dispatched first and clears the word
+  // before anything else; a wait that runs out does so a millisecond later at the
+  // earliest.
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       ptx::mbar_init(s.full(i), 1);
@@ -316,6 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&p.tmW);
     ptx::prefetch_tmap(&p.tmX);
+    if (p.y_tma) ptx::prefetch_tmap(&p.tmY);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(ptx::smem_u32(s.tmem_slot), kTmemCols);
@@ -327,19 +439,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *s.tmem_slot;
 
   if (warp == 0) {
-    if (ptx::elect_one()) producer(p, s, rank, u0, du);
+    if (ptx::elect_one()) producer(p, s, w, rank);
     __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && ptx::elect_one()) mma_issuer(p, s, tmem, u0, du);
+    if (rank == 0 && ptx::elect_one()) mma_issuer(p, s, w, tmem);
     __syncwarp();
   } else if (warp < 2 + kEpiWarps) {
     if (p.y_f32)
-      epilogue<true>(p, s, tmem, rank, warp, lane, u0, du);
+      epilogue<float>(p, s, w, tmem, rank, warp, lane);
     else
-      epilogue<false>(p, s, tmem, rank, warp, lane, u0, du);
+      epilogue<__nv_bfloat16>(p, s, w, tmem, rank, warp, lane);
     __syncwarp();
   } else {
-    scale_writer(p, s, tmem, rank, warp, lane, u0, du);
+    scale_writer(p, s, w, tmem, rank, warp, lane);
     __syncwarp();
   }
 
