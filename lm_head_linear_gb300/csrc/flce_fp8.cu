@@ -30,19 +30,20 @@ flce_status matrix_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwiz
 }
 
 // Co-resident CTA pairs per device, queried once.
+template <bool TOKENS_M>
 flce_status resident_pairs(int dev, int sms, int* pairs) {
   static std::mutex mu;
   static int known[64] = {};
   std::lock_guard<std::mutex> lk(mu);
   if (known[dev] == 0) {
-    CUDA_TRY(cudaFuncSetAttribute(fp8::linear_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    CUDA_TRY(cudaFuncSetAttribute(fp8::linear_fp8_kernel<TOKENS_M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   fp8::kSmemLimit));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * std::max(sms / 2, 1));
     cfg.blockDim = dim3(fp8::kThreads);
     cfg.dynamicSmemBytes = fp8::kSmemLimit;
     int n = 0;
-    CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, fp8::linear_fp8_kernel, &cfg));
+    CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, fp8::linear_fp8_kernel<TOKENS_M>, &cfg));
     known[dev] = std::max(1, std::min(n, sms / 2));
   }
   *pairs = known[dev];
@@ -116,7 +117,6 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   flce_status st = current_device(&dev, &sms);
   if (st != FLCE_OK) return st;
   if ((st = get_encoder()) != FLCE_OK) return st;
-  if ((st = resident_pairs(dev, sms, &pairs)) != FLCE_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T == 0) {
     CUDA_TRY(cudaMemsetAsync(workspace, 0, kHeaderBytes, s));
@@ -124,25 +124,43 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   }
   fp8::Params p;
   std::memset(&p, 0, sizeof(p));
-  // Token tiles of equal width: as few as hold T, each rounded up to 32 tokens.
+  const int64_t es = y_dtype == FLCE_DTYPE_F32 ? 4 : 2;
+  p.y_tma = !off16(y) && (ldy * es) % 16 == 0;
+  // Vocabulary on M: token tiles of equal width, as few as hold T, rounded up to 32.
   const int64_t tiles = cdiv(T, fp8::kMaxN);
-  p.n = static_cast<int32_t>(cdiv(cdiv(T, tiles), 32) * 32);
-  p.n_tiles = static_cast<int32_t>(cdiv(T, p.n));
-  const int64_t units = cdiv(V, 2 * fp8::kRowsCta) * p.n_tiles;
+  int64_t n = cdiv(cdiv(T, tiles), 32) * 32, n_tiles = cdiv(T, n), m_tiles = cdiv(V, 2 * fp8::kRowsCta);
+  // Tokens on M where more than one token tile is needed anyway and rounding T up to
+  // 256 does not cost more than its cheaper epilogue gains.
+  bool tokens_m = false;
+  if (n_tiles > 1 && p.y_tma) {
+    const int64_t mt = cdiv(T, 2 * fp8::kRowsCta), nt = cdiv(V, fp8::kMaxN);
+    const double padded = static_cast<double>(mt * 2 * fp8::kRowsCta) * static_cast<double>(nt * fp8::kMaxN);
+    if (padded <= 1.1 * static_cast<double>(n * n_tiles) * static_cast<double>(m_tiles * 2 * fp8::kRowsCta)) {
+      tokens_m = true;
+      n = fp8::kMaxN, n_tiles = nt, m_tiles = mt;
+    }
+  }
+  if ((st = tokens_m ? resident_pairs<true>(dev, sms, &pairs) : resident_pairs<false>(dev, sms, &pairs)) != FLCE_OK)
+    return st;
+  const int64_t units = m_tiles * n_tiles;
   if (units >= (int64_t(1) << 31) - 1024) return fail(FLCE_ERR_INVALID_ARG, "T x V is too large");
+  p.n = static_cast<int32_t>(n), p.n_tiles = static_cast<int32_t>(n_tiles), p.m_tiles = static_cast<int32_t>(m_tiles);
   p.units = static_cast<int32_t>(units);
   p.stage_bytes = fp8::kABytes + p.n / 2 * fp8::kBlockK;
   p.stages = std::min((fp8::kSmemLimit - 1024 - fp8::kStagingBytes - fp8::kSmemTail) / p.stage_bytes, fp8::kMaxStages);
-  const int64_t es = y_dtype == FLCE_DTYPE_F32 ? 4 : 2;
-  p.y_tma = !off16(y) && (ldy * es) % 16 == 0;
-  if ((st = matrix_map(&p.tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, W, K, V, K, fp8::kBlockK,
-                       p.n_tiles == 1 ? 32 : fp8::kRowsCta)) != FLCE_OK)
+  const bool granules = !tokens_m && n_tiles == 1;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  if ((st = matrix_map(tokens_m ? &p.tmB : &p.tmA, u8, CU_TENSOR_MAP_SWIZZLE_128B, W, K, V, K, fp8::kBlockK,
+                       tokens_m ? p.n / 2 : (granules ? 32 : fp8::kRowsCta))) != FLCE_OK)
     return st;
-  if ((st = matrix_map(&p.tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, x, K, T, K, fp8::kBlockK,
-                       p.n / 2)) != FLCE_OK)
+  if ((st = matrix_map(tokens_m ? &p.tmA : &p.tmB, u8, CU_TENSOR_MAP_SWIZZLE_128B, x, K, T, K, fp8::kBlockK,
+                       tokens_m ? fp8::kRowsCta : p.n / 2)) != FLCE_OK)
     return st;
+  const CUtensorMapSwizzle y_swizzle = !tokens_m  ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                       : es == 4 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                 : CU_TENSOR_MAP_SWIZZLE_64B;
   if (p.y_tma && (st = matrix_map(&p.tmY, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                  CU_TENSOR_MAP_SWIZZLE_NONE, y, V, T, ldy * es, 32, 32)) != FLCE_OK)
+                                  y_swizzle, y, V, T, ldy * es, 32, 32)) != FLCE_OK)
     return st;
   p.sx = x_scale, p.sw = W_scale, p.y = y, p.ldy = ldy;
   p.status = static_cast<int32_t*>(workspace);
@@ -150,12 +168,15 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   p.T = static_cast<int32_t>(T), p.K = static_cast<int32_t>(K), p.V = static_cast<int32_t>(V);
   p.kb = static_cast<int32_t>(cdiv(K, fp8::kBlockK));
   p.y_f32 = y_dtype == FLCE_DTYPE_F32;
-  const int64_t shares = p.n_tiles == 1 ? cdiv(V, fp8::kGranule) : units;  // a pair takes at least one
+  const int64_t shares = granules ? cdiv(V, fp8::kGranule) : units;  // a pair takes at least one
   const int grid = 2 * static_cast<int>(std::min<int64_t>(pairs, shares));
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + fp8::kStagingBytes + fp8::kSmemTail;
   KernelScope ks(FLCE_KERNEL_LINEAR_FP8, s, 2.0 * T * K * V,
                  1.0 * T * K + 1.0 * V * K + (p.y_f32 ? 4.0 : 2.0) * T * V);
-  fp8::linear_fp8_kernel<<<grid, fp8::kThreads, smem, s>>>(p);
+  if (tokens_m)
+    fp8::linear_fp8_kernel<true><<<grid, fp8::kThreads, smem, s>>>(p);
+  else
+    fp8::linear_fp8_kernel<false><<<grid, fp8::kThreads, smem, s>>>(p);
   ks.done();
   return check_launch("linear_fp8");
 }

@@ -8,11 +8,13 @@
 // their way into the fp32 accumulator, and no partial sum leaves TMEM before the
 // whole K loop is done.
 //
-// Orientation: the vocabulary is the M side (256 rows per SM pair, 128 per CTA)
-// and the tokens are the N side (up to 224 per tile).  A decoding step of a few
-// tokens then runs narrow tiles (N = 32) over wide W tiles, bound by reading W;
-// a prompt runs 256 x 224 tiles.  In the accumulator a lane is a vocabulary row,
-// so a warp's store of one token's logits is contiguous.
+// Two orientations of the 256 x N tile of an SM pair (128 rows of the M side per CTA):
+//   vocabulary on M, tokens on N (N = 32 .. 224): a decoding step of a few tokens
+//     runs narrow tiles over wide W tiles and is bound by reading W;
+//   tokens on M, vocabulary on N = 224: a prompt.  A lane of the accumulator is then
+//     a token and its columns are consecutive logits, which go to the staging buffer
+//     16 bytes at a time (with the vocabulary on M they take a 2-byte store each, which
+//     cost 160 us of 1443 us at 8192 x 2048 x 124,160).
 //
 // A CTA has 10 warps: the TMA producer, the MMA issuer (even CTA of the pair),
 // four epilogue warps and four scale warps.  The scale bytes come from their plain
@@ -55,9 +57,9 @@ constexpr uint64_t kSettleNs = 200000ull;
 static_assert(kScaleBase + kScaleStages * kScaleCols <= static_cast<int>(kTmemCols), "TMEM columns");
 
 struct Params {
-  CUtensorMap tmW;   // [V, K] bytes, box 128 x 128 rows (one token tile: x 32 rows)
-  CUtensorMap tmX;   // [T, K] bytes, box 128 x N / 2 rows
-  CUtensorMap tmY;   // [T, V] logits, box 32 vocabulary rows x 32 tokens (y_tma)
+  CUtensorMap tmA;   // the M side, [rows, K] bytes, box 128 x 128 rows (one token tile: x 32 rows)
+  CUtensorMap tmB;   // the N side, box 128 x N / 2 rows
+  CUtensorMap tmY;   // [T, V] logits, box 32 logits x 32 tokens (y_tma)
   const uint8_t* sx; // [T, kb]
   const uint8_t* sw; // [ceil(V / 128), kb]
   void* y;
@@ -66,8 +68,8 @@ struct Params {
   uint64_t timeout_ns;
   int32_t T, K, V;
   int32_t kb;        // K blocks
-  int32_t n;         // tokens per tile (a multiple of 32 up to kMaxN)
-  int32_t n_tiles, units;
+  int32_t n;         // N (a multiple of 32 up to kMaxN)
+  int32_t n_tiles, m_tiles, units;
   int32_t stages, stage_bytes;
   int32_t y_f32;
   int32_t y_tma;     // y's rows start on 16-byte boundaries: stored by TMA, else by plain stores
@@ -106,15 +108,15 @@ struct Slot {
   }
 };
 
-// The tiles of one pair.  Several token tiles: tiles of 256 rows, tokens fastest
+// The tiles of one pair.  Several token tiles: tiles of 256 M rows, tokens fastest
 // (the pairs in flight share W's rows and the tokens stay in L2), strided over the
 // pairs.  One token tile (decoding, bound by reading W): every pair takes an equal
 // share of W in granules of 64 rows, in tiles of up to four; 485 tiles of 256 rows over
 // 76 pairs would leave 9 % of them idle in the last round.
 struct Unit {
-  int row;    // this CTA's first row of W
+  int row;    // this CTA's first row of the M side
   int boxes;  // 32-row boxes this CTA holds (4: a full tile)
-  int t0;
+  int n0;     // the tile's first row of the N side
 };
 struct Work {
   int first, count, step;  // tile indexes
@@ -122,10 +124,11 @@ struct Work {
 };
 constexpr int kGranule = 64;
 
+template <bool TOKENS_M>
 __device__ __forceinline__ Work work_of(const Params& p) {
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
   Work w{pair, p.units, pairs, 0, 0};
-  if (p.n_tiles == 1) {
+  if (!TOKENS_M && p.n_tiles == 1) {
     const int64_t total = (static_cast<int64_t>(p.V) + kGranule - 1) / kGranule;
     w.g0 = static_cast<int>(total * pair / pairs);
     w.g1 = static_cast<int>(total * (pair + 1) / pairs);
@@ -134,18 +137,24 @@ __device__ __forceinline__ Work work_of(const Params& p) {
   return w;
 }
 
+template <bool TOKENS_M>
 __device__ __forceinline__ Unit unit_of(const Params& p, const Work& w, int u, uint32_t rank) {
   Unit r;
-  if (p.n_tiles == 1) {
+  if constexpr (TOKENS_M) {
+    const int nb = u / p.m_tiles;
+    r.boxes = 4;
+    r.row = (2 * (u - nb * p.m_tiles) + static_cast<int>(rank)) * kRowsCta;
+    r.n0 = nb * p.n;
+  } else if (p.n_tiles == 1) {
     const int g = w.g0 + 4 * u;
     r.boxes = min(4, w.g1 - g);
     r.row = g * kGranule + static_cast<int>(rank) * 32 * r.boxes;
-    r.t0 = 0;
+    r.n0 = 0;
   } else {
     const int m = u / p.n_tiles;
     r.boxes = 4;
     r.row = (2 * m + static_cast<int>(rank)) * kRowsCta;
-    r.t0 = (u - m * p.n_tiles) * p.n;
+    r.n0 = (u - m * p.n_tiles) * p.n;
   }
   return r;
 }
@@ -158,16 +167,17 @@ __device__ __forceinline__ void arrive_even(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(ptx::mapa(bar, 0)) : "memory");
 }
 
-// Both CTAs: this CTA's 128 rows of W and its half of the tokens.
+// Both CTAs: this CTA's 128 rows of the M side and its half of the N side.
+template <bool TOKENS_M>
 __device__ __forceinline__ void producer(const Params& p, const Smem& s, const Work& w, uint32_t rank) {
   Slot at;
   uint32_t used = 0;
   bool ok = true;
-  const bool small = p.n_tiles == 1;
+  const bool small = !TOKENS_M && p.n_tiles == 1;
   const int b_bytes = p.stage_bytes - kABytes;
   for (int u = w.first; u < w.count && ok; u += w.step) {
-    const Unit un = unit_of(p, w, u, rank);
-    const int tok = un.t0 + static_cast<int>(rank) * (p.n / 2);
+    const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
+    const int n_row = un.n0 + static_cast<int>(rank) * (p.n / 2);
     const uint32_t tx = 2u * static_cast<uint32_t>(un.boxes * 32 * kBlockK + b_bytes);
     for (int kb = 0; kb < p.kb; ++kb) {
       if (!ptx::wait_bounded_cluster(s.empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
@@ -180,11 +190,11 @@ __device__ __forceinline__ void producer(const Params& p, const Smem& s, const W
       const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes);
       if (small) {
         for (int b = 0; b < un.boxes; ++b)
-          ptx::tma_load_2d_pair(a + b * 32 * kBlockK, &p.tmW, kb * kBlockK, un.row + 32 * b, full);
+          ptx::tma_load_2d_pair(a + b * 32 * kBlockK, &p.tmA, kb * kBlockK, un.row + 32 * b, full);
       } else {
-        ptx::tma_load_2d_pair(a, &p.tmW, kb * kBlockK, un.row, full);
+        ptx::tma_load_2d_pair(a, &p.tmA, kb * kBlockK, un.row, full);
       }
-      ptx::tma_load_2d_pair(a + kABytes, &p.tmX, kb * kBlockK, tok, full);
+      ptx::tma_load_2d_pair(a + kABytes, &p.tmB, kb * kBlockK, n_row, full);
       used |= 1u << at.i;
       at.next(p.stages);
     }
@@ -250,8 +260,9 @@ __device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int g, int kb
   return w;
 }
 
-// The words of one scale stage: this CTA's rows 32 j .. and the tile's tokens
-// 32 j + lane, K blocks 4 g .. 4 g + 3.
+// The words of one scale stage, K blocks 4 g .. 4 g + 3: column j of the M side (this
+// CTA's rows 32 j + lane) and of the N side (the tile's rows 32 j + lane).  Tokens have
+// a word for each row; W's 32 rows of a column lie in one 128-row block.
 struct ScaleWords {
   uint32_t a[4], b[8];
 };
@@ -260,6 +271,7 @@ struct ScaleWords {
 // row r of A (or B) is lane r % 32, column r / 32, in every quarter.  The words of
 // the next stage are loaded before this one's TMEM stage is waited for, so a
 // load's latency does not stand between two stages.
+template <bool TOKENS_M>
 __device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, const Work& w, uint32_t tmem,
                                              uint32_t rank, int warp, int lane) {
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -267,19 +279,34 @@ __device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, con
   const bool words_w = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sw) & 3) == 0;
   const int groups = (p.kb + 3) / 4;
   const int last_block = (p.V + kRowsCta - 1) / kRowsCta - 1;
+  const auto of_token = [&](int t, int g) {
+    return t < p.T ? scale_word(p.sx + static_cast<int64_t>(t) * p.kb, g, p.kb, words_x) : 0x7f7f7f7fu;
+  };
+  const auto of_block = [&](int b, int g) {
+    return scale_word(p.sw + static_cast<int64_t>(min(b, last_block)) * p.kb, g, p.kb, words_w);
+  };
   const auto load = [&](int u, int g) {
     ScaleWords r;
-    const Unit un = unit_of(p, w, u, rank);
-    // four 32-row columns touch at most two of W's row blocks
-    const int b0 = min(un.row / kRowsCta, last_block), b1 = min((un.row + 96) / kRowsCta, last_block);
-    const uint32_t w0 = scale_word(p.sw + static_cast<int64_t>(b0) * p.kb, g, p.kb, words_w);
-    const uint32_t w1 = b1 == b0 ? w0 : scale_word(p.sw + static_cast<int64_t>(b1) * p.kb, g, p.kb, words_w);
+    const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
+    if constexpr (TOKENS_M) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.a[j] = (un.row + 32 * j) / kRowsCta <= b0 ? w0 : w1;
+      for (int j = 0; j < 4; ++j) r.a[j] = of_token(un.row + 32 * j + lane, g);
+      // 224 rows touch at most three blocks
+      const int b0 = un.n0 / kRowsCta;
+      const uint32_t w0 = of_block(b0, g), w1 = of_block(b0 + 1, g), w2 = of_block(b0 + 2, g);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int t = un.t0 + 32 * j + lane;
-      r.b[j] = 32 * j < p.n && t < p.T ? scale_word(p.sx + static_cast<int64_t>(t) * p.kb, g, p.kb, words_x) : 0x7f7f7f7fu;
+      for (int j = 0; j < 8; ++j) {
+        const int b = (un.n0 + 32 * j) / kRowsCta - b0;
+        r.b[j] = b == 0 ? w0 : b == 1 ? w1 : w2;
+      }
+    } else {
+      // four 32-row columns touch at most two blocks
+      const int b0 = un.row / kRowsCta;
+      const uint32_t w0 = of_block(b0, g), w1 = of_block((un.row + 96) / kRowsCta, g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r.a[j] = (un.row + 32 * j) / kRowsCta == b0 ? w0 : w1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r.b[j] = 32 * j < p.n ? of_token(un.n0 + 32 * j + lane, g) : 0x7f7f7f7fu;
     }
     return r;
   };
@@ -311,12 +338,46 @@ __device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, con
   }
 }
 
-// A warp's 32 rows x 32 tokens at a time.  In TMEM a lane is a vocabulary row and a
-// column a token; the staging buffer holds them token by token (32 lanes write one
-// token's 32 consecutive logits: no bank conflict), and one TMA store puts the box
-// into y, clipped at T and V.  Plain stores from the registers took 500 us more of
-// the 1.75 ms at 8192 x 2048 x 124,160: 64-byte pieces, one instruction each.
+// Tokens on M: lane = token, column = logit.  32 logits of 32 tokens at a time: each
+// lane writes its 64 (fp32: 128) bytes as 16-byte pieces in the TMA's 64-byte (128-byte)
+// swizzle, which keeps the eight lanes of a phase on different banks, and one TMA
+// store puts the box into y, clipped at T and V.
 template <typename E>
+__device__ __forceinline__ void store_tokens_m(const Params& p, uint32_t buf, const uint32_t (&r)[32], int lane) {
+  if constexpr (sizeof(E) == 4) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      ptx::st_shared_v4(buf + lane * 128 + ((k ^ (lane & 7)) << 4), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t h[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        h[i] = ptx::pack_bf16x2(__uint_as_float(r[8 * k + 2 * i]), __uint_as_float(r[8 * k + 2 * i + 1]));
+      ptx::st_shared_v4(buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4), h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+
+// Vocabulary on M: lane = vocabulary row, column = token.  The staging buffer holds
+// the box token by token (32 lanes write one token's 32 consecutive logits: no bank
+// conflict).
+template <typename E>
+__device__ __forceinline__ void store_vocab_m(uint32_t buf, const uint32_t (&r)[32], int lane) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if constexpr (sizeof(E) == 4)
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + j * 128 + lane * 4), "r"(r[j]) : "memory");
+    else
+      asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + j * 64 + lane * 2),
+                   "h"(__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j]))))
+                   : "memory");
+  }
+}
+
+// A warp's 32 lanes x 32 columns at a time.
+template <typename E, bool TOKENS_M>
 __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const Work& w, uint32_t tmem, uint32_t rank,
                                          int warp, int lane) {
   const int q = warp & 3;
@@ -324,7 +385,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
   Slot acc;
   uint32_t box = 0;
   for (int u = w.first; u < w.count; u += w.step) {
-    const Unit un = unit_of(p, w, u, rank);
+    const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
     if (!ptx::wait_bounded_cluster(s.acc_full(acc.i), acc.phase, p.timeout_ns, s.abort_flag)) {
       give_up(p, s);
       break;
@@ -332,42 +393,39 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
     __syncwarp();
     ptx::tc_fence_after();
     const uint32_t col = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.i * kMaxN;
-    const int v0 = un.row + q * 32;
-    if (q < un.boxes && v0 < p.V) {
+    const int m0 = un.row + q * 32;
+    const int m_end = TOKENS_M ? p.T : p.V, n_end = TOKENS_M ? p.V : p.T;
+    if (q < un.boxes && m0 < m_end) {
 #pragma unroll 1
-      for (int c = 0; c < p.n && un.t0 + c < p.T; c += 32) {
+      for (int c = 0; c < p.n && un.n0 + c < n_end; c += 32) {
         uint32_t r[32];
         ptx::tmem_ld32(col + c, r);
-        const int t0 = un.t0 + c;
-        if (p.y_tma) {
+        const int n0 = un.n0 + c;
+        if (TOKENS_M || p.y_tma) {
           const uint32_t buf = staging + (box & 1u) * (kStagingWarp / 2);
           if (lane == 0) ptx::bulk_wait_read<1>();  // the store before last has read this buffer
           __syncwarp();
           ptx::tmem_wait_ld32(r);
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if constexpr (sizeof(E) == 4)
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + j * 128 + lane * 4), "r"(r[j]) : "memory");
-            else
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + j * 64 + lane * 2),
-                           "h"(__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j]))))
-                           : "memory");
-          }
+          if constexpr (TOKENS_M)
+            store_tokens_m<E>(p, buf, r, lane);
+          else
+            store_vocab_m<E>(buf, r, lane);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            ptx::tma_store_2d(&p.tmY, buf, v0, t0);
+            ptx::tma_store_2d(&p.tmY, buf, TOKENS_M ? n0 : m0, TOKENS_M ? m0 : n0);
             ptx::bulk_commit();
           }
           ++box;
         } else {
+          // rows of y that do not start on 16 bytes: a warp's store is one token's 32 logits
           ptx::tmem_wait_ld32(r);
-          const int v = v0 + lane;
+          const int v = m0 + lane;
           if (v < p.V) {
-            E* y = static_cast<E*>(p.y) + static_cast<int64_t>(t0) * p.ldy + v;
+            E* y = static_cast<E*>(p.y) + static_cast<int64_t>(n0) * p.ldy + v;
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              if (t0 + j < p.T) {
+              if (n0 + j < p.T) {
                 if constexpr (sizeof(E) == 4)
                   y[j * p.ldy] = __uint_as_float(r[j]);
                 else
@@ -387,6 +445,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
   __syncwarp();
 }
 
+template <bool TOKENS_M>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_fp8_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -400,7 +459,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
-  const Work w = work_of(p);
+  const Work w = work_of<TOKENS_M>(p);
 
   // The status of this call.  The first CTA is dispatched first and clears the word
   // before anything else; a wait that runs out does so a millisecond later at the
@@ -425,8 +484,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::fence_proxy_async_smem();
   }
   if (warp == 0 && lane == 0) {
-    ptx::prefetch_tmap(&p.tmW);
-    ptx::prefetch_tmap(&p.tmX);
+    ptx::prefetch_tmap(&p.tmA);
+    ptx::prefetch_tmap(&p.tmB);
     if (p.y_tma) ptx::prefetch_tmap(&p.tmY);
   }
   if (warp == 1) {
@@ -439,19 +498,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *s.tmem_slot;
 
   if (warp == 0) {
-    if (ptx::elect_one()) producer(p, s, w, rank);
+    if (ptx::elect_one()) producer<TOKENS_M>(p, s, w, rank);
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0 && ptx::elect_one()) mma_issuer(p, s, w, tmem);
     __syncwarp();
   } else if (warp < 2 + kEpiWarps) {
     if (p.y_f32)
-      epilogue<float>(p, s, w, tmem, rank, warp, lane);
+      epilogue<float, TOKENS_M>(p, s, w, tmem, rank, warp, lane);
     else
-      epilogue<__nv_bfloat16>(p, s, w, tmem, rank, warp, lane);
+      epilogue<__nv_bfloat16, TOKENS_M>(p, s, w, tmem, rank, warp, lane);
     __syncwarp();
   } else {
-    scale_writer(p, s, w, tmem, rank, warp, lane);
+    scale_writer<TOKENS_M>(p, s, w, tmem, rank, warp, lane);
     __syncwarp();
   }
 
