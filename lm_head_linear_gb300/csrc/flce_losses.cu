@@ -11,21 +11,31 @@ using namespace flce::host;
 
 namespace {
 
-constexpr int64_t kPolicyBlockTokens = loss::kPolicyThreads * loss::kPolicyTokens;
+constexpr int64_t kClusterTokens = loss::kClusterThreads * loss::kGroup;  // of one CTA
 
-// Header (status) | block_sum | block_count | seq_count
+// Header (status, ticket) | block_sum | block_count | block_bad | words | seq_count.
+// Both forms of the call fit: the larger one is laid out.
+constexpr size_t kTicketOff = 16;
 struct PolicyLayout {
-  int64_t blocks;
-  size_t sum_off, count_off, seq_off, total;
+  int64_t chunk, blocks;  // the counting launch: tokens of a block, blocks (at most kMaxBlocks)
+  int64_t ctas;           // the second launch
+  size_t sum_off, count_off, bad_off, words_off, seq_off, total;
 };
 PolicyLayout policy_layout(int64_t T, int64_t S) {
   PolicyLayout L;
-  L.blocks = std::max<int64_t>(cdiv(T, kPolicyBlockTokens), 1);
+  const int64_t steps = std::max<int64_t>(cdiv(T, loss::kStep), 1);
+  L.chunk = cdiv(steps, loss::kMaxBlocks) * loss::kStep;
+  L.blocks = std::max<int64_t>(cdiv(T, L.chunk), 1);
+  L.ctas = std::min<int64_t>(steps, 2 * loss::kMaxBlocks);
   size_t off = kHeaderBytes;
   L.sum_off = off;
-  off = align_up(off + sizeof(double) * loss::kSums * L.blocks, 256);
+  off = align_up(off + sizeof(double) * loss::kSums * L.ctas, 256);
   L.count_off = off;
   off = align_up(off + sizeof(int32_t) * L.blocks, 256);
+  L.bad_off = off;
+  off = align_up(off + sizeof(int32_t) * L.blocks, 256);
+  L.words_off = off;
+  off = align_up(off + sizeof(uint2) * static_cast<size_t>(cdiv(std::max<int64_t>(T, 1), 32)), 256);
   L.seq_off = off;
   off = align_up(off + sizeof(int32_t) * std::max<int64_t>(S, 1), 256);
   L.total = off;
@@ -55,9 +65,7 @@ flce_status largest_cluster(int dev, int* ctas) {
   static int known[64] = {};
   std::lock_guard<std::mutex> lk(mu);
   if (known[dev] == 0) {
-    const void* kernels[] = {reinterpret_cast<const void*>(loss::policy_cluster_kernel<1>),
-                             reinterpret_cast<const void*>(loss::policy_cluster_kernel<2>),
-                             reinterpret_cast<const void*>(loss::policy_cluster_kernel<4>),
+    const void* kernels[] = {reinterpret_cast<const void*>(loss::policy_cluster_kernel),
                              reinterpret_cast<const void*>(loss::preference_kernel<true>)};
     int most = loss::kClusterCtas;
     for (const void* k : kernels) {
@@ -86,6 +94,22 @@ flce_status launch_cluster(void (*kernel)(P), const P& p, int64_t grid, int ctas
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim.x = static_cast<unsigned>(ctas), at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
+  return FLCE_OK;
+}
+
+// A launch that may be dispatched while the one before it on the stream still runs
+// (the kernel waits for it with griddepcontrol.wait).
+template <typename P>
+flce_status launch_dependent(void (*kernel)(P), const P& p, int64_t grid, int threads, cudaStream_t s) {
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
@@ -163,30 +187,25 @@ flce_status flce_policy_loss(const float* dloss, const float* logp, const float*
   p.status = reinterpret_cast<int32_t*>(ws);
   p.block_sum = reinterpret_cast<double*>(ws + L.sum_off);
   p.block_count = reinterpret_cast<int32_t*>(ws + L.count_off);
+  p.block_bad = reinterpret_cast<int32_t*>(ws + L.bad_off);
+  p.words = reinterpret_cast<uint2*>(ws + L.words_off);
   p.seq_count = reinterpret_cast<int32_t*>(ws + L.seq_off);
+  p.ticket = reinterpret_cast<int32_t*>(ws + kTicketOff);
   p.vec = !(off16(logp) || off16(old_logp) || off16(ref_logp) || (!advantages_per_sequence && off16(advantages)) ||
             off16(targets) || off16(dlogp) ||
             (reduction == FLCE_REDUCTION_NONE && (off16(loss) || off16(dloss))));
   int most = 0;
   if ((st = largest_cluster(dev, &most)) != FLCE_OK) return st;
   KernelScope ks(FLCE_KERNEL_POLICY_LOSS, s, 20.0 * T, T * (12.0 + (ref_logp ? 4.0 : 0.0) + 8.0 + (dlogp ? 4.0 : 0.0)));
-  constexpr int64_t kCtaTokens = loss::kClusterThreads * loss::kGroup;
-  if (T <= most * kCtaTokens * 4) {
-    p.blocks = pow2_up(cdiv(T, kCtaTokens), most);
-    const int64_t groups = cdiv(T, kCtaTokens * p.blocks);
-    st = groups <= 1   ? launch_cluster(loss::policy_cluster_kernel<1>, p, p.blocks, p.blocks, loss::kClusterThreads, s)
-         : groups == 2 ? launch_cluster(loss::policy_cluster_kernel<2>, p, p.blocks, p.blocks, loss::kClusterThreads, s)
-                       : launch_cluster(loss::policy_cluster_kernel<4>, p, p.blocks, p.blocks, loss::kClusterThreads, s);
-    if (st != FLCE_OK) return st;
+  if (T <= most * kClusterTokens) {
+    p.blocks = pow2_up(cdiv(T, kClusterTokens), most);
+    st = launch_cluster(loss::policy_cluster_kernel, p, p.blocks, p.blocks, loss::kClusterThreads, s);
   } else {
-    p.blocks = static_cast<int32_t>(L.blocks);
-    CUDA_TRY(cudaMemsetAsync(ws, 0, kHeaderBytes, s));
-    if (reduction == FLCE_REDUCTION_SEQUENCE_MEAN)
-      CUDA_TRY(cudaMemsetAsync(p.seq_count, 0, sizeof(int32_t) * std::max<int64_t>(n_seqs, 1), s));
-    loss::policy_count_kernel<<<p.blocks, loss::kPolicyThreads, 0, s>>>(p);
-    loss::policy_main_kernel<<<p.blocks, loss::kPolicyThreads, 0, s>>>(p);
-    loss::policy_reduce_kernel<<<1, loss::kPolicyThreads, 0, s>>>(p);
+    p.blocks = static_cast<int32_t>(L.blocks), p.chunk = static_cast<int32_t>(L.chunk);
+    loss::policy_count_kernel<<<p.blocks, loss::kManyThreads, 0, s>>>(p);
+    st = launch_dependent(loss::policy_main_kernel, p, L.ctas, loss::kManyThreads, s);
   }
+  if (st != FLCE_OK) return st;
   ks.done();
   return check_launch("policy_loss");
 }
@@ -256,7 +275,7 @@ flce_status flce_preference_loss(const float* dloss, const float* logp, const fl
     // enough CTAs to fill the device, of at least 2048 tokens each
     p.ctas = pow2_up(std::min<int64_t>(mean / 2048, 2 * sms / n_pairs), 8);
     st = launch_cluster(loss::preference_kernel<false>, p, n_pairs * p.ctas, p.ctas, loss::kPairThreads, s);
-    if (st == FLCE_OK) loss::preference_reduce_kernel<<<1, loss::kReduceThreads, 0, s>>>(p);
+    if (st == FLCE_OK) st = launch_dependent(loss::preference_reduce_kernel, p, 1, loss::kReduceThreads, s);
   }
   if (st != FLCE_OK) return st;
   ks.done();

@@ -30,21 +30,6 @@ __device__ __forceinline__ float clamp_ratio(float v) {
   return v > kMaxLogRatio ? kMaxLogRatio : (v < -kMaxLogRatio ? -kMaxLogRatio : v);
 }
 
-// ------------------------------------------------------------------ sequences
-// Index s with cu[s] <= t < cu[s + 1] over cu [n + 1], or -1 when t lies in none.
-// Any contents of cu give an index in [-1, n - 1].
-__device__ __forceinline__ int find_sequence(const int64_t* cu, int n, int64_t t) {
-  int lo = 0, hi = n + 1;  // the first index with cu[index] > t lies in [lo, hi]
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] > t)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return lo > n ? -1 : lo - 1;  // lo == 0: before the first sequence; lo == n + 1: after the last
-}
-
 // ------------------------------------------------------------------ policy loss
 struct PolicyParams {
   const float* dloss;    // [1] or [T] (NONE), nullptr: ones
@@ -66,10 +51,14 @@ struct PolicyParams {
   float kl_coef;
   // workspace
   int32_t* status;
-  int32_t* seq_count;    // [S] valid tokens of each sequence (SEQUENCE_MEAN)
-  int32_t* block_count;  // [blocks]
-  double* block_sum;     // [blocks][5]
-  int32_t blocks;        // CTAs of the launches over token blocks, or of the one cluster
+  int32_t* ticket;       // CTAs of the second launch that are done
+  int32_t* seq_count;    // [S] valid tokens of each sequence (the one-cluster form)
+  int32_t* block_count;  // [blocks] valid tokens of a block of `chunk` tokens
+  int32_t* block_bad;    // [blocks]
+  uint2* words;          // [ceil(T / 32)] mask of 32 tokens, valid tokens of the block before them
+  double* block_sum;     // [CTAs of the second launch][5]
+  int32_t blocks;        // blocks of the first launch, or CTAs of the one cluster
+  int32_t chunk;         // tokens of a block
   int32_t vec;           // every per-token array is 16-byte aligned
 };
 
@@ -113,8 +102,6 @@ __device__ __forceinline__ PolicyTerm policy_token(const PolicyParams& p, float 
   return o;
 }
 
-constexpr int kPolicyThreads = 256;
-constexpr int kPolicyTokens = 4;  // per thread
 constexpr int kSums = 5;          // loss, kl, cut, log ratio, ratio
 
 // Sum over the block in a fixed order; the result on thread 0.
@@ -132,108 +119,15 @@ __device__ __forceinline__ E block_sum(E v, E* sh) {
   return s;
 }
 
-// A token counts when its target is not ignore_index and, with sequences given,
-// it lies in one of them.
-__device__ __forceinline__ bool token_valid(const PolicyParams& p, int64_t t, int* seq) {
-  *seq = 0;
-  if (t >= p.T || p.targets[t] == p.ignore_index) return false;
-  if (p.cu) {
-    *seq = find_sequence(p.cu, p.S, t);
-    if (*seq < 0) return false;
-  }
-  return true;
-}
-
-// Counts: valid tokens of each block, and of each sequence (integers: the order of
-// the atomics does not change them).  Also checks cu.
-__global__ void __launch_bounds__(kPolicyThreads) policy_count_kernel(const PolicyParams p) {
-  __shared__ int sh[kPolicyThreads / 32];
-  int n = 0;
-  for (int k = 0; k < kPolicyTokens; ++k) {
-    const int64_t t = (static_cast<int64_t>(blockIdx.x) * kPolicyTokens + k) * kPolicyThreads + threadIdx.x;
-    int s;
-    if (token_valid(p, t, &s)) {
-      ++n;
-      if (p.reduction == kSequenceMean) atomicAdd(p.seq_count + s, 1);
-    }
-  }
-  n = block_sum<int, kPolicyThreads>(n, sh);
-  if (threadIdx.x == 0) p.block_count[blockIdx.x] = n;
-  if (p.cu) {
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kPolicyThreads;
-    bool bad = false;
-    for (int64_t s = static_cast<int64_t>(blockIdx.x) * kPolicyThreads + threadIdx.x; s <= p.S; s += stride) {
-      const int64_t a = s ? p.cu[s - 1] : 0, b = p.cu[s];
-      bad = bad || b < a || b > p.T;
-    }
-    if (bad) atomicCAS(p.status, 0, kStatusSequences);
-  }
-}
-
-__global__ void __launch_bounds__(kPolicyThreads) policy_main_kernel(const PolicyParams p) {
-  __shared__ double sh[kPolicyThreads / 32];
-  __shared__ int sh_i[kPolicyThreads / 32];
-  __shared__ float scale;
-  // the weight that all tokens share: 1, 1 / n_valid or 1 / (sequences with a valid token)
-  int c = 0;
-  if (p.reduction == kMean)
-    for (int i = threadIdx.x; i < p.blocks; i += kPolicyThreads) c += p.block_count[i];
-  if (p.reduction == kSequenceMean)
-    for (int i = threadIdx.x; i < p.S; i += kPolicyThreads) c += p.seq_count[i] > 0;
-  c = block_sum<int, kPolicyThreads>(c, sh_i);
-  if (threadIdx.x == 0) scale = p.reduction == kMean || p.reduction == kSequenceMean ? 1.0f / fmaxf(c, 1.0f) : 1.0f;
-  __syncthreads();
-  const float up = p.dloss && p.reduction != kNone ? p.dloss[0] : 1.0f;
-  float sum[kSums] = {};
-  for (int k = 0; k < kPolicyTokens; ++k) {
-    const int64_t t = (static_cast<int64_t>(blockIdx.x) * kPolicyTokens + k) * kPolicyThreads + threadIdx.x;
-    if (t >= p.T) break;
-    int s;
-    float l = 0.0f, g = 0.0f;
-    if (token_valid(p, t, &s)) {
-      const PolicyTerm o =
-          policy_token(p, p.logp[t], p.old_logp[t], p.ref ? p.ref[t] : 0.0f, p.adv[p.adv_per_seq ? s : t]);
-      const float w = p.reduction == kSequenceMean ? scale / p.seq_count[s] : scale;
-      l = o.loss;
-      g = o.grad * w * (p.reduction == kNone && p.dloss ? p.dloss[t] : up);
-      sum[0] += p.reduction == kSequenceMean ? o.loss * w : o.loss;
-      sum[1] += o.kl, sum[2] += o.cut, sum[3] += o.d, sum[4] += o.rho;
-    }
-    if (p.dlogp) p.dlogp[t] = g;
-    if (p.loss && p.reduction == kNone) p.loss[t] = l;
-  }
-  for (int i = 0; i < kSums; ++i) {
-    const double s = block_sum<double, kPolicyThreads>(static_cast<double>(sum[i]), sh);
-    if (threadIdx.x == 0) p.block_sum[blockIdx.x * kSums + i] = s;
-  }
-}
-
-__global__ void __launch_bounds__(kPolicyThreads) policy_reduce_kernel(const PolicyParams p) {
-  __shared__ double sh[kPolicyThreads / 32];
-  __shared__ long long sh_n[kPolicyThreads / 32];
-  long long n = 0;
-  double sum[kSums] = {};
-  for (int b = threadIdx.x; b < p.blocks; b += kPolicyThreads) {
-    n += p.block_count[b];
-    for (int i = 0; i < kSums; ++i) sum[i] += p.block_sum[b * kSums + i];
-  }
-  n = block_sum<long long, kPolicyThreads>(n, sh_n);
-  for (int i = 0; i < kSums; ++i) sum[i] = block_sum<double, kPolicyThreads>(sum[i], sh);
-  if (threadIdx.x != 0) return;
-  const double inv = n > 0 ? 1.0 / static_cast<double>(n) : 0.0;
-  if (p.loss && p.reduction != kNone) p.loss[0] = static_cast<float>(p.reduction == kMean ? sum[0] * inv : sum[0]);
-  if (p.stats)
-    for (int i = 1; i < kSums; ++i) p.stats[i - 1] = static_cast<float>(sum[i] * inv);
-  if (p.n_valid) *p.n_valid = n;
-}
-
 // ------------------------------------------------------------------ policy loss in one launch
-// Up to kClusterCtas * 512 * 16 tokens: one cluster of CTAs.  A token's loss and
+// Up to 16 * 512 * 4 = 32,768 tokens: one cluster of CTAs.  A token's loss and
 // gradient do not depend on how many tokens count; only the common weight does.
-// So every thread reads its tokens once and keeps the unscaled gradients in
+// So every thread reads its four tokens once and keeps the unscaled gradients in
 // registers while the counts go round the cluster through distributed shared
 // memory (or, per sequence, through integer atomics in the workspace), and scales
 // and stores them after one cluster barrier.  No second launch, no second reading.
+// Beyond that the 16 SMs of a cluster are too few (131,072 tokens in 61 sequences: 25.5
+// us with four such steps a thread), and the two launches further down take over.
 constexpr int kClusterCtas = 16;
 constexpr int kClusterThreads = 512;
 constexpr int kGroup = 4;            // consecutive tokens of a thread and step
@@ -297,15 +191,16 @@ struct Offsets {
   const int64_t* cu;
   int n;       // sequences
   __device__ __forceinline__ int64_t at(int i) const { return sh ? sh[i] : __ldg(cu + i); }
-  // as find_sequence()
+  // Index s with cu[s] <= t < cu[s + 1], or -1 when t lies in none.  Any contents of cu
+  // give an index in [-1, n - 1].
   __device__ __forceinline__ int find(int64_t t) const {
-    int lo = 0, hi = n + 1;
+    int lo = 0, hi = n + 1;  // the first index with cu[index] > t lies in [lo, hi]
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
       if (at(mid) > t) hi = mid;
       else lo = mid + 1;
     }
-    return lo > n ? -1 : lo - 1;
+    return lo > n ? -1 : lo - 1;  // lo == 0: before the first sequence; n + 1: after the last
   }
   // the sequence of token t + 1 .. from the one of an earlier token
   __device__ __forceinline__ int step(int s, int64_t t) const {
@@ -315,7 +210,104 @@ struct Offsets {
   }
 };
 
-template <int NG>
+// Four tokens of a thread: their inputs, and what does not depend on the counts.
+struct Tokens4 {
+  float4 lp, old, ref, adv;
+  uint32_t mask;               // bit j: token t + j counts
+  int seq0;                    // sequence of the first token that counts
+  float grad[kGroup], val[kGroup];
+};
+
+__device__ __forceinline__ void load_tokens(const PolicyParams& p, int64_t t, int left, bool vec, Tokens4& q) {
+  q.mask = valid4(p.targets, p.ignore_index, t, left, vec);
+  q.lp = load4(p.logp, t, left, vec);
+  q.old = load4(p.old_logp, t, left, vec);
+  if (p.ref) q.ref = load4(p.ref, t, left, vec);
+  if (!p.adv_per_seq) q.adv = load4(p.adv, t, left, vec);
+}
+
+// [first, end): the tokens that lie in a sequence.
+__device__ __forceinline__ void eval_tokens(const PolicyParams& p, const Offsets& off, bool by_seq, int64_t first,
+                                            int64_t end, int64_t t, Tokens4& q, float (&sum)[kSums], int& n) {
+  uint32_t m = q.mask;
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j)
+    if (t + j < first || t + j >= end) m &= ~(1u << j);
+  int s = -1;
+  float A_seq = 0.0f;
+  if (by_seq && m) {
+    s = off.find(t + __ffs(m) - 1);
+    if (s < 0) m = 0;
+    else if (p.adv_per_seq) A_seq = __ldg(p.adv + s);
+  }
+  q.seq0 = s;
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j) {
+    q.grad[j] = q.val[j] = 0.0f;
+    if (!(m >> j & 1u)) continue;
+    float A = lane4(q.adv, j);
+    if (by_seq) {
+      const int was = s;
+      s = off.step(s, t + j);
+      if (s < 0) {  // only where cu is not in order
+        m &= ~(1u << j);
+        continue;
+      }
+      if (p.adv_per_seq) {
+        if (s != was) A_seq = __ldg(p.adv + s);
+        A = A_seq;
+      }
+    }
+    const PolicyTerm o = policy_token(p, lane4(q.lp, j), lane4(q.old, j), lane4(q.ref, j), A);
+    q.grad[j] = o.grad;
+    q.val[j] = o.loss;
+    sum[0] += o.loss, sum[1] += o.kl, sum[2] += o.cut, sum[3] += o.d, sum[4] += o.rho;
+    ++n;
+  }
+  q.mask = m;
+}
+
+// SEQUENCE_MEAN: every token's weight from its sequence's count; the weighted loss is returned.
+template <typename Count>
+__device__ __forceinline__ float weigh_tokens(const Offsets& off, int64_t t, float scale, Tokens4& q, Count count) {
+  float total = 0.0f;
+  int s = q.seq0;
+  float w = q.mask ? scale / static_cast<float>(count(s)) : 0.0f;
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j)
+    if (q.mask >> j & 1u) {
+      const int was = s;
+      s = off.step(s, t + j);
+      if (s != was) w = scale / static_cast<float>(count(s));
+      q.grad[j] *= w;
+      total = fmaf(q.val[j], w, total);
+    }
+  return total;
+}
+
+__device__ __forceinline__ void store_tokens(const PolicyParams& p, int64_t t, int left, bool vec, float scale, Tokens4& q) {
+  if (p.dlogp) {
+    const float up = p.dloss && p.reduction != kNone ? __ldg(p.dloss) : 1.0f;
+    float4 u = make_float4(up, up, up, up);
+    if (p.reduction == kNone && p.dloss) u = load4(p.dloss, t, left, vec);
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) q.grad[j] = q.mask >> j & 1u ? q.grad[j] * scale * lane4(u, j) : 0.0f;
+    store4(p.dlogp, t, left, vec, q.grad);
+  }
+  if (p.loss && p.reduction == kNone) store4(p.loss, t, left, vec, q.val);
+}
+
+// The scalar outputs from the summed terms: thread i < kSums holds sum i.
+__device__ __forceinline__ void store_scalars(const PolicyParams& p, int i, double v, int64_t valid) {
+  const double inv = valid > 0 ? 1.0 / static_cast<double>(valid) : 0.0;
+  if (i == 0) {
+    if (p.loss && p.reduction != kNone) p.loss[0] = static_cast<float>(p.reduction == kMean ? v * inv : v);
+    if (p.n_valid) *p.n_valid = valid;
+  } else if (p.stats) {
+    p.stats[i - 1] = static_cast<float>(v * inv);
+  }
+}
+
 __global__ void __launch_bounds__(kClusterThreads) policy_cluster_kernel(const PolicyParams p) {
   constexpr int kWarps = kClusterThreads / 32;
   __shared__ int32_t cu_sh[kCuShared];
@@ -328,6 +320,11 @@ __global__ void __launch_bounds__(kClusterThreads) policy_cluster_kernel(const P
   const int ctas = p.blocks;
   const bool seq_mean = p.reduction == kSequenceMean;
   const bool by_seq = seq_mean || p.adv_per_seq;
+  const int64_t t = static_cast<int64_t>(kGroup) * (rank * kClusterThreads + tid);
+  const int left = static_cast<int>(min(max(p.T - t, int64_t(0)), int64_t(kGroup)));
+  const bool vec = p.vec && left == kGroup;
+  Tokens4 q{};
+  if (left > 0) load_tokens(p, t, left, vec, q);
 
   if (seq_mean)
     for (int i = rank * kClusterThreads + tid; i < p.S; i += ctas * kClusterThreads) p.seq_count[i] = 0;
@@ -348,86 +345,35 @@ __global__ void __launch_bounds__(kClusterThreads) policy_cluster_kernel(const P
   if (rank == 0 && tid == 0) *p.status = 0;
   cluster_arrive();  // zeroed counts, and: every CTA of the cluster is running
 
-  float grad[NG][kGroup], val[NG][kGroup];
-  uint32_t mask[NG];
-  int seq0[NG];
   float sum[kSums] = {};
   int n = 0;
-#pragma unroll
-  for (int k = 0; k < NG; ++k) {
-    const int64_t t = static_cast<int64_t>(kGroup) * ((static_cast<int64_t>(k) * ctas + rank) * kClusterThreads + tid);
-    const int left = static_cast<int>(min(max(p.T - t, int64_t(0)), int64_t(kGroup)));
-    const bool vec = p.vec && left == kGroup;
-    mask[k] = 0;
-    seq0[k] = -1;
-#pragma unroll
-    for (int j = 0; j < kGroup; ++j) grad[k][j] = val[k][j] = 0.0f;
-    if (left > 0) {
-      uint32_t m = valid4(p.targets, p.ignore_index, t, left, vec);
-      const float4 lp = load4(p.logp, t, left, vec), old = load4(p.old_logp, t, left, vec);
-      float4 ref = make_float4(0.0f, 0.0f, 0.0f, 0.0f), adv = ref;
-      if (p.ref) ref = load4(p.ref, t, left, vec);
-      if (!p.adv_per_seq) adv = load4(p.adv, t, left, vec);
-      if (p.cu) {
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j)
-          if (t + j < first_tok || t + j >= end_tok) m &= ~(1u << j);
-      }
-      int s = -1;
-      if (by_seq && m) {
-        s = seq0[k] = off.find(t + __ffs(m) - 1);
-        if (s < 0) m = 0;
-      }
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
-        if (!(m >> j & 1u)) continue;
-        float A = lane4(adv, j);
-        if (by_seq) {
-          s = off.step(s, t + j);
-          if (s < 0) {  // only where cu is not in order
-            m &= ~(1u << j);
-            continue;
-          }
-          if (p.adv_per_seq) A = __ldg(p.adv + s);
-        }
-        const PolicyTerm o = policy_token(p, lane4(lp, j), lane4(old, j), lane4(ref, j), A);
-        grad[k][j] = o.grad;
-        val[k][j] = o.loss;
-        sum[0] += o.loss, sum[1] += o.kl, sum[2] += o.cut, sum[3] += o.d, sum[4] += o.rho;
-        ++n;
-      }
-      mask[k] = m;
-    }
-  }
+  if (left > 0) eval_tokens(p, off, by_seq, first_tok, end_tok, t, q, sum, n);
 
   cluster_wait();
   if (seq_mean) {
     // valid tokens of each sequence: one atomic for a warp whose tokens lie in one
     // sequence, else one for each run of a thread's tokens
+    int s = q.seq0;
+    bool one = true;
 #pragma unroll
-    for (int k = 0; k < NG; ++k) {
-      const int64_t t = static_cast<int64_t>(kGroup) * ((static_cast<int64_t>(k) * ctas + rank) * kClusterThreads + tid);
-      int s = seq0[k], run = 0, last = s;
-      bool one = true;
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j)
-        if (mask[k] >> j & 1u) {
-          s = off.step(s, t + j);
-          one = one && s == seq0[k];
-          last = s;
-        }
-      const unsigned has = __ballot_sync(0xffffffffu, mask[k] != 0);
-      if (has == 0) continue;
-      const int lead = __shfl_sync(0xffffffffu, seq0[k], __ffs(has) - 1);
-      const bool same = mask[k] == 0 || (one && seq0[k] == lead);
+    for (int j = 0; j < kGroup; ++j)
+      if (q.mask >> j & 1u) {
+        s = off.step(s, t + j);
+        one = one && s == q.seq0;
+      }
+    const unsigned has = __ballot_sync(0xffffffffu, q.mask != 0);
+    if (has) {
+      const int lead = __shfl_sync(0xffffffffu, q.seq0, __ffs(has) - 1);
+      const bool same = q.mask == 0 || (one && q.seq0 == lead);
       if (__all_sync(0xffffffffu, same)) {
-        const int c = __reduce_add_sync(0xffffffffu, __popc(mask[k]));
+        const int c = __reduce_add_sync(0xffffffffu, __popc(q.mask));
         if (lane == 0) atomicAdd(p.seq_count + lead, c);
-      } else if (mask[k]) {
-        s = last = seq0[k];
+      } else if (q.mask) {
+        int run = 0, last = q.seq0;
+        s = last;
 #pragma unroll
         for (int j = 0; j < kGroup; ++j)
-          if (mask[k] >> j & 1u) {
+          if (q.mask >> j & 1u) {
             s = off.step(s, t + j);
             if (s != last) {
               atomicAdd(p.seq_count + last, run);
@@ -452,21 +398,8 @@ __global__ void __launch_bounds__(kClusterThreads) policy_cluster_kernel(const P
       total = a;
     }
     __syncthreads();
-    const float scale = 1.0f / fmaxf(static_cast<float>(total), 1.0f);
-    sum[0] = 0.0f;
-#pragma unroll
-    for (int k = 0; k < NG; ++k) {
-      const int64_t t = static_cast<int64_t>(kGroup) * ((static_cast<int64_t>(k) * ctas + rank) * kClusterThreads + tid);
-      int s = seq0[k];
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j)
-        if (mask[k] >> j & 1u) {
-          s = off.step(s, t + j);
-          const float w = scale / static_cast<float>(__ldcg(p.seq_count + s));
-          grad[k][j] *= w;
-          sum[0] = fmaf(val[k][j], w, sum[0]);
-        }
-    }
+    sum[0] = weigh_tokens(off, t, 1.0f / fmaxf(static_cast<float>(total), 1.0f), q,
+                          [&](int i) { return __ldcg(p.seq_count + i); });
   }
 
   // this CTA's sums: fp32 in a warp, 64 bits across warps; one thread per sum pushes them
@@ -494,35 +427,195 @@ __global__ void __launch_bounds__(kClusterThreads) policy_cluster_kernel(const P
 
   int valid = 0;
   for (int i = 0; i < ctas; ++i) valid += cta_n[i];
-  const float scale = p.reduction == kMean ? 1.0f / fmaxf(static_cast<float>(valid), 1.0f) : 1.0f;
-  const float up = p.dloss && p.reduction != kNone ? p.dloss[0] : 1.0f;
-#pragma unroll
-  for (int k = 0; k < NG; ++k) {
-    const int64_t t = static_cast<int64_t>(kGroup) * ((static_cast<int64_t>(k) * ctas + rank) * kClusterThreads + tid);
-    const int left = static_cast<int>(min(max(p.T - t, int64_t(0)), int64_t(kGroup)));
-    if (left <= 0) continue;
-    const bool vec = p.vec && left == kGroup;
-    if (p.dlogp) {
-      float4 u = make_float4(up, up, up, up);
-      if (p.reduction == kNone && p.dloss) u = load4(p.dloss, t, left, vec);
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) grad[k][j] = mask[k] >> j & 1u ? grad[k][j] * scale * lane4(u, j) : 0.0f;
-      store4(p.dlogp, t, left, vec, grad[k]);
-    }
-    if (p.loss && p.reduction == kNone) store4(p.loss, t, left, vec, val[k]);
-  }
+  if (left > 0)
+    store_tokens(p, t, left, vec, p.reduction == kMean ? 1.0f / fmaxf(static_cast<float>(valid), 1.0f) : 1.0f, q);
   if (rank == 0 && tid < kSums) {
     double v = 0.0;
     for (int i = 0; i < ctas; ++i) v += cta_sum[i][tid];
-    const double inv = valid > 0 ? 1.0 / static_cast<double>(valid) : 0.0;
-    if (tid == 0) {
-      if (p.loss && p.reduction != kNone) p.loss[0] = static_cast<float>(p.reduction == kMean ? v * inv : v);
-      if (p.n_valid) *p.n_valid = valid;
-    } else if (p.stats) {
-      p.stats[tid - 1] = static_cast<float>(v * inv);
-    }
+    store_scalars(p, tid, v, valid);
   }
   if (bad && tid == 0) atomicCAS(p.status, 0, kStatusSequences);
+}
+
+// ------------------------------------------------------------------ policy loss in two launches
+// More tokens: first the counts alone, from the targets, then everything else with
+// the weights known.  The counts are kept so that the number of valid tokens before
+// any token is three loads: a prefix over blocks (each CTA of the second launch adds
+// up the at most 1024 block counts), one within the block for every 32 tokens, and
+// their mask.  A sequence's count is the difference of two, without atomics or an
+// array to clear.  The second launch is dispatched while the first still runs and
+// loads its tokens before it waits for it; its last CTA adds up the sums in order.
+constexpr int kManyThreads = 256;
+constexpr int kMaxBlocks = 1024;
+constexpr int kStep = kManyThreads * kGroup;  // tokens a CTA takes at a time
+
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kManyThreads) policy_count_kernel(const PolicyParams p) {
+  constexpr int kWarps = kManyThreads / 32;
+  __shared__ int warp_n[kWarps];
+  launch_dependents();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t first = p.cu ? p.cu[0] : 0, end = p.cu ? p.cu[p.S] : p.T;
+  const int64_t b0 = static_cast<int64_t>(blockIdx.x) * p.chunk, b1 = min(b0 + p.chunk, int64_t(p.T));
+  int before = 0;  // valid tokens of the block so far
+  for (int64_t base = b0; base < b1; base += kStep) {
+    const int64_t t = base + kGroup * tid;
+    const int left = static_cast<int>(min(max(b1 - t, int64_t(0)), int64_t(kGroup)));
+    uint32_t m = left > 0 ? valid4(p.targets, p.ignore_index, t, left, p.vec && left == kGroup) : 0;
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j)
+      if (t + j < first || t + j >= end) m &= ~(1u << j);
+    // eight threads make a word of 32 tokens
+    uint32_t word = m << (4 * (lane & 7));
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, d);
+    const int c = __popc(m);
+    const int all = __reduce_add_sync(0xffffffffu, c);
+    __syncthreads();
+    if (lane == 0) warp_n[warp] = all;
+    __syncthreads();
+    int at = before;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) at += warp_n[i];
+      before += warp_n[i];
+    }
+    // words of this warp before this one
+    const int w = __popc(word);
+    const int w0 = __shfl_sync(0xffffffffu, w, 0), w1 = __shfl_sync(0xffffffffu, w, 8), w2 = __shfl_sync(0xffffffffu, w, 16);
+    at += (lane >= 8 ? w0 : 0) + (lane >= 16 ? w1 : 0) + (lane >= 24 ? w2 : 0);
+    if ((lane & 7) == 0 && t < b1) p.words[t / 32] = make_uint2(word, static_cast<uint32_t>(at));
+  }
+  bool bad = false;
+  if (p.cu)
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kManyThreads + tid; i <= p.S;
+         i += static_cast<int64_t>(gridDim.x) * kManyThreads) {
+      const int64_t a = i ? p.cu[i - 1] : 0, b = p.cu[i];
+      bad = bad || b < a || b > p.T;
+    }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) {
+    p.block_count[blockIdx.x] = before;
+    p.block_bad[blockIdx.x] = bad;
+    if (blockIdx.x == 0) *p.ticket = 0;
+  }
+}
+
+__global__ void __launch_bounds__(kManyThreads) policy_main_kernel(const PolicyParams p) {
+  constexpr int kWarps = kManyThreads / 32;
+  __shared__ int32_t cu_sh[kCuShared];
+  __shared__ int prefix[kMaxBlocks + 1];  // valid tokens before each block
+  __shared__ float warp_sum[kWarps][kSums];
+  __shared__ int warp_n[kWarps];
+  __shared__ int last;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool seq_mean = p.reduction == kSequenceMean;
+  const bool by_seq = seq_mean || p.adv_per_seq;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kStep;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kStep + kGroup * tid;
+  int left = static_cast<int>(min(max(p.T - t, int64_t(0)), int64_t(kGroup)));
+  Tokens4 q{};
+  if (left > 0) load_tokens(p, t, left, p.vec && left == kGroup, q);
+  Offsets off{by_seq && p.S < kCuShared ? cu_sh : nullptr, p.cu, p.S};
+  if (off.sh)
+    for (int i = tid; i <= p.S; i += kManyThreads)
+      cu_sh[i] = static_cast<int32_t>(min(max(p.cu[i], int64_t(0)), int64_t(p.T)));
+  const int64_t first = p.cu ? p.cu[0] : 0, end = p.cu ? p.cu[p.S] : p.T;
+
+  wait_prerequisites();
+  // exclusive prefix of the block counts: four blocks a thread
+  {
+    constexpr int kEach = kMaxBlocks / kManyThreads;
+    int c[kEach], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int b = tid * kEach + i;
+      c[i] = b < p.blocks ? __ldcg(p.block_count + b) : 0;
+      mine += c[i];
+    }
+    int inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    if (lane == 31) warp_n[warp] = inc;
+    __syncthreads();
+    int at = inc - mine;
+    for (int i = 0; i < warp; ++i) at += warp_n[i];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      prefix[tid * kEach + i] = at;
+      at += c[i];
+    }
+    if (tid == kManyThreads - 1) prefix[kMaxBlocks] = at;
+    __syncthreads();
+  }
+  const int valid = prefix[kMaxBlocks];
+  // valid tokens before token i, 0 <= i <= T
+  const auto before = [&](int64_t i) {
+    if (i >= p.T) return valid;
+    const uint2 w = __ldcg(p.words + i / 32);
+    return prefix[i / p.chunk] + static_cast<int>(w.y) + __popc(w.x & ((1u << (i & 31)) - 1u));
+  };
+  const auto offset = [&](int i) { return min(max(off.at(i), int64_t(0)), int64_t(p.T)); };
+  const auto count = [&](int s) { return before(offset(s + 1)) - before(offset(s)); };
+  float scale = p.reduction == kMean ? 1.0f / fmaxf(static_cast<float>(valid), 1.0f) : 1.0f;
+  if (seq_mean) {
+    int c = 0;
+    for (int i = tid; i < p.S; i += kManyThreads) c += count(i) > 0;
+    c = __reduce_add_sync(0xffffffffu, c);
+    __syncthreads();
+    if (lane == 0) warp_n[warp] = c;
+    __syncthreads();
+    c = 0;
+    for (int i = 0; i < kWarps; ++i) c += warp_n[i];
+    scale = 1.0f / fmaxf(static_cast<float>(c), 1.0f);
+  }
+
+  float sum[kSums] = {};
+  while (left > 0) {
+    const bool vec = p.vec && left == kGroup;
+    int n = 0;
+    const float old_total = sum[0];
+    eval_tokens(p, off, by_seq, first, end, t, q, sum, n);
+    if (seq_mean) sum[0] = old_total + weigh_tokens(off, t, scale, q, count);
+    store_tokens(p, t, left, vec, seq_mean ? 1.0f : scale, q);
+    t += stride;
+    left = static_cast<int>(min(max(p.T - t, int64_t(0)), int64_t(kGroup)));
+    if (left > 0) load_tokens(p, t, left, p.vec && left == kGroup, q);
+  }
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) {
+    const float v = warp_total(sum[i]);
+    if (lane == 0) warp_sum[warp][i] = v;
+  }
+  __syncthreads();
+  if (tid < kSums) {
+    double v = 0.0;
+    for (int i = 0; i < kWarps; ++i) v += static_cast<double>(warp_sum[i][tid]);
+    p.block_sum[static_cast<int64_t>(blockIdx.x) * kSums + tid] = v;
+    __threadfence();
+  }
+  __syncthreads();
+  if (tid == 0) last = atomicAdd(p.ticket, 1) == static_cast<int>(gridDim.x) - 1;
+  __syncthreads();
+  if (!last) return;
+  // the last CTA: all sums are in memory; warp i adds up sum i, 32 CTAs at a time in order
+  __threadfence();
+  if (warp < kSums) {
+    double v = 0.0;
+    for (int b = lane; b < static_cast<int>(gridDim.x); b += 32) v += __ldcg(p.block_sum + static_cast<int64_t>(b) * kSums + warp);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (lane == 0) store_scalars(p, warp, v, valid);
+  } else if (warp == kSums) {
+    int bad = 0;
+    for (int b = lane; b < p.blocks; b += 32) bad |= __ldcg(p.block_bad + b);
+    bad = __any_sync(0xffffffffu, bad);
+    if (lane == 0) *p.status = bad ? kStatusSequences : 0;
+  }
 }
 
 // ------------------------------------------------------------------ preference loss
@@ -593,6 +686,7 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const Preferen
   const int rank = blockIdx.x % ctas;
   const int share = SOLO ? 1 : ctas;      // CTAs working on one pair
   const int part = SOLO ? 0 : rank;
+  if (!SOLO) launch_dependents();
   cluster_arrive();  // matched by the wait before the first access to another CTA
   bool arrived = true;
   double loss_sum = 0.0;
@@ -732,11 +826,12 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const Preferen
 constexpr int kReduceThreads = 256;
 
 __global__ void __launch_bounds__(kReduceThreads) preference_reduce_kernel(const PreferenceParams p) {
+  wait_prerequisites();
   __shared__ double sh[kReduceThreads / 32];
   __shared__ int sh_n[kReduceThreads / 32];
   double s = 0.0;
   int bad = 0;
-  for (int i = threadIdx.x; i < p.P; i += kReduceThreads) s += p.pair_loss[i], bad += p.pair_bad[i];
+  for (int i = threadIdx.x; i < p.P; i += kReduceThreads) s += __ldcg(p.pair_loss + i), bad += __ldcg(p.pair_bad + i);
   s = block_sum<double, kReduceThreads>(s, sh);
   bad = block_sum<int, kReduceThreads>(bad, sh_n);
   if (threadIdx.x != 0) return;

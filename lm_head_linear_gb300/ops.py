@@ -14,9 +14,11 @@ from typing import Optional
 
 import torch
 
-from .binding import REDUCTIONS, _check, _out, load_library
+from . import binding
+from .binding import REDUCTIONS, _check, load_library
 
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # flce_dtype
+_F32, _I64 = torch.float32, torch.int64
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -24,16 +26,24 @@ def _stream(stream, device) -> int:
     return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
+def _out(out: Optional[dict], key: str, shape, dtype, device) -> torch.Tensor:
+    """A new tensor, or the caller's out[key], checked."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return binding._out(out, key, shape, dtype, device)
+
+
 def _rows(name: str, t: torch.Tensor, shape, device, dtypes=_DTYPES) -> int:
     """Checks a [T, Hd] tensor with contiguous rows; returns its row stride in elements."""
-    if t.dtype not in dtypes or t.shape != shape or t.device != device or t.stride(1) != 1:
+    ld, step = t.stride() if t.dim() == 2 else (0, 0)
+    if t.dtype not in dtypes or t.shape != shape or t.device != device or step != 1:
         raise ValueError(f"{name} must be a {' or '.join(map(str, dtypes))} tensor of shape {tuple(shape)} on {device} "
                          f"with contiguous rows, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-    return t.stride(0) if shape[0] > 1 else shape[1]
+    return ld if shape[0] > 1 else shape[1]
 
 
 def _vector(name: str, t: torch.Tensor, n: int, dtype, device):
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
@@ -79,7 +89,7 @@ def flce_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[
             h = torch.empty(shape, dtype=residual.dtype, device=dev)
         ldh = _rows("out['h']", h, shape, dev, (residual.dtype,))
     y = _out(out, "y", shape, torch.bfloat16, dev) if normed else None
-    rstd = _out(out, "rstd", T, torch.float32, dev) if save_rstd else None
+    rstd = _out(out, "rstd", T, _F32, dev) if save_rstd else None
     q = _out(out, "q", shape, torch.float8_e4m3fn, dev) if fp8 else None
     qs = _out(out, "q_scale", (T, (Hd + 127) // 128), torch.float8_e8m0fnu, dev) if fp8 else None
     _check(lib.flce_add_rms_norm(
@@ -108,10 +118,10 @@ def flce_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.
     ldh = _rows("h", h, shape, dev)
     lddy = _rows("dy", dy, shape, dev)
     w_dtype = _weight(weight, Hd, dev)
-    _vector("rstd", rstd, T, torch.float32, dev)
+    _vector("rstd", rstd, T, _F32, dev)
     lddh = _rows("dh", dh, shape, dev, (h.dtype,)) if dh is not None else 0
     dx = _out(out, "dx", shape, h.dtype, dev)
-    dw = _out(out, "dweight", Hd, torch.float32, dev)
+    dw = _out(out, "dweight", Hd, _F32, dev)
     ws = _ws(lib.flce_add_rms_norm_backward_workspace_size(T, Hd), dev, workspace)
     _check(lib.flce_add_rms_norm_backward(
         dy.data_ptr(), _DTYPES[dy.dtype], lddy, h.data_ptr(), _DTYPES[h.dtype], ldh, weight.data_ptr(), w_dtype,
@@ -253,20 +263,20 @@ def flce_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: tor
         n_seqs = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
         if n_seqs < 0:
             raise ValueError("cu_seqlens must be a tensor [n_seqs + 1]")
-        _vector("cu_seqlens", cu_seqlens, n_seqs + 1, torch.int64, dev)
-    _vector("logp", logp, T, torch.float32, dev)
-    _vector("old_logp", old_logp, T, torch.float32, dev)
-    _vector("advantages", advantages, n_seqs if per_sequence else T, torch.float32, dev)
-    _vector("targets", targets, T, torch.int64, dev)
+        _vector("cu_seqlens", cu_seqlens, n_seqs + 1, _I64, dev)
+    _vector("logp", logp, T, _F32, dev)
+    _vector("old_logp", old_logp, T, _F32, dev)
+    _vector("advantages", advantages, n_seqs if per_sequence else T, _F32, dev)
+    _vector("targets", targets, T, _I64, dev)
     if ref_logp is not None:
-        _vector("ref_logp", ref_logp, T, torch.float32, dev)
+        _vector("ref_logp", ref_logp, T, _F32, dev)
     if dloss is not None:
         dloss = dloss.reshape(-1)
-        _vector("dloss", dloss, T if red == 0 else 1, torch.float32, dev)
-    loss = _out(out, "loss", T if red == 0 else 1, torch.float32, dev) if forward else None
-    dlogp = _out(out, "dlogp", T, torch.float32, dev) if grad else None
-    stats = _out(out, "stats", 4, torch.float32, dev)
-    n_valid = _out(out, "n_valid", 1, torch.int64, dev)
+        _vector("dloss", dloss, T if red == 0 else 1, _F32, dev)
+    loss = _out(out, "loss", T if red == 0 else 1, _F32, dev) if forward else None
+    dlogp = _out(out, "dlogp", T, _F32, dev) if grad else None
+    stats = _out(out, "stats", 4, _F32, dev)
+    n_valid = _out(out, "n_valid", 1, _I64, dev)
     ws = _ws(lib.flce_policy_loss_workspace_size(T, n_seqs), dev, workspace)
     _check(lib.flce_policy_loss(
         dloss.data_ptr() if dloss is not None else None, logp.data_ptr(), old_logp.data_ptr(),
@@ -332,18 +342,18 @@ def flce_preference_loss(logp: torch.Tensor, targets: torch.Tensor, cu_seqlens: 
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] % 2 == 0:
         raise ValueError("cu_seqlens must be a tensor [2 n_pairs + 1]")
     P = cu_seqlens.shape[0] // 2
-    _vector("cu_seqlens", cu_seqlens, 2 * P + 1, torch.int64, dev)
-    _vector("logp", logp, T, torch.float32, dev)
-    _vector("targets", targets, T, torch.int64, dev)
+    _vector("cu_seqlens", cu_seqlens, 2 * P + 1, _I64, dev)
+    _vector("logp", logp, T, _F32, dev)
+    _vector("targets", targets, T, _I64, dev)
     if ref_logp is not None:
-        _vector("ref_logp", ref_logp, T, torch.float32, dev)
+        _vector("ref_logp", ref_logp, T, _F32, dev)
     if dloss is not None:
         dloss = dloss.reshape(-1)
-        _vector("dloss", dloss, P if red == 0 else 1, torch.float32, dev)
-    loss = _out(out, "loss", P if red == 0 else 1, torch.float32, dev) if forward else None
-    dlogp = _out(out, "dlogp", T, torch.float32, dev) if grad else None
-    chosen = _out(out, "chosen", P, torch.float32, dev)
-    rejected = _out(out, "rejected", P, torch.float32, dev)
+        _vector("dloss", dloss, P if red == 0 else 1, _F32, dev)
+    loss = _out(out, "loss", P if red == 0 else 1, _F32, dev) if forward else None
+    dlogp = _out(out, "dlogp", T, _F32, dev) if grad else None
+    chosen = _out(out, "chosen", P, _F32, dev)
+    rejected = _out(out, "rejected", P, _F32, dev)
     ws = _ws(lib.flce_preference_loss_workspace_size(P), dev, workspace)
     _check(lib.flce_preference_loss(
         dloss.data_ptr() if dloss is not None else None, logp.data_ptr(),

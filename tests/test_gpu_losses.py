@@ -106,7 +106,7 @@ def check_policy(args, ref_kw, **kw):
     return loss, dlogp, stats, ws
 
 
-@pytest.mark.parametrize("T", [1, 2, 31, 33, 1000, 1025, 4096, 16385, 70001, 300007])
+@pytest.mark.parametrize("T", [1, 2, 31, 33, 1000, 1025, 4096, 16385, 32768, 32769, 70001, 300007, 1100003])
 @pytest.mark.parametrize("reduction", ["mean", "sum", "none", "sequence_mean"])
 def test_policy(cuda_device, T, reduction):
     logp, old, ref, adv, y, g = draw(T, cuda_device, seed=T)
