@@ -1,5 +1,6 @@
 // Host side of the residual add + RMS norm entry points of include/flce.h.
 #include <algorithm>
+#include <mutex>
 
 #include "flce_host.cuh"
 #include "norm_kernels.cuh"
@@ -17,23 +18,23 @@ int64_t size_of(int32_t d) { return d == FLCE_DTYPE_F32 ? 4 : 2; }
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 bool bad_ld(int64_t ld, int64_t Hd, int32_t dtype) { return ld < Hd || (ld * size_of(dtype)) % 16 != 0; }
 
-// Vectors per thread and threads per row.  Few rows: one vector per thread, the
-// shortest chain from load to store.  Many: more per thread, so that a row needs
-// fewer warps and a warp has more loads in flight.
+// Vectors per thread and threads per row.  Up to a row per SM: one vector per thread,
+// the shortest chain from load to store.  More rows: two (1000 x 2048: 3.7 us against
+// 4.5 us with four), and from 16 rows per SM on four, which needs fewer warps for a row
+// and has more loads of a warp in flight (65,536 x 2048 to 8 bits: 135 us against 146 us
+// with two, 164 us with one and 149 us with eight).
 struct Shape {
   int nv, group, threads;
 };
-Shape pick_shape(int64_t T, int64_t Hd, int sms, int nv_many, int threads_many) {
+Shape pick_shape(int64_t T, int64_t Hd, int sms) {
   const int nvec = static_cast<int>(Hd / kVec);
-  int nv = 1;
-  if (T > sms) nv = nv_many;
+  int nv = T <= sms ? 1 : T <= 16 * sms ? 2 : 4;
   while (cdiv(cdiv(nvec, nv), 32) * 32 > norm::max_threads(nv)) nv *= 2;
   while (nv > 1 && (nv / 2) * 32 >= nvec) nv /= 2;  // a warp would leave whole steps idle
   Shape s;
   s.nv = nv;
   s.group = static_cast<int>(cdiv(cdiv(nvec, nv), 32) * 32);
-  s.threads = T > sms ? std::max(s.group, threads_many / s.group * s.group) : s.group;
-  s.threads = std::min(s.threads, norm::max_threads(nv) / s.group * s.group);
+  s.threads = T > sms ? std::max(s.group, 128 / s.group * s.group) : s.group;
   return s;
 }
 
@@ -45,17 +46,54 @@ template <typename TX, typename TR>
 void launch_fwd_nv(const norm::FwdParams& p, const Shape& s, int64_t blocks, cudaStream_t st) {
   if (s.nv == 1) launch_fwd<TX, TR, 1>(p, s, blocks, st);
   else if (s.nv == 2) launch_fwd<TX, TR, 2>(p, s, blocks, st);
-  else if (s.nv == 4) launch_fwd<TX, TR, 4>(p, s, blocks, st);
-  else launch_fwd<TX, TR, 8>(p, s, blocks, st);
+  else launch_fwd<TX, TR, 4>(p, s, blocks, st);
 }
 
+// The backward: eight vectors per thread (2048 channels a warp), as many groups as fit
+// 384 threads and an SM's shared memory with a stage each, and the stages that then fit.
+constexpr int kBwdSmem = 224 * 1024;
+struct BwdShape {
+  int nv, group, threads, stages;
+  size_t smem;
+};
+BwdShape pick_bwd_shape(int64_t Hd, int64_t row_bytes) {
+  const int nvec = static_cast<int>(Hd / kVec);
+  BwdShape s;
+  s.nv = 8;
+  while (s.nv > 1 && (s.nv / 2) * 32 >= nvec) s.nv /= 2;
+  s.group = static_cast<int>(cdiv(cdiv(nvec, s.nv), 32) * 32);
+  int groups = norm::kBwdThreads / s.group;
+  groups = static_cast<int>(std::max<int64_t>(std::min<int64_t>(groups, kBwdSmem / row_bytes), 1));
+  s.threads = groups * s.group;
+  const int64_t per_stage = groups * row_bytes;
+  s.stages = static_cast<int>(std::max<int64_t>(std::min<int64_t>(kBwdSmem / per_stage, norm::kBwdMaxStages), 1));
+  s.smem = std::max<size_t>(static_cast<size_t>(s.stages) * per_stage, groups > 1 ? sizeof(float) * groups * Hd : 0);
+  return s;
+}
+
+template <typename TY, typename TH, int NV>
+flce_status launch_bwd(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, cudaStream_t st) {
+  static std::mutex mu;
+  static bool set[64] = {};
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (dev >= 0 && dev < 64 && !set[dev]) {
+      CUDA_TRY(cudaFuncSetAttribute(norm::norm_backward_kernel<TY, TH, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kBwdSmem));
+      set[dev] = true;
+    }
+  }
+  norm::norm_backward_kernel<TY, TH, NV><<<static_cast<unsigned>(blocks), s.threads, s.smem, st>>>(p);
+  return FLCE_OK;
+}
 template <typename TY, typename TH>
-void launch_bwd_nv(const norm::BwdParams& p, const Shape& s, int64_t blocks, size_t smem, cudaStream_t st) {
-  const unsigned b = static_cast<unsigned>(blocks);
-  if (s.nv == 1) norm::norm_backward_kernel<TY, TH, 1><<<b, s.threads, smem, st>>>(p);
-  else if (s.nv == 2) norm::norm_backward_kernel<TY, TH, 2><<<b, s.threads, smem, st>>>(p);
-  else if (s.nv == 4) norm::norm_backward_kernel<TY, TH, 4><<<b, s.threads, smem, st>>>(p);
-  else norm::norm_backward_kernel<TY, TH, 8><<<b, s.threads, smem, st>>>(p);
+flce_status launch_bwd_nv(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, cudaStream_t st) {
+  if (s.nv == 1) return launch_bwd<TY, TH, 1>(p, s, blocks, st);
+  if (s.nv == 2) return launch_bwd<TY, TH, 2>(p, s, blocks, st);
+  if (s.nv == 4) return launch_bwd<TY, TH, 4>(p, s, blocks, st);
+  return launch_bwd<TY, TH, 8>(p, s, blocks, st);
 }
 
 flce_status check_sizes(int64_t T, int64_t Hd) {
@@ -98,7 +136,7 @@ flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const
   p.y = static_cast<uint16_t*>(y), p.rstd = rstd, p.q = static_cast<uint8_t*>(q), p.qs = q_scale;
   p.ldx = ldx, p.ldr = ldr, p.ldh = ldh, p.T = T, p.Hd = static_cast<int32_t>(Hd);
   p.w_f32 = weight_dtype == FLCE_DTYPE_F32, p.eps = eps, p.inv_hd = 1.0f / static_cast<float>(Hd);
-  const Shape s = pick_shape(T, Hd, sms, 4, 256);
+  const Shape s = pick_shape(T, Hd, sms);
   p.group = s.group;
   const int64_t blocks = cdiv(T, s.threads / s.group);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -155,26 +193,35 @@ flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
   p.lddy = lddy, p.ldh = ldh, p.lddh = lddh, p.T = T, p.Hd = static_cast<int32_t>(Hd);
   p.w_f32 = weight_dtype == FLCE_DTYPE_F32, p.inv_hd = 1.0f / static_cast<float>(Hd);
-  const Shape s = pick_shape(T, Hd, sms, 2, 256);
-  p.group = s.group;
-  const int groups = s.threads / s.group;
-  const size_t smem = groups > 1 ? sizeof(float) * static_cast<size_t>(groups) * Hd : 0;
-  const int64_t blocks = std::min<int64_t>(std::min<int64_t>(cdiv(T, groups), 3ll * sms), kMaxNormBlocks);
+  p.status = static_cast<int32_t*>(workspace);
+  p.timeout_ns = wait_limit_ns(0);
+  const BwdShape s = pick_bwd_shape(Hd, Hd * (size_of(dy_dtype) + (dh ? 2 : 1) * size_of(h_dtype)));
+  p.group = s.group, p.stages = s.stages;
+  const int64_t blocks = std::min<int64_t>(std::min<int64_t>(cdiv(T, s.threads / s.group), sms), kMaxNormBlocks);
   const double n = static_cast<double>(T) * Hd;
   {
     KernelScope ks(FLCE_KERNEL_NORM_BWD, cs, 10.0 * n,
                    n * (size_of(dy_dtype) + (dh ? 3.0 : 2.0) * size_of(h_dtype)) + 4.0 * Hd);
     const bool yf = dy_dtype == FLCE_DTYPE_F32, hf = h_dtype == FLCE_DTYPE_F32;
-    if (yf && hf) launch_bwd_nv<float, float>(p, s, blocks, smem, cs);
-    else if (yf) launch_bwd_nv<float, uint16_t>(p, s, blocks, smem, cs);
-    else if (hf) launch_bwd_nv<uint16_t, float>(p, s, blocks, smem, cs);
-    else launch_bwd_nv<uint16_t, uint16_t>(p, s, blocks, smem, cs);
+    st = yf && hf ? launch_bwd_nv<float, float>(p, s, blocks, cs)
+         : yf     ? launch_bwd_nv<float, uint16_t>(p, s, blocks, cs)
+         : hf     ? launch_bwd_nv<uint16_t, float>(p, s, blocks, cs)
+                  : launch_bwd_nv<uint16_t, uint16_t>(p, s, blocks, cs);
+    if (st != FLCE_OK) return st;
     ks.done();
     if ((st = check_launch("norm_bwd")) != FLCE_OK) return st;
   }
   KernelScope ks(FLCE_KERNEL_NORM_DW, cs, 0.0, 4.0 * blocks * Hd + 4.0 * Hd);
-  norm::norm_dw_kernel<<<static_cast<unsigned>(cdiv(Hd, 32)), 32 * norm::kDwSlices, 0, cs>>>(
-      p.partial, static_cast<int>(blocks), p.Hd, dweight, static_cast<int32_t*>(workspace));
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(Hd, 32)));
+  cfg.blockDim = dim3(32 * norm::kDwSlices);
+  cfg.stream = cs;
+  cfg.attrs = &at, cfg.numAttrs = 1;
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, norm::norm_dw_kernel, static_cast<const float*>(p.partial),
+                              static_cast<int>(blocks), p.Hd, dweight));
   ks.done();
   return check_launch("norm_dw");
 }

@@ -60,6 +60,53 @@ __device__ __forceinline__ void store8(E* p, const Raw8& r) {
   if constexpr (sizeof(E) == 4) *reinterpret_cast<uint4*>(p + 4) = r.b;
 }
 
+// ------------------------------------------------------------------ pairs
+// Two fp32 numbers in a 64-bit register: one instruction multiplies or adds both.
+using F2 = unsigned long long;
+
+__device__ __forceinline__ F2 pair(uint32_t lo, uint32_t hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 both(float v) { return pair(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ void split(F2 v, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  lo = __uint_as_float(a), hi = __uint_as_float(b);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+constexpr int kPairs = kVec / 2;
+
+template <typename E>
+__device__ __forceinline__ void unpack_pairs(const Raw8& r, F2 (&v)[kPairs]) {
+  if constexpr (sizeof(E) == 4) {
+    v[0] = pair(r.a.x, r.a.y), v[1] = pair(r.a.z, r.a.w), v[2] = pair(r.b.x, r.b.y), v[3] = pair(r.b.z, r.b.w);
+  } else {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) v[i] = pair(w[i] << 16, w[i] & 0xffff0000u);
+  }
+}
+
+template <typename E>
+__device__ __forceinline__ Raw8 pack_pairs(const F2 (&v)[kPairs]) {
+  float f[kVec];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) split(v[i], f[2 * i], f[2 * i + 1]);
+  return pack8<E>(f);
+}
+
 // ------------------------------------------------------------------ e4m3 with a power-of-two scale
 // E8M0 byte of the smallest 2^e with amax / 2^e <= 448 = 1.75 * 2^8, e >= -126.
 // From amax's own exponent and mantissa (amax is finite and not negative).
