@@ -49,6 +49,7 @@ from .ops import (  # noqa: F401
     flce_preference_loss,
     flce_preference_loss_workspace_size,
     flce_quantize_fp8,
+    load_operators,
     policy_loss,
     preference_loss,
 )

@@ -1,8 +1,10 @@
-"""In-tree build of the CUDA library ``_lib/libflce.so`` for sm_103a.
+"""In-tree build of the CUDA library ``_lib/libflce.so`` for sm_103a, and of the
+Python module ``_lib/flce_ops.so`` that calls its operators.
 
 Plain ``nvcc``: a few translation units compiled side by side, one
 ``-gencode`` (compute_103a -> sm_103a), static CUDA runtime,
-position-independent shared object.  Run as ``python -m lm_head_linear_gb300.build``.
+position-independent shared object.  The module is host C++ against torch's
+headers, linked to the library.  Run as ``python -m lm_head_linear_gb300.build``.
 """
 
 from __future__ import annotations
@@ -11,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +27,9 @@ DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
     "flce_host.cuh", "flce_kernels.cuh", "fp8_kernels.cuh", "loss_kernels.cuh", "norm_kernels.cuh", "ptx.cuh",
     "vec8.cuh")] + [
     os.path.join(INCLUDE, "flce.h")]
+
+OPS_SOURCE = os.path.join(CSRC, "ops_binding.cpp")
+OPS_PATH = os.path.join(LIB_DIR, "flce_ops.so")
 
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 
@@ -45,11 +51,27 @@ def link_command(objs, out: str = LIB_PATH) -> list:
     return [nvcc_path(), GENCODE, "-shared", "-Xcompiler", "-fPIC", "-o", out, *objs]
 
 
+def ops_commands(obj: str, out: str) -> list:
+    """Compile and link commands of the Python module (host compiler, torch's headers and libraries)."""
+    import torch
+    from torch.utils import cpp_extension
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    abi = int(torch.compiled_with_cxx11_abi())
+    dirs = cpp_extension.include_paths() + [sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [[cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-c",
+             *(f"-isystem{d}" for d in dirs), "-o", obj, OPS_SOURCE],
+            [cxx, "-shared", "-o", out, obj, f"-L{libs}", f"-L{LIB_DIR}", "-lflce", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+             "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]]
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(OPS_PATH)):
         return False
     t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(f) <= t for f in DEPENDS)
+    return all(os.path.getmtime(f) <= t for f in DEPENDS) and all(
+        os.path.getmtime(f) <= os.path.getmtime(OPS_PATH) for f in (OPS_SOURCE, os.path.join(INCLUDE, "flce.h")))
 
 
 def _run(cmd, verbose: bool) -> None:
@@ -57,7 +79,7 @@ def _run(cmd, verbose: bool) -> None:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     if verbose and (res.stdout or res.stderr):
         print(res.stdout + res.stderr, flush=True)
 
@@ -69,10 +91,15 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     tmp = LIB_PATH + ".tmp"
     objs = [os.path.join(LIB_DIR, os.path.basename(src) + ".o") for src in SOURCES]
-    with ThreadPoolExecutor(len(SOURCES)) as pool:
-        list(pool.map(lambda so: _run(compile_command(*so, extra), verbose), zip(SOURCES, objs)))
+    ops_obj, ops_tmp = os.path.join(LIB_DIR, "ops_binding.o"), OPS_PATH + ".tmp"
+    ops_compile, ops_link = ops_commands(ops_obj, ops_tmp)
+    jobs = [compile_command(src, obj, extra) for src, obj in zip(SOURCES, objs)] + [ops_compile]
+    with ThreadPoolExecutor(len(jobs)) as pool:
+        list(pool.map(lambda cmd: _run(cmd, verbose), jobs))
     _run(link_command(objs, tmp), verbose)
     os.replace(tmp, LIB_PATH)
+    _run(ops_link, verbose)
+    os.replace(ops_tmp, OPS_PATH)
     return LIB_PATH
 
 

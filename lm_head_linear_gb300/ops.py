@@ -2,64 +2,41 @@
 product in 8 bits, and the policy and preference losses on the log-probabilities
 it returns.
 
-As in :mod:`.binding`: arguments are checked, outputs and workspaces allocated
+As in :mod:`.binding`, arguments are checked, outputs and workspaces allocated
 with torch (or taken from the caller), and the library's kernels do the work.
-These calls can be a few microseconds long on the GPU, so their Python side is
-kept short: pointers go to ctypes as plain integers.
+These calls are a few microseconds long on the GPU, so the checking and calling is
+compiled (``csrc/ops_binding.cpp``, built into ``_lib/flce_ops.so``); there is no
+fallback for it.
 """
 
 from __future__ import annotations
 
+import importlib.util
+import os
 from typing import Optional
 
 import torch
 
-from . import binding
-from .binding import REDUCTIONS, _check, load_library
+from .binding import LIB_PATH, REDUCTIONS, _check, load_library
 
-_DTYPES = {torch.bfloat16: 0, torch.float32: 1}  # flce_dtype
-_F32, _I64 = torch.float32, torch.int64
-_raw_stream = torch._C._cuda_getCurrentRawStream
+OPS_PATH = os.path.join(os.path.dirname(LIB_PATH), "flce_ops.so")
+_OPS = None
 
 
-def _stream(stream, device) -> int:
-    return _raw_stream(device.index) if stream is None else stream.cuda_stream
-
-
-def _out(out: Optional[dict], key: str, shape, dtype, device) -> torch.Tensor:
-    """A new tensor, or the caller's out[key], checked."""
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return binding._out(out, key, shape, dtype, device)
-
-
-def _rows(name: str, t: torch.Tensor, shape, device, dtypes=_DTYPES) -> int:
-    """Checks a [T, Hd] tensor with contiguous rows; returns its row stride in elements."""
-    ld, step = t.stride() if t.dim() == 2 else (0, 0)
-    if t.dtype not in dtypes or t.shape != shape or t.device != device or step != 1:
-        raise ValueError(f"{name} must be a {' or '.join(map(str, dtypes))} tensor of shape {tuple(shape)} on {device} "
-                         f"with contiguous rows, got {t.dtype} {tuple(t.shape)} on {t.device}, strides {t.stride()}")
-    return ld if shape[0] > 1 else shape[1]
-
-
-def _vector(name: str, t: torch.Tensor, n: int, dtype, device):
-    if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}, "
-                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-
-
-def _ws(nbytes: int, device, workspace: Optional[torch.Tensor]) -> torch.Tensor:
-    if workspace is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    if workspace.device != device or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"the workspace must be a contiguous uint8 tensor on {device}")
-    return workspace
-
-
-def _weight(weight: torch.Tensor, Hd: int, device) -> int:
-    if weight.dtype not in _DTYPES or weight.shape != (Hd,) or weight.device != device or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous bfloat16 or float32 tensor of {Hd} elements on {device}")
-    return _DTYPES[weight.dtype]
+def load_operators():
+    """The compiled module (raises if it was not built)."""
+    global _OPS
+    if _OPS is None:
+        load_library()
+        if not os.path.exists(OPS_PATH):
+            raise RuntimeError(f"{OPS_PATH} is missing: build it with `python -m lm_head_linear_gb300.build` "
+                               "(there is no fallback implementation)")
+        spec = importlib.util.spec_from_file_location("flce_ops", OPS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_check(_check)
+        _OPS = module
+    return _OPS
 
 
 def flce_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -73,31 +50,7 @@ def flce_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[
     ``save_rstd``; None where not asked for.  ``out`` may hold preallocated tensors
     under those names (``h`` may be the residual).
     """
-    if not x.is_cuda or x.dim() != 2:
-        raise ValueError("x must be a CUDA tensor [T, Hd]")
-    lib = load_library()
-    dev, shape = x.device, x.shape
-    T, Hd = shape
-    ldx = _rows("x", x, shape, dev)
-    w_dtype = _weight(weight, Hd, dev)
-    h, ldr, ldh, r_dtype = x, 0, 0, 0
-    if residual is not None:
-        ldr = _rows("residual", residual, shape, dev)
-        r_dtype = _DTYPES[residual.dtype]
-        h = (out or {}).get("h")
-        if h is None:
-            h = torch.empty(shape, dtype=residual.dtype, device=dev)
-        ldh = _rows("out['h']", h, shape, dev, (residual.dtype,))
-    y = _out(out, "y", shape, torch.bfloat16, dev) if normed else None
-    rstd = _out(out, "rstd", T, _F32, dev) if save_rstd else None
-    q = _out(out, "q", shape, torch.float8_e4m3fn, dev) if fp8 else None
-    qs = _out(out, "q_scale", (T, (Hd + 127) // 128), torch.float8_e8m0fnu, dev) if fp8 else None
-    _check(lib.flce_add_rms_norm(
-        x.data_ptr(), _DTYPES[x.dtype], ldx, residual.data_ptr() if residual is not None else None, r_dtype, ldr,
-        weight.data_ptr(), w_dtype, T, Hd, eps, h.data_ptr() if residual is not None else None, ldh,
-        y.data_ptr() if normed else None, rstd.data_ptr() if save_rstd else None, q.data_ptr() if fp8 else None,
-        qs.data_ptr() if fp8 else None, _stream(stream, dev)))
-    return y, h, rstd, q, qs
+    return (_OPS or load_operators()).add_rms_norm(x, weight, residual, eps, normed, fp8, save_rstd, stream, out)
 
 
 def flce_add_rms_norm_backward_workspace_size(T: int, Hd: int) -> int:
@@ -110,24 +63,7 @@ def flce_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.
     """Run ``flce_add_rms_norm_backward``; returns ``(dx [T, Hd] in h's dtype, dweight [Hd] fp32, workspace)``.
     ``dx`` is the gradient of x and of the residual; ``dh`` an upstream gradient on h.
     ``out`` may hold preallocated ``dx`` and ``dweight`` tensors."""
-    if not h.is_cuda or h.dim() != 2:
-        raise ValueError("h must be a CUDA tensor [T, Hd]")
-    lib = load_library()
-    dev, shape = h.device, h.shape
-    T, Hd = shape
-    ldh = _rows("h", h, shape, dev)
-    lddy = _rows("dy", dy, shape, dev)
-    w_dtype = _weight(weight, Hd, dev)
-    _vector("rstd", rstd, T, _F32, dev)
-    lddh = _rows("dh", dh, shape, dev, (h.dtype,)) if dh is not None else 0
-    dx = _out(out, "dx", shape, h.dtype, dev)
-    dw = _out(out, "dweight", Hd, _F32, dev)
-    ws = _ws(lib.flce_add_rms_norm_backward_workspace_size(T, Hd), dev, workspace)
-    _check(lib.flce_add_rms_norm_backward(
-        dy.data_ptr(), _DTYPES[dy.dtype], lddy, h.data_ptr(), _DTYPES[h.dtype], ldh, weight.data_ptr(), w_dtype,
-        rstd.data_ptr(), dh.data_ptr() if dh is not None else None, lddh, T, Hd, dx.data_ptr(), dw.data_ptr(),
-        ws.data_ptr(), ws.numel(), _stream(stream, dev)))
-    return dx, dw, ws
+    return (_OPS or load_operators()).add_rms_norm_backward(dy, h, weight, rstd, dh, workspace, stream, out)
 
 
 class AddRMSNorm(torch.autograd.Function):
@@ -169,32 +105,11 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6):
     return AddRMSNorm.apply(x, weight, residual, eps)
 
 
-# Scales are E8M0 bytes: torch's float8_e8m0fnu, or the bytes as uint8.
-_SCALES = (torch.float8_e8m0fnu, torch.uint8)
-
-
-def _blocks(name: str, q: torch.Tensor, scale: torch.Tensor, block_rows: int, device):
-    if q.dtype != torch.float8_e4m3fn or q.dim() != 2 or q.device != device or not q.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float8_e4m3fn matrix on {device}")
-    want = ((q.shape[0] + block_rows - 1) // block_rows, (q.shape[1] + 127) // 128)
-    if scale.dtype not in _SCALES or scale.shape != want or scale.device != device or not scale.is_contiguous():
-        raise ValueError(f"{name}'s scales must be a contiguous float8_e8m0fnu or uint8 tensor of shape {want} on {device}, "
-                         f"got {scale.dtype} {tuple(scale.shape)} on {scale.device}")
-
-
 def flce_quantize_fp8(a: torch.Tensor, block_rows: int = 128, stream=None, out: Optional[dict] = None):
     """Run ``flce_quantize_fp8``; returns ``(q float8_e4m3fn [rows, K], q_scale float8_e8m0fnu)``: one scale
     per ``block_rows`` x 128 block, 128 for weights, 1 for activations.  ``out`` may hold preallocated
     ``q`` and ``q_scale`` tensors."""
-    if not a.is_cuda or a.dim() != 2:
-        raise ValueError("a must be a CUDA matrix")
-    dev, (rows, K) = a.device, a.shape
-    lda = _rows("a", a, a.shape, dev)
-    q = _out(out, "q", (rows, K), torch.float8_e4m3fn, dev)
-    qs = _out(out, "q_scale", ((rows + block_rows - 1) // max(block_rows, 1), (K + 127) // 128), torch.float8_e8m0fnu, dev)
-    _check(load_library().flce_quantize_fp8(a.data_ptr(), _DTYPES[a.dtype], lda, rows, K, block_rows, q.data_ptr(),
-                                            qs.data_ptr(), _stream(stream, dev)))
-    return q, qs
+    return (_OPS or load_operators()).quantize_fp8(a, block_rows, stream, out)
 
 
 def flce_linear_fp8_workspace_size(T: int, K: int, V: int) -> int:
@@ -206,27 +121,14 @@ def flce_linear_fp8(x: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, W_s
                     out: Optional[dict] = None):
     """Run ``flce_linear_fp8``; returns ``(y [T, V], workspace)`` in ``dtype`` (bfloat16 or float32).
 
-    ``x`` [T, K] and ``W`` [V, K] are float8_e4m3fn with one E8M0 scale per row and 128
-    channels (``x_scale`` [T, ceil(K/128)]) and per 128 x 128 block (``W_scale``): what
-    :func:`flce_add_rms_norm` and :func:`flce_quantize_fp8` write.  ``out`` may hold a
-    preallocated ``y``, whose rows may be longer than V.
+    ``x`` [T, K] and ``W`` [V, K] are float8_e4m3fn with one E8M0 scale (float8_e8m0fnu, or
+    its bytes as uint8) per row and 128 channels (``x_scale`` [T, ceil(K/128)]) and per 128 x
+    128 block (``W_scale``): what :func:`flce_add_rms_norm` and :func:`flce_quantize_fp8`
+    write.  ``out`` may hold a preallocated ``y``, whose rows may be longer than V.
     """
-    if not x.is_cuda or x.dim() != 2 or W.dim() != 2 or W.shape[1] != x.shape[1]:
-        raise ValueError("x [T, K] and W [V, K] must be CUDA matrices of equal K")
-    lib = load_library()
-    dev, (T, K), V = x.device, x.shape, W.shape[0]
-    _blocks("x", x, x_scale, 1, dev)
-    _blocks("W", W, W_scale, 128, dev)
-    if dtype not in _DTYPES:
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise ValueError("dtype must be bfloat16 or float32")
-    y = (out or {}).get("y")
-    if y is None:
-        y = torch.empty((T, V), dtype=dtype, device=dev)
-    ldy = _rows("out['y']", y, torch.Size((T, V)), dev, (dtype,))
-    ws = _ws(256, dev, workspace)
-    _check(lib.flce_linear_fp8(x.data_ptr(), x_scale.data_ptr(), W.data_ptr(), W_scale.data_ptr(), T, K, V, y.data_ptr(),
-                               _DTYPES[dtype], ldy, ws.data_ptr(), ws.numel(), _stream(stream, dev)))
-    return y, ws
+    return (_OPS or load_operators()).linear_fp8(x, x_scale, W, W_scale, dtype is torch.float32, workspace, stream, out)
 
 
 POLICY_REDUCTIONS = {"none": 0, "mean": 1, "sum": 2, "sequence_mean": 3}
@@ -253,38 +155,9 @@ def flce_policy_loss(logp: torch.Tensor, old_logp: torch.Tensor, advantages: tor
     is [T], or with ``per_sequence`` one per sequence of ``cu_seqlens``.  ``out`` may
     hold preallocated ``loss``, ``dlogp``, ``stats`` and ``n_valid`` tensors.
     """
-    if not logp.is_cuda or logp.dim() != 1:
-        raise ValueError("logp must be a CUDA tensor [T]")
-    lib = load_library()
-    dev, T = logp.device, logp.shape[0]
-    red = POLICY_REDUCTIONS[reduction]
-    n_seqs = 0
-    if cu_seqlens is not None:
-        n_seqs = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else -1
-        if n_seqs < 0:
-            raise ValueError("cu_seqlens must be a tensor [n_seqs + 1]")
-        _vector("cu_seqlens", cu_seqlens, n_seqs + 1, _I64, dev)
-    _vector("logp", logp, T, _F32, dev)
-    _vector("old_logp", old_logp, T, _F32, dev)
-    _vector("advantages", advantages, n_seqs if per_sequence else T, _F32, dev)
-    _vector("targets", targets, T, _I64, dev)
-    if ref_logp is not None:
-        _vector("ref_logp", ref_logp, T, _F32, dev)
-    if dloss is not None:
-        dloss = dloss.reshape(-1)
-        _vector("dloss", dloss, T if red == 0 else 1, _F32, dev)
-    loss = _out(out, "loss", T if red == 0 else 1, _F32, dev) if forward else None
-    dlogp = _out(out, "dlogp", T, _F32, dev) if grad else None
-    stats = _out(out, "stats", 4, _F32, dev)
-    n_valid = _out(out, "n_valid", 1, _I64, dev)
-    ws = _ws(lib.flce_policy_loss_workspace_size(T, n_seqs), dev, workspace)
-    _check(lib.flce_policy_loss(
-        dloss.data_ptr() if dloss is not None else None, logp.data_ptr(), old_logp.data_ptr(),
-        ref_logp.data_ptr() if ref_logp is not None else None, advantages.data_ptr(), per_sequence, targets.data_ptr(),
-        cu_seqlens.data_ptr() if cu_seqlens is not None else None, n_seqs, T, ignore_index, red, clip_low, clip_high,
-        dual_clip, kl_coef, KL_KINDS[kl], loss.data_ptr() if forward else None, dlogp.data_ptr() if grad else None,
-        stats.data_ptr(), n_valid.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream, dev)))
-    return loss, dlogp, stats, n_valid, ws
+    return (_OPS or load_operators()).policy_loss(logp, old_logp, advantages, targets, ref_logp, cu_seqlens, per_sequence,
+                                        ignore_index, POLICY_REDUCTIONS[reduction], clip_low, clip_high, dual_clip,
+                                        kl_coef, KL_KINDS[kl], dloss, forward, grad, workspace, stream, out)
 
 
 class PolicyLoss(torch.autograd.Function):
@@ -334,34 +207,9 @@ def flce_preference_loss(logp: torch.Tensor, targets: torch.Tensor, cu_seqlens: 
     (None without ``grad``).  ``out`` may hold preallocated ``loss``, ``dlogp``, ``chosen``
     and ``rejected`` tensors.
     """
-    if not logp.is_cuda or logp.dim() != 1:
-        raise ValueError("logp must be a CUDA tensor [T]")
-    lib = load_library()
-    dev, T = logp.device, logp.shape[0]
-    red = REDUCTIONS[reduction]
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] % 2 == 0:
-        raise ValueError("cu_seqlens must be a tensor [2 n_pairs + 1]")
-    P = cu_seqlens.shape[0] // 2
-    _vector("cu_seqlens", cu_seqlens, 2 * P + 1, _I64, dev)
-    _vector("logp", logp, T, _F32, dev)
-    _vector("targets", targets, T, _I64, dev)
-    if ref_logp is not None:
-        _vector("ref_logp", ref_logp, T, _F32, dev)
-    if dloss is not None:
-        dloss = dloss.reshape(-1)
-        _vector("dloss", dloss, P if red == 0 else 1, _F32, dev)
-    loss = _out(out, "loss", P if red == 0 else 1, _F32, dev) if forward else None
-    dlogp = _out(out, "dlogp", T, _F32, dev) if grad else None
-    chosen = _out(out, "chosen", P, _F32, dev)
-    rejected = _out(out, "rejected", P, _F32, dev)
-    ws = _ws(lib.flce_preference_loss_workspace_size(P), dev, workspace)
-    _check(lib.flce_preference_loss(
-        dloss.data_ptr() if dloss is not None else None, logp.data_ptr(),
-        ref_logp.data_ptr() if ref_logp is not None else None, targets.data_ptr(), cu_seqlens.data_ptr(), P, T,
-        ignore_index, red, PREFERENCE_KINDS[kind], beta, label_smoothing, margin, length_normalize,
-        loss.data_ptr() if forward else None, dlogp.data_ptr() if grad else None, chosen.data_ptr(),
-        rejected.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream, dev)))
-    return loss, dlogp, chosen, rejected, ws
+    return (_OPS or load_operators()).preference_loss(logp, targets, cu_seqlens, ref_logp, ignore_index, REDUCTIONS[reduction],
+                                            PREFERENCE_KINDS[kind], beta, label_smoothing, margin, length_normalize,
+                                            dloss, forward, grad, workspace, stream, out)
 
 
 class PreferenceLoss(torch.autograd.Function):
