@@ -132,7 +132,7 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   // Tokens on M where more than one token tile is needed anyway and rounding T up to
   // 256 does not cost more than its cheaper epilogue gains.
   bool tokens_m = false;
-  if (n_tiles > 1 && p.y_tma) {
+  if (n_tiles > 1) {
     const int64_t mt = cdiv(T, 2 * fp8::kRowsCta), nt = cdiv(V, fp8::kMaxN);
     const double padded = static_cast<double>(mt * 2 * fp8::kRowsCta) * static_cast<double>(nt * fp8::kMaxN);
     if (padded <= 1.1 * static_cast<double>(n * n_tiles) * static_cast<double>(m_tiles * 2 * fp8::kRowsCta)) {
@@ -156,9 +156,7 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   if ((st = matrix_map(tokens_m ? &p.tmA : &p.tmB, u8, CU_TENSOR_MAP_SWIZZLE_128B, x, K, T, K, fp8::kBlockK,
                        tokens_m ? fp8::kRowsCta : p.n / 2)) != FLCE_OK)
     return st;
-  const CUtensorMapSwizzle y_swizzle = !tokens_m  ? CU_TENSOR_MAP_SWIZZLE_NONE
-                                       : es == 4 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                                 : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapSwizzle y_swizzle = es == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   if (p.y_tma && (st = matrix_map(&p.tmY, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                                   y_swizzle, y, V, T, ldy * es, 32, 32)) != FLCE_OK)
     return st;

@@ -268,11 +268,13 @@ flce_status flce_preference_loss(const float* dloss, const float* logp, const fl
   int most = 0;
   if ((st = largest_cluster(dev, &most)) != FLCE_OK) return st;
   const int64_t mean = cdiv(T, n_pairs);
-  if (cdiv(n_pairs, most) * std::max<int64_t>(mean, 512) <= 8192) {
+  // One cluster while every CTA has at most one pair (a second one costs another 2 us:
+  // 17 pairs of 2 x 329 tokens 8.3 us, in two launches 5.7); else a cluster per pair, with
+  // enough CTAs to fill the device, of at least 2048 tokens each.
+  if (n_pairs <= most && mean <= 8192) {
     p.ctas = pow2_up(n_pairs, most);
     st = launch_cluster(loss::preference_kernel<true>, p, p.ctas, p.ctas, loss::kPairThreads, s);
   } else {
-    // enough CTAs to fill the device, of at least 2048 tokens each
     p.ctas = pow2_up(std::min<int64_t>(mean / 2048, 2 * sms / n_pairs), 8);
     st = launch_cluster(loss::preference_kernel<false>, p, n_pairs * p.ctas, p.ctas, loss::kPairThreads, s);
     if (st == FLCE_OK) st = launch_dependent(loss::preference_reduce_kernel, p, 1, loss::kReduceThreads, s);

@@ -49,22 +49,25 @@ void launch_fwd_nv(const norm::FwdParams& p, const Shape& s, int64_t blocks, cud
   else launch_fwd<TX, TR, 4>(p, s, blocks, st);
 }
 
-// The backward: eight vectors per thread (2048 channels a warp), as many groups as fit
-// 384 threads and an SM's shared memory with a stage each, and the stages that then fit.
+// The backward: eight or four vectors per thread, whichever leaves fewer idle (2048
+// channels are one warp); as many groups as fit 384 threads and an SM's shared memory
+// with a stage each, but no more than spread the rows over the SMs; and the stages
+// that then fit.
 constexpr int kBwdSmem = 224 * 1024;
 struct BwdShape {
   int nv, group, threads, stages;
   size_t smem;
 };
-BwdShape pick_bwd_shape(int64_t Hd, int64_t row_bytes) {
-  const int nvec = static_cast<int>(Hd / kVec);
+BwdShape pick_bwd_shape(int64_t T, int64_t Hd, int64_t row_bytes, int sms) {
+  const int64_t nvec = Hd / kVec;
+  const auto group_of = [&](int nv) { return cdiv(cdiv(nvec, nv), 32) * 32; };
   BwdShape s;
-  s.nv = 8;
+  s.nv = group_of(4) <= norm::kBwdThreads && 4 * group_of(4) < 8 * group_of(8) ? 4 : 8;
   while (s.nv > 1 && (s.nv / 2) * 32 >= nvec) s.nv /= 2;
-  s.group = static_cast<int>(cdiv(cdiv(nvec, s.nv), 32) * 32);
-  int groups = norm::kBwdThreads / s.group;
-  groups = static_cast<int>(std::max<int64_t>(std::min<int64_t>(groups, kBwdSmem / row_bytes), 1));
-  s.threads = groups * s.group;
+  s.group = static_cast<int>(group_of(s.nv));
+  int64_t groups = std::min<int64_t>(norm::kBwdThreads / s.group, kBwdSmem / row_bytes);
+  groups = std::max<int64_t>(std::min<int64_t>(groups, cdiv(T, sms)), 1);
+  s.threads = static_cast<int>(groups) * s.group;
   const int64_t per_stage = groups * row_bytes;
   s.stages = static_cast<int>(std::max<int64_t>(std::min<int64_t>(kBwdSmem / per_stage, norm::kBwdMaxStages), 1));
   s.smem = std::max<size_t>(static_cast<size_t>(s.stages) * per_stage, groups > 1 ? sizeof(float) * groups * Hd : 0);
@@ -195,7 +198,7 @@ flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t
   p.w_f32 = weight_dtype == FLCE_DTYPE_F32, p.inv_hd = 1.0f / static_cast<float>(Hd);
   p.status = static_cast<int32_t*>(workspace);
   p.timeout_ns = wait_limit_ns(0);
-  const BwdShape s = pick_bwd_shape(Hd, Hd * (size_of(dy_dtype) + (dh ? 2 : 1) * size_of(h_dtype)));
+  const BwdShape s = pick_bwd_shape(T, Hd, Hd * (size_of(dy_dtype) + (dh ? 2 : 1) * size_of(h_dtype)), sms);
   p.group = s.group, p.stages = s.stages;
   const int64_t blocks = std::min<int64_t>(std::min<int64_t>(cdiv(T, s.threads / s.group), sms), kMaxNormBlocks);
   const double n = static_cast<double>(T) * Hd;

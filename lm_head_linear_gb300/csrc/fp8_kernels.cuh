@@ -13,8 +13,8 @@
 //     runs narrow tiles over wide W tiles and is bound by reading W;
 //   tokens on M, vocabulary on N = 224: a prompt.  A lane of the accumulator is then
 //     a token and its columns are consecutive logits, which go to the staging buffer
-//     16 bytes at a time (with the vocabulary on M they take a 2-byte store each, which
-//     cost 160 us of 1443 us at 8192 x 2048 x 124,160).
+//     16 bytes at a time (with the vocabulary on M they take a 2-byte store each:
+//     8192 x 2048 x 124,160 takes 1358 us this way and 1443 us that way).
 //
 // A CTA has 10 warps: the TMA producer, the MMA issuer (even CTA of the pair),
 // four epilogue warps and four scale warps.  The scale bytes come from their plain
@@ -72,7 +72,7 @@ struct Params {
   int32_t n_tiles, m_tiles, units;
   int32_t stages, stage_bytes;
   int32_t y_f32;
-  int32_t y_tma;     // y's rows start on 16-byte boundaries: stored by TMA, else by plain stores
+  int32_t y_tma;     // y's rows start on 16-byte boundaries: boxes leave by TMA, else row by row
 };
 
 // full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], scale_full[4], scale_empty[4], drain
@@ -338,16 +338,24 @@ __device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, con
   }
 }
 
-// Tokens on M: lane = token, column = logit.  32 logits of 32 tokens at a time: each
-// lane writes its 64 (fp32: 128) bytes as 16-byte pieces in the TMA's 64-byte (128-byte)
-// swizzle, which keeps the eight lanes of a phase on different banks, and one TMA
-// store puts the box into y, clipped at T and V.
+// Staging of 32 logits of 32 tokens: token rows of 64 (fp32: 128) bytes in the TMA's
+// 64-byte (128-byte) swizzle, 16-byte piece k of row r at k ^ (r / 2 % 4) (k ^ r % 8).
 template <typename E>
-__device__ __forceinline__ void store_tokens_m(const Params& p, uint32_t buf, const uint32_t (&r)[32], int lane) {
+__device__ __forceinline__ uint32_t staged(uint32_t buf, int row, int piece) {
+  if constexpr (sizeof(E) == 4)
+    return buf + row * 128 + ((piece ^ (row & 7)) << 4);
+  else
+    return buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+
+// Tokens on M: lane = token, column = logit.  Each lane writes its row in 16-byte
+// pieces; the swizzle keeps the eight lanes of a phase on different banks.
+template <typename E>
+__device__ __forceinline__ void stage_tokens_m(uint32_t buf, const uint32_t (&r)[32], int lane) {
   if constexpr (sizeof(E) == 4) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      ptx::st_shared_v4(buf + lane * 128 + ((k ^ (lane & 7)) << 4), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+      ptx::st_shared_v4(staged<E>(buf, lane, k), r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -355,24 +363,65 @@ __device__ __forceinline__ void store_tokens_m(const Params& p, uint32_t buf, co
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         h[i] = ptx::pack_bf16x2(__uint_as_float(r[8 * k + 2 * i]), __uint_as_float(r[8 * k + 2 * i + 1]));
-      ptx::st_shared_v4(buf + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4), h[0], h[1], h[2], h[3]);
+      ptx::st_shared_v4(staged<E>(buf, lane, k), h[0], h[1], h[2], h[3]);
     }
   }
 }
 
-// Vocabulary on M: lane = vocabulary row, column = token.  The staging buffer holds
-// the box token by token (32 lanes write one token's 32 consecutive logits: no bank
-// conflict).
+// Vocabulary on M: lane = vocabulary row, column = token: one token's 32 logits at a
+// time, 32 lanes on consecutive addresses.
 template <typename E>
-__device__ __forceinline__ void store_vocab_m(uint32_t buf, const uint32_t (&r)[32], int lane) {
+__device__ __forceinline__ void stage_vocab_m(uint32_t buf, const uint32_t (&r)[32], int lane) {
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     if constexpr (sizeof(E) == 4)
-      asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + j * 128 + lane * 4), "r"(r[j]) : "memory");
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(staged<E>(buf, j, lane >> 2) + (lane & 3) * 4), "r"(r[j]) : "memory");
     else
-      asm volatile("st.shared.b16 [%0], %1;" ::"r"(buf + j * 64 + lane * 2),
+      asm volatile("st.shared.b16 [%0], %1;" ::"r"(staged<E>(buf, j, lane >> 3) + (lane & 7) * 2),
                    "h"(__bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[j]))))
                    : "memory");
+  }
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// The staged box into rows of y that do not start on 16 bytes: tokens t0 .., logits
+// v0 .. v0 + 31, clipped at T and V.  fp32: a token a step.  bf16: two tokens a step, a
+// half warp each, in 32-bit words.  A half warp's rows are an even number of rows
+// apart, so all of them start on an even element or all on an odd one; in the odd
+// case the words are made of two staged ones, and the first and last logit go alone.
+template <typename E>
+__device__ __forceinline__ void store_rows(const Params& p, uint32_t buf, int t0, int v0, int lane) {
+  const int tokens = p.T - t0, logits = min(32, p.V - v0);
+  if constexpr (sizeof(E) == 4) {
+    float* y = static_cast<float*>(p.y) + static_cast<int64_t>(t0) * p.ldy + v0 + lane;
+#pragma unroll
+    for (int r = 0; r < 32; ++r, y += p.ldy) {
+      const uint32_t v = ld_shared_u32(staged<E>(buf, r, lane >> 2) + (lane & 3) * 4);
+      if (r < tokens && lane < logits) *y = __uint_as_float(v);
+    }
+  } else {
+    const int w = lane & 15, half = lane >> 4, next = min(w + 1, 15);
+    uint16_t* y = static_cast<uint16_t*>(p.y) + static_cast<int64_t>(t0 + half) * p.ldy + v0;
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(y) >> 1) & 1;
+    const int e = 2 * w + odd;  // this lane's first logit
+    const bool word = e + 1 < logits, one = e + 1 == logits, head = odd && w == 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, y += 2 * p.ldy) {
+      // row 2 i + half
+      const uint32_t lo = ld_shared_u32(buf + (2 * i + half) * 64 + (((w >> 2) ^ (i & 3)) << 4) + (w & 3) * 4);
+      const uint32_t hi = ld_shared_u32(buf + (2 * i + half) * 64 + (((next >> 2) ^ (i & 3)) << 4) + (next & 3) * 4);
+      const uint32_t v = odd ? __funnelshift_r(lo, hi, 16) : lo;
+      if (2 * i + half < tokens) {
+        if (word) *reinterpret_cast<uint32_t*>(y + e) = v;
+        if (one) y[e] = static_cast<uint16_t>(v);
+        if (head) y[0] = static_cast<uint16_t>(lo);
+      }
+    }
   }
 }
 
@@ -401,39 +450,26 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
         uint32_t r[32];
         ptx::tmem_ld32(col + c, r);
         const int n0 = un.n0 + c;
-        if (TOKENS_M || p.y_tma) {
-          const uint32_t buf = staging + (box & 1u) * (kStagingWarp / 2);
-          if (lane == 0) ptx::bulk_wait_read<1>();  // the store before last has read this buffer
-          __syncwarp();
-          ptx::tmem_wait_ld32(r);
-          if constexpr (TOKENS_M)
-            store_tokens_m<E>(p, buf, r, lane);
-          else
-            store_vocab_m<E>(buf, r, lane);
+        const uint32_t buf = staging + (box & 1u) * (kStagingWarp / 2);
+        if (lane == 0) ptx::bulk_wait_read<1>();  // the store before last has read this buffer
+        __syncwarp();
+        ptx::tmem_wait_ld32(r);
+        if constexpr (TOKENS_M)
+          stage_tokens_m<E>(buf, r, lane);
+        else
+          stage_vocab_m<E>(buf, r, lane);
+        if (p.y_tma) {
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             ptx::tma_store_2d(&p.tmY, buf, TOKENS_M ? n0 : m0, TOKENS_M ? m0 : n0);
             ptx::bulk_commit();
           }
-          ++box;
         } else {
-          // rows of y that do not start on 16 bytes: a warp's store is one token's 32 logits
-          ptx::tmem_wait_ld32(r);
-          const int v = m0 + lane;
-          if (v < p.V) {
-            E* y = static_cast<E*>(p.y) + static_cast<int64_t>(n0) * p.ldy + v;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (n0 + j < p.T) {
-                if constexpr (sizeof(E) == 4)
-                  y[j * p.ldy] = __uint_as_float(r[j]);
-                else
-                  y[j * p.ldy] = __float2bfloat16_rn(__uint_as_float(r[j]));
-              }
-            }
-          }
+          __syncwarp();
+          store_rows<E>(p, buf, TOKENS_M ? m0 : n0, TOKENS_M ? n0 : m0, lane);
         }
+        ++box;
       }
     }
     ptx::tc_fence_before();

@@ -18,7 +18,8 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 SHAPES = [(1, 16, 1), (1, 128, 256), (32, 128, 256), (33, 144, 300), (64, 512, 512), (65, 640, 129), (1, 2048, 4096), (17, 1040, 4097),
           (128, 4096, 1000), (224, 256, 513), (225, 384, 640), (300, 512, 4097), (1000, 1168, 2047), (449, 2048, 20000),
-          (256, 128, 8), (512, 640, 232), (1024, 272, 4104), (2000, 1040, 1000)]
+          (256, 128, 8), (512, 640, 232), (1024, 272, 4104), (2000, 1040, 1000),
+          (256, 256, 1), (511, 144, 33), (513, 400, 4099), (768, 272, 1026), (700, 128, 900), (150, 256, 2050)]
 
 
 def value(q, s, rows):
