@@ -171,10 +171,9 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + fp8::kStagingBytes + fp8::kSmemTail;
   KernelScope ks(FLCE_KERNEL_LINEAR_FP8, s, 2.0 * T * K * V,
                  1.0 * T * K + 1.0 * V * K + (p.y_f32 ? 4.0 : 2.0) * T * V);
-  if (tokens_m)
-    fp8::linear_fp8_kernel<true><<<grid, fp8::kThreads, smem, s>>>(p);
-  else
-    fp8::linear_fp8_kernel<false><<<grid, fp8::kThreads, smem, s>>>(p);
+  st = launch_overlapped(tokens_m ? fp8::linear_fp8_kernel<true> : fp8::linear_fp8_kernel<false>, dim3(grid),
+                         fp8::kThreads, smem, s, p);
+  if (st != FLCE_OK) return st;
   ks.done();
   return check_launch("linear_fp8");
 }

@@ -103,22 +103,6 @@ flce_status launch_cluster(void (*kernel)(P), const P& p, int64_t grid, int ctas
   return FLCE_OK;
 }
 
-// A launch that may be dispatched while the one before it on the stream still runs
-// (the kernel waits for it with griddepcontrol.wait).
-template <typename P>
-flce_status launch_dependent(void (*kernel)(P), const P& p, int64_t grid, int threads, cudaStream_t s) {
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.stream = s;
-  cfg.attrs = &at, cfg.numAttrs = 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, p));
-  return FLCE_OK;
-}
-
 int pow2_up(int64_t v, int most) {
   int r = 1;
   while (r < v && r < most) r *= 2;
@@ -203,7 +187,7 @@ flce_status flce_policy_loss(const float* dloss, const float* logp, const float*
   } else {
     p.blocks = static_cast<int32_t>(L.blocks), p.chunk = static_cast<int32_t>(L.chunk);
     loss::policy_count_kernel<<<p.blocks, loss::kManyThreads, 0, s>>>(p);
-    st = launch_dependent(loss::policy_main_kernel, p, L.ctas, loss::kManyThreads, s);
+    st = launch_overlapped(loss::policy_main_kernel, dim3(static_cast<unsigned>(L.ctas)), loss::kManyThreads, 0, s, p);
   }
   if (st != FLCE_OK) return st;
   ks.done();
@@ -277,7 +261,7 @@ flce_status flce_preference_loss(const float* dloss, const float* logp, const fl
   } else {
     p.ctas = pow2_up(std::min<int64_t>(mean / 2048, 2 * sms / n_pairs), 8);
     st = launch_cluster(loss::preference_kernel<false>, p, n_pairs * p.ctas, p.ctas, loss::kPairThreads, s);
-    if (st == FLCE_OK) st = launch_dependent(loss::preference_reduce_kernel, p, 1, loss::kReduceThreads, s);
+    if (st == FLCE_OK) st = launch_overlapped(loss::preference_reduce_kernel, dim3(1), loss::kReduceThreads, 0, s, p);
   }
   if (st != FLCE_OK) return st;
   ks.done();

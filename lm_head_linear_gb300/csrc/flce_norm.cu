@@ -38,15 +38,12 @@ Shape pick_shape(int64_t T, int64_t Hd, int sms) {
   return s;
 }
 
-template <typename TX, typename TR, int NV>
-void launch_fwd(const norm::FwdParams& p, const Shape& s, int64_t blocks, cudaStream_t st) {
-  norm::add_rms_norm_kernel<TX, TR, NV><<<static_cast<unsigned>(blocks), s.threads, 0, st>>>(p);
-}
 template <typename TX, typename TR>
-void launch_fwd_nv(const norm::FwdParams& p, const Shape& s, int64_t blocks, cudaStream_t st) {
-  if (s.nv == 1) launch_fwd<TX, TR, 1>(p, s, blocks, st);
-  else if (s.nv == 2) launch_fwd<TX, TR, 2>(p, s, blocks, st);
-  else launch_fwd<TX, TR, 4>(p, s, blocks, st);
+flce_status launch_fwd(const norm::FwdParams& p, const Shape& s, int64_t blocks, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(blocks));
+  if (s.nv == 1) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 1>, grid, s.threads, 0, st, p);
+  if (s.nv == 2) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 2>, grid, s.threads, 0, st, p);
+  return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 4>, grid, s.threads, 0, st, p);
 }
 
 // The backward: eight or four vectors per thread, whichever leaves fewer idle (2048
@@ -88,8 +85,8 @@ flce_status launch_bwd(const norm::BwdParams& p, const BwdShape& s, int64_t bloc
       set[dev] = true;
     }
   }
-  norm::norm_backward_kernel<TY, TH, NV><<<static_cast<unsigned>(blocks), s.threads, s.smem, st>>>(p);
-  return FLCE_OK;
+  return launch_overlapped(norm::norm_backward_kernel<TY, TH, NV>, dim3(static_cast<unsigned>(blocks)), s.threads, s.smem,
+                           st, p);
 }
 template <typename TY, typename TH>
 flce_status launch_bwd_nv(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, cudaStream_t st) {
@@ -148,10 +145,11 @@ flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const
                  n * (size_of(x_dtype) + (residual ? 2.0 * size_of(residual_dtype) : 0.0) + (y ? 2.0 : 0.0) +
                       (q ? 1.0 + 1.0 / 128 : 0.0)));
   const bool xf = x_dtype == FLCE_DTYPE_F32, rf = residual ? residual_dtype == FLCE_DTYPE_F32 : xf;
-  if (xf && rf) launch_fwd_nv<float, float>(p, s, blocks, cs);
-  else if (xf) launch_fwd_nv<float, uint16_t>(p, s, blocks, cs);
-  else if (rf) launch_fwd_nv<uint16_t, float>(p, s, blocks, cs);
-  else launch_fwd_nv<uint16_t, uint16_t>(p, s, blocks, cs);
+  st = xf && rf ? launch_fwd<float, float>(p, s, blocks, cs)
+       : xf     ? launch_fwd<float, uint16_t>(p, s, blocks, cs)
+       : rf     ? launch_fwd<uint16_t, float>(p, s, blocks, cs)
+                : launch_fwd<uint16_t, uint16_t>(p, s, blocks, cs);
+  if (st != FLCE_OK) return st;
   ks.done();
   return check_launch("add_rms_norm");
 }
@@ -215,16 +213,9 @@ flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t
     if ((st = check_launch("norm_bwd")) != FLCE_OK) return st;
   }
   KernelScope ks(FLCE_KERNEL_NORM_DW, cs, 0.0, 4.0 * blocks * Hd + 4.0 * Hd);
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(Hd, 32)));
-  cfg.blockDim = dim3(32 * norm::kDwSlices);
-  cfg.stream = cs;
-  cfg.attrs = &at, cfg.numAttrs = 1;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, norm::norm_dw_kernel, static_cast<const float*>(p.partial),
-                              static_cast<int>(blocks), p.Hd, dweight));
+  st = launch_overlapped(norm::norm_dw_kernel, dim3(static_cast<unsigned>(cdiv(Hd, 32))), 32 * norm::kDwSlices, 0, cs,
+                         static_cast<const float*>(p.partial), static_cast<int>(blocks), p.Hd, dweight);
+  if (st != FLCE_OK) return st;
   ks.done();
   return check_launch("norm_dw");
 }

@@ -497,10 +497,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = ptx::cluster_ctarank();
   const Work w = work_of<TOKENS_M>(p);
 
-  // The status of this call.  The first CTA is dispatched first and clears the word
-  // before anything else; a wait that runs out does so a millisecond later at the
-  // earliest.
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       ptx::mbar_init(s.full(i), 1);
@@ -528,10 +524,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ptx::tmem_alloc_pair(ptx::smem_u32(s.tmem_slot), kTmemCols);
     ptx::tmem_relinquish_pair();
   }
+  ptx::launch_dependents();
   ptx::tc_fence_before();
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = *s.tmem_slot;
+  // Up to here nothing has touched global memory.
+  ptx::wait_prerequisites();
+  // The status of this call.  The first CTA is dispatched first and clears the word
+  // before anything else; a wait that runs out does so a millisecond later at the
+  // earliest.
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
   if (warp == 0) {
     if (ptx::elect_one()) producer<TOKENS_M>(p, s, w, rank);

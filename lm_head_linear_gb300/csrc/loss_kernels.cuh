@@ -449,13 +449,10 @@ constexpr int kManyThreads = 256;
 constexpr int kMaxBlocks = 1024;
 constexpr int kStep = kManyThreads * kGroup;  // tokens a CTA takes at a time
 
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __global__ void __launch_bounds__(kManyThreads) policy_count_kernel(const PolicyParams p) {
   constexpr int kWarps = kManyThreads / 32;
   __shared__ int warp_n[kWarps];
-  launch_dependents();
+  ptx::launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t first = p.cu ? p.cu[0] : 0, end = p.cu ? p.cu[p.S] : p.T;
   const int64_t b0 = static_cast<int64_t>(blockIdx.x) * p.chunk, b1 = min(b0 + p.chunk, int64_t(p.T));
@@ -523,7 +520,7 @@ __global__ void __launch_bounds__(kManyThreads) policy_main_kernel(const PolicyP
       cu_sh[i] = static_cast<int32_t>(min(max(p.cu[i], int64_t(0)), int64_t(p.T)));
   const int64_t first = p.cu ? p.cu[0] : 0, end = p.cu ? p.cu[p.S] : p.T;
 
-  wait_prerequisites();
+  ptx::wait_prerequisites();
   // exclusive prefix of the block counts: four blocks a thread
   {
     constexpr int kEach = kMaxBlocks / kManyThreads;
@@ -686,7 +683,7 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const Preferen
   const int rank = blockIdx.x % ctas;
   const int share = SOLO ? 1 : ctas;      // CTAs working on one pair
   const int part = SOLO ? 0 : rank;
-  if (!SOLO) launch_dependents();
+  if (!SOLO) ptx::launch_dependents();
   cluster_arrive();  // matched by the wait before the first access to another CTA
   bool arrived = true;
   double loss_sum = 0.0;
@@ -826,7 +823,7 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const Preferen
 constexpr int kReduceThreads = 256;
 
 __global__ void __launch_bounds__(kReduceThreads) preference_reduce_kernel(const PreferenceParams p) {
-  wait_prerequisites();
+  ptx::wait_prerequisites();
   __shared__ double sh[kReduceThreads / 32];
   __shared__ int sh_n[kReduceThreads / 32];
   double s = 0.0;

@@ -94,6 +94,8 @@ struct FwdParams {
 template <typename TX, typename TR, int NV>
 __global__ void __launch_bounds__(max_threads(NV)) add_rms_norm_kernel(const FwdParams p) {
   __shared__ float red[32];
+  ptx::launch_dependents();
+  ptx::wait_prerequisites();
   const int g = threadIdx.x / p.group;
   const int i = threadIdx.x - g * p.group;
   const int warps = p.group >> 5;
@@ -250,10 +252,6 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups + g;
   uint8_t* mine = ring + static_cast<size_t>(g) * p.stages * row_bytes;
   uint64_t* bars = full + g * kBwdMaxStages;
-  // The status of this call: cleared by the first CTA, dispatched first; a wait that
-  // runs out sets it a millisecond later at the earliest.
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the group's first thread: the copies of row `row` into stage `slot`
   const auto fill = [&](int64_t row, int slot) {
     if (row >= p.T) return;
@@ -270,7 +268,12 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
     ptx::fence_barrier_init();
     ptx::fence_proxy_async_smem();
   }
+  ptx::launch_dependents();
   __syncthreads();
+  ptx::wait_prerequisites();
+  // The status of this call: cleared by the first CTA, dispatched first; a wait that
+  // runs out sets it a millisecond later at the earliest.
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
   if (i == 0)
     for (int k = 0; k < p.stages; ++k) fill(row0 + k * step, k);
 
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(32 * kDwSlices) norm_dw_kernel(const float* pa
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.0f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  ptx::wait_prerequisites();
   if (c < Hd)
     for (int b = slice; b < blocks; b += kDwSlices) s += __ldcg(partial + static_cast<int64_t>(b) * Hd + c);
   sh[slice][lane] = s;

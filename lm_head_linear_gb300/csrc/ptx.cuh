@@ -137,6 +137,15 @@ __device__ __forceinline__ bool wait_bounded_cluster(uint32_t bar, uint32_t pari
   }
 }
 
+// ---------------------------------------------------------------- dependent launches
+// Returns once the kernels before this one on the stream are complete and their
+// writes visible (at once where the launch allowed no overlap).
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Lets the next kernel on the stream be dispatched, if its launch allows it, as soon
+// as every CTA of this one has come here or left.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 __device__ __forceinline__ void prefetch_tmap(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
