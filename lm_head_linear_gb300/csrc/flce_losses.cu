@@ -13,9 +13,9 @@ namespace {
 
 constexpr int64_t kClusterTokens = loss::kClusterThreads * loss::kGroup;  // of one CTA
 
-// Header (status, ticket) | block_sum | block_count | block_bad | words | seq_count.
+// Header (status, ticket, nonempty) | block_sum | block_count | block_bad | words | seq_count.
 // Both forms of the call fit: the larger one is laid out.
-constexpr size_t kTicketOff = 16;
+constexpr size_t kTicketOff = 16, kNonemptyOff = 32;
 struct PolicyLayout {
   int64_t chunk, blocks;  // the counting launch: tokens of a block, blocks (at most kMaxBlocks)
   int64_t ctas;           // the second launch
@@ -175,6 +175,7 @@ flce_status flce_policy_loss(const float* dloss, const float* logp, const float*
   p.words = reinterpret_cast<uint2*>(ws + L.words_off);
   p.seq_count = reinterpret_cast<int32_t*>(ws + L.seq_off);
   p.ticket = reinterpret_cast<int32_t*>(ws + kTicketOff);
+  p.nonempty = reinterpret_cast<int32_t*>(ws + kNonemptyOff);
   p.vec = !(off16(logp) || off16(old_logp) || off16(ref_logp) || (!advantages_per_sequence && off16(advantages)) ||
             off16(targets) || off16(dlogp) ||
             (reduction == FLCE_REDUCTION_NONE && (off16(loss) || off16(dloss))));
@@ -187,6 +188,9 @@ flce_status flce_policy_loss(const float* dloss, const float* logp, const float*
   } else {
     p.blocks = static_cast<int32_t>(L.blocks), p.chunk = static_cast<int32_t>(L.chunk);
     loss::policy_count_kernel<<<p.blocks, loss::kManyThreads, 0, s>>>(p);
+    if (reduction == FLCE_REDUCTION_SEQUENCE_MEAN && n_seqs >= loss::kCuShared)
+      loss::policy_nonempty_kernel<<<static_cast<unsigned>(std::min<int64_t>(cdiv(n_seqs, loss::kManyThreads), sms)),
+                                     loss::kManyThreads, 0, s>>>(p);
     st = launch_overlapped(loss::policy_main_kernel, dim3(static_cast<unsigned>(L.ctas)), loss::kManyThreads, 0, s, p);
   }
   if (st != FLCE_OK) return st;

@@ -52,7 +52,7 @@ constexpr int kStagingBytes = kEpiWarps * kStagingWarp;
 constexpr int kSmemTail = 512;
 constexpr int kSmemLimit = 232448;
 constexpr int kStatusTimeout = 7;
-constexpr uint64_t kDrainNs = 2000000000ull;
+constexpr uint64_t kDrainNs = 200000000ull;   // for copies and MMAs in flight when a kernel gives up
 constexpr uint64_t kSettleNs = 200000ull;
 static_assert(kScaleBase + kScaleStages * kScaleCols <= static_cast<int>(kTmemCols), "TMEM columns");
 
@@ -203,7 +203,8 @@ __device__ __forceinline__ void producer(const Params& p, const Smem& s, const W
   // last armed phase has completed
   if (rank == 0)
     for (int i = 0; i < p.stages; ++i)
-      if (used & (1u << i)) ptx::wait_bounded(s.full(i), i < at.i ? at.phase : at.phase ^ 1u, kDrainNs, nullptr);
+      if ((used & (1u << i)) && !ptx::wait_bounded(s.full(i), i < at.i ? at.phase : at.phase ^ 1u, kDrainNs, nullptr))
+        break;  // the odd CTA gave up before its half: what it did issue has landed by now
 }
 
 // Even CTA only.

@@ -51,12 +51,13 @@ struct PolicyParams {
   float kl_coef;
   // workspace
   int32_t* status;
-  int32_t* ticket;       // CTAs of the second launch that are done
+  int32_t* ticket;       // CTAs of the main launch that are done
+  int32_t* nonempty;     // sequences with a valid token (many sequences)
   int32_t* seq_count;    // [S] valid tokens of each sequence (the one-cluster form)
   int32_t* block_count;  // [blocks] valid tokens of a block of `chunk` tokens
   int32_t* block_bad;    // [blocks]
   uint2* words;          // [ceil(T / 32)] mask of 32 tokens, valid tokens of the block before them
-  double* block_sum;     // [CTAs of the second launch][5]
+  double* block_sum;     // [CTAs of the main launch][5]
   int32_t blocks;        // blocks of the first launch, or CTAs of the one cluster
   int32_t chunk;         // tokens of a block
   int32_t vec;           // every per-token array is 16-byte aligned
@@ -495,8 +496,64 @@ __global__ void __launch_bounds__(kManyThreads) policy_count_kernel(const Policy
   if (tid == 0) {
     p.block_count[blockIdx.x] = before;
     p.block_bad[blockIdx.x] = bad;
-    if (blockIdx.x == 0) *p.ticket = 0;
+    if (blockIdx.x == 0) *p.ticket = 0, *p.nonempty = 0;
   }
+}
+
+// Valid tokens before each block into prefix[0 .. kMaxBlocks], the last one their total.
+__device__ __forceinline__ void block_prefix(const PolicyParams& p, int* prefix, int* warp_n) {
+  constexpr int kEach = kMaxBlocks / kManyThreads;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int c[kEach], mine = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = tid * kEach + i;
+    c[i] = b < p.blocks ? __ldcg(p.block_count + b) : 0;
+    mine += c[i];
+  }
+  int inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == 31) warp_n[warp] = inc;
+  __syncthreads();
+  int at = inc - mine;
+  for (int i = 0; i < warp; ++i) at += warp_n[i];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    prefix[tid * kEach + i] = at;
+    at += c[i];
+  }
+  if (tid == kManyThreads - 1) prefix[kMaxBlocks] = at;
+  __syncthreads();
+}
+
+// Valid tokens before token i, 0 <= i <= T; and of sequence s.
+__device__ __forceinline__ int tokens_before(const PolicyParams& p, const int* prefix, int64_t i) {
+  if (i >= p.T) return prefix[kMaxBlocks];
+  const uint2 w = __ldcg(p.words + i / 32);
+  return prefix[i / p.chunk] + static_cast<int>(w.y) + __popc(w.x & ((1u << (i & 31)) - 1u));
+}
+__device__ __forceinline__ int tokens_of(const PolicyParams& p, const int* prefix, const Offsets& off, int s) {
+  const int64_t a = min(max(off.at(s), int64_t(0)), int64_t(p.T)), b = min(max(off.at(s + 1), int64_t(0)), int64_t(p.T));
+  return tokens_before(p, prefix, b) - tokens_before(p, prefix, a);
+}
+
+// SEQUENCE_MEAN with many sequences: how many have a valid token, counted once
+// instead of by every CTA of the main launch.
+__global__ void __launch_bounds__(kManyThreads) policy_nonempty_kernel(const PolicyParams p) {
+  __shared__ int prefix[kMaxBlocks + 1];
+  __shared__ int warp_n[kManyThreads / 32];
+  ptx::launch_dependents();
+  block_prefix(p, prefix, warp_n);
+  const Offsets off{nullptr, p.cu, p.S};
+  int c = 0;
+  for (int s = blockIdx.x * kManyThreads + threadIdx.x; s < p.S; s += gridDim.x * kManyThreads)
+    c += tokens_of(p, prefix, off, s) > 0;
+  c = __reduce_add_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0 && c) atomicAdd(p.nonempty, c);
 }
 
 __global__ void __launch_bounds__(kManyThreads) policy_main_kernel(const PolicyParams p) {
@@ -521,45 +578,13 @@ __global__ void __launch_bounds__(kManyThreads) policy_main_kernel(const PolicyP
   const int64_t first = p.cu ? p.cu[0] : 0, end = p.cu ? p.cu[p.S] : p.T;
 
   ptx::wait_prerequisites();
-  // exclusive prefix of the block counts: four blocks a thread
-  {
-    constexpr int kEach = kMaxBlocks / kManyThreads;
-    int c[kEach], mine = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int b = tid * kEach + i;
-      c[i] = b < p.blocks ? __ldcg(p.block_count + b) : 0;
-      mine += c[i];
-    }
-    int inc = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += o;
-    }
-    if (lane == 31) warp_n[warp] = inc;
-    __syncthreads();
-    int at = inc - mine;
-    for (int i = 0; i < warp; ++i) at += warp_n[i];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      prefix[tid * kEach + i] = at;
-      at += c[i];
-    }
-    if (tid == kManyThreads - 1) prefix[kMaxBlocks] = at;
-    __syncthreads();
-  }
+  block_prefix(p, prefix, warp_n);
   const int valid = prefix[kMaxBlocks];
-  // valid tokens before token i, 0 <= i <= T
-  const auto before = [&](int64_t i) {
-    if (i >= p.T) return valid;
-    const uint2 w = __ldcg(p.words + i / 32);
-    return prefix[i / p.chunk] + static_cast<int>(w.y) + __popc(w.x & ((1u << (i & 31)) - 1u));
-  };
-  const auto offset = [&](int i) { return min(max(off.at(i), int64_t(0)), int64_t(p.T)); };
-  const auto count = [&](int s) { return before(offset(s + 1)) - before(offset(s)); };
+  const auto count = [&](int i) { return tokens_of(p, prefix, off, i); };
   float scale = p.reduction == kMean ? 1.0f / fmaxf(static_cast<float>(valid), 1.0f) : 1.0f;
-  if (seq_mean) {
+  if (seq_mean && !off.sh) {
+    scale = 1.0f / fmaxf(static_cast<float>(__ldcg(p.nonempty)), 1.0f);
+  } else if (seq_mean) {
     int c = 0;
     for (int i = tid; i < p.S; i += kManyThreads) c += count(i) > 0;
     c = __reduce_add_sync(0xffffffffu, c);

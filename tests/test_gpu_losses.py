@@ -154,6 +154,29 @@ def test_policy_masks(cuda_device, reduction):
     assert dlogp.numel() == 0 and int(n) == 0 and bool((stats == 0).all()) and bool((loss == 0).all())
 
 
+@pytest.mark.parametrize("T,S", [(5000, 4500), (32768, 4095), (32768, 9000), (60000, 4095), (60000, 4096), (200000, 30000)])
+@pytest.mark.parametrize("reduction", ["sequence_mean", "mean"])
+def test_policy_many_sequences(cuda_device, T, S, reduction):
+    """More offsets than shared memory keeps, with empty and fully masked sequences among them."""
+    logp, old, ref, adv, y, g = draw(T, cuda_device, seed=S, mask=0.5)
+    cuts = torch.randint(0, T + 1, (S - 1,), generator=g, device=cuda_device).sort().values
+    cu = torch.cat([cuts.new_zeros(1), cuts, cuts.new_full((1,), T)])
+    advs = torch.randn(S, generator=g, device=cuda_device)
+    kw = dict(reduction=reduction, kl_coef=0.05, kl="k3")
+    check_policy((logp, old, ref, advs, y), dict(kw, cu=cu, per_sequence=True), cu_seqlens=cu, per_sequence=True, **kw)
+
+
+@pytest.mark.parametrize("T", [100, 50000])
+def test_policy_without_sequences(cuda_device, T):
+    """No sequence at all: no token counts."""
+    logp, old, _, adv, y, _ = draw(T, cuda_device)
+    cu = torch.zeros(1, dtype=torch.int64, device=cuda_device)
+    for red in ("mean", "sequence_mean", "sum", "none"):
+        loss, dlogp, stats, n, ws = flce.flce_policy_loss(logp, old, adv, y, cu_seqlens=cu, reduction=red)
+        assert bool((loss == 0).all()) and bool((dlogp == 0).all()) and bool((stats == 0).all()) and int(n) == 0
+        assert flce.flce_read_device_status(ws) == 0
+
+
 def test_policy_extreme_ratios(cuda_device):
     """Log ratios far beyond the clamp stay finite and carry no gradient from the ratio; a NaN in a trained
     token is not hidden; zero advantages and exact clip borders."""
@@ -206,6 +229,11 @@ def test_policy_bad_sequences_are_flagged(cuda_device):
     for cu in ([0, 500, 400, 1000], [0, 500, 1001], [-1, 1000], [2 ** 40, 3]):
         cu = torch.tensor(cu, dtype=torch.int64, device=cuda_device)
         *_, ws = flce.flce_policy_loss(logp, old, adv, y, cu_seqlens=cu, reduction="sequence_mean")
+        assert flce.flce_read_device_status(ws) == 8
+    big = draw(40000, cuda_device)
+    for cu in ([0, 30000, 20000, 40000], [0, 20000, 40001], [-1, 40000], [2 ** 40, 3], [0] * 5000 + [39999, 1, 40000]):
+        cu = torch.tensor(cu, dtype=torch.int64, device=cuda_device)
+        *_, ws = flce.flce_policy_loss(big[0], big[1], big[3], big[4], cu_seqlens=cu, reduction="sequence_mean")
         assert flce.flce_read_device_status(ws) == 8
     *_, ws = flce.flce_policy_loss(logp, old, adv, y, workspace=ws)
     assert flce.flce_read_device_status(ws) == 0
