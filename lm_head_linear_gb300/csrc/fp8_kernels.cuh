@@ -400,28 +400,47 @@ __device__ __forceinline__ void store_rows(const Params& p, uint32_t buf, int t0
   const int tokens = p.T - t0, logits = min(32, p.V - v0);
   if constexpr (sizeof(E) == 4) {
     float* y = static_cast<float*>(p.y) + static_cast<int64_t>(t0) * p.ldy + v0 + lane;
+    uint32_t v[32];
 #pragma unroll
-    for (int r = 0; r < 32; ++r, y += p.ldy) {
-      const uint32_t v = ld_shared_u32(staged<E>(buf, r, lane >> 2) + (lane & 3) * 4);
-      if (r < tokens && lane < logits) *y = __uint_as_float(v);
+    for (int r = 0; r < 32; ++r) v[r] = ld_shared_u32(staged<E>(buf, r, lane >> 2) + (lane & 3) * 4);
+    if (lane < logits) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r, y += p.ldy)
+        if (r < tokens) *y = __uint_as_float(v[r]);
     }
   } else {
     const int w = lane & 15, half = lane >> 4, next = min(w + 1, 15);
     uint16_t* y = static_cast<uint16_t*>(p.y) + static_cast<int64_t>(t0 + half) * p.ldy + v0;
     const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(y) >> 1) & 1;
     const int e = 2 * w + odd;  // this lane's first logit
-    const bool word = e + 1 < logits, one = e + 1 == logits, head = odd && w == 0;
+    uint32_t lo[16], hi[16];    // row 2 i + half
 #pragma unroll
-    for (int i = 0; i < 16; ++i, y += 2 * p.ldy) {
-      // row 2 i + half
-      const uint32_t lo = ld_shared_u32(buf + (2 * i + half) * 64 + (((w >> 2) ^ (i & 3)) << 4) + (w & 3) * 4);
-      const uint32_t hi = ld_shared_u32(buf + (2 * i + half) * 64 + (((next >> 2) ^ (i & 3)) << 4) + (next & 3) * 4);
-      const uint32_t v = odd ? __funnelshift_r(lo, hi, 16) : lo;
-      if (2 * i + half < tokens) {
-        if (word) *reinterpret_cast<uint32_t*>(y + e) = v;
-        if (one) y[e] = static_cast<uint16_t>(v);
-        if (head) y[0] = static_cast<uint16_t>(lo);
+    for (int i = 0; i < 16; ++i)
+      lo[i] = ld_shared_u32(buf + (2 * i + half) * 64 + (((w >> 2) ^ (i & 3)) << 4) + (w & 3) * 4);
+    if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        hi[i] = ld_shared_u32(buf + (2 * i + half) * 64 + (((next >> 2) ^ (i & 3)) << 4) + (next & 3) * 4);
+        hi[i] = odd ? __funnelshift_r(lo[i], hi[i], 16) : lo[i];
       }
+      if (odd && w == 0) {
+        uint16_t* y0 = y;
+#pragma unroll
+        for (int i = 0; i < 16; ++i, y0 += 2 * p.ldy)
+          if (2 * i + half < tokens) *y0 = static_cast<uint16_t>(lo[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) lo[i] = hi[i];
+    }
+    y += e;
+    if (e + 1 < logits) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i, y += 2 * p.ldy)
+        if (2 * i + half < tokens) *reinterpret_cast<uint32_t*>(y) = lo[i];
+    } else if (e + 1 == logits) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i, y += 2 * p.ldy)
+        if (2 * i + half < tokens) *y = static_cast<uint16_t>(lo[i]);
     }
   }
 }
