@@ -16,8 +16,8 @@
 //     16 bytes at a time (with the vocabulary on M they take a 2-byte store each:
 //     8192 x 2048 x 124,160 takes 1358 us this way and 1443 us that way).
 //
-// A CTA has 10 warps: the TMA producer, the MMA issuer (even CTA of the pair),
-// four epilogue warps and four scale warps.  The scale bytes come from their plain
+// A CTA has 14 warps: the TMA producer, the MMA issuer (even CTA of the pair),
+// eight epilogue warps and four scale warps.  The scale bytes come from their plain
 // row-major arrays: a scale warp loads, for the 32 TMEM lanes it may write, the
 // words of four consecutive K blocks and stores them to TMEM, four blocks a stage.
 // 224, not 256, tokens per tile: two accumulators (448 columns) and four stages
@@ -43,11 +43,11 @@ constexpr int kMaxStages = 12;
 constexpr int kScaleStages = 4;
 constexpr int kScaleCols = 16;                // columns of a scale stage: A's at +0 (4), B's at +8 (8)
 constexpr int kScaleBase = 2 * kMaxN;         // 448
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;   // two for each quarter of the TMEM lanes, on alternate columns
 constexpr int kScaleWarps = 4;
 constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
 constexpr uint32_t kTmemCols = 512;
-constexpr int kStagingWarp = 2 * 32 * 32 * 4;  // two 32 x 32 boxes of up to 4 bytes for each epilogue warp
+constexpr int kStagingWarp = 32 * 32 * 4;  // of an epilogue warp: two 32 x 32 boxes of bf16 or one of fp32
 constexpr int kStagingBytes = kEpiWarps * kStagingWarp;
 constexpr int kSmemTail = 512;
 constexpr int kSmemLimit = 232448;
@@ -449,8 +449,8 @@ __device__ __forceinline__ void store_rows(const Params& p, uint32_t buf, int t0
 template <typename E, bool TOKENS_M>
 __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const Work& w, uint32_t tmem, uint32_t rank,
                                          int warp, int lane) {
-  const int q = warp & 3;
-  const uint32_t staging = ptx::smem_u32(s.staging) + q * kStagingWarp;
+  const int q = warp & 3, part = (warp - 2) >> 2;
+  const uint32_t staging = ptx::smem_u32(s.staging) + (warp - 2) * kStagingWarp;
   Slot acc;
   uint32_t box = 0;
   for (int u = w.first; u < w.count; u += w.step) {
@@ -466,12 +466,13 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
     const int m_end = TOKENS_M ? p.T : p.V, n_end = TOKENS_M ? p.V : p.T;
     if (q < un.boxes && m0 < m_end) {
 #pragma unroll 1
-      for (int c = 0; c < p.n && un.n0 + c < n_end; c += 32) {
+      for (int c = 32 * part; c < p.n && un.n0 + c < n_end; c += 64) {
         uint32_t r[32];
         ptx::tmem_ld32(col + c, r);
         const int n0 = un.n0 + c;
-        const uint32_t buf = staging + (box & 1u) * (kStagingWarp / 2);
-        if (lane == 0) ptx::bulk_wait_read<1>();  // the store before last has read this buffer
+        constexpr int kBoxes = kStagingWarp / (32 * 32 * static_cast<int>(sizeof(E)));
+        const uint32_t buf = staging + (box % kBoxes) * (kStagingWarp / kBoxes);
+        if (lane == 0) ptx::bulk_wait_read<kBoxes - 1>();  // the store that used this buffer has read it
         __syncwarp();
         ptx::tmem_wait_ld32(r);
         if constexpr (TOKENS_M)
