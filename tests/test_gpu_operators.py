@@ -236,3 +236,57 @@ def test_timing_aid_names_the_operators(cuda_device):
     assert set(stats) == {"add_rms_norm", "linear_fp8", "policy_loss", "preference_loss", "norm_bwd", "norm_dw"}
     assert all(v["launches"] == 1 and v["total_ms"] > 0 for v in stats.values())
     assert stats["linear_fp8"]["flops"] == pytest.approx(2.0 * 600 * 512 * 3001)
+
+
+def test_example_moves_the_policy(cuda_device):
+    """The example's chain on a small size: finite figures, and the updates do what the losses ask for."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "rl_step.py")
+    spec = importlib.util.spec_from_file_location("rl_step", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    log = module.run(sequences=8, length=64, hidden=256, vocab=1003, steps=4, seed=1)
+    assert all(np.isfinite(v) for m in log for v in m.values())
+    policy = [m for m in log if "policy_loss" in m]
+    # the first step starts from the rollout policy: ratio 1, no KL, nothing clipped
+    assert policy[0]["ratio"] == 1.0 and policy[0]["kl"] == 0.0 and policy[0]["clipped"] == 0.0
+    assert policy[-1]["policy_loss"] < policy[0]["policy_loss"]
+    prefs = [m for m in log if "preference_loss" in m]
+    assert prefs[-1]["preference_loss"] < prefs[0]["preference_loss"] and prefs[-1]["margin"] > prefs[0]["margin"]
+
+
+def test_chain_gradients_against_plain_autograd(cuda_device):
+    """Norm, head, policy loss and back: gradients of the norm's weight, the head and the
+    inputs against torch autograd of the same formulas in 64 bits (on the bf16 norm the head sees)."""
+    T, Hd, V = 96, 128, 500
+    g = torch.Generator(device=cuda_device).manual_seed(3)
+    x = torch.randn(T, Hd, generator=g, device=cuda_device).to(BF)
+    r = torch.randn(T, Hd, generator=g, device=cuda_device).to(BF)
+    w = torch.rand(Hd, generator=g, device=cuda_device) + 0.5
+    W = (torch.randn(V, Hd, generator=g, device=cuda_device) * 0.1).to(BF)
+    y = torch.randint(0, V, (T,), generator=g, device=cuda_device)
+    y[::5] = IGN
+    adv = torch.randn(T, generator=g, device=cuda_device)
+    old = -6 + 0.3 * torch.randn(T, generator=g, device=cuda_device)
+    ins = [t.clone().requires_grad_(True) for t in (x, r, w, W)]
+    h, _ = flce.add_rms_norm(ins[0], ins[2], ins[1])
+    logp = flce.linear_log_probs(h, ins[3], y, IGN)
+    loss, _ = flce.policy_loss(logp, old, adv, y, old + 0.1, kl_coef=0.1, reduction="mean")
+    loss.backward()
+    # the reference: 64 bits, with the roundings to bf16 that the definitions have (h and the norm) passed straight through
+    ref = [t.detach().double().requires_grad_(True) for t in (x, r, w, W)]
+    s = ref[0] + ref[1]
+    s = s + ((x.float() + r.float()).to(BF).double() - s).detach()
+    n = s / torch.sqrt((s * s).mean(1, keepdim=True) + 1e-6) * ref[2]
+    n = n + (h.detach().double() - n).detach()
+    z = torch.log_softmax(n @ ref[3].t(), dim=1)
+    at = (y != IGN).nonzero()[:, 0]
+    lp = z[at, y[at]]
+    d = lp - old.double()[at]
+    A = adv.double()[at]
+    e = old.double()[at] + 0.1 - lp
+    per = -torch.minimum(d.exp() * A, d.exp().clamp(0.8, 1.2) * A) + 0.1 * (e.exp() - 1 - e)
+    per.mean().backward()
+    for got, want in zip(ins, ref):
+        assert float((got.grad.double() - want.grad).norm() / want.grad.norm()) <= 1e-2  # the framework's bar for gradients
