@@ -251,91 +251,121 @@ __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const
   ptx::wait_bounded(s.drain(), 0, kDrainNs, nullptr);
 }
 
-// The E8M0 bytes of K blocks 4 g .. 4 g + 3 of one row as a word (127, scale 1, past the end).
-__device__ __forceinline__ uint32_t scale_word(const uint8_t* row, int g, int kb, bool words) {
-  if (words) return __ldg(reinterpret_cast<const uint32_t*>(row) + g);
-  uint32_t w = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w |= static_cast<uint32_t>(4 * g + j < kb ? __ldg(row + 4 * g + j) : 127) << (8 * j);
+// Four scale bytes from any byte address: the two aligned words they lie in, loaded
+// here, and combined by bytes_of() when they are used, so that nothing waits for the
+// loads before.  Bytes of the pair outside the array are never touched.
+struct TwoWords {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ TwoWords load_words(const uint8_t* base, int64_t bytes, int64_t at) {
+  const uint8_t* a = base + at;
+  const uint8_t* p = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(a) & ~uintptr_t(3));
+  TwoWords w;
+  if (p >= base && p + 8 <= base + bytes) {
+    w.lo = __ldg(reinterpret_cast<const uint32_t*>(p));
+    w.hi = __ldg(reinterpret_cast<const uint32_t*>(p) + 1);
+  } else {  // the array's first or last bytes
+    w.lo = w.hi = 0;
+    for (int j = 0; j < 8; ++j)
+      if (p + j >= base && p + j < base + bytes) {
+        const uint32_t v = static_cast<uint32_t>(__ldg(p + j)) << (8 * (j & 3));
+        if (j < 4) w.lo |= v;
+        else w.hi |= v;
+      }
+  }
   return w;
 }
+__device__ __forceinline__ uint32_t bytes_of(const TwoWords& w, const uint8_t* base, int64_t at) {
+  return __funnelshift_r(w.lo, w.hi, 8 * (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(base + at)) & 3u));
+}
 
-// The words of one scale stage, K blocks 4 g .. 4 g + 3: column j of the M side (this
-// CTA's rows 32 j + lane) and of the N side (the tile's rows 32 j + lane).  Tokens have
-// a word for each row; W's 32 rows of a column lie in one 128-row block.
+// What one scale stage is made of, K blocks 4 g .. 4 g + 3: a word for each token row
+// of a column (32 j + lane), and one for each 128-row block of W that the columns
+// touch.  Bytes of a word past the last K block belong to the next row and are not
+// selected by any product.
+template <bool TOKENS_M>
 struct ScaleWords {
-  uint32_t a[4], b[8];
+  static constexpr int kTokens = TOKENS_M ? 4 : 8;  // columns of the tokens' side
+  static constexpr int kBlocks = TOKENS_M ? 3 : 2;  // 224 (128) rows from a multiple of 32 on
+  TwoWords t[kTokens], w[kBlocks];
+  int t0, r0, g;                                    // first token, first row of W
 };
 
 // Each of the four warps writes the same words to its own quarter of the lanes:
 // row r of A (or B) is lane r % 32, column r / 32, in every quarter.  The words of
-// the next stage are loaded before this one's TMEM stage is waited for, so a
-// load's latency does not stand between two stages.
+// the next two stages are on their way while one is written: nothing but the store
+// uses them, so a load's latency does not stand between two stages.
 template <bool TOKENS_M>
 __device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, const Work& w, uint32_t tmem,
                                              uint32_t rank, int warp, int lane) {
+  using Words = ScaleWords<TOKENS_M>;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  const bool words_x = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sx) & 3) == 0;
-  const bool words_w = (p.kb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.sw) & 3) == 0;
   const int groups = (p.kb + 3) / 4;
   const int last_block = (p.V + kRowsCta - 1) / kRowsCta - 1;
-  const auto of_token = [&](int t, int g) {
-    return t < p.T ? scale_word(p.sx + static_cast<int64_t>(t) * p.kb, g, p.kb, words_x) : 0x7f7f7f7fu;
-  };
-  const auto of_block = [&](int b, int g) {
-    return scale_word(p.sw + static_cast<int64_t>(min(b, last_block)) * p.kb, g, p.kb, words_w);
-  };
-  const auto load = [&](int u, int g) {
-    ScaleWords r;
-    const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
-    if constexpr (TOKENS_M) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r.a[j] = of_token(un.row + 32 * j + lane, g);
-      // 224 rows touch at most three blocks
-      const int b0 = un.n0 / kRowsCta;
-      const uint32_t w0 = of_block(b0, g), w1 = of_block(b0 + 1, g), w2 = of_block(b0 + 2, g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int b = (un.n0 + 32 * j) / kRowsCta - b0;
-        r.b[j] = b == 0 ? w0 : b == 1 ? w1 : w2;
-      }
-    } else {
-      // four 32-row columns touch at most two blocks
-      const int b0 = un.row / kRowsCta;
-      const uint32_t w0 = of_block(b0, g), w1 = of_block((un.row + 96) / kRowsCta, g);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) r.a[j] = (un.row + 32 * j) / kRowsCta == b0 ? w0 : w1;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r.b[j] = 32 * j < p.n ? of_token(un.n0 + 32 * j + lane, g) : 0x7f7f7f7fu;
-    }
-    return r;
+  const int64_t x_bytes = static_cast<int64_t>(p.T) * p.kb, w_bytes = static_cast<int64_t>(last_block + 1) * p.kb;
+  const auto token_at = [&](const Words& r, int j) { return static_cast<int64_t>(r.t0 + 32 * j + lane) * p.kb + 4 * r.g; };
+  const auto block_at = [&](const Words& r, int b) {
+    return static_cast<int64_t>(min(r.r0 / kRowsCta + b, last_block)) * p.kb + 4 * r.g;
   };
   Slot at;
-  int u = w.first, g = 0;
-  if (u >= w.count) return;
-  ScaleWords now = load(u, g);
-  while (true) {
+  int u = w.first, g = 0;  // of the next load
+  const auto next = [&](Words& r) {
+    if (u >= w.count) return false;
+    const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
+    r.t0 = TOKENS_M ? un.row : un.n0;
+    r.r0 = TOKENS_M ? un.n0 : un.row;
+    r.g = g;
+#pragma unroll
+    for (int j = 0; j < Words::kTokens; ++j)
+      if (r.t0 + 32 * j + lane < p.T && (TOKENS_M || 32 * j < p.n)) r.t[j] = load_words(p.sx, x_bytes, token_at(r, j));
+#pragma unroll
+    for (int b = 0; b < Words::kBlocks; ++b) r.w[b] = load_words(p.sw, w_bytes, block_at(r, b));
     if (++g == groups) g = 0, u += w.step;
-    const bool more = u < w.count;
-    ScaleWords next;
-    if (more) next = load(u, g);
+    return true;
+  };
+  const auto put = [&](const Words& r) {
     if (!ptx::wait_bounded_cluster(s.scale_empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
       give_up(p, s);
-      return;
+      return false;
     }
+    uint32_t tw[Words::kTokens], ww[Words::kBlocks];
+#pragma unroll
+    for (int j = 0; j < Words::kTokens; ++j)  // rows past T meet zeros: any scale but NaN will do
+      tw[j] = r.t0 + 32 * j + lane < p.T ? bytes_of(r.t[j], p.sx, token_at(r, j)) : 0x7f7f7f7fu;
+#pragma unroll
+    for (int b = 0; b < Words::kBlocks; ++b) ww[b] = bytes_of(r.w[b], p.sw, block_at(r, b));
+    const int off = (r.r0 / 32) & 3;
+    const auto block_word = [&](int j) {
+      const int b = (off + j) >> 2;
+      return b == 0 ? ww[0] : b == 1 ? ww[1] : ww[Words::kBlocks - 1];
+    };
     ptx::tc_fence_after();
     __syncwarp();
     const uint32_t col = tmem + lanes + kScaleBase + at.i * kScaleCols;
-    ptx::tmem_st4(col, now.a[0], now.a[1], now.a[2], now.a[3]);
-    ptx::tmem_st8(col + 8, now.b);
+    if constexpr (TOKENS_M) {
+      ptx::tmem_st4(col, tw[0], tw[1], tw[2], tw[3]);
+      const uint32_t b[8] = {block_word(0), block_word(1), block_word(2), block_word(3),
+                             block_word(4), block_word(5), block_word(6), block_word(6)};
+      ptx::tmem_st8(col + 8, b);
+    } else {
+      ptx::tmem_st4(col, block_word(0), block_word(1), block_word(2), block_word(3));
+      ptx::tmem_st8(col + 8, tw);
+    }
     ptx::tmem_wait_st();
     ptx::tc_fence_before();
     __syncwarp();
     if (lane == 0) arrive_even(s.scale_full(at.i));
     at.next(kScaleStages);
-    if (!more) return;
-    now = next;
+    return true;
+  };
+  // Two sets of registers in turn: copying one to the other would wait for its loads.
+  Words x, y;
+  bool more_x = next(x), more_y = next(y);
+  while (more_x) {
+    if (!put(x)) return;
+    more_x = next(x);
+    if (!more_y || !put(y)) return;
+    more_y = next(y);
   }
 }
 
