@@ -635,17 +635,22 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const E* a, int
   const int kb = static_cast<int>(blockIdx.x - rb * nb);
   const int c = kb * 128 + (threadIdx.x & 15) * kVec;
   const int64_t r0 = rb * 128 + (threadIdx.x >> 4);
-  float v[kSteps][kVec];
+  Raw8 raw[kSteps];  // as loaded: the unpacked floats of eight rows would halve the loads in flight
   float m[kSteps];
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int64_t r = r0 + i * (kQuantThreads / 16);
-    m[i] = 0.0f;
-    if (r < R && c < K) {
-      unpack8<E>(load8(a + r * lda + c), v[i]);
+    if (r < R && c < K) raw[i] = load8(a + r * lda + c);
+  }
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) m[i] = fmaxf(m[i], fabsf(v[i][j]));
+  for (int i = 0; i < kSteps; ++i) {
+    m[i] = 0.0f;
+    if (r0 + i * (kQuantThreads / 16) < R && c < K) {
+      float v[kVec];
+      unpack8<E>(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) m[i] = fmaxf(m[i], fabsf(v[j]));
     }
     amax = fmaxf(amax, m[i]);
   }
@@ -670,7 +675,9 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const E* a, int
     }
     if (r < R && c < K) {
       const uint32_t e = e8m0_of(top);
-      *reinterpret_cast<uint2*>(q + r * K + c) = to_e4m3x8(v[i], inv_scale(e));
+      float v[kVec];
+      unpack8<E>(raw[i], v);
+      *reinterpret_cast<uint2*>(q + r * K + c) = to_e4m3x8(v, inv_scale(e));
       if (!SQUARE && (threadIdx.x & 15) == 0) qs[r * nb + kb] = static_cast<uint8_t>(e);
     }
   }
