@@ -85,14 +85,14 @@ flce_status check_launch(const char* what);
 // Launches a kernel that begins with griddepcontrol.wait: it may be dispatched, and
 // set itself up, while the kernel before it on the stream is still finishing.
 template <typename... Params, typename... Args>
-flce_status launch_overlapped(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+flce_status launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                               const Args&... args) {
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &at, cfg.numAttrs = 1;

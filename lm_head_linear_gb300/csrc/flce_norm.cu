@@ -18,32 +18,33 @@ int64_t size_of(int32_t d) { return d == FLCE_DTYPE_F32 ? 4 : 2; }
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 bool bad_ld(int64_t ld, int64_t Hd, int32_t dtype) { return ld < Hd || (ld * size_of(dtype)) % 16 != 0; }
 
-// Vectors per thread and threads per row.  Up to a row per SM: one vector per thread,
-// the shortest chain from load to store.  More rows: two (1000 x 2048: 3.7 us against
-// 4.5 us with four), and from 16 rows per SM on four, which needs fewer warps for a row
-// and has more loads of a warp in flight (65,536 x 2048 to 8 bits: 135 us against 146 us
-// with two, 164 us with one and 149 us with eight).
+// Vectors of 8 channels per thread and threads per row.  Up to a row per SM: one vector
+// per thread, the shortest chain from load to store.  More rows: two (1531 x 4112 from
+// fp32: 14.6 us, 18.4 us as one run of two), and from 16 rows per SM on four in runs of
+// two, which needs fewer warps for a row, has more loads of a warp in flight and half the
+// scales to work out (65,536 x 2048 to 8 bits: 141 us against 146 us with four runs of
+// one, both with a slower rounding; 135 us now).
 struct Shape {
-  int nv, group, threads;
+  int vecs, group, threads;
 };
 Shape pick_shape(int64_t T, int64_t Hd, int sms) {
   const int nvec = static_cast<int>(Hd / kVec);
-  int nv = T <= sms ? 1 : T <= 16 * sms ? 2 : 4;
-  while (cdiv(cdiv(nvec, nv), 32) * 32 > norm::max_threads(nv)) nv *= 2;
-  while (nv > 1 && (nv / 2) * 32 >= nvec) nv /= 2;  // a warp would leave whole steps idle
+  int vecs = T <= sms ? 1 : T <= 16 * sms ? 2 : 4;
+  while (cdiv(cdiv(nvec, vecs), 32) * 32 > norm::max_threads(vecs)) vecs *= 2;
+  while (vecs > 1 && (vecs / 2) * 32 >= nvec) vecs /= 2;  // a warp would leave whole steps idle
   Shape s;
-  s.nv = nv;
-  s.group = static_cast<int>(cdiv(cdiv(nvec, nv), 32) * 32);
+  s.vecs = vecs;
+  s.group = static_cast<int>(cdiv(cdiv(nvec, vecs), 32) * 32);
   s.threads = T > sms ? std::max(s.group, 128 / s.group * s.group) : s.group;
   return s;
 }
-
-template <typename TX, typename TR>
-flce_status launch_fwd(const norm::FwdParams& p, const Shape& s, int64_t blocks, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(blocks));
-  if (s.nv == 1) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 1>, grid, s.threads, 0, st, p);
-  if (s.nv == 2) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 2>, grid, s.threads, 0, st, p);
-  return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 4>, grid, s.threads, 0, st, p);
+template <typename TX, typename TR, bool EXACT>
+flce_status launch_fwd(const norm::FwdParams& p, const Shape& s, cudaStream_t st) {
+  const int rows = s.threads / s.group;
+  const dim3 grid(static_cast<unsigned>(cdiv(p.T, rows))), block(s.group, rows);
+  if (s.vecs == 1) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 1, 1, EXACT>, grid, block, 0, st, p);
+  if (s.vecs == 2) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 2, 1, EXACT>, grid, block, 0, st, p);
+  return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 2, 2, EXACT>, grid, block, 0, st, p);
 }
 
 // The backward: eight or four vectors per thread, whichever leaves fewer idle (2048
@@ -135,20 +136,22 @@ flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const
   p.x = x, p.r = residual, p.w = weight, p.h = h;
   p.y = static_cast<uint16_t*>(y), p.rstd = rstd, p.q = static_cast<uint8_t*>(q), p.qs = q_scale;
   p.ldx = ldx, p.ldr = ldr, p.ldh = ldh, p.T = T, p.Hd = static_cast<int32_t>(Hd);
-  p.w_f32 = weight_dtype == FLCE_DTYPE_F32, p.eps = eps, p.inv_hd = 1.0f / static_cast<float>(Hd);
+  p.w_f32 = weight_dtype == FLCE_DTYPE_F32, p.eps = eps;
+  p.inv_hd = static_cast<float>(1.0 / static_cast<double>(Hd));
+  p.inv_hd_lo = static_cast<float>(1.0 / static_cast<double>(Hd) - static_cast<double>(p.inv_hd));
   const Shape s = pick_shape(T, Hd, sms);
-  p.group = s.group;
-  const int64_t blocks = cdiv(T, s.threads / s.group);
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const double n = static_cast<double>(T) * Hd;
   KernelScope ks(FLCE_KERNEL_ADD_RMS_NORM, cs, 8.0 * n,
                  n * (size_of(x_dtype) + (residual ? 2.0 * size_of(residual_dtype) : 0.0) + (y ? 2.0 : 0.0) +
                       (q ? 1.0 + 1.0 / 128 : 0.0)));
   const bool xf = x_dtype == FLCE_DTYPE_F32, rf = residual ? residual_dtype == FLCE_DTYPE_F32 : xf;
-  st = xf && rf ? launch_fwd<float, float>(p, s, blocks, cs)
-       : xf     ? launch_fwd<float, uint16_t>(p, s, blocks, cs)
-       : rf     ? launch_fwd<uint16_t, float>(p, s, blocks, cs)
-                : launch_fwd<uint16_t, uint16_t>(p, s, blocks, cs);
+  if (rf)  // h in fp32
+    st = xf ? launch_fwd<float, float, false>(p, s, cs) : launch_fwd<uint16_t, float, false>(p, s, cs);
+  else if (p.w_f32)
+    st = xf ? launch_fwd<float, uint16_t, false>(p, s, cs) : launch_fwd<uint16_t, uint16_t, false>(p, s, cs);
+  else
+    st = xf ? launch_fwd<float, uint16_t, true>(p, s, cs) : launch_fwd<uint16_t, uint16_t, true>(p, s, cs);
   if (st != FLCE_OK) return st;
   ks.done();
   return check_launch("add_rms_norm");

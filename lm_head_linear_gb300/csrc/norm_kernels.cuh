@@ -20,24 +20,11 @@
 namespace flce {
 namespace norm {
 
-// Threads per CTA for a thread that holds NV vectors (its row values live in
-// registers: 8 NV floats, plus the raw loads).
-__host__ __device__ constexpr int max_threads(int nv) { return nv <= 2 ? 1024 : (nv <= 4 ? 512 : 256); }
+// Threads per row at most for a thread that holds `vecs` vectors of 8 channels (their
+// values live in registers, next to the raw loads).
+__host__ __device__ constexpr int max_threads(int vecs) { return vecs == 1 ? 1024 : 512; }
 
 // Eight weights, bf16 or fp32 (read by every row: they stay in L1).
-__device__ __forceinline__ void load_weight8(const void* w, bool w_f32, int c, float (&v)[kVec]) {
-  Raw8 r;
-  if (w_f32) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(w) + c);
-    r.a = __ldg(p);
-    r.b = __ldg(p + 1);
-    unpack8<float>(r, v);
-  } else {
-    r.a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c));
-    unpack8<uint16_t>(r, v);
-  }
-}
-
 __device__ __forceinline__ void load_weight_pairs(const void* w, bool w_f32, int c, F2 (&v)[kPairs]) {
   Raw8 r;
   if (w_f32) {
@@ -59,15 +46,14 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Sum over the `warps` warps of this thread's row group, in warp order (the same
-// result on every thread).  `slot` holds `warps` floats per group; a barrier lies
-// between one sum's last read and the next one's first write.
-__device__ __forceinline__ float group_sum(float v, float* slot, int warps, int warp_in_group) {
-  v = warp_sum(v);
-  if (warps == 1) return v;
-  if ((threadIdx.x & 31) == 0) slot[warp_in_group] = v;
+// result on every thread).  `slot` holds `warps` of them per group.
+__device__ __forceinline__ Twofold group_sum(float v, Twofold* slot, int warps, int warp_in_group) {
+  Twofold s = warp_sum_twofold(v);
+  if (warps == 1) return s;
+  if ((threadIdx.x & 31) == 0) slot[warp_in_group] = s;
   __syncthreads();
-  float s = 0.0f;
-  for (int i = 0; i < warps; ++i) s += slot[i];
+  s = slot[0];
+  for (int i = 1; i < warps; ++i) s = s + slot[i];
   return s;
 }
 
@@ -84,85 +70,161 @@ struct FwdParams {
   int64_t ldx, ldr, ldh;
   int64_t T;
   int32_t Hd;
-  int32_t group;   // threads per row (a multiple of 32)
   int32_t w_f32;
-  float eps, inv_hd;
+  float eps, inv_hd, inv_hd_lo;  // inv_hd + inv_hd_lo = 1 / Hd
 };
 
 // One row per group of `group` threads; thread i of the group holds channels
-// 8 (i + group k) .., k < NV.
-template <typename TX, typename TR, int NV>
-__global__ void __launch_bounds__(max_threads(NV)) add_rms_norm_kernel(const FwdParams p) {
-  __shared__ float red[32];
+// 8 B (i + group k) .., k < NV: NV runs of B vectors.
+//
+// An e4m3 number is the 64-bit definition's but for one in 10^7: an error of rstd moves
+// a whole row against the rounding boundaries (3e-8, half a unit of fp32, changes one
+// element in a million), so the sum of squares over the threads and rstd carry what fp32
+// rounds off, the products are rounded once, and that once to odd, so that the rounding
+// to four bits sees the value itself and not a rounded one.  Of the 134 M numbers of
+// 65,536 x 2048 7 to 20 differ from the definition's; 61 to 102 did with each step
+// rounded to nearest.  EXACT: h and w are bf16, so that h w is exact in fp32.
+//
+// Bound by memory: 65,536 x 2048 with residual to 8 bits (943 MB) takes 135 us, 7.0 TB/s,
+// with 60 % of the issue slots taken; pairs of channels go through one instruction.
+// Rounding to odd by both directed roundings and a choice took 146 us, twofold sums from
+// the first square on 170 us: the issue slots ran out.
+template <typename TX, typename TR, int NV, int B, bool EXACT>
+__global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const FwdParams p) {
+  constexpr int kRun = B * kVec, kRunPairs = B * kPairs, kBlockRuns = 128 / kRun;
+  __shared__ Twofold red[32];
   ptx::launch_dependents();
   ptx::wait_prerequisites();
-  const int g = threadIdx.x / p.group;
-  const int i = threadIdx.x - g * p.group;
-  const int warps = p.group >> 5;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / p.group) + g;
+  const int group = blockDim.x, g = threadIdx.y, i = threadIdx.x;  // threads per row: a multiple of 32
+  const int warps = group >> 5;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * blockDim.y + g;
   const bool live = row < p.T;
-  const int nvec = p.Hd / kVec;
   const TX* x = static_cast<const TX*>(p.x) + (live ? row : 0) * p.ldx;
   const TR* r = p.r ? static_cast<const TR*>(p.r) + (live ? row : 0) * p.ldr : nullptr;
 
-  Raw8 rx[NV], rr[NV];
+  Raw8 rx[NV][B], rr[NV][B];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = i + k * p.group;
-    if (live && c < nvec) {
-      rx[k] = load8(x + c * kVec);
-      if (r) rr[k] = load8(r + c * kVec);
+    const int c = (i + k * group) * kRun;
+    if (live && c < p.Hd) {
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        rx[k][b] = load8(x + c + b * kVec);
+        if (r) rr[k][b] = load8(r + c + b * kVec);
+      }
     }
   }
-  float v[NV][kVec];
-  float ss = 0.0f;
+  F2 v[NV][kRunPairs];
+  F2 sq[kRunPairs] = {};  // 8 B chains of NV squares
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = i + k * p.group;
-    if (live && c < nvec) {
-      unpack8<TX>(rx[k], v[k]);
-      if (r) {
-        float o[kVec];
-        unpack8<TR>(rr[k], o);
+    const int c = (i + k * group) * kRun;
+    if (live && c < p.Hd) {
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) o[j] += v[k][j];
-        const Raw8 packed = pack8<TR>(o);
-        store8(static_cast<TR*>(p.h) + row * p.ldh + c * kVec, packed);
-        unpack8<TR>(packed, v[k]);
+      for (int b = 0; b < B; ++b) {
+        F2 o[kPairs];
+        unpack_pairs<TX>(rx[k][b], o);
+        if (r) {
+          F2 a[kPairs];
+          unpack_pairs<TR>(rr[k][b], a);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) o[j] = add2(a[j], o[j]);
+          const Raw8 packed = pack_pairs<TR>(o);
+          store8(static_cast<TR*>(p.h) + row * p.ldh + c + b * kVec, packed);
+          unpack_pairs<TR>(packed, o);
+        }
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          v[k][b * kPairs + j] = o[j];
+          sq[b * kPairs + j] = fma2(o[j], o[j], sq[b * kPairs + j]);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) ss = fmaf(v[k][j], v[k][j], ss);
     } else {
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[k][j] = 0.0f;
+      for (int j = 0; j < kRunPairs; ++j) v[k][j] = 0;
     }
   }
-  ss = group_sum(ss, red + g * warps, warps, i >> 5);
-  const float rstd = rsqrtf(fmaf(ss, p.inv_hd, p.eps));
-  if (live && i == 0 && p.rstd) p.rstd[row] = rstd;
+  float even, odd;
+#pragma unroll
+  for (int d = kRunPairs / 2; d > 0; d >>= 1) {
+#pragma unroll
+    for (int j = 0; j < d; ++j) sq[j] = add2(sq[j], sq[j + d]);
+  }
+  split(sq[0], even, odd);
+  const Twofold ss = group_sum(even + odd, red + g * warps, warps, i >> 5);
+  // mean = ss / Hd + eps, then rstd as hi + lo by one Newton step on rsqrtf()'s value
+  Twofold mean{ss.hi * p.inv_hd, 0.0f};
+  mean.lo = fmaf(ss.hi, p.inv_hd, -mean.hi) + fmaf(ss.hi, p.inv_hd_lo, ss.lo * p.inv_hd);
+  mean = mean + Twofold{p.eps, 0.0f};
+  float hi = rsqrtf(mean.hi), lo = 0.0f;
+  if (mean.hi > 0.0f && mean.hi < INFINITY) {
+    const float t = mean.hi * hi, te = fmaf(mean.hi, hi, -t) + mean.lo * hi;
+    const float step = 0.5f * hi * (fmaf(-t, hi, 1.0f) - te * hi);
+    const float better = hi + step;
+    lo = step - (better - hi);
+    hi = better;
+  }
+  if (live && i == 0 && p.rstd) p.rstd[row] = hi;
+  const F2 hi2 = both(hi), lo2 = both(lo), minus = both(-1.0f);
+  // Rounding to odd: towards zero, and the last bit set where that cut something off.
+  // With lo != 0 every product but 0 is cut (the odd part of hi + lo alone has more than
+  // 24 bits); with lo == 0 the bit stays as it is, and what is exact stays exact.
+  const uint32_t odd_bit = lo != 0.0f ? 1u : 0u;
   const int nblk = (p.Hd + 127) / 128;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int c = i + k * p.group;
-    const bool mine = live && c < nvec;
+    const int run = i + k * group, c = run * kRun;
+    const bool mine = live && c < p.Hd;
+    float y[kRun];
+    float amax = 0.0f;
     if (mine) {
-      float w[kVec];
-      load_weight8(p.w, p.w_f32 != 0, c * kVec, w);
+      F2 rest[kRunPairs];
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) v[k][j] = v[k][j] * rstd * w[j];
-      if (p.y) store8(p.y + row * p.Hd + c * kVec, pack8<uint16_t>(v[k]));
+      for (int b = 0; b < B; ++b) {
+        F2 w[kPairs];
+        load_weight_pairs(p.w, !EXACT && p.w_f32 != 0, c + b * kVec, w);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {  // h w (hi + lo) = a hi + rest, a = round(h w)
+          F2& h = v[k][b * kPairs + j];
+          F2& t = rest[b * kPairs + j];
+          const F2 a = mul2(h, w[j]);
+          t = mul2(a, lo2);
+          if constexpr (!EXACT) t = fma2(fma2(h, w[j], mul2(a, minus)), hi2, t);
+          h = a;
+        }
+        if (p.y) {
+          F2 s[kPairs];
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) s[j] = mul2(v[k][b * kPairs + j], hi2);
+          store8(p.y + row * p.Hd + c + b * kVec, pack_pairs<uint16_t>(s));
+        }
+      }
+      if (p.q) {  // rounded to odd; fmaxf drops NaN: the scale comes from the block's numbers, a NaN stays NaN in q
+#pragma unroll
+        for (int j = 0; j < kRunPairs; ++j) {
+          split(fma2_zero(v[k][j], hi2, rest[j]), y[2 * j], y[2 * j + 1]);
+#pragma unroll
+          for (int b = 2 * j; b < 2 * j + 2; ++b) {
+            y[b] = __uint_as_float(__float_as_uint(y[b]) | odd_bit);
+            amax = fmaxf(amax, fabsf(y[b]));
+          }
+        }
+      }
     }
     if (p.q) {  // the same for every thread of the launch
-      // fmaxf drops NaN: the scale comes from the block's numbers, a NaN stays NaN in q
-      float a = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) a = fmaxf(a, fabsf(v[k][j]));
-#pragma unroll
-      for (int d = kBlockVecs / 2; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+      for (int d = kBlockRuns / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
       if (mine) {
-        const uint32_t e = e8m0_of(a);
-        *reinterpret_cast<uint2*>(p.q + row * p.Hd + c * kVec) = to_e4m3x8(v[k], inv_scale(e));
-        if ((threadIdx.x & (kBlockVecs - 1)) == 0) p.qs[row * nblk + c / kBlockVecs] = static_cast<uint8_t>(e);
+        const uint32_t e = e8m0_of(amax);  // the odd bit of a zero is below the least scale
+        uint8_t* q = p.q + row * p.Hd + c;
+        const uint2 a = to_e4m3x8(y, inv_scale(e));
+        if constexpr (B == 2) {
+          const uint2 b = to_e4m3x8(y + kVec, inv_scale(e));
+          *reinterpret_cast<uint4*>(q) = make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+          *reinterpret_cast<uint2*>(q) = a;
+        }
+        if ((i & (kBlockRuns - 1)) == 0) p.qs[row * nblk + run / kBlockRuns] = static_cast<uint8_t>(e);
       }
     }
   }

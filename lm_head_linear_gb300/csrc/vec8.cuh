@@ -10,7 +10,6 @@
 namespace flce {
 
 constexpr int kVec = 8;            // channels per thread and step: one 16-byte bf16 load
-constexpr int kBlockVecs = 16;     // 16 threads x 8 channels: one block of 128
 
 // ------------------------------------------------------------------ 8-channel loads and stores
 struct Raw8 {
@@ -85,6 +84,16 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ F2 fma2_zero(F2 a, F2 b, F2 c) {  // rounded towards zero
+  F2 r;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 constexpr int kPairs = kVec / 2;
 
@@ -107,6 +116,28 @@ __device__ __forceinline__ Raw8 pack_pairs(const F2 (&v)[kPairs]) {
   return pack8<E>(f);
 }
 
+// ------------------------------------------------------------------ sums of twice 24 bits
+// hi + lo, with |lo| at most half a unit of hi: what an addition rounds off is kept
+// (Knuth's two-sum).
+struct Twofold {
+  float hi, lo;
+};
+__device__ __forceinline__ Twofold operator+(Twofold a, Twofold b) {
+  Twofold r;
+  r.hi = a.hi + b.hi;
+  const float t = r.hi - a.hi;
+  r.lo = (a.hi - (r.hi - t)) + (b.hi - t) + (a.lo + b.lo);
+  return r;
+}
+// Sum over the warp.  The first three steps add 16, 8 and 4 pairs, whose rounding
+// errors average out over the pairs; the last two keep theirs.
+__device__ __forceinline__ Twofold warp_sum_twofold(float v) {
+#pragma unroll
+  for (int d = 16; d > 2; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  Twofold t = Twofold{v, 0.0f} + Twofold{__shfl_xor_sync(0xffffffffu, v, 2), 0.0f};
+  return t + Twofold{__shfl_xor_sync(0xffffffffu, t.hi, 1), __shfl_xor_sync(0xffffffffu, t.lo, 1)};
+}
+
 // ------------------------------------------------------------------ e4m3 with a power-of-two scale
 // E8M0 byte of the smallest 2^e with amax / 2^e <= 448 = 1.75 * 2^8, e >= -126.
 // From amax's own exponent and mantissa (amax is finite and not negative).
@@ -120,11 +151,15 @@ __device__ __forceinline__ uint32_t e8m0_of(float amax) {
 __device__ __forceinline__ float inv_scale(uint32_t e8m0) { return __uint_as_float((254u - e8m0) << 23); }
 
 // Eight floats to e4m3, round to nearest even, |v| > 448 to 448, NaN kept.
-__device__ __forceinline__ uint2 to_e4m3x8(const float (&v)[kVec], float inv) {
+__device__ __forceinline__ uint2 to_e4m3x8(const float* v, float inv) {
   uint16_t h[4];
+  const F2 by = both(inv);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(v[2 * i + 1] * inv), "f"(v[2 * i] * inv));
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    split(mul2(pair(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1])), by), lo, hi);
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(hi), "f"(lo));
+  }
   return make_uint2(h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16));
 }
 
