@@ -23,7 +23,7 @@ bool bad_ld(int64_t ld, int64_t Hd, int32_t dtype) { return ld < Hd || (ld * siz
 // fp32: 14.6 us, 18.4 us as one run of two), and from 16 rows per SM on four in runs of
 // two, which needs fewer warps for a row, has more loads of a warp in flight and half the
 // scales to work out (65,536 x 2048 to 8 bits: 141 us against 146 us with four runs of
-// one, both with a slower rounding; 135 us now).
+// one, both with a slower rounding; 138 us now).
 struct Shape {
   int vecs, group, threads;
 };

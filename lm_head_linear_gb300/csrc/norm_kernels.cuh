@@ -47,7 +47,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Sum over the `warps` warps of this thread's row group, in warp order (the same
 // result on every thread).  `slot` holds `warps` of them per group.
-__device__ __forceinline__ Twofold group_sum(float v, Twofold* slot, int warps, int warp_in_group) {
+__device__ __forceinline__ Twofold group_sum(Twofold v, Twofold* slot, int warps, int warp_in_group) {
   Twofold s = warp_sum_twofold(v);
   if (warps == 1) return s;
   if ((threadIdx.x & 31) == 0) slot[warp_in_group] = s;
@@ -77,18 +77,20 @@ struct FwdParams {
 // One row per group of `group` threads; thread i of the group holds channels
 // 8 B (i + group k) .., k < NV: NV runs of B vectors.
 //
-// An e4m3 number is the 64-bit definition's but for one in 10^7: an error of rstd moves
+// An e4m3 number is the 64-bit definition's but for one in 10^8: an error of rstd moves
 // a whole row against the rounding boundaries (3e-8, half a unit of fp32, changes one
-// element in a million), so the sum of squares over the threads and rstd carry what fp32
-// rounds off, the products are rounded once, and that once to odd, so that the rounding
-// to four bits sees the value itself and not a rounded one.  Of the 134 M numbers of
-// 65,536 x 2048 7 to 20 differ from the definition's; 61 to 102 did with each step
-// rounded to nearest.  EXACT: h and w are bf16, so that h w is exact in fp32.
+// element in a million), so the sums of squares and rstd carry what fp32 rounds off, the
+// products are rounded once, and that once to odd, so that the rounding to four bits
+// sees the value itself and not a rounded one.  Of the 134 M numbers of 65,536 x 2048
+// one or none differs from the definition's; 61 to 102 did with each step rounded to
+// nearest, 7 to 20 with plain sums of 32 squares.  EXACT: h and w are bf16, so that h w
+// is exact in fp32.
 //
-// Bound by memory: 65,536 x 2048 with residual to 8 bits (943 MB) takes 135 us, 7.0 TB/s,
-// with 60 % of the issue slots taken; pairs of channels go through one instruction.
-// Rounding to odd by both directed roundings and a choice took 146 us, twofold sums from
-// the first square on 170 us: the issue slots ran out.
+// Bound by memory: 65,536 x 2048 with residual to 8 bits (941 MB) takes 138 us, 6.8 TB/s,
+// with 64 % of the issue slots taken (135 us with plain sums of 32 squares); pairs of
+// channels go through one instruction.  Rounding to odd by both directed roundings and a
+// choice took 10 us more, and exact squares from the first on another 25: the issue
+// slots ran out.
 template <typename TX, typename TR, int NV, int B, bool EXACT>
 __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const FwdParams p) {
   constexpr int kRun = B * kVec, kRunPairs = B * kPairs, kBlockRuns = 128 / kRun;
@@ -144,14 +146,16 @@ __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const
       for (int j = 0; j < kRunPairs; ++j) v[k][j] = 0;
     }
   }
-  float even, odd;
+  F2 off = 0;  // what the sums below round off
 #pragma unroll
   for (int d = kRunPairs / 2; d > 0; d >>= 1) {
 #pragma unroll
-    for (int j = 0; j < d; ++j) sq[j] = add2(sq[j], sq[j + d]);
+    for (int j = 0; j < d; ++j) sq[j] = add2(sq[j], sq[j + d], off);
   }
+  float even, odd, even_lo, odd_lo;
   split(sq[0], even, odd);
-  const Twofold ss = group_sum(even + odd, red + g * warps, warps, i >> 5);
+  split(off, even_lo, odd_lo);
+  const Twofold ss = group_sum(Twofold{even, even_lo} + Twofold{odd, odd_lo}, red + g * warps, warps, i >> 5);
   // mean = ss / Hd + eps, then rstd as hi + lo by one Newton step on rsqrtf()'s value
   Twofold mean{ss.hi * p.inv_hd, 0.0f};
   mean.lo = fmaf(ss.hi, p.inv_hd, -mean.hi) + fmaf(ss.hi, p.inv_hd_lo, ss.lo * p.inv_hd);

@@ -95,6 +95,14 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   return r;
 }
 
+// a + b, and what it rounds off added to `off` (Knuth's two-sum).
+__device__ __forceinline__ F2 add2(F2 a, F2 b, F2& off) {
+  const F2 minus = both(-1.0f);
+  const F2 s = add2(a, b), t = fma2(a, minus, s);
+  off = add2(off, add2(fma2(fma2(t, minus, s), minus, a), fma2(t, minus, b)));
+  return s;
+}
+
 constexpr int kPairs = kVec / 2;
 
 template <typename E>
@@ -117,8 +125,7 @@ __device__ __forceinline__ Raw8 pack_pairs(const F2 (&v)[kPairs]) {
 }
 
 // ------------------------------------------------------------------ sums of twice 24 bits
-// hi + lo, with |lo| at most half a unit of hi: what an addition rounds off is kept
-// (Knuth's two-sum).
+// hi + lo: what an addition rounds off is kept.
 struct Twofold {
   float hi, lo;
 };
@@ -129,13 +136,11 @@ __device__ __forceinline__ Twofold operator+(Twofold a, Twofold b) {
   r.lo = (a.hi - (r.hi - t)) + (b.hi - t) + (a.lo + b.lo);
   return r;
 }
-// Sum over the warp.  The first three steps add 16, 8 and 4 pairs, whose rounding
-// errors average out over the pairs; the last two keep theirs.
-__device__ __forceinline__ Twofold warp_sum_twofold(float v) {
+__device__ __forceinline__ Twofold warp_sum_twofold(Twofold t) {
 #pragma unroll
-  for (int d = 16; d > 2; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  Twofold t = Twofold{v, 0.0f} + Twofold{__shfl_xor_sync(0xffffffffu, v, 2), 0.0f};
-  return t + Twofold{__shfl_xor_sync(0xffffffffu, t.hi, 1), __shfl_xor_sync(0xffffffffu, t.lo, 1)};
+  for (int d = 16; d > 0; d >>= 1)
+    t = t + Twofold{__shfl_xor_sync(0xffffffffu, t.hi, d), __shfl_xor_sync(0xffffffffu, t.lo, d)};
+  return t;
 }
 
 // ------------------------------------------------------------------ e4m3 with a power-of-two scale
