@@ -126,7 +126,9 @@ __device__ __forceinline__ E block_sum(E v, E* sh) {
 // So every thread reads its four tokens once and keeps the unscaled gradients in
 // registers while the counts go round the cluster through distributed shared
 // memory (or, per sequence, through integer atomics in the workspace), and scales
-// and stores them after one cluster barrier.  No second launch, no second reading.
+// and stores them after one cluster barrier.  No second launch, no second reading:
+// 32,768 tokens take 6.5 us, whose bytes (0.9 MB) would take 0.1 us; the rest is the
+// launch, one round of loads, the barrier and the tree of the sums.
 // Beyond that the 16 SMs of a cluster are too few (131,072 tokens in 61 sequences: 25.5
 // us with four such steps a thread), and the two launches further down take over.
 constexpr int kClusterCtas = 16;
@@ -446,6 +448,7 @@ __global__ void __launch_bounds__(kClusterThreads) policy_cluster_kernel(const P
 // their mask.  A sequence's count is the difference of two, without atomics or an
 // array to clear.  The second launch is dispatched while the first still runs and
 // loads its tokens before it waits for it; its last CTA adds up the sums in order.
+// 131,072 tokens in 61 sequences (3.1 MB, 0.5 us): 11.8 us, latency again, of two launches.
 constexpr int kManyThreads = 256;
 constexpr int kMaxBlocks = 1024;
 constexpr int kStep = kManyThreads * kGroup;  // tokens a CTA takes at a time
@@ -695,6 +698,8 @@ constexpr int kPairCtas = 16;
 //          scalar loss is summed through distributed shared memory: one launch.
 //   else   one cluster per pair, whose CTAs share the pair's tokens and exchange
 //          their sums; preference_reduce_kernel adds the pairs' losses.
+// 16 pairs of 2 x 200 tokens take 5.0 us, 128 of 2 x 4096 (21 MB, 3.1 us at the copy's
+// rate) 10.2 us: the second reading comes from L2, the launches' latency is the rest.
 template <bool SOLO>
 __global__ void __launch_bounds__(kPairThreads) preference_kernel(const PreferenceParams p) {
   __shared__ float warp_s[kPairThreads / 32];
