@@ -14,7 +14,9 @@
 //   tokens on M, vocabulary on N = 224: a prompt.  A lane of the accumulator is then
 //     a token and its columns are consecutive logits, which go to the staging buffer
 //     16 bytes at a time (with the vocabulary on M they take a 2-byte store each:
-//     8192 x 2048 x 124,160 takes 1358 us this way and 1443 us that way).
+//     8192 x 2048 x 124,160 takes 1358 us this way and 1443 us that way).  Stored from
+//     the registers straight to the rows, without the staging buffer and TMA, it takes
+//     1540 us with 32 bytes a store and 1720 us with 16, against 1450 us on that box.
 //
 // A CTA has 14 warps: the TMA producer, the MMA issuer (even CTA of the pair),
 // eight epilogue warps and four scale warps.  The scale bytes come from their plain
