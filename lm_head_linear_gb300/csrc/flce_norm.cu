@@ -47,32 +47,37 @@ flce_status launch_fwd(const norm::FwdParams& p, const Shape& s, cudaStream_t st
   return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 2, 2, EXACT>, grid, block, 0, st, p);
 }
 
-// The backward: eight or four vectors per thread, whichever leaves fewer idle (2048
-// channels are one warp); as many groups as fit 384 threads and an SM's shared memory
-// with a stage each, but no more than spread the rows over the SMs; and the stages
-// that then fit.
-constexpr int kBwdSmem = 224 * 1024;
+// The backward: four vectors per thread (two or one where they cover a row), and as many
+// groups as fit 512 threads and an SM's shared memory with a stage each beside the weights,
+// but no more than spread the rows over the SMs; and the stages that then fit.  bf16
+// weights always leave room for a stage: 14 bytes a channel, 16384 channels, 224 KB.  fp32
+// weights next to fp32 rows of dy, h and dh of more than 14336 channels do not.
+constexpr int64_t kBwdSmem = 224 * 1024;
 struct BwdShape {
   int nv, group, threads, stages;
+  bool w_shared;
   size_t smem;
 };
-BwdShape pick_bwd_shape(int64_t T, int64_t Hd, int64_t row_bytes, int sms) {
+BwdShape pick_bwd_shape(int64_t T, int64_t Hd, int64_t row_bytes, bool w_f32, int sms) {
   const int64_t nvec = Hd / kVec;
-  const auto group_of = [&](int nv) { return cdiv(cdiv(nvec, nv), 32) * 32; };
   BwdShape s;
-  s.nv = group_of(4) <= norm::kBwdThreads && 4 * group_of(4) < 8 * group_of(8) ? 4 : 8;
+  s.nv = 4;
   while (s.nv > 1 && (s.nv / 2) * 32 >= nvec) s.nv /= 2;
-  s.group = static_cast<int>(group_of(s.nv));
-  int64_t groups = std::min<int64_t>(norm::kBwdThreads / s.group, kBwdSmem / row_bytes);
+  s.group = static_cast<int>(cdiv(cdiv(nvec, s.nv), 32) * 32);
+  int64_t w_bytes = Hd * (w_f32 ? 4 : 2);
+  s.w_shared = row_bytes + w_bytes <= kBwdSmem;
+  if (!s.w_shared) w_bytes = 0;
+  const int64_t room = kBwdSmem - w_bytes;
+  int64_t groups = std::min<int64_t>(norm::kBwdThreads / s.group, room / row_bytes);
   groups = std::max<int64_t>(std::min<int64_t>(groups, cdiv(T, sms)), 1);
   s.threads = static_cast<int>(groups) * s.group;
   const int64_t per_stage = groups * row_bytes;
-  s.stages = static_cast<int>(std::max<int64_t>(std::min<int64_t>(kBwdSmem / per_stage, norm::kBwdMaxStages), 1));
-  s.smem = std::max<size_t>(static_cast<size_t>(s.stages) * per_stage, groups > 1 ? sizeof(float) * groups * Hd : 0);
+  s.stages = static_cast<int>(std::min<int64_t>(room / per_stage, norm::kBwdMaxStages));
+  s.smem = std::max<size_t>(s.stages * per_stage + w_bytes, groups > 1 ? sizeof(float) * groups * Hd : 0);
   return s;
 }
 
-template <typename TY, typename TH, int NV>
+template <typename TY, typename TH, int NV, bool W32>
 flce_status launch_bwd(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, cudaStream_t st) {
   static std::mutex mu;
   static bool set[64] = {};
@@ -81,20 +86,25 @@ flce_status launch_bwd(const norm::BwdParams& p, const BwdShape& s, int64_t bloc
   {
     std::lock_guard<std::mutex> lk(mu);
     if (dev >= 0 && dev < 64 && !set[dev]) {
-      CUDA_TRY(cudaFuncSetAttribute(norm::norm_backward_kernel<TY, TH, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kBwdSmem));
+      CUDA_TRY(cudaFuncSetAttribute(norm::norm_backward_kernel<TY, TH, NV, W32>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem));
       set[dev] = true;
     }
   }
-  return launch_overlapped(norm::norm_backward_kernel<TY, TH, NV>, dim3(static_cast<unsigned>(blocks)), s.threads, s.smem,
-                           st, p);
+  return launch_overlapped(norm::norm_backward_kernel<TY, TH, NV, W32>, dim3(static_cast<unsigned>(blocks)),
+                           s.threads, s.smem, st, p);
 }
-template <typename TY, typename TH>
+
+template <typename TY, typename TH, bool W32>
 flce_status launch_bwd_nv(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, cudaStream_t st) {
-  if (s.nv == 1) return launch_bwd<TY, TH, 1>(p, s, blocks, st);
-  if (s.nv == 2) return launch_bwd<TY, TH, 2>(p, s, blocks, st);
-  if (s.nv == 4) return launch_bwd<TY, TH, 4>(p, s, blocks, st);
-  return launch_bwd<TY, TH, 8>(p, s, blocks, st);
+  if (s.nv == 1) return launch_bwd<TY, TH, 1, W32>(p, s, blocks, st);
+  if (s.nv == 2) return launch_bwd<TY, TH, 2, W32>(p, s, blocks, st);
+  return launch_bwd<TY, TH, 4, W32>(p, s, blocks, st);
+}
+
+template <typename TY, typename TH>
+flce_status launch_bwd_types(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, bool w_f32, cudaStream_t st) {
+  return w_f32 ? launch_bwd_nv<TY, TH, true>(p, s, blocks, st) : launch_bwd_nv<TY, TH, false>(p, s, blocks, st);
 }
 
 flce_status check_sizes(int64_t T, int64_t Hd) {
@@ -196,21 +206,22 @@ flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t
   p.dy = dy, p.h = h, p.w = weight, p.rstd = rstd, p.dh = dh, p.dx = dx;
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
   p.lddy = lddy, p.ldh = ldh, p.lddh = lddh, p.T = T, p.Hd = static_cast<int32_t>(Hd);
-  p.w_f32 = weight_dtype == FLCE_DTYPE_F32, p.inv_hd = 1.0f / static_cast<float>(Hd);
+  p.inv_hd = 1.0f / static_cast<float>(Hd);
   p.status = static_cast<int32_t*>(workspace);
   p.timeout_ns = wait_limit_ns(0);
-  const BwdShape s = pick_bwd_shape(T, Hd, Hd * (size_of(dy_dtype) + (dh ? 2 : 1) * size_of(h_dtype)), sms);
-  p.group = s.group, p.stages = s.stages;
+  const BwdShape s = pick_bwd_shape(T, Hd, Hd * (size_of(dy_dtype) + (dh ? 2 : 1) * size_of(h_dtype)),
+                                    weight_dtype == FLCE_DTYPE_F32, sms);
+  p.group = s.group, p.stages = s.stages, p.w_shared = s.w_shared;
   const int64_t blocks = std::min<int64_t>(std::min<int64_t>(cdiv(T, s.threads / s.group), sms), kMaxNormBlocks);
   const double n = static_cast<double>(T) * Hd;
   {
     KernelScope ks(FLCE_KERNEL_NORM_BWD, cs, 10.0 * n,
                    n * (size_of(dy_dtype) + (dh ? 3.0 : 2.0) * size_of(h_dtype)) + 4.0 * Hd);
-    const bool yf = dy_dtype == FLCE_DTYPE_F32, hf = h_dtype == FLCE_DTYPE_F32;
-    st = yf && hf ? launch_bwd_nv<float, float>(p, s, blocks, cs)
-         : yf     ? launch_bwd_nv<float, uint16_t>(p, s, blocks, cs)
-         : hf     ? launch_bwd_nv<uint16_t, float>(p, s, blocks, cs)
-                  : launch_bwd_nv<uint16_t, uint16_t>(p, s, blocks, cs);
+    const bool yf = dy_dtype == FLCE_DTYPE_F32, hf = h_dtype == FLCE_DTYPE_F32, wf = weight_dtype == FLCE_DTYPE_F32;
+    st = yf && hf ? launch_bwd_types<float, float>(p, s, blocks, wf, cs)
+         : yf     ? launch_bwd_types<float, uint16_t>(p, s, blocks, wf, cs)
+         : hf     ? launch_bwd_types<uint16_t, float>(p, s, blocks, wf, cs)
+                  : launch_bwd_types<uint16_t, uint16_t>(p, s, blocks, wf, cs);
     if (st != FLCE_OK) return st;
     ks.done();
     if ((st = check_launch("norm_bwd")) != FLCE_OK) return st;

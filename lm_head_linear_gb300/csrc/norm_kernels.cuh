@@ -244,12 +244,13 @@ __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const
 // A row is needed twice, before and after its mean, and nothing of the next row
 // depends on it: every group has a ring of shared-memory stages of its own, into
 // which one of its threads copies the rows of dy, h and dh ahead (bulk copies), so
-// loads stay in flight across the reductions.  A group is one warp up to 2048
-// channels, and no group waits for another: with 12 warps an SM's loads and arithmetic
-// overlap even where shared memory has one stage for each.  32,768 x 2048 with dh, 537
-// MB, both launches: 100 us; 8 warps with two stages each 111 us, one ring for the CTA
-// with its barriers 102 us, loads into registers 112 us.
-constexpr int kBwdThreads = 384;
+// loads stay in flight across the reductions.  The weights, which every row needs
+// twice, are in shared memory too: what the stages leave of L1 does not hold them
+// against the stores.  32,768 x 2048 with dh (537 MB), both launches:
+//     16 warps, two to a row, two stages, weights in shared memory    87 us
+//     the same, weights through L1                                   111 us (98 with one stage)
+//     12 warps, one to a row, one stage, weights through L1          102 us
+constexpr int kBwdThreads = 512;
 constexpr int kBwdMaxStages = 8;
 constexpr int kBwdMaxGroups = kBwdThreads / 32;
 constexpr int kStatusTimeout = 7;  // FLCE_ERR_TIMEOUT
@@ -269,7 +270,7 @@ struct BwdParams {
   int32_t Hd;
   int32_t group;
   int32_t stages;
-  int32_t w_f32;
+  int32_t w_shared;   // the weights are kept in shared memory
   float inv_hd;
 };
 
@@ -301,9 +302,10 @@ __device__ __forceinline__ bool group_any(int g, int threads, bool v) {
   return r != 0;
 }
 
-template <typename TY, typename TH, int NV>
+// W32: fp32 weights (bf16 ones always fit beside the stages).
+template <typename TY, typename TH, int NV, bool W32>
 __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdParams p) {
-  // groups x stages x (dy, h, dh rows); afterwards the CTA's dw
+  // groups x stages x (dy, h, dh rows), weights; afterwards the CTA's dw
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[kBwdThreads / 32];
   __shared__ __align__(8) uint64_t full[kBwdMaxGroups * kBwdMaxStages];
@@ -340,6 +342,20 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
   // The status of this call: cleared by the first CTA, dispatched first; a wait that
   // runs out sets it a millisecond later at the earliest.
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
+  const uint32_t w_at = static_cast<uint32_t>(groups * p.stages) * row_bytes;
+  if (p.w_shared) {
+    for (int k = threadIdx.x; k < (W32 ? 2 : 1) * nvec; k += blockDim.x)
+      reinterpret_cast<uint4*>(ring + w_at)[k] = __ldg(static_cast<const uint4*>(p.w) + k);
+    __syncthreads();
+  }
+  const auto weight_pairs = [&](int c, F2 (&v)[kPairs]) {
+    if constexpr (!W32)
+      unpack_pairs<uint16_t>(load8(reinterpret_cast<const uint16_t*>(ring + w_at) + c * kVec), v);
+    else if (p.w_shared)
+      unpack_pairs<float>(load8(reinterpret_cast<const float*>(ring + w_at) + c * kVec), v);
+    else
+      load_weight_pairs(p.w, true, c * kVec, v);
+  };
   if (i == 0)
     for (int k = 0; k < p.stages; ++k) fill(row0 + k * step, k);
 
@@ -374,7 +390,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
         F2 y[kPairs], hv[kPairs], w[kPairs];
         unpack_pairs<TY>(load8(dy + c * kVec), y);
         unpack_pairs<TH>(load8(h + c * kVec), hv);
-        load_weight_pairs(p.w, p.w_f32 != 0, c * kVec, w);
+        weight_pairs(c, w);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           const F2 q = mul2(y[j], hv[j]);
@@ -404,7 +420,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
         F2 y[kPairs], hv[kPairs], w[kPairs], d[kPairs];
         unpack_pairs<TY>(load8(dy + c * kVec), y);
         unpack_pairs<TH>(load8(h + c * kVec), hv);
-        load_weight_pairs(p.w, p.w_f32 != 0, c * kVec, w);
+        weight_pairs(c, w);
         if (p.dh) {
           unpack_pairs<TH>(load8(dh + c * kVec), d);
 #pragma unroll

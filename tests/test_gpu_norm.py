@@ -151,6 +151,26 @@ def test_backward(cuda_device, T, Hd, h_dtype, dy_dtype, with_dh):
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("T,Hd", [(1, 16), (5, 144), (700, 2048), (33, 4112), (160, 14336), (160, 14352), (157, 16384)])
+@pytest.mark.parametrize("h_dtype,dy_dtype", [(F32, F32), (BF, F32), (F32, BF), (BF, BF)])
+def test_backward_with_weights_in_32_bits(cuda_device, T, Hd, h_dtype, dy_dtype):
+    """fp32 weights, which for the widest fp32 rows do not fit beside them on chip."""
+    h, w, _, g = make(T, Hd, h_dtype, None, cuda_device, seed=T + Hd, w_dtype=F32)
+    dy = torch.randn(T, Hd, generator=g, device=cuda_device).to(dy_dtype)
+    dh = torch.randn(T, Hd, generator=g, device=cuda_device).to(h_dtype)
+    _, _, rstd, _, _ = flce.flce_add_rms_norm(h, w, save_rstd=True)
+    dx, dw, ws = flce.flce_add_rms_norm_backward(dy, h, w, rstd, dh=dh)
+    assert flce.flce_read_device_status(ws) == 0
+    h64, dy64 = h.double(), dy.double()
+    r = 1 / torch.sqrt((h64 * h64).mean(1, keepdim=True) + EPS)
+    u = dy64 * w.double()
+    want = r * (u - h64 * r ** 2 * (u * h64).mean(1, keepdim=True)) + dh.double()
+    size = r * (u.abs() + h64.abs() * r ** 2 * (u * h64).abs().mean(1, keepdim=True)) + dh.double().abs()
+    assert bool(((dx.double() - want).abs() <= 1e-5 * size + (half_step_bf16(want) * (1 + 1e-9) if h_dtype == BF else 0)).all())
+    terms = dy64 * h64 * r
+    assert bool(((dw.double() - terms.sum(0)).abs() <= 2e-5 * terms.abs().sum(0)).all())
+
+
 def test_gradient_against_differences(cuda_device):
     """Directional derivatives of sum(y dy) + sum(h dh) by central differences in 64 bits."""
     T, Hd = 6, 96
