@@ -6,14 +6,15 @@
 // Bound: bytes (28 and 20 per token, a few operations each), and below about a
 // million tokens latency: launches and the reduction's steps.
 //
-// Sums: fp32 over the few tokens of one thread, 64 bits across threads and
-// blocks, in a fixed order.
+// Sums: fp32 over the few tokens of one warp (with what it rounds off, where log
+// ratios cancel), 64 bits across warps and blocks, in a fixed order.
 #pragma once
 
 #include <cstdint>
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"
+#include "vec8.cuh"
 
 namespace flce {
 namespace loss {
@@ -691,6 +692,9 @@ constexpr int kSideWarps = kSide / 32;
 constexpr int kKept = 8;             // steps whose mask bits a thread keeps for the second pass
 constexpr int kPairCtas = 16;
 
+// Log ratios cancel in the sums, so these keep what fp32 additions round off, within
+// a thread and a warp, and are 64 bits wide from there on.
+//
 // Both answers of a pair at once, one per half of the CTA.  One reading gives the
 // sums; the gradient is one number per sequence, so the second pass only stores
 // (the mask bits of the first 8 x 1024 tokens stay in a register).
@@ -702,7 +706,7 @@ constexpr int kPairCtas = 16;
 // rate) 10.2 us: the second reading comes from L2, the launches' latency is the rest.
 template <bool SOLO>
 __global__ void __launch_bounds__(kPairThreads) preference_kernel(const PreferenceParams p) {
-  __shared__ float warp_s[kPairThreads / 32];
+  __shared__ double warp_s[kPairThreads / 32];
   __shared__ int warp_n[kPairThreads / 32];
   __shared__ double cta_s[2][kPairCtas];  // by CTA of the cluster: sums of the two answers; SOLO: [0] the losses
   __shared__ int cta_n[2][kPairCtas];     // counts; SOLO: [0] malformed pairs
@@ -731,7 +735,7 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const Preferen
     const int64_t lo = side ? at[1] : at[0], hi = side ? at[2] : at[1];
     const int64_t g0 = lo & ~int64_t(kGroup - 1);
     const int64_t stride = static_cast<int64_t>(kGroup) * kSide * share;
-    float sum = 0.0f;
+    Twofold sum{0.0f, 0.0f};
     int n = 0, step = 0;
     uint32_t kept = 0;
     for (int64_t t = g0 + static_cast<int64_t>(kGroup) * (part * kSide + i); t < hi; t += stride, ++step) {
@@ -744,18 +748,24 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const Preferen
 #pragma unroll
       for (int j = 0; j < kGroup; ++j) {
         if (t + j < lo || t + j >= hi) m &= ~(1u << j);
-        if (m >> j & 1u) sum += lane4(lp, j) - lane4(ref, j);
+        if (m >> j & 1u) {  // the sum, and what it rounds off
+          const float d = lane4(lp, j) - lane4(ref, j), s = sum.hi + d, b = s - sum.hi;
+          sum.lo += (sum.hi - (s - b)) + (d - b);
+          sum.hi = s;
+        }
       }
       n += __popc(m);
       if (step < kKept) kept |= m << (4 * step);
     }
-    const float ws = warp_total(sum);
+    const Twofold all = warp_sum_twofold(sum);
+    // (the low part of an infinite sum is NaN)
+    const double ws = isfinite(all.hi) ? static_cast<double>(all.hi) + static_cast<double>(all.lo) : all.hi;
     const int wn = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) warp_s[warp] = ws, warp_n[warp] = wn;
     __syncthreads();
     if (warp == 0) {
       // lanes 0 .. 7: the chosen answer's warps, 8 .. 15 the rejected one's
-      double S = lane < 2 * kSideWarps ? static_cast<double>(warp_s[lane]) : 0.0;
+      double S = lane < 2 * kSideWarps ? warp_s[lane] : 0.0;
       int c = lane < 2 * kSideWarps ? warp_n[lane] : 0;
 #pragma unroll
       for (int d = kSideWarps / 2; d > 0; d >>= 1) {

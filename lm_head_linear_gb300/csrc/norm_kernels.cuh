@@ -246,10 +246,11 @@ __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const
 // which one of its threads copies the rows of dy, h and dh ahead (bulk copies), so
 // loads stay in flight across the reductions.  The weights, which every row needs
 // twice, are in shared memory too: what the stages leave of L1 does not hold them
-// against the stores.  32,768 x 2048 with dh (537 MB), both launches:
-//     16 warps, two to a row, two stages, weights in shared memory    87 us
-//     the same, weights through L1                                   111 us (98 with one stage)
-//     12 warps, one to a row, one stage, weights through L1          102 us
+// against the stores.  32,768 x 2048 with dh (537 MB): 87 us, both launches.  After the
+// forward that wrote its inputs, the two together:
+//     16 warps, two to a row, two stages, weights in shared memory   166 us
+//     the same, weights through L1                                   181 us (169 with one stage)
+//     12 warps, one to a row, one stage, weights through L1          172 us
 constexpr int kBwdThreads = 512;
 constexpr int kBwdMaxStages = 8;
 constexpr int kBwdMaxGroups = kBwdThreads / 32;
