@@ -126,28 +126,32 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   std::memset(&p, 0, sizeof(p));
   const int64_t es = y_dtype == FLCE_DTYPE_F32 ? 4 : 2;
   p.y_tma = !off16(y) && (ldy * es) % 16 == 0;
-  // Vocabulary on M: token tiles of equal width, as few as hold T, rounded up to 32.
-  const int64_t tiles = cdiv(T, fp8::kMaxN);
-  int64_t n = cdiv(cdiv(T, tiles), 32) * 32, n_tiles = cdiv(T, n), m_tiles = cdiv(V, 2 * fp8::kRowsCta);
-  // Tokens on M where more than one token tile is needed anyway and rounding T up to
-  // 256 does not cost more than its cheaper epilogue gains.
+  if ((st = resident_pairs<true>(dev, sms, &pairs)) != FLCE_OK || (st = resident_pairs<false>(dev, sms, &pairs)) != FLCE_OK)
+    return st;
+  // One token tile: the vocabulary on M.  More: the side and the width of the tiles that
+  // take the fewest rounds times what a round costs, which is about its operands' rows (128 and
+  // N of each CTA), and a tenth more with the vocabulary on M for its epilogue.  Large
+  // problems get N = 224; small ones narrower tiles on more of the SM pairs (301 x 1040 x
+  // 4097: 96 tokens, 68 pairs, 9.0 us; 160 tokens, 34 pairs, 9.8 us.  400 x 4096 x 32,000:
+  // tokens on M 44.7 us, vocabulary on M 47.9 us).
   bool tokens_m = false;
-  if (n_tiles > 1) {
-    const int64_t mt = cdiv(T, 2 * fp8::kRowsCta), nt = cdiv(V, fp8::kMaxN);
-    const double padded = static_cast<double>(mt * 2 * fp8::kRowsCta) * static_cast<double>(nt * fp8::kMaxN);
-    if (padded <= 1.1 * static_cast<double>(n * n_tiles) * static_cast<double>(m_tiles * 2 * fp8::kRowsCta)) {
-      tokens_m = true;
-      n = fp8::kMaxN, n_tiles = nt, m_tiles = mt;
+  int64_t n = cdiv(T, 32) * 32, n_tiles = 1, m_tiles = cdiv(V, 2 * fp8::kRowsCta);
+  double least = 0.0;
+  for (int side = 0; side < 2 && T > fp8::kMaxN; ++side) {
+    const int64_t mt = cdiv(side ? T : V, 2 * fp8::kRowsCta);
+    for (int64_t w = fp8::kMaxN; w >= 32; w -= 32) {
+      const int64_t nt = cdiv(side ? V : T, w);
+      const double cost = static_cast<double>(cdiv(mt * nt, pairs)) * static_cast<double>(128 + w) * (side ? 1.0 : 1.1);
+      if (least == 0.0 || cost < least) least = cost, tokens_m = side, n = w, n_tiles = nt, m_tiles = mt;
     }
   }
-  if ((st = tokens_m ? resident_pairs<true>(dev, sms, &pairs) : resident_pairs<false>(dev, sms, &pairs)) != FLCE_OK)
-    return st;
   const int64_t units = m_tiles * n_tiles;
   if (units >= (int64_t(1) << 31) - 1024) return fail(FLCE_ERR_INVALID_ARG, "T x V is too large");
   p.n = static_cast<int32_t>(n), p.n_tiles = static_cast<int32_t>(n_tiles), p.m_tiles = static_cast<int32_t>(m_tiles);
   p.units = static_cast<int32_t>(units);
   p.stage_bytes = fp8::kABytes + p.n / 2 * fp8::kBlockK;
-  p.stages = std::min((fp8::kSmemLimit - 1024 - fp8::kStagingBytes - fp8::kSmemTail) / p.stage_bytes, fp8::kMaxStages);
+  p.staging_bytes = tokens_m && es == 2 && !p.y_tma ? fp8::kImageBytes : fp8::kStagingBytes;
+  p.stages = std::min((fp8::kSmemLimit - 1024 - p.staging_bytes - fp8::kSmemTail) / p.stage_bytes, fp8::kMaxStages);
   const bool granules = !tokens_m && n_tiles == 1;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   if ((st = matrix_map(tokens_m ? &p.tmB : &p.tmA, u8, CU_TENSOR_MAP_SWIZZLE_128B, W, K, V, K, fp8::kBlockK,
@@ -168,7 +172,7 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   p.y_f32 = y_dtype == FLCE_DTYPE_F32;
   const int64_t shares = granules ? cdiv(V, fp8::kGranule) : units;  // a pair takes at least one
   const int grid = 2 * static_cast<int>(std::min<int64_t>(pairs, shares));
-  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + fp8::kStagingBytes + fp8::kSmemTail;
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + p.staging_bytes + fp8::kSmemTail;
   KernelScope ks(FLCE_KERNEL_LINEAR_FP8, s, 2.0 * T * K * V,
                  1.0 * T * K + 1.0 * V * K + (p.y_f32 ? 4.0 : 2.0) * T * V);
   st = launch_overlapped(tokens_m ? fp8::linear_fp8_kernel<true> : fp8::linear_fp8_kernel<false>, dim3(grid),

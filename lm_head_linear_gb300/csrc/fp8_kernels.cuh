@@ -11,12 +11,13 @@
 // Two orientations of the 256 x N tile of an SM pair (128 rows of the M side per CTA):
 //   vocabulary on M, tokens on N (N = 32 .. 224): a decoding step of a few tokens
 //     runs narrow tiles over wide W tiles and is bound by reading W;
-//   tokens on M, vocabulary on N = 224: a prompt.  A lane of the accumulator is then
+//   tokens on M, vocabulary on N: a prompt.  A lane of the accumulator is then
 //     a token and its columns are consecutive logits, which go to the staging buffer
 //     16 bytes at a time (with the vocabulary on M they take a 2-byte store each:
 //     8192 x 2048 x 124,160 takes 1358 us this way and 1443 us that way).  Stored from
 //     the registers straight to the rows, without the staging buffer and TMA, it takes
 //     1540 us with 32 bytes a store and 1720 us with 16, against 1450 us on that box.
+//     N falls below 224 where the tiles would not fill the device (flce_fp8.cu).
 //
 // A CTA has 14 warps: the TMA producer, the MMA issuer (even CTA of the pair),
 // eight epilogue warps and four scale warps.  The scale bytes come from their plain
@@ -59,6 +60,12 @@ constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
 constexpr uint32_t kTmemCols = 512;
 constexpr int kStagingWarp = 32 * 32 * 4;  // of an epilogue warp: two 32 x 32 boxes of bf16 or one of fp32
 constexpr int kStagingBytes = kEpiWarps * kStagingWarp;
+// Whole rows of a bf16 tile (see store_images): a row's bytes and what it lies off 16, an
+// odd number of 16-byte pieces, and a skew of one piece every eight rows.
+constexpr int kImagePitch = kMaxN * 2 + 16;
+constexpr int kImageWarp = 32 * kImagePitch + 64;  // 32 rows
+constexpr int kImageBytes = 4 * kImageWarp;
+static_assert(kImagePitch % 32 == 16, "image pitch");
 constexpr int kSmemTail = 512;
 constexpr int kSmemLimit = 232448;
 constexpr int kStatusTimeout = 7;
@@ -80,7 +87,7 @@ struct Params {
   int32_t kb;        // K blocks
   int32_t n;         // N (a multiple of 32 up to kMaxN)
   int32_t n_tiles, m_tiles, units;
-  int32_t stages, stage_bytes;
+  int32_t stages, stage_bytes, staging_bytes;
   int32_t y_f32;
   int32_t y_tma;     // y's rows start on 16-byte boundaries: boxes leave by TMA, else row by row
 };
@@ -434,7 +441,8 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
 // v0 .. v0 + 31, clipped at T and V.  fp32: a token a step.  bf16: two tokens a step, a
 // half warp each, in 32-bit words.  A half warp's rows are an even number of rows
 // apart, so all of them start on an even element or all on an odd one; in the odd
-// case the words are made of two staged ones, and the first and last logit go alone.
+// case the words are made of two staged ones.  The first or last logit that is left
+// over goes alone, for all 32 tokens at once.
 template <typename E>
 __device__ __forceinline__ void store_rows(const Params& p, uint32_t buf, int t0, int v0, int lane) {
   const int tokens = p.T - t0, logits = min(32, p.V - v0);
@@ -463,12 +471,6 @@ __device__ __forceinline__ void store_rows(const Params& p, uint32_t buf, int t0
         hi[i] = ld_shared_u32(buf + (2 * i + half) * 64 + (((next >> 2) ^ (i & 3)) << 4) + (next & 3) * 4);
         hi[i] = odd ? __funnelshift_r(lo[i], hi[i], 16) : lo[i];
       }
-      if (odd && w == 0) {
-        uint16_t* y0 = y;
-#pragma unroll
-        for (int i = 0; i < 16; ++i, y0 += 2 * p.ldy)
-          if (2 * i + half < tokens) *y0 = static_cast<uint16_t>(lo[i]);
-      }
 #pragma unroll
       for (int i = 0; i < 16; ++i) lo[i] = hi[i];
     }
@@ -477,12 +479,123 @@ __device__ __forceinline__ void store_rows(const Params& p, uint32_t buf, int t0
 #pragma unroll
       for (int i = 0; i < 16; ++i, y += 2 * p.ldy)
         if (2 * i + half < tokens) *reinterpret_cast<uint32_t*>(y) = lo[i];
-    } else if (e + 1 == logits) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i, y += 2 * p.ldy)
-        if (2 * i + half < tokens) *y = static_cast<uint16_t>(lo[i]);
+    }
+    // the logits without a partner, a row per lane: the first where it starts odd, the last
+    if (lane < tokens) {
+      uint16_t* row = static_cast<uint16_t*>(p.y) + static_cast<int64_t>(t0 + lane) * p.ldy + v0;
+      const int alone = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1) & 1;
+      const auto element = [&](int k) {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(staged<E>(buf, lane, k >> 3) + (k & 7) * 2) : "memory");
+        return v;
+      };
+      if (alone) row[0] = element(0);
+      if (((logits - alone) & 1) && logits > alone) row[logits - 1] = element(logits - 1);
     }
   }
+}
+
+// bf16, tokens on M, rows of y off 16 bytes (an odd vocabulary).  The two warps of a
+// quarter put its 32 rows into shared memory whole, each as it lies in memory (its first
+// byte d bytes into a 16-byte piece); then one warp has the copy engine store every row's
+// whole pieces, and the other stores the up to 14 bytes before and behind them.  4189 x
+// 224 x 226,081 takes 574 us, 2048 x 1024 x 50,257 90 us; with store_rows(), whose 64
+// bytes of a row are three sectors, two of them partial, and 18 stores a box, 1177 and 119.
+__device__ __forceinline__ uint32_t image_row(uint32_t image, int lane) { return image + lane * kImagePitch + (lane >> 3) * 16; }
+__device__ __forceinline__ uint32_t image_offset(const Params& p, int token, int logit) {
+  return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p.y)) +
+          2u * (static_cast<uint32_t>(token) * static_cast<uint32_t>(p.ldy) + static_cast<uint32_t>(logit))) & 15u;
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(v)) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// Columns c .. c + 31 of this lane's row, into its image that starts d bytes after `row`.
+__device__ __forceinline__ void stage_image(uint32_t row, uint32_t d, int c, const uint32_t (&r)[32]) {
+  uint32_t h[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) h[k] = ptx::pack_bf16x2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+  const bool odd = (d & 2u) != 0;  // words of columns 1 and 2, 3 and 4, ..
+  const uint32_t at = row + d + 2 * c;
+  const uint32_t words = at + (d & 2u);
+#pragma unroll
+  for (int k = 0; k < 15; ++k) st_shared_u32(words + 4 * k, odd ? __funnelshift_r(h[k], h[k + 1], 16) : h[k]);
+  if (odd) {
+    st_shared_u16(at, h[0]);
+    st_shared_u16(at + 62, h[15] >> 16);
+  } else {
+    st_shared_u32(words + 60, h[15]);
+  }
+}
+
+// The whole pieces of this lane's row (`bytes` long), `to` its first byte in memory less d.
+__device__ __forceinline__ void store_pieces(uint32_t row, uint32_t d, uint32_t bytes, uint8_t* to) {
+  const uint32_t begin = d ? 16u : 0u, end = (d + bytes) & ~15u;
+  if (end > begin)
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to + begin), "r"(row + begin),
+                 "r"(end - begin)
+                 : "memory");
+}
+// And what lies around them, in words and one element at each end.
+__device__ __forceinline__ void store_ends(uint32_t row, uint32_t d, uint32_t bytes, uint8_t* to) {
+  const uint32_t te = d + bytes, tail = max(te & ~15u, d ? 16u : 0u);
+  if (d & 2u) *reinterpret_cast<uint16_t*>(to + d) = static_cast<uint16_t>(ld_shared_u16(row + d));
+  if (te & 2u) *reinterpret_cast<uint16_t*>(to + te - 2) = static_cast<uint16_t>(ld_shared_u16(row + te - 2));
+#pragma unroll
+  for (uint32_t k = 4; k < 16; k += 4)
+    if (d && k >= d && k + 4 <= te) *reinterpret_cast<uint32_t*>(to + k) = ld_shared_u32(row + k);
+#pragma unroll
+  for (uint32_t k = 0; k < 12; k += 4)
+    if (tail + k + 4 <= te) *reinterpret_cast<uint32_t*>(to + tail + k) = ld_shared_u32(row + tail + k);
+}
+
+// Both warps of a quarter of the lanes: a barrier, and whether any thread passed true.
+__device__ __forceinline__ bool quarter_any(int q, bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %2, 0;\n\t"
+      "bar.red.or.pred b, %1, 64, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(1 + q), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+
+// A tile's rows through images, for store_images' two warps.
+__device__ __forceinline__ void store_images(const Params& p, uint32_t image, const Unit& un, uint32_t col, int q, int part,
+                                             int lane) {
+  const int m0 = un.row + q * 32, token = m0 + lane;
+  const uint32_t d = image_offset(p, token, un.n0), row = image_row(image, lane);
+  const int logits = min(p.n, p.V - un.n0);
+  if (part == 0) ptx::bulk_wait_read<0>();  // this lane's copy of the tile before
+  quarter_any(q, false);                    // every row's, and its ends
+#pragma unroll 1
+  for (int c = 32 * part; c < logits; c += 64) {
+    uint32_t r[32];
+    ptx::tmem_ld32(col + c, r);
+    ptx::tmem_wait_ld32(r);
+    stage_image(row, d, c, r);
+  }
+  ptx::fence_proxy_async_smem();
+  quarter_any(q, false);
+  if (token < p.T) {
+    uint8_t* to = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.y) + static_cast<int64_t>(token) * p.ldy + un.n0) - d;
+    if (part == 0) store_pieces(row, d, 2u * static_cast<uint32_t>(logits), to);
+    else store_ends(row, d, 2u * static_cast<uint32_t>(logits), to);
+  }
+  if (part == 0) ptx::bulk_commit();
+  __syncwarp();
 }
 
 // A warp's 32 lanes x 32 columns at a time.
@@ -491,11 +604,15 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
                                          int warp, int lane) {
   const int q = warp & 3, part = (warp - 2) >> 2;
   const uint32_t staging = ptx::smem_u32(s.staging) + (warp - 2) * kStagingWarp;
+  constexpr bool kMayImage = TOKENS_M && sizeof(E) == 2;
+  const bool images = kMayImage && !p.y_tma;
   Slot acc;
   uint32_t box = 0;
   for (int u = w.first; u < w.count; u += w.step) {
     const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
-    if (!ptx::wait_bounded_cluster(s.acc_full(acc.i), acc.phase, p.timeout_ns, s.abort_flag)) {
+    bool ok = ptx::wait_bounded_cluster(s.acc_full(acc.i), acc.phase, p.timeout_ns, s.abort_flag);
+    if (images) ok = !quarter_any(q, !ok);  // its two warps meet at barriers: both go on, or neither
+    if (!ok) {
       give_up(p, s);
       break;
     }
@@ -504,7 +621,9 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
     const uint32_t col = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.i * kMaxN;
     const int m0 = un.row + q * 32;
     const int m_end = TOKENS_M ? p.T : p.V, n_end = TOKENS_M ? p.V : p.T;
-    if (q < un.boxes && m0 < m_end) {
+    if (images) {
+      if (m0 < m_end) store_images(p, ptx::smem_u32(s.staging) + q * kImageWarp, un, col, q, part, lane);
+    } else if (q < un.boxes && m0 < m_end) {
 #pragma unroll 1
       for (int c = 32 * part; c < p.n && un.n0 + c < n_end; c += 64) {
         uint32_t r[32];
@@ -526,7 +645,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
             ptx::tma_store_2d(&p.tmY, buf, TOKENS_M ? n0 : m0, TOKENS_M ? m0 : n0);
             ptx::bulk_commit();
           }
-        } else {
+        } else if constexpr (!kMayImage) {
           __syncwarp();
           store_rows<E>(p, buf, TOKENS_M ? m0 : n0, TOKENS_M ? n0 : m0, lane);
         }
@@ -538,7 +657,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
     if (lane == 0) arrive_even(s.acc_empty(acc.i));
     acc.next(2);
   }
-  if (lane == 0) ptx::bulk_wait<0>();  // shared memory stays until the stores have read it
+  if (lane == 0 || images) ptx::bulk_wait<0>();  // shared memory stays until the stores have read it
   __syncwarp();
 }
 
@@ -549,7 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Smem s;
   s.stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   s.staging = s.stages + p.stages * p.stage_bytes;
-  uint8_t* tail = s.staging + kStagingBytes;
+  uint8_t* tail = s.staging + p.staging_bytes;
   s.bars = reinterpret_cast<uint64_t*>(tail);
   s.tmem_slot = reinterpret_cast<uint32_t*>(tail + kBars * 8);
   s.abort_flag = reinterpret_cast<volatile int*>(tail + kBars * 8 + 4);

@@ -162,3 +162,20 @@ def test_refusals(cuda_device):
     with pytest.raises(flce.FlceError) as e:
         flce.flce_quantize_fp8(torch.zeros(4, 32, device=cuda_device), block_rows=64)
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("T,K,V", [(225, 128, 33), (256, 16, 447), (300, 144, 4097), (513, 272, 1111), (260, 128, 17),
+                                   (700, 640, 9001), (2048, 128, 2003)])
+@pytest.mark.parametrize("offset,pad", [(0, 0), (1, 0), (2, 1), (3, 2), (5, 4), (6, 7), (7, 9), (8, 3), (0, 6)])
+def test_rows_of_any_alignment(cuda_device, T, K, V, offset, pad):
+    """bf16 rows that start `offset` elements into a buffer and lie V + pad apart: exact values, and nothing
+    written before, between or behind the rows."""
+    x, sx, W, sw = whole(T, K, V, cuda_device, seed=T + V + offset)
+    want = (value(x, sx, 1) @ value(W, sw, 128).t()).float().to(BF)
+    buf = torch.full((T * (V + pad) + 64,), 7.0, dtype=BF, device=cuda_device)
+    y = torch.as_strided(buf, (T, V), (V + pad, 1), 16 + offset)
+    out, ws = flce.flce_linear_fp8(x, sx, W, sw, out={"y": y})
+    assert flce.flce_read_device_status(ws) == 0
+    assert torch.equal(y, want)
+    y.fill_(7.0)
+    assert bool((buf == 7.0).all())
