@@ -26,8 +26,8 @@
 // 224, not 256, tokens per tile: two accumulators (448 columns) and four stages
 // of scales (64 columns) fill the 512 columns of TMEM.
 //
-// Bound: few tokens by reading W (1 x 2048 x 124,160: 43.2 us for 254 MB, of which a
-// kernel that only reads takes 37.1; 93 x 4096 x 248,320: 159 us, 6.7 TB/s); a prompt by
+// Bound: few tokens by reading W (1 x 2048 x 124,160: 43 us for 254 MB, of which a
+// kernel that only reads takes 37.1; 93 x 4096 x 248,320: 157 to 160 us, 6.7 TB/s); a prompt by
 // shared memory and the clock.  A K block of a 256 x 224 tile keeps the tensor pipe busy
 // for 448 cycles, shared memory for about 480 (operands in by TMA, out to the MMA) and
 // for 56 more of the epilogue's transposes; it measures 535 cycles at K = 2048 and 503 at

@@ -702,8 +702,8 @@ constexpr int kPairCtas = 16;
 //          scalar loss is summed through distributed shared memory: one launch.
 //   else   one cluster per pair, whose CTAs share the pair's tokens and exchange
 //          their sums; preference_reduce_kernel adds the pairs' losses.
-// 16 pairs of 2 x 200 tokens take 5.0 us, 128 of 2 x 4096 (21 MB, 3.1 us at the copy's
-// rate) 10.2 us: the second reading comes from L2, the launches' latency is the rest.
+// 16 pairs of 2 x 200 tokens take 5.2 us, 128 of 2 x 4096 (21 MB, 3.1 us at the copy's
+// rate) 10.4 us: the second reading comes from L2, the launches' latency is the rest.
 template <bool SOLO>
 __global__ void __launch_bounds__(kPairThreads) preference_kernel(const PreferenceParams p) {
   __shared__ double warp_s[kPairThreads / 32];
