@@ -1,0 +1,36 @@
+"""Edges of the operators around the head: long runs of empty sequences."""
+
+import pytest
+import torch
+
+import lm_head_linear_gb300 as flce
+
+from test_gpu_losses import check_policy, draw
+
+pytestmark = pytest.mark.gpu
+
+
+def milliseconds(f):
+    f()
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    f()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b)
+
+
+@pytest.mark.parametrize("T", [4000, 50000])
+def test_policy_across_many_empty_sequences(cuda_device, T):
+    """300,000 empty sequences between two tokens of one thread: the same values, and no thread
+    walks past them one by one (at 0.4 us each that took 120 ms)."""
+    logp, old, ref, adv, y, g = draw(T, cuda_device, seed=11)
+    n = 300_000
+    cu = torch.cat([torch.tensor([0, 1, 1, 7], device=cuda_device), torch.full((n,), 2002, device=cuda_device),
+                    torch.tensor([2003, 2003, 3001, T], device=cuda_device)])
+    advs = torch.randn(cu.numel() - 1, generator=g, device=cuda_device)
+    for red in ("sequence_mean", "mean"):
+        kw = dict(reduction=red, kl_coef=0.05, kl="k2")
+        check_policy((logp, old, ref, advs, y), dict(kw, cu=cu, per_sequence=True), cu_seqlens=cu, per_sequence=True, **kw)
+        call = lambda: flce.flce_policy_loss(logp, old, advs, y, ref_logp=ref, cu_seqlens=cu, per_sequence=True, **kw)
+        assert milliseconds(call) < 10.0
