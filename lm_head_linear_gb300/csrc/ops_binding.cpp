@@ -8,7 +8,9 @@
 // module is linked against it and adds no computation.
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Device.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -165,8 +167,20 @@ Tensor workspace_of(PyObject* o, size_t bytes, const Tensor& like) {
   return t;
 }
 
+// The library works on the current device: every entry point makes that the tensors'
+// (an OnDevice on its stack) before it allocates or calls, and takes no stream of another.
+using OnDevice = c10::cuda::CUDAGuard;
+
 void* stream_of(PyObject* o, const Tensor& like) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream(like.device().index()).stream();
+  if (PyObject* d = PyObject_GetAttrString(o, "device")) {
+    const bool known = THPDevice_Check(d);
+    const at::Device dev = known ? reinterpret_cast<THPDevice*>(d)->device : like.device();
+    Py_DECREF(d);
+    if (dev != like.device()) bad("the stream is on %s, the tensors are on %s", dev.str().c_str(), like.device().str().c_str());
+  } else {
+    PyErr_Clear();  // a handle alone
+  }
   PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
   if (!h) throw Raised{};
   void* s = PyLong_AsVoidPtr(h);
@@ -225,6 +239,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* r = optional_tensor(a[2], "residual");
     matrix(x, "x");
     const at::Device dev = x.device();
+    const OnDevice on(dev);
     const int64_t T = x.size(0), Hd = x.size(1);
     const int32_t x_type = dtype_of(x, "x");
     const int64_t ldx = rows_of(x, "x", T, Hd, dev);
@@ -262,6 +277,7 @@ PyObject* add_rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* dh = optional_tensor(a[4], "dh");
     matrix(h, "h");
     const at::Device dev = h.device();
+    const OnDevice on(dev);
     const int64_t T = h.size(0), Hd = h.size(1);
     const int32_t h_type = dtype_of(h, "h"), y_type = dtype_of(dy, "dy");
     const int64_t ldh = rows_of(h, "h", T, Hd, dev), lddy = rows_of(dy, "dy", T, Hd, dev);
@@ -288,6 +304,7 @@ PyObject* quantize_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     arguments(n, 4);
     const Tensor& m = tensor(a[0], "a");
     matrix(m, "a");
+    const OnDevice on(m.device());
     const int64_t rows = m.size(0), K = m.size(1), block = integer(a[1]);
     const int32_t type = dtype_of(m, "a");
     const int64_t ld = rows_of(m, "a", rows, K, m.device());
@@ -320,6 +337,7 @@ PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& Ws = tensor(a[3], "W_scale");
     matrix(x, "x");
     matrix(W, "W");
+    const OnDevice on(x.device());
     const int64_t T = x.size(0), K = x.size(1), V = W.size(0);
     if (W.size(1) != K) bad("x [T, K] and W [V, K] must have equal K");
     blocks(x, xs, "x", 1, x.device());
@@ -363,6 +381,7 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor* ref = optional_tensor(a[4], "ref_logp");
     const Tensor* cu = optional_tensor(a[5], "cu_seqlens");
     const at::Device dev = logp.device();
+    const OnDevice on(dev);
     const int64_t T = logp.size(0);
     const bool per_seq = truth(a[6]);
     int64_t S = 0;
@@ -405,6 +424,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& cu = tensor(a[2], "cu_seqlens");
     const Tensor* ref = optional_tensor(a[3], "ref_logp");
     const at::Device dev = logp.device();
+    const OnDevice on(dev);
     const int64_t T = logp.size(0);
     if (cu.dim() != 1 || cu.size(0) % 2 == 0) bad("cu_seqlens must be a tensor [2 n_pairs + 1], got %s", text_of(cu).c_str());
     const int64_t P = cu.size(0) / 2;

@@ -1,4 +1,4 @@
-"""Edges of the operators around the head: long runs of empty sequences."""
+"""Edges of the operators around the head: long runs of empty sequences, streams of other devices."""
 
 import pytest
 import torch
@@ -34,3 +34,28 @@ def test_policy_across_many_empty_sequences(cuda_device, T):
         check_policy((logp, old, ref, advs, y), dict(kw, cu=cu, per_sequence=True), cu_seqlens=cu, per_sequence=True, **kw)
         call = lambda: flce.flce_policy_loss(logp, old, advs, y, ref_logp=ref, cu_seqlens=cu, per_sequence=True, **kw)
         assert milliseconds(call) < 10.0
+
+
+class OtherDevice:
+    """What a stream of another device looks like (its handle is the current one: nothing can go wrong on it)."""
+    device = torch.device("cuda", 1)
+
+    def __init__(self):
+        self.cuda_stream = torch.cuda.current_stream().cuda_stream
+
+
+def test_a_stream_of_another_device_is_refused(cuda_device):
+    x = torch.randn(4, 128, device=cuda_device)
+    w = torch.ones(128, device=cuda_device)
+    logp, old, _, adv, y, _ = draw(16, cuda_device)
+    cu = torch.tensor([0, 8, 16], device=cuda_device)
+    _, h, rstd, q, qs = flce.flce_add_rms_norm(x, w, fp8=True, save_rstd=True, stream=torch.cuda.current_stream())
+    Wq, Ws = flce.flce_quantize_fp8(x)
+    s = OtherDevice()
+    for call in (lambda: flce.flce_add_rms_norm(x, w, stream=s), lambda: flce.flce_add_rms_norm_backward(x, h, w, rstd, stream=s),
+                 lambda: flce.flce_quantize_fp8(x, stream=s), lambda: flce.flce_linear_fp8(q, qs, Wq, Ws, stream=s),
+                 lambda: flce.flce_policy_loss(logp, old, adv, y, stream=s),
+                 lambda: flce.flce_preference_loss(logp, y, cu, stream=s)):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
+    assert torch.cuda.current_device() == cuda_device.index
