@@ -127,10 +127,23 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream_handle(stream) -> ctypes.c_void_p:
+def _stream_handle(stream, device) -> ctypes.c_void_p:
+    """The handle of ``stream``, which has to be one of ``device``; None: that device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(device)
+    elif getattr(stream, "device", device) != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _call(fn, device, stream, *args):
+    """``fn(*args, stream)`` with ``device`` current: the library works on the current device."""
+    handle = _stream_handle(stream, device)
+    if device.index in (None, torch.cuda.current_device()):
+        _check(fn(*args, handle))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, handle))
 
 
 def _check_inputs(H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor):
@@ -233,9 +246,8 @@ def _forward(entry, size_fn, H, W, targets, ignore_index, reduction, workspace, 
     n_valid = _out(out, "n_valid", 1, torch.int64, dev)
     need = getattr(lib, size_fn)(T, Hd, V)
     ws = _workspace(need, dev, workspace)
-    st = getattr(lib, entry)(_ptr(H), _ptr(W), _ptr(targets), T, Hd, V, int(ignore_index), red, _ptr(loss),
-                             _ptr(lse), _ptr(logp), _ptr(n_valid), _ptr(ws), ws.numel(), _stream_handle(stream))
-    _check(st)
+    _call(getattr(lib, entry), dev, stream, _ptr(H), _ptr(W), _ptr(targets), T, Hd, V, int(ignore_index), red,
+          _ptr(loss), _ptr(lse), _ptr(logp), _ptr(n_valid), _ptr(ws), ws.numel())
     return loss, lse, logp, n_valid, ws
 
 
@@ -269,16 +281,12 @@ def flce_backward(dloss: Optional[torch.Tensor], H: torch.Tensor, W: torch.Tenso
     need = lib.flce_backward_workspace_size(T, Hd, V)
     ws = _workspace(need, dev, workspace)
     if dlogp is None:
-        st = lib.flce_backward(_ptr(dloss), _ptr(H), _ptr(W), _ptr(targets), _ptr(lse), T, Hd, V, int(ignore_index),
-                               red, _ptr(dH), _ptr(dW), _ptr(ws), ws.numel(), _stream_handle(stream))
+        _call(lib.flce_backward, dev, stream, _ptr(dloss), _ptr(H), _ptr(W), _ptr(targets), _ptr(lse), T, Hd, V,
+              int(ignore_index), red, _ptr(dH), _ptr(dW), _ptr(ws), ws.numel())
     else:
-        st = lib.flce_backward_logp(_ptr(dloss), _ptr(dlogp), _ptr(H), _ptr(W), _ptr(targets), _ptr(lse), T, Hd, V,
-                                    int(ignore_index), red, _ptr(dH), _ptr(dW), _ptr(ws), ws.numel(),
-                                    _stream_handle(stream))
-    _check(st)
+        _call(lib.flce_backward_logp, dev, stream, _ptr(dloss), _ptr(dlogp), _ptr(H), _ptr(W), _ptr(targets),
+              _ptr(lse), T, Hd, V, int(ignore_index), red, _ptr(dH), _ptr(dW), _ptr(ws), ws.numel())
     return dH, dW, ws
-
-
 
 
 def flce_score(H: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
@@ -306,8 +314,8 @@ def _score(entry, size_fn, H, W, targets, ignore_index, workspace, stream, out):
     lse = _out(out, "lse", T, torch.float32, dev)
     argmax = _out(out, "argmax", T, torch.int64, dev)
     ws = _workspace(getattr(lib, size_fn)(T, Hd, V), dev, workspace)
-    _check(getattr(lib, entry)(_ptr(H), _ptr(W), _ptr(targets), T, Hd, V, int(ignore_index), _ptr(logp), _ptr(lse),
-                               _ptr(argmax), _ptr(ws), ws.numel(), _stream_handle(stream)))
+    _call(getattr(lib, entry), dev, stream, _ptr(H), _ptr(W), _ptr(targets), T, Hd, V, int(ignore_index), _ptr(logp),
+          _ptr(lse), _ptr(argmax), _ptr(ws), ws.numel())
     return logp, lse, argmax, ws
 
 
@@ -324,9 +332,8 @@ def flce_forward_shard(H: torch.Tensor, W_shard: torch.Tensor, targets: torch.Te
     shard_lse = _out(out, "shard_lse", T, torch.float32, dev)
     shard_zy = _out(out, "shard_zy", T, torch.float32, dev)
     ws = _workspace(lib.flce_forward_workspace_size(T, Hd, Vs), dev, workspace)
-    _check(lib.flce_forward_shard(_ptr(H), _ptr(W_shard), _ptr(targets), T, Hd, Vs, int(vocab_offset), int(V_total),
-                                  int(ignore_index), _ptr(shard_lse), _ptr(shard_zy), _ptr(ws), ws.numel(),
-                                  _stream_handle(stream)))
+    _call(lib.flce_forward_shard, dev, stream, _ptr(H), _ptr(W_shard), _ptr(targets), T, Hd, Vs, int(vocab_offset),
+          int(V_total), int(ignore_index), _ptr(shard_lse), _ptr(shard_zy), _ptr(ws), ws.numel())
     return shard_lse, shard_zy, ws
 
 
@@ -352,9 +359,8 @@ def flce_combine_shards(shard_lse: torch.Tensor, shard_zy: torch.Tensor, targets
     logp = _out(out, "logp", T, torch.float32, dev)
     n_valid = _out(out, "n_valid", 1, torch.int64, dev)
     ws = _workspace(lib.flce_combine_workspace_size(T, n_shards), dev, workspace)
-    _check(lib.flce_combine_shards(_ptr(shard_lse), _ptr(shard_zy), n_shards, _ptr(targets), T, int(V_total),
-                                   int(ignore_index), red, _ptr(loss), _ptr(lse), _ptr(logp), _ptr(n_valid),
-                                   _ptr(ws), ws.numel(), _stream_handle(stream)))
+    _call(lib.flce_combine_shards, dev, stream, _ptr(shard_lse), _ptr(shard_zy), n_shards, _ptr(targets), T,
+          int(V_total), int(ignore_index), red, _ptr(loss), _ptr(lse), _ptr(logp), _ptr(n_valid), _ptr(ws), ws.numel())
     return loss, lse, logp, n_valid, ws
 
 
@@ -377,16 +383,16 @@ def flce_backward_shard(dloss: torch.Tensor, H: torch.Tensor, W_shard: torch.Ten
     dH = _out(out, "dH", (T, Hd), torch.bfloat16, dev)
     dW = _out(out, "dW", (Vs, Hd), torch.float32, dev)
     ws = _workspace(lib.flce_backward_workspace_size(T, Hd, Vs), dev, workspace)
-    _check(lib.flce_backward_shard(_ptr(dloss), _ptr(H), _ptr(W_shard), _ptr(targets), _ptr(lse.contiguous()), T, Hd,
-                                   Vs, int(vocab_offset), int(V_total), int(ignore_index), red, _ptr(dH), _ptr(dW),
-                                   _ptr(ws), ws.numel(), _stream_handle(stream)))
+    _call(lib.flce_backward_shard, dev, stream, _ptr(dloss), _ptr(H), _ptr(W_shard), _ptr(targets),
+          _ptr(lse.contiguous()), T, Hd, Vs, int(vocab_offset), int(V_total), int(ignore_index), red, _ptr(dH), _ptr(dW),
+          _ptr(ws), ws.numel())
     return dH, dW, ws
 
 
 def flce_read_device_status(workspace: torch.Tensor, stream=None) -> int:
     lib = load_library()
     v = ctypes.c_int32(-1)
-    _check(lib.flce_read_device_status(_ptr(workspace), _stream_handle(stream), ctypes.byref(v)))
+    _call(lambda ws, st: lib.flce_read_device_status(ws, st, ctypes.byref(v)), workspace.device, stream, _ptr(workspace))
     return int(v.value)
 
 
@@ -394,7 +400,7 @@ def flce_selftest_wait_timeout(timeout_ns: int, device=None, stream=None) -> int
     """Run the bounded-wait self-test; returns the device status it produced."""
     lib = load_library()
     ws = torch.empty(256, dtype=torch.uint8, device=device or torch.device("cuda"))
-    _check(lib.flce_selftest_wait_timeout(_ptr(ws), int(timeout_ns), _stream_handle(stream)))
+    _call(lib.flce_selftest_wait_timeout, ws.device, stream, _ptr(ws), int(timeout_ns))
     return flce_read_device_status(ws, stream)
 
 
