@@ -305,13 +305,16 @@ PyObject* quantize_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& m = tensor(a[0], "a");
     matrix(m, "a");
     const OnDevice on(m.device());
-    const int64_t rows = m.size(0), K = m.size(1), block = integer(a[1]);
+    const int64_t rows = m.size(0), K = m.size(1);
+    // 0, which the library refuses, for what it does not know: the number of scales that
+    // are allocated and its 32-bit argument have to mean the same
+    const int32_t block = integer(a[1]) == 128 ? 128 : integer(a[1]) == 1 ? 1 : 0;
     const int32_t type = dtype_of(m, "a");
     const int64_t ld = rows_of(m, "a", rows, K, m.device());
     const int64_t per = block < 1 ? 1 : block;
     const Tensor q = output(a[3], "q", {rows, K}, ScalarType::Float8_e4m3fn, m);
     const Tensor qs = output(a[3], "q_scale", {(rows + per - 1) / per, (K + 127) / 128}, ScalarType::Float8_e8m0fnu, m);
-    check(flce_quantize_fp8(ptr(m), type, ld, rows, K, static_cast<int32_t>(block), ptr(q), ptr<uint8_t>(qs),
+    check(flce_quantize_fp8(ptr(m), type, ld, rows, K, block, ptr(q), ptr<uint8_t>(qs),
                             stream_of(a[2], m)));
     return tuple_of(q, qs);
   });

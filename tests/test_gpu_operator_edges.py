@@ -59,3 +59,11 @@ def test_a_stream_of_another_device_is_refused(cuda_device):
         with pytest.raises(ValueError, match="cuda:1"):
             call()
     assert torch.cuda.current_device() == cuda_device.index
+
+
+@pytest.mark.parametrize("block_rows", [2 ** 32 + 128, 2 ** 32 + 1, -2 ** 32 + 128, 0, -1, 127, 2 ** 31])
+def test_quantize_refuses_block_sizes_that_only_look_right_in_32_bits(cuda_device, block_rows):
+    """Taken as 128 they would have the kernel write more scales than were allocated."""
+    with pytest.raises(flce.FlceError) as e:
+        flce.flce_quantize_fp8(torch.randn(512, 128, device=cuda_device), block_rows=block_rows)
+    assert e.value.status == 1
