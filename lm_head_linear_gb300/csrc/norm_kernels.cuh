@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const
   const F2 hi2 = both(hi), lo2 = both(lo), minus = both(-1.0f);
   // Rounding to odd: towards zero, and the last bit set where that cut something off.
   // With lo != 0 every product but 0 is cut (the odd part of hi + lo alone has more than
-  // 24 bits); with lo == 0 the bit stays as it is, and what is exact stays exact.
+  // 24 bits).  With lo == 0, hi is a power of two (or 0 or infinite): what is cut is what
+  // h w rounds off, nothing where that is exact, so what is exact stays exact.
   const uint32_t odd_bit = lo != 0.0f ? 1u : 0u;
   const int nblk = (p.Hd + 127) / 128;
 #pragma unroll
@@ -207,9 +208,17 @@ __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const
 #pragma unroll
         for (int j = 0; j < kRunPairs; ++j) {
           split(fma2_zero(v[k][j], hi2, rest[j]), y[2 * j], y[2 * j + 1]);
+          uint32_t bit[2] = {odd_bit, odd_bit};
+          if constexpr (!EXACT) {
+            if (odd_bit == 0) {  // the same for the whole row
+              float cut[2];
+              split(rest[j], cut[0], cut[1]);
+              bit[0] = cut[0] != 0.0f, bit[1] = cut[1] != 0.0f;
+            }
+          }
 #pragma unroll
           for (int b = 2 * j; b < 2 * j + 2; ++b) {
-            y[b] = __uint_as_float(__float_as_uint(y[b]) | odd_bit);
+            y[b] = __uint_as_float(__float_as_uint(y[b]) | bit[b - 2 * j]);
             amax = fmaxf(amax, fabsf(y[b]));
           }
         }

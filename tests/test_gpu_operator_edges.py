@@ -6,6 +6,7 @@ import torch
 import lm_head_linear_gb300 as flce
 
 from test_gpu_losses import check_policy, draw
+from test_gpu_norm import BF, F32
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,35 @@ def test_quantize_refuses_block_sizes_that_only_look_right_in_32_bits(cuda_devic
     with pytest.raises(flce.FlceError) as e:
         flce.flce_quantize_fp8(torch.randn(512, 128, device=cuda_device), block_rows=block_rows)
     assert e.value.status == 1
+
+
+def nearest_e4m3(v):
+    """|v| <= 448 in 64 bits to the nearest e4m3 number, ties to even."""
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -20))).clamp(min=-6) - 3)
+    return torch.round(v / step) * step
+
+
+@pytest.mark.parametrize("x_dtype", [BF, F32])
+@pytest.mark.parametrize("T,Hd", [(2, 128), (200, 512), (5000, 512)])
+def test_products_beside_a_tie_where_rstd_is_a_power_of_two(cuda_device, x_dtype, T, Hd):
+    """rstd is 1 and h w lies off the middle of two e4m3 numbers by less than fp32 resolves: rounded
+    once, it goes to the nearer one (no tolerance)."""
+    u = 2.0 ** -23
+    if x_dtype == BF:
+        h = torch.full((Hd,), 0.5, device=cuda_device)
+        h[:Hd * 3 // 8] = 1.5           # mean square 1
+    else:
+        k = torch.arange(Hd // 2, device=cuda_device) % 4 + 1
+        h = torch.cat([1 + k * u, 1 - k * u])  # squares 1 +- 2 k u and less than u / 2
+    middle = 1 + (2 * (torch.arange(Hd, device=cuda_device) % 8).double() + 1) / 16
+    w = (middle / h.double()).float()
+    w = torch.where(torch.arange(Hd, device=cuda_device) % 3 == 0, torch.nextafter(w, 2 * w), w)
+    y = h.double() * w.double()
+    off = y - middle
+    assert float(off.abs().max()) < 4 * u and int((off != 0).sum()) > Hd // 2
+    x = h.expand(T, Hd).to(x_dtype).contiguous()
+    _, _, rstd, q, qs = flce.flce_add_rms_norm(x, w, eps=0.0, normed=False, fp8=True, save_rstd=True)
+    assert bool((rstd == 1).all())
+    s = torch.ldexp(torch.ones((), dtype=torch.float64, device=cuda_device), qs.view(torch.uint8).int() - 127)
+    s = s.repeat_interleave(128, 1)
+    assert torch.equal(q.double(), nearest_e4m3(y / s))
