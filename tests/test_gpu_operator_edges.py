@@ -100,3 +100,24 @@ def test_products_beside_a_tie_where_rstd_is_a_power_of_two(cuda_device, x_dtype
     s = torch.ldexp(torch.ones((), dtype=torch.float64, device=cuda_device), qs.view(torch.uint8).int() - 127)
     s = s.repeat_interleave(128, 1)
     assert torch.equal(q.double(), nearest_e4m3(y / s))
+
+
+@pytest.mark.parametrize("T", [4001, 40001])
+def test_k3_keeps_its_digits_near_zero(cuda_device, T):
+    """e^e - 1 - e from e = 10^-7 to 8 in both signs.  Bound: below 1/2 the sum of the series, five roundings of at
+    most 2^-24; above, one unit in the last place of expm1 (at most 2^-23 of it) against a value that is at least
+    0.22 of it, and the subtraction's rounding: below 12 x 2^-24 in either case."""
+    size = torch.logspace(-7, 0.9, T // 2, device=cuda_device)
+    ref = torch.cat([size, -size, torch.zeros(1, device=cuda_device)])
+    zero = torch.zeros(T, device=cuda_device)
+    y = torch.ones(T, dtype=torch.int64, device=cuda_device)
+    kw = dict(ref_logp=ref, kl_coef=1.0, kl="k3")
+    loss, dlogp, _, _, _ = flce.flce_policy_loss(zero, zero, zero, y, reduction="none", **kw)
+    e = ref.double()
+    want = torch.expm1(e) - e
+    assert bool(((loss.double() - want).abs() <= 12 * 2.0 ** -24 * want).all())
+    assert bool(((dlogp.double() + torch.expm1(e)).abs() <= 2 ** -22 * torch.expm1(e).abs()).all())
+    near = torch.full((T,), 3e-6, device=cuda_device)  # a policy that has hardly moved: the mean over tokens
+    stats = flce.flce_policy_loss(zero, zero, zero, y, **dict(kw, ref_logp=near))[2]
+    e = near.double()[0]
+    assert float(stats[0]) == pytest.approx(float(e * e / 2 + e * e * e / 6), rel=1e-6)
