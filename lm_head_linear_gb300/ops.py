@@ -95,9 +95,9 @@ class AddRMSNorm(torch.autograd.Function):
 
 
 def _dense_rows(t: torch.Tensor) -> torch.Tensor:
-    """A gradient as the kernels take it (expanded and transposed ones are copied)."""
+    """A gradient as the kernels take it (expanded, transposed and misaligned ones are copied)."""
     return t if t.stride(1) == 1 and t.stride(0) >= t.shape[1] and t.data_ptr() % 16 == 0 and \
-        t.stride(0) * t.element_size() % 16 == 0 else t.contiguous()
+        t.stride(0) * t.element_size() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
 def add_rms_norm(x, weight, residual=None, eps: float = 1e-6):

@@ -121,3 +121,18 @@ def test_k3_keeps_its_digits_near_zero(cuda_device, T):
     stats = flce.flce_policy_loss(zero, zero, zero, y, **dict(kw, ref_logp=near))[2]
     e = near.double()[0]
     assert float(stats[0]) == pytest.approx(float(e * e / 2 + e * e * e / 6), rel=1e-6)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_gradients_off_16_bytes(cuda_device, dtype):
+    """Contiguous upstream gradients that start one element into a buffer (slices of a flat one)."""
+    T, Hd = 6, 64
+    x = torch.randn(T, Hd, device=cuda_device).to(dtype).requires_grad_(True)
+    w = torch.rand(Hd, device=cuda_device).requires_grad_(True)
+    flat = [torch.randn(1 + T * Hd, device=cuda_device).to(t)[1:] for t in (BF, dtype)]
+    dy, dh = (f.view(T, Hd) for f in flat)
+    got, want = [], []
+    for grads, into in (((dy, dh), got), ((dy.clone(), dh.clone()), want)):
+        y, h = flce.add_rms_norm(x, w)
+        into += torch.autograd.grad([y, h], [x, w], grads)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
