@@ -9,6 +9,7 @@ fallback: if the library is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -427,6 +428,32 @@ def flce_profile_collect() -> dict:
     return res
 
 
+class _FirstOrderOnly(torch.autograd.Function):
+    """A gradient as it is, that raises where it is differentiated."""
+
+    @staticmethod
+    def forward(ctx, t):
+        return t.view_as(t)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the library's operators have first derivatives only: "
+                           "a gradient that went through one cannot be differentiated")
+
+
+def first_order(backward):
+    """For an autograd Function's backward that calls the library: its gradients raise where they are
+    differentiated in turn (``create_graph``), instead of standing for constants there."""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        return tuple(None if t is None else _FirstOrderOnly.apply(t.detach().requires_grad_()) for t in out)
+    return run
+
+
 class LinearCrossEntropy(torch.autograd.Function):
     """autograd wrapper: forward runs ``flce_forward_valid`` (rows with an ignored target
     cost nothing), backward ``flce_backward`` (``flce_backward_logp`` when a gradient
@@ -448,6 +475,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         return loss, logp
 
     @staticmethod
+    @first_order
     def backward(ctx, dloss, dlogp):
         H, W, targets, lse = ctx.saved_tensors
         dH, dW, _ = flce_backward(dloss, H, W, targets, lse, ctx.ignore_index, ctx.reduction, dlogp=dlogp)

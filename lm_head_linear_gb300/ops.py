@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from .binding import LIB_PATH, REDUCTIONS, _check, load_library
+from .binding import LIB_PATH, REDUCTIONS, _check, first_order, load_library
 
 OPS_PATH = os.path.join(os.path.dirname(LIB_PATH), "flce_ops.so")
 _OPS = None
@@ -82,16 +82,19 @@ class AddRMSNorm(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy, dh):
-        h, weight, rstd = ctx.saved_tensors
-        if dy is None and dh is None:
+        if dy is not None:
+            return AddRMSNorm._through_the_norm(ctx, dy, dh)
+        if dh is None:
             return None, None, None, None
-        if dy is None:
-            dx, dw = dh, None
-        else:
-            dx, dw, _ = flce_add_rms_norm_backward(_dense_rows(dy), h, weight, rstd,
-                                                   dh=None if dh is None else _dense_rows(dh.to(h.dtype)))
-            dw = dw.to(weight.dtype)
-        return dx.to(ctx.x_dtype), dw, dx if ctx.has_residual else None, None
+        return dh.to(ctx.x_dtype), None, dh if ctx.has_residual else None, None
+
+    @staticmethod
+    @first_order
+    def _through_the_norm(ctx, dy, dh):
+        h, weight, rstd = ctx.saved_tensors
+        dx, dw, _ = flce_add_rms_norm_backward(_dense_rows(dy), h, weight, rstd,
+                                               dh=None if dh is None else _dense_rows(dh.to(h.dtype)))
+        return dx.to(ctx.x_dtype), dw.to(weight.dtype), dx if ctx.has_residual else None, None
 
 
 def _dense_rows(t: torch.Tensor) -> torch.Tensor:
@@ -174,6 +177,7 @@ class PolicyLoss(torch.autograd.Function):
         return (loss if kwargs.get("reduction") == "none" else loss.reshape(())), stats
 
     @staticmethod
+    @first_order
     def backward(ctx, dloss, _):
         logp, old_logp, advantages, targets, ref_logp, cu_seqlens = ctx.saved_tensors
         _, dlogp, _, _, _ = flce_policy_loss(logp, old_logp, advantages, targets, ref_logp=ref_logp,
@@ -226,6 +230,7 @@ class PreferenceLoss(torch.autograd.Function):
         return (loss if kwargs.get("reduction") == "none" else loss.reshape(())), chosen, rejected
 
     @staticmethod
+    @first_order
     def backward(ctx, dloss, _c, _r):
         logp, targets, cu_seqlens, ref_logp = ctx.saved_tensors
         _, dlogp, _, _, _ = flce_preference_loss(logp, targets, cu_seqlens, ref_logp=ref_logp,

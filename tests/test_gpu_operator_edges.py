@@ -136,3 +136,30 @@ def test_norm_gradients_off_16_bytes(cuda_device, dtype):
         y, h = flce.add_rms_norm(x, w)
         into += torch.autograd.grad([y, h], [x, w], grads)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_second_derivatives_raise(cuda_device):
+    """A gradient that went through an operator is no constant: differentiating it says so.  A gradient of
+    the residual sum alone is linear, and has its second derivative."""
+    logp, old, ref, adv, y, _ = draw(64, cuda_device, mask=0.0)
+    cu = torch.tensor([0, 20, 64], device=cuda_device)
+    lp = logp.clone().requires_grad_(True)
+    x = torch.randn(8, 64, device=cuda_device).to(BF).requires_grad_(True)
+    w = torch.ones(64, device=cuda_device).requires_grad_(True)
+    r = torch.randn(8, 64, device=cuda_device).to(BF).requires_grad_(True)
+    W = torch.randn(100, 64, device=cuda_device).to(BF).requires_grad_(True)
+    yh = torch.arange(8, device=cuda_device)
+    for loss, wrt in ((flce.policy_loss(lp, old, adv, y, ref, kl_coef=0.1)[0], lp),
+                      (flce.preference_loss(lp, y, cu, ref)[0], lp),
+                      (flce.add_rms_norm(x, w, r)[0].float().square().sum(), r),
+                      (flce.add_rms_norm(x, w)[0].float().sum(), w),
+                      (flce.linear_cross_entropy(x, W, yh), x)):
+        plain, = torch.autograd.grad(loss, wrt, retain_graph=True)
+        g, = torch.autograd.grad(loss, wrt, create_graph=True)
+        assert torch.equal(g, plain) and not plain.requires_grad
+        with pytest.raises(RuntimeError, match="first derivatives only"):
+            (g * wrt).sum().backward()
+    h = flce.add_rms_norm(x, w, r)[1]
+    g, = torch.autograd.grad(h.float().pow(3).sum(), x, create_graph=True)
+    second, = torch.autograd.grad(g.float().sum(), r)
+    assert torch.allclose(second.float(), 6 * h.detach().float(), rtol=2.0 ** -7)
