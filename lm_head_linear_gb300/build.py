@@ -4,7 +4,8 @@ Python module ``_lib/flce_ops.so`` that calls its operators.
 Plain ``nvcc``: a few translation units compiled side by side, one
 ``-gencode`` (compute_103a -> sm_103a), static CUDA runtime,
 position-independent shared object.  The module is host C++ against torch's
-headers, linked to the library.  Run as ``python -m lm_head_linear_gb300.build``.
+headers, linked to the library; where it does not build, the library still does.
+Run as ``python -m lm_head_linear_gb300.build``.
 """
 
 from __future__ import annotations
@@ -14,6 +15,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -84,22 +86,35 @@ def _run(cmd, verbose: bool) -> None:
         print(res.stdout + res.stderr, flush=True)
 
 
+def _compile_ops(obj: str, out: str, verbose: bool) -> list:
+    """Compiles the Python module; returns its link command."""
+    compile_cmd, link_cmd = ops_commands(obj, out)
+    _run(compile_cmd, verbose)
+    return link_cmd
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile the library if any source is newer than it; returns its path."""
+    """Compile the library if any source is newer than it; returns its path.
+
+    The library needs nvcc alone.  Where the Python module cannot be built (torch's headers or libraries, or
+    Python's, are missing) a warning says why, and :func:`.ops.load_operators` raises."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(LIB_DIR, exist_ok=True)
-    tmp = LIB_PATH + ".tmp"
+    tmp, ops_tmp = LIB_PATH + ".tmp", OPS_PATH + ".tmp"
     objs = [os.path.join(LIB_DIR, os.path.basename(src) + ".o") for src in SOURCES]
-    ops_obj, ops_tmp = os.path.join(LIB_DIR, "ops_binding.o"), OPS_PATH + ".tmp"
-    ops_compile, ops_link = ops_commands(ops_obj, ops_tmp)
-    jobs = [compile_command(src, obj, extra) for src, obj in zip(SOURCES, objs)] + [ops_compile]
-    with ThreadPoolExecutor(len(jobs)) as pool:
-        list(pool.map(lambda cmd: _run(cmd, verbose), jobs))
+    with ThreadPoolExecutor(len(SOURCES) + 1) as pool:
+        ops = pool.submit(_compile_ops, os.path.join(LIB_DIR, "ops_binding.o"), ops_tmp, verbose)
+        list(pool.map(lambda job: _run(compile_command(*job, extra), verbose), zip(SOURCES, objs)))
     _run(link_command(objs, tmp), verbose)
     os.replace(tmp, LIB_PATH)
-    _run(ops_link, verbose)
-    os.replace(ops_tmp, OPS_PATH)
+    try:
+        _run(ops.result(), verbose)
+        os.replace(ops_tmp, OPS_PATH)
+    except Exception as e:  # whatever torch's build helpers raise where something is missing
+        if os.path.exists(OPS_PATH):
+            os.remove(OPS_PATH)  # an older one, of another interface
+        warnings.warn(f"{LIB_PATH} is built; {OPS_PATH} could not be: {e}")
     return LIB_PATH
 
 
