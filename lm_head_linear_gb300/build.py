@@ -68,8 +68,23 @@ def ops_commands(obj: str, out: str) -> list:
              "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]]
 
 
+def running() -> str:
+    """What the compiled Python module depends on besides its sources: torch's C++ interface has no stable ABI."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def ops_built_for() -> str:
+    """running() as it was when the module was built ("" if that is not known)."""
+    try:
+        with open(OPS_PATH + ".for") as fh:
+            return fh.read()
+    except OSError:
+        return ""
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(OPS_PATH)):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(OPS_PATH) and ops_built_for() == running()):
         return False
     t = os.path.getmtime(LIB_PATH)
     return all(os.path.getmtime(f) <= t for f in DEPENDS) and all(
@@ -111,6 +126,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     try:
         _run(ops.result(), verbose)
         os.replace(ops_tmp, OPS_PATH)
+        with open(OPS_PATH + ".for", "w") as fh:
+            fh.write(running())
     except Exception as e:  # whatever torch's build helpers raise where something is missing
         if os.path.exists(OPS_PATH):
             os.remove(OPS_PATH)  # an older one, of another interface

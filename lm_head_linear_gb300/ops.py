@@ -31,6 +31,10 @@ def load_operators():
         if not os.path.exists(OPS_PATH):
             raise RuntimeError(f"{OPS_PATH} is missing: build it with `python -m lm_head_linear_gb300.build` "
                                "(there is no fallback implementation)")
+        from .build import ops_built_for, running  # here: `python -m` runs that module itself
+        if ops_built_for() != running():
+            raise RuntimeError(f"{OPS_PATH} was built for {ops_built_for() or 'an unknown torch'}, this is {running()}: "
+                               "build it again with `python -m lm_head_linear_gb300.build`")
         spec = importlib.util.spec_from_file_location("flce_ops", OPS_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

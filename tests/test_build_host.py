@@ -6,8 +6,10 @@ import sys
 import types
 
 import pytest
+import torch
 
 from lm_head_linear_gb300 import build as b
+from lm_head_linear_gb300 import ops
 
 
 @pytest.fixture
@@ -60,3 +62,20 @@ def test_a_library_that_fails_to_build_raises(tree):
     with pytest.raises(RuntimeError, match="compiler's text"):
         b.build()
     assert tree.built() == (False, False)
+
+
+def test_a_module_built_for_another_torch_is_stale(tree, monkeypatch):
+    """torch's C++ interface has no stable ABI: a module built against another version is built again, and not loaded."""
+    b.build()
+    assert b.up_to_date()
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not b.up_to_date()
+    monkeypatch.setattr(ops, "_OPS", None)
+    monkeypatch.setattr(ops, "OPS_PATH", b.OPS_PATH)
+    monkeypatch.setattr(ops, "load_library", lambda: None)
+    with pytest.raises(RuntimeError, match="build it again"):
+        ops.load_operators()
+    b.build()
+    assert b.up_to_date()
+    os.remove(b.OPS_PATH + ".for")
+    assert not b.up_to_date()
