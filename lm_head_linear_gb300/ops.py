@@ -190,11 +190,15 @@ class PolicyLoss(torch.autograd.Function):
         return dlogp, None, None, None, None, None, None
 
 
-def policy_loss(logp, old_logp, advantages, targets, ref_logp=None, cu_seqlens=None, **kwargs):
+def policy_loss(logp, old_logp, advantages, targets, ref_logp=None, cu_seqlens=None, workspace=None, **kwargs):
     """Clipped policy loss with a KL term, differentiable in ``logp``; returns ``(loss, stats)``.
     Keyword arguments as :func:`flce_policy_loss` (per_sequence, ignore_index, reduction, clip_low,
-    clip_high, dual_clip, kl_coef, kl)."""
-    return PolicyLoss.apply(logp, old_logp, advantages, targets, ref_logp, cu_seqlens, kwargs)
+    clip_high, dual_clip, kl_coef, kl).
+
+    Malformed ``cu_seqlens`` are found on the GPU and make the results mean nothing: pass a ``workspace`` (uint8,
+    :func:`flce_policy_loss_workspace_size` bytes) and look at it with :func:`.binding.flce_read_device_status`, which
+    waits for the GPU.  Forward and backward both use it and leave their status there."""
+    return PolicyLoss.apply(logp, old_logp, advantages, targets, ref_logp, cu_seqlens, dict(kwargs, workspace=workspace))
 
 
 def flce_preference_loss_workspace_size(n_pairs: int) -> int:
@@ -242,9 +246,9 @@ class PreferenceLoss(torch.autograd.Function):
         return dlogp, None, None, None, None
 
 
-def preference_loss(logp, targets, cu_seqlens, ref_logp=None, **kwargs):
+def preference_loss(logp, targets, cu_seqlens, ref_logp=None, workspace=None, **kwargs):
     """Preference loss on paired log ratios, differentiable in ``logp``; returns
     ``(loss, chosen_rewards, rejected_rewards)``.  Keyword arguments as
     :func:`flce_preference_loss` (ignore_index, reduction, kind, beta, label_smoothing, margin,
-    length_normalize)."""
-    return PreferenceLoss.apply(logp, targets, cu_seqlens, ref_logp, kwargs)
+    length_normalize); ``workspace`` (:func:`flce_preference_loss_workspace_size` bytes) as in :func:`policy_loss`."""
+    return PreferenceLoss.apply(logp, targets, cu_seqlens, ref_logp, dict(kwargs, workspace=workspace))

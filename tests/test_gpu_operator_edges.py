@@ -163,3 +163,22 @@ def test_second_derivatives_raise(cuda_device):
     g, = torch.autograd.grad(h.float().pow(3).sum(), x, create_graph=True)
     second, = torch.autograd.grad(g.float().sum(), r)
     assert torch.allclose(second.float(), 6 * h.detach().float(), rtol=2.0 ** -7)
+
+
+def test_status_of_the_differentiable_losses(cuda_device):
+    """With a workspace of the caller's, malformed sequences are known after the forward and after the backward."""
+    logp, old, ref, adv, y, _ = draw(100, cuda_device)
+    for policy in (True, False):
+        n = flce.flce_policy_loss_workspace_size(100, 2) if policy else flce.flce_preference_loss_workspace_size(1)
+        for cu, want in (([0, 60, 40], 8), ([0, 60, 100], 0)):
+            cu = torch.tensor(cu, device=cuda_device)
+            ws = torch.full((n,), 255, dtype=torch.uint8, device=cuda_device)
+            x = logp.clone().requires_grad_(True)
+            if policy:
+                loss = flce.policy_loss(x, old, adv, y, ref, cu, workspace=ws, reduction="sequence_mean")[0]
+            else:
+                loss = flce.preference_loss(x, y, cu, ref, workspace=ws)[0]
+            assert flce.flce_read_device_status(ws) == want
+            ws.fill_(255)
+            loss.backward()
+            assert flce.flce_read_device_status(ws) == want
