@@ -717,7 +717,7 @@ constexpr int kPairCtas = 16;
 // Both answers of a pair at once, one per half of the CTA.  One reading gives the
 // sums; the gradient is one number per sequence, so the second pass only stores
 // (the mask bits of the first 8 x 1024 tokens stay in a register).
-//   SOLO   one cluster holds every pair, CTA r takes pairs r, r + CTAs, ...; the
+//   SOLO   one cluster holds every pair, one to a CTA (the last CTAs may have none); the
 //          scalar loss is summed through distributed shared memory: one launch.
 //   else   one cluster per pair, whose CTAs share the pair's tokens and exchange
 //          their sums; preference_reduce_kernel adds the pairs' losses.
@@ -741,7 +741,8 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const Preferen
   bool arrived = true;
   double loss_sum = 0.0;
   int bad_sum = 0;
-  for (int pair = SOLO ? rank : blockIdx.x / ctas; pair < p.P; pair += SOLO ? ctas : p.P) {
+  const int pair = SOLO ? rank : blockIdx.x / ctas;
+  if (pair < p.P) {
     int64_t at[3];
     bool bad = false;
 #pragma unroll
@@ -824,8 +825,8 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const Preferen
           if (p.loss && p.reduction == kNone) p.loss[pair] = value;
           if (!SOLO) p.pair_loss[pair] = value, p.pair_bad[pair] = bad;
         }
-        loss_sum += value;
-        bad_sum += bad;
+        loss_sum = value;
+        bad_sum = bad;
       }
     } else if (!SOLO && ctas > 1) {
       cluster_wait();
