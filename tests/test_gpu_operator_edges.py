@@ -1,10 +1,12 @@
-"""Edges of the operators around the head: long runs of empty sequences, streams of other devices."""
+"""Edges of the operators around the head: long runs of empty sequences, streams of other devices, values beside a
+tie, digits near zero, gradients off 16 bytes, second derivatives, device status, scales and values at the ends of their range."""
 
 import pytest
 import torch
 
 import lm_head_linear_gb300 as flce
 
+from test_gpu_linear_fp8 import whole
 from test_gpu_losses import check_policy, draw
 from test_gpu_norm import BF, F32
 
@@ -182,3 +184,56 @@ def test_status_of_the_differentiable_losses(cuda_device):
             ws.fill_(255)
             loss.backward()
             assert flce.flce_read_device_status(ws) == want
+
+
+@pytest.mark.parametrize("T,V", [(1, 300), (40, 600), (240, 700), (600, 257)])
+def test_scale_bytes_at_the_ends_of_their_range(cuda_device, T, V):
+    """Byte 0 is 2^-127, 254 is 2^127, and 255 a NaN that reaches its own row (or 128 columns) and nothing else."""
+    K = 384
+    x, sx, W, sw = whole(T, K, V, cuda_device, seed=V)
+    for j, (a, b) in enumerate(((0, 254), (254, 0), (127, 127))):
+        sx[:, j], sw[:, j] = a, b
+    want = x.double() @ W.double().t()  # every block's scales multiply to 1
+    y, ws = flce.flce_linear_fp8(x, sx, W, sw, dtype=F32)
+    assert torch.equal(y.double(), want)
+    rows, blocks = [T // 2], [0, (V - 1) // 128]  # the last one reaches past V
+    sx, sw = torch.full_like(sx, 127), torch.full_like(sw, 127)
+    sx[rows, 1] = 255
+    sw[blocks[0], 2], sw[blocks[1], 0] = 255, 255
+    for dtype in (F32, BF):
+        y, ws = flce.flce_linear_fp8(x, sx, W, sw, dtype=dtype, workspace=ws)
+        assert flce.flce_read_device_status(ws) == 0
+        nan = torch.zeros(T, V, dtype=torch.bool, device=cuda_device)
+        nan[rows] = True
+        for b in blocks:
+            nan[:, 128 * b:128 * b + 128] = True
+        assert torch.equal(torch.isnan(y), nan)
+        assert torch.equal(y[~nan], want.to(dtype)[~nan])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_of_zeros_nan_and_infinities(cuda_device, dtype, block_rows):
+    """A block of zeros has the least scale; a NaN stays one and leaves its block's scale alone; an infinity
+    saturates at the scale of the largest finite numbers."""
+    R, K = 300, 400
+    a = torch.randn(R, K, device=cuda_device).to(dtype)
+    a[128:256, 128:256] = 0
+    a[0, 0] = 0
+    a[5, 300] = float("nan")
+    a[6, 256:384] = float("nan")
+    a[260, 3], a[260, 4] = float("inf"), -float("inf")
+    q, s = flce.flce_quantize_fp8(a, block_rows=block_rows)
+    clean = a.clone()
+    clean[torch.isnan(a)] = 0
+    q0, s0 = flce.flce_quantize_fp8(clean, block_rows=block_rows)
+    U8 = torch.uint8
+    assert torch.equal(s.view(U8), s0.view(U8))
+    assert torch.equal(torch.isnan(q.float()), torch.isnan(a))
+    assert torch.equal(q.float()[~torch.isnan(a)], q0.float()[~torch.isnan(a)])
+    per = 128 // block_rows  # rows of scales for 128 of the matrix
+    assert bool((s.view(U8)[per:2 * per, 1] == 1).all()) and bool((q.float()[128:256, 128:256] == 0).all())
+    at = 260 if block_rows == 1 else 2
+    assert int(s.view(U8)[at, 0]) == 247 and q.float()[260, 3] == 448 and q.float()[260, 4] == -448
+    rest = slice(260, 261) if block_rows == 1 else slice(256, 300)
+    assert int((q.float()[rest, :128] != 0).sum()) == 2  # what 2^120 leaves of the others
