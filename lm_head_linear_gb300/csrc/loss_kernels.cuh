@@ -35,16 +35,10 @@ __device__ __forceinline__ float clamp_ratio(float v) {
 // 10^-6, where kl is 5 10^-13, all but three bits of it), so below 1/2 the power series is
 // summed: v^2 (1/2! + v/3! + .. + v^7/9!), the next term below 3 10^-9 of the first.
 __device__ __forceinline__ float exp_above_line(float v, float em) {
-  if (!(fabsf(v) < 0.5f)) return em - v;
-  float s = 1.0f / 362880.0f;
-  s = fmaf(s, v, 1.0f / 40320.0f);
-  s = fmaf(s, v, 1.0f / 5040.0f);
-  s = fmaf(s, v, 1.0f / 720.0f);
-  s = fmaf(s, v, 1.0f / 120.0f);
-  s = fmaf(s, v, 1.0f / 24.0f);
-  s = fmaf(s, v, 1.0f / 6.0f);
-  s = fmaf(s, v, 0.5f);
-  return v * v * s;
+  const float v2 = v * v;  // pairs of terms in v^2: a shorter chain than one after the other
+  const float a = fmaf(1.0f / 6.0f, v, 0.5f), b = fmaf(1.0f / 120.0f, v, 1.0f / 24.0f);
+  const float c = fmaf(1.0f / 5040.0f, v, 1.0f / 720.0f), d = fmaf(1.0f / 362880.0f, v, 1.0f / 40320.0f);
+  return fabsf(v) < 0.5f ? v2 * fmaf(fmaf(fmaf(d, v2, c), v2, b), v2, a) : em - v;
 }
 
 // ------------------------------------------------------------------ policy loss

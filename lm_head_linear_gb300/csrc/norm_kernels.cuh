@@ -206,21 +206,23 @@ __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const
       }
       if (p.q) {  // rounded to odd; fmaxf drops NaN: the scale comes from the block's numbers, a NaN stays NaN in q
 #pragma unroll
-        for (int j = 0; j < kRunPairs; ++j) {
-          split(fma2_zero(v[k][j], hi2, rest[j]), y[2 * j], y[2 * j + 1]);
-          uint32_t bit[2] = {odd_bit, odd_bit};
-          if constexpr (!EXACT) {
-            if (odd_bit == 0) {  // the same for the whole row
+        for (int j = 0; j < kRunPairs; ++j) split(fma2_zero(v[k][j], hi2, rest[j]), y[2 * j], y[2 * j + 1]);
+        if constexpr (!EXACT) {
+          if (odd_bit == 0) {  // rare, and the same for the whole row
+#pragma unroll
+            for (int j = 0; j < kRunPairs; ++j) {
               float cut[2];
               split(rest[j], cut[0], cut[1]);
-              bit[0] = cut[0] != 0.0f, bit[1] = cut[1] != 0.0f;
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+                if (cut[b] != 0.0f) y[2 * j + b] = __uint_as_float(__float_as_uint(y[2 * j + b]) | 1u);
             }
           }
+        }
 #pragma unroll
-          for (int b = 2 * j; b < 2 * j + 2; ++b) {
-            y[b] = __uint_as_float(__float_as_uint(y[b]) | bit[b - 2 * j]);
-            amax = fmaxf(amax, fabsf(y[b]));
-          }
+        for (int b = 0; b < kRun; ++b) {
+          y[b] = __uint_as_float(__float_as_uint(y[b]) | odd_bit);
+          amax = fmaxf(amax, fabsf(y[b]));
         }
       }
     }
