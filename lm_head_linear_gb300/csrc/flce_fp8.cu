@@ -125,7 +125,8 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
   fp8::Params p;
   std::memset(&p, 0, sizeof(p));
   const int64_t es = y_dtype == FLCE_DTYPE_F32 ? 4 : 2;
-  p.y_tma = !off16(y) && (ldy * es) % 16 == 0;
+  p.v_tma = static_cast<int32_t>(V & ~(16 / es - 1));
+  p.y_tma = !off16(y) && (ldy * es) % 16 == 0 && p.v_tma > 0;
   if ((st = resident_pairs<true>(dev, sms, &pairs)) != FLCE_OK || (st = resident_pairs<false>(dev, sms, &pairs)) != FLCE_OK)
     return st;
   // One token tile: the vocabulary on M.  More: the side and the width of the tiles that
@@ -162,7 +163,7 @@ flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, const void* W
     return st;
   const CUtensorMapSwizzle y_swizzle = es == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   if (p.y_tma && (st = matrix_map(&p.tmY, es == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                                  y_swizzle, y, V, T, ldy * es, 32, 32)) != FLCE_OK)
+                                  y_swizzle, y, p.v_tma, T, ldy * es, 32, 32)) != FLCE_OK)
     return st;
   p.sx = x_scale, p.sw = W_scale, p.y = y, p.ldy = ldy;
   p.status = static_cast<int32_t*>(workspace);

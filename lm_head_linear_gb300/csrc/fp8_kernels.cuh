@@ -76,7 +76,7 @@ static_assert(kScaleBase + kScaleStages * kScaleCols <= static_cast<int>(kTmemCo
 struct Params {
   CUtensorMap tmA;   // the M side, [rows, K] bytes, box 128 x 128 rows (one token tile: x 32 rows)
   CUtensorMap tmB;   // the N side, box 128 x N / 2 rows
-  CUtensorMap tmY;   // [T, V] logits, box 32 logits x 32 tokens (y_tma)
+  CUtensorMap tmY;   // [T, v_tma] logits, box 32 logits x 32 tokens (y_tma)
   const uint8_t* sx; // [T, kb]
   const uint8_t* sw; // [ceil(V / 128), kb]
   void* y;
@@ -90,6 +90,7 @@ struct Params {
   int32_t stages, stage_bytes, staging_bytes;
   int32_t y_f32;
   int32_t y_tma;     // y's rows start on 16-byte boundaries: boxes leave by TMA, else row by row
+  int32_t v_tma;     // V rounded down to whole 16 bytes: TMA writes 16-byte pieces, also past its bounds
 };
 
 // full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], scale_full[4], scale_empty[4], drain
@@ -495,6 +496,27 @@ __device__ __forceinline__ void store_rows(const Params& p, uint32_t buf, int t0
   }
 }
 
+// The up to 14 bytes of each row that TMA leaves of a box: logits v_tma .. V - 1, a row
+// per lane.  TMA stores whole 16-byte pieces, so a box clipped inside one would write
+// zeros over what follows the row's last logit.
+template <typename E>
+__device__ __forceinline__ void store_tail(const Params& p, uint32_t buf, int t0, int v0, int lane) {
+  if (t0 + lane >= p.T) return;
+  E* y = static_cast<E*>(p.y) + static_cast<int64_t>(t0 + lane) * p.ldy;
+  constexpr int kPiece = 16 / static_cast<int>(sizeof(E));
+  for (int v = p.v_tma; v < p.V; ++v) {
+    const int k = v - v0;
+    const uint32_t a = staged<E>(buf, lane, k / kPiece) + (k % kPiece) * static_cast<int>(sizeof(E));
+    if constexpr (sizeof(E) == 4) {
+      y[v] = __uint_as_float(ld_shared_u32(a));
+    } else {
+      uint16_t h;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(a) : "memory");
+      y[v] = __ushort_as_bfloat16(h);
+    }
+  }
+}
+
 // bf16, tokens on M, rows of y off 16 bytes (an odd vocabulary).  The two warps of a
 // quarter put its 32 rows into shared memory whole, each as it lies in memory (its first
 // byte d bytes into a 16-byte piece); then one warp has the copy engine store every row's
@@ -639,11 +661,20 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
         else
           stage_vocab_m<E>(buf, r, lane);
         if (p.y_tma) {
+          const int v0 = TOKENS_M ? n0 : m0, t0 = TOKENS_M ? m0 : n0;
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) {
-            ptx::tma_store_2d(&p.tmY, buf, TOKENS_M ? n0 : m0, TOKENS_M ? m0 : n0);
-            ptx::bulk_commit();
+          if (v0 + 32 <= p.v_tma) {
+            if (lane == 0) {
+              ptx::tma_store_2d(&p.tmY, buf, v0, t0);
+              ptx::bulk_commit();
+            }
+          } else {
+            if (lane == 0) {
+              if (v0 < p.v_tma) ptx::tma_store_2d(&p.tmY, buf, v0, t0);
+              ptx::bulk_commit();
+            }
+            store_tail<E>(p, buf, t0, v0, lane);
           }
         } else if constexpr (!kMayImage) {
           __syncwarp();

@@ -6,7 +6,7 @@ import torch
 
 import lm_head_linear_gb300 as flce
 
-from test_gpu_linear_fp8 import whole
+from test_gpu_linear_fp8 import value, whole
 from test_gpu_losses import check_policy, draw
 from test_gpu_norm import BF, F32
 
@@ -237,3 +237,20 @@ def test_quantize_of_zeros_nan_and_infinities(cuda_device, dtype, block_rows):
     assert int(s.view(U8)[at, 0]) == 247 and q.float()[260, 3] == 448 and q.float()[260, 4] == -448
     rest = slice(260, 261) if block_rows == 1 else slice(256, 300)
     assert int((q.float()[rest, :128] != 0).sum()) == 2  # what 2^120 leaves of the others
+
+
+@pytest.mark.parametrize("T,K,V", [(1, 128, 9), (3, 288, 75), (40, 144, 4097), (224, 16, 33), (225, 64, 859), (300, 144, 2),
+                                   (400, 304, 4588), (600, 1008, 167), (512, 128, 1030), (130, 128, 255)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_logits_into_columns_of_a_wider_buffer(cuda_device, T, K, V, dtype):
+    """Rows on 16 bytes that end inside 16 bytes (one shard's columns of a buffer that holds all): what lies
+    before, between and behind the rows keeps its values."""
+    x, sx, W, sw = whole(T, K, V, cuda_device, seed=V)
+    want = (value(x, sx, 1) @ value(W, sw, 128).t()).float().to(dtype)
+    per = 16 // want.element_size()
+    for ld in (-(-V // per) * per, (-(-V // per) + 3) * per):
+        buf = torch.full((T, ld), 7.0, dtype=dtype, device=cuda_device)
+        _, ws = flce.flce_linear_fp8(x, sx, W, sw, dtype=dtype, out={"y": buf[:, :V]})
+        assert flce.flce_read_device_status(ws) == 0
+        assert torch.equal(buf[:, :V], want)
+        assert bool((buf[:, V:] == 7.0).all())
