@@ -287,8 +287,8 @@ FLCE_API flce_status flce_backward_shard(const float* dloss, const void* H, cons
  * Residual add and root-mean-square norm, the last step before the LM head:
  *   h = x + residual, rounded to the residual's type (h = x without a residual)
  *   rstd_t = (mean_c h_{t,c}^2 + eps)^(-1/2),  y_{t,c} = h_{t,c} rstd_t w_c
- * with sums in fp32 over the rounded h, the value every later reader of the
- * residual stream sees.  Any of three outputs:
+ * over the rounded h, the value every later reader of the residual stream sees; the
+ * squares are fp32, their sum and rstd carry what fp32 rounds off.  Any of three outputs:
  *   y        [T, Hd] bf16 or NULL   what flce_forward takes as H
  *   q        [T, Hd] e4m3 or NULL   y in 8 bits, what flce_linear_fp8 takes, with
  *   q_scale  [T, ceil(Hd/128)]      one E8M0 byte s per row and 128 channels: the value
@@ -326,20 +326,22 @@ FLCE_API flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype
                                                 size_t workspace_bytes, void* stream);
 
 /* ---- the head's product in 8 bits ---------------------------------------------
- * For rollouts, and for scoring by a policy that is not trained: logits from e4m3
- * operands with one power-of-two scale (an E8M0 byte s, worth 2^(s - 127); 255 is
- * NaN) per block of 128 along K.
+ * For decoding (rollouts), and where logits are wanted as such (scores of given tokens
+ * without [T x V] logits are flce_score's): logits from e4m3 operands with one
+ * power-of-two scale (an E8M0 byte s, worth 2^(s - 127); 255 is NaN) per block of 128
+ * along K.
  *
  * flce_quantize_fp8 lays out a matrix: a [rows, K] bf16 or fp32 (row stride lda)
  *   q        [rows, K] e4m3
  *   q_scale  [ceil(rows / block_rows), ceil(K/128)], block_rows 128 for weights (128 x 128
- *            blocks), 1 for activations; the scale rule is flce_add_rms_norm's. */
+ *            blocks), 1 for activations; the scale rule is flce_add_rms_norm's, and an
+ *            infinity saturates: +-448 at the scale of the largest finite numbers, 2^120. */
 FLCE_API flce_status flce_quantize_fp8(const void* a, int32_t a_dtype, int64_t lda, int64_t rows, int64_t K,
                                        int32_t block_rows, void* q, uint8_t* q_scale, void* stream);
 
 /* y[t, v] = sum_b 2^(x_scale[t, b] + W_scale[v / 128, b] - 254) sum_{k in block b} x[t, k] W[v, k]
  *   x [T, K] e4m3, x_scale [T, ceil(K/128)];  W [V, K] e4m3, W_scale [ceil(V/128), ceil(K/128)]
- *   y [T, V] bf16 or fp32 (y_dtype), row stride ldy >= V elements
+ *   y [T, V] bf16 or fp32 (y_dtype), row stride ldy >= V elements; nothing else is written
  * fp32 accumulation over the whole of K, one rounding to bf16.  K: a multiple of 16
  * (the last block may be short).  x and W 16-byte aligned and contiguous.
  *   workspace, workspace_bytes  >= flce_linear_fp8_workspace_size(T, K, V); its status word

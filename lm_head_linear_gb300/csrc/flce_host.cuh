@@ -82,8 +82,10 @@ struct KernelScope {
 
 flce_status check_launch(const char* what);
 
-// Launches a kernel that begins with griddepcontrol.wait: it may be dispatched, and
-// set itself up, while the kernel before it on the stream is still finishing.
+// Launches a kernel that may be dispatched, and set itself up, while the kernel before it
+// on the stream is still finishing.  Every thread of it waits (griddepcontrol.wait)
+// before it touches global memory; policy_main_kernel alone reads inputs earlier, which
+// an ordinary launch before it (policy_count_kernel) has made complete.
 template <typename... Params, typename... Args>
 flce_status launch_overlapped(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                               const Args&... args) {

@@ -187,6 +187,7 @@ flce_status flce_policy_loss(const float* dloss, const float* logp, const float*
     st = launch_cluster(loss::policy_cluster_kernel, p, p.blocks, p.blocks, loss::kClusterThreads, s);
   } else {
     p.blocks = static_cast<int32_t>(L.blocks), p.chunk = static_cast<int32_t>(L.chunk);
+    // an ordinary launch: policy_main_kernel reads its inputs before its wait
     loss::policy_count_kernel<<<p.blocks, loss::kManyThreads, 0, s>>>(p);
     if (reduction == FLCE_REDUCTION_SEQUENCE_MEAN && n_seqs >= loss::kCuShared)
       loss::policy_nonempty_kernel<<<static_cast<unsigned>(std::min<int64_t>(cdiv(n_seqs, loss::kManyThreads), sms)),

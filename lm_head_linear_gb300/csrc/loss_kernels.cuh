@@ -6,8 +6,10 @@
 // Bound: bytes (28 and 20 per token, a few operations each), and below about a
 // million tokens latency: launches and the reduction's steps.
 //
-// Sums: fp32 over the few tokens of one warp (with what it rounds off, where log
-// ratios cancel), 64 bits across warps and blocks, in a fixed order.
+// Sums, all in a fixed order.  Policy: fp32 over the tokens of one warp (four of each
+// thread; beyond 2 M tokens several steps of four), 64 bits across warps and blocks.
+// Preference, where log ratios cancel: fp32 with what it rounds off over a warp, 64
+// bits from there on.
 #pragma once
 
 #include <cstdint>
@@ -137,7 +139,7 @@ __device__ __forceinline__ E block_sum(E v, E* sh) {
 // registers while the counts go round the cluster through distributed shared
 // memory (or, per sequence, through integer atomics in the workspace), and scales
 // and stores them after one cluster barrier.  No second launch, no second reading:
-// 32,768 tokens take 6.5 us, whose bytes (0.9 MB) would take 0.1 us; the rest is the
+// 32,768 tokens take 6.7 us, whose bytes (0.9 MB) would take 0.1 us; the rest is the
 // launch, one round of loads, the barrier and the tree of the sums.
 // Beyond that the 16 SMs of a cluster are too few (131,072 tokens in 61 sequences: 25.5
 // us with four such steps a thread), and the two launches further down take over.
@@ -462,6 +464,8 @@ __global__ void __launch_bounds__(kClusterThreads) policy_cluster_kernel(const P
 // their mask.  A sequence's count is the difference of two, without atomics or an
 // array to clear.  The second launch is dispatched while the first still runs and
 // loads its tokens before it waits for it; its last CTA adds up the sums in order.
+// Those early loads are safe because the count launch is an ordinary one: whatever wrote
+// the inputs is complete before it starts.  It must not be dispatched early itself.
 // 131,072 tokens in 61 sequences (3.1 MB, 0.5 us): 11.8 us, latency again, of two launches.
 constexpr int kManyThreads = 256;
 constexpr int kMaxBlocks = 1024;
@@ -715,8 +719,10 @@ constexpr int kPairCtas = 16;
 //          scalar loss is summed through distributed shared memory: one launch.
 //   else   one cluster per pair, whose CTAs share the pair's tokens and exchange
 //          their sums; preference_reduce_kernel adds the pairs' losses.
-// 16 pairs of 2 x 200 tokens take 5.2 us, 128 of 2 x 4096 (21 MB, 3.1 us at the copy's
-// rate) 10.4 us: the second reading comes from L2, the launches' latency is the rest.
+// 16 pairs of 2 x 200 tokens take 5.3 us.  128 of 2 x 4096 (21 MB, 3.1 us at the copy's
+// rate) take 10.4 us, most of it here: a step's loads are used before the next step's are
+// issued, and a ragged batch waits for its longest answer's three or four steps.  The
+// second reading comes from L2.
 template <bool SOLO>
 __global__ void __launch_bounds__(kPairThreads) preference_kernel(const PreferenceParams p) {
   __shared__ double warp_s[kPairThreads / 32];
