@@ -297,7 +297,7 @@ FLCE_API flce_status flce_backward_shard(const float* dloss, const void* H, cons
  *                                   the block's largest |y| to 448 or less; q is rounded
  *                                   once, from the product itself, to nearest even.  A
  *                                   NaN stays NaN and does not count for its block's
- *                                   scale; |h w| has to stay within fp32.
+ *                                   scale; |h w| and h^2 have to stay within fp32.
  *   rstd     [T] fp32 or NULL       for the backward
  * Inputs: x [T, Hd] (row stride ldx elements), residual [T, Hd] (ldr) or NULL, each
  * bf16 or fp32 (flce_dtype), weight [Hd] bf16 or fp32.  h [T, Hd] (ldh, the
