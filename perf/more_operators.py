@@ -107,7 +107,7 @@ def _e4m3(y):
 
 
 def _e2m1(y):
-    """Packed 4-bit codes [R, 64 nb] and scale bytes [R, 4 nb] of y [R, K], nb = ceil(K / 128): the layout the
+    """Packed 4-bit codes [R, 64 nb] and scale bytes [nb, R, 4] of y [R, K], nb = ceil(K / 128): the layout the
     head's weights come in (the first of two channels in the low bits, rows padded with zeros to whole blocks)."""
     R, K = y.shape
     nb = -(-K // BLOCK)
@@ -119,7 +119,7 @@ def _e2m1(y):
     m = (torch.round(m / step) * step).clamp(max=E2M1_MAX)
     code = torch.where(m < 2.0, 2.0 * m, torch.where(m < 4.0, m + 2.0, 0.5 * m + 4.0)).to(torch.uint8)
     code = (code + torch.signbit(a).to(torch.uint8) * 8).view(R, nb * BLOCK // 2, 2)
-    return code[:, :, 0] + code[:, :, 1] * 16, (e + 127).to(torch.uint8)
+    return code[:, :, 0] + code[:, :, 1] * 16, (e + 127).to(torch.uint8).view(R, nb, 4).transpose(0, 1)
 
 
 def prepare(case, seed):
@@ -131,7 +131,7 @@ def prepare(case, seed):
         xq, e = _e4m3(x)
         parts = [_e2m1(_randn(g, min(32768, c["V"] - v), c["K"]) * 0.02) for v in range(0, c["V"], 32768)]
         return {"c": c, "xq": xq, "xs": (e + 127).to(torch.uint8), "Wq": torch.cat([p[0] for p in parts]),
-                "Ws": torch.cat([p[1] for p in parts]), "ws": torch.empty(1024, dtype=torch.uint8, device=DEV),
+                "Ws": torch.cat([p[1] for p in parts], dim=1).contiguous(), "ws": torch.empty(1024, dtype=torch.uint8, device=DEV),
                 "y": torch.empty(c["T"], c["V"], dtype=torch.bfloat16, device=DEV)}
     if c["op"] == "sample":
         T, V = c["T"], c["V"]
@@ -176,7 +176,8 @@ def run(state):
 
 
 def _dequantize_fp4(q, e, K, dtype):
-    """[R, K] values of packed codes and scale bytes."""
+    """[R, K] values of packed codes and scale bytes [nb, R, 4]."""
+    e = e.transpose(0, 1).reshape(q.shape[0], -1)
     code = torch.stack([q & 15, q >> 4], dim=2).view(q.shape[0], -1)
     m = (code & 7).to(dtype)
     m = torch.where(m < 4, 0.5 * m, torch.where(m < 6, m - 2.0, 2.0 * m - 8.0))
@@ -197,7 +198,7 @@ def _linear(s):
     x = _dequantize_fp8(s["xq"], s["xs"].int() - 127, torch.float32)
     y = torch.empty(s["c"]["T"], s["c"]["V"], dtype=torch.bfloat16, device=DEV)
     for v in range(0, s["c"]["V"], 32768):
-        W = _dequantize_fp4(s["Wq"][v:v + 32768], s["Ws"][v:v + 32768], s["c"]["K"], torch.float32)
+        W = _dequantize_fp4(s["Wq"][v:v + 32768], s["Ws"][:, v:v + 32768], s["c"]["K"], torch.float32)
         y[:, v:v + 32768] = x @ W.t()
     return y
 
@@ -290,7 +291,8 @@ def exact(case, seed):
         x = s["xq"].double() * sx
         y = torch.empty(c["T"], c["V"], dtype=torch.float64, device=DEV)
         for v in range(0, c["V"], 16384):
-            q, sw = s["Wq"][v:v + 16384].int(), torch.exp2(s["Ws"][v:v + 16384].double() - 127)
+            q = s["Wq"][v:v + 16384].int()
+            sw = torch.exp2(s["Ws"][:, v:v + 16384].double() - 127).permute(1, 0, 2).reshape(q.shape[0], 4 * nb)
             W = torch.empty(q.shape[0], nb * BLOCK, dtype=torch.float64, device=DEV)
             W[:, 0::2], W[:, 1::2] = e2m1[q % 16], e2m1[q // 16]
             W *= sw.unsqueeze(2).expand(-1, -1, GROUP).reshape(W.shape)
