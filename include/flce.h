@@ -351,6 +351,32 @@ FLCE_API flce_status flce_linear_fp8(const void* x, const uint8_t* x_scale, cons
                                      int64_t T, int64_t K, int64_t V, void* y, int32_t y_dtype, int64_t ldy,
                                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- the head's product with 4-bit weights -------------------------------------
+ * For decoding, which reading the weights bounds: as flce_linear_fp8, with half the bytes of
+ * W.  The weights are e2m1 numbers (+-0, 0.5, 1, 1.5, 2, 3, 4, 6; two to a byte, the first of
+ * two channels in its low bits) with one E8M0 scale per row and group of 32 channels.
+ *
+ * flce_quantize_fp4 lays out a matrix: a [rows, K] bf16 or fp32 (row stride lda), K a
+ * multiple of 16, kb = ceil(K/128)
+ *   q        [rows, 64 kb] bytes, filled up with zeros from channel K on; 16-byte aligned
+ *            (flce_linear_fp4 wants 32)
+ *   q_scale  [kb, rows, 4]: byte (b, r, j) is the scale of channels 128 b + 32 j .. + 31 of row r
+ * Scale rule: the smallest 2^e with amax / 2^e <= 6, -126 <= e <= 125; numbers are rounded once,
+ * to nearest even, and those above 6 2^125 saturate.  A group that holds a NaN gets the scale
+ * NaN (255) and zeros. */
+FLCE_API flce_status flce_quantize_fp4(const void* a, int32_t a_dtype, int64_t lda, int64_t rows, int64_t K, void* q,
+                                       uint8_t* q_scale, void* stream);
+
+/* y[t, v] = sum_g 2^(x_scale[t, g / 4] + W_scale[g / 4, v, g % 4] - 254) sum_{k in group g} x[t, k] W[v, k]
+ *   x [T, K] e4m3, x_scale [T, kb] as flce_linear_fp8 takes them
+ *   W [V, 64 kb] bytes, W_scale [kb, V, 4] as flce_quantize_fp4 writes them; numbers from channel K
+ *   on must be zeros and their scales not NaN.  W 32-byte aligned, W_scale 4-byte aligned
+ *   y, workspace as flce_linear_fp8's */
+FLCE_API size_t flce_linear_fp4_workspace_size(int64_t T, int64_t K, int64_t V);
+FLCE_API flce_status flce_linear_fp4(const void* x, const uint8_t* x_scale, const void* W, const uint8_t* W_scale,
+                                     int64_t T, int64_t K, int64_t V, void* y, int32_t y_dtype, int64_t ldy,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- objectives on logp ------------------------------------------------------
  * Both take the per-token log-probabilities that the forward returns and give
  * the gradient that flce_backward_logp takes as dlogp: forward, loss, backward
@@ -484,7 +510,9 @@ typedef enum flce_kernel_kind {
   FLCE_KERNEL_PREFERENCE_LOSS = 13, /* flce_preference_loss, all launches of a call */
   FLCE_KERNEL_QUANTIZE_FP8 = 14,  /* a matrix to e4m3 with block scales */
   FLCE_KERNEL_LINEAR_FP8 = 15,    /* the 8-bit head product */
-  FLCE_KERNEL_KINDS = 16
+  FLCE_KERNEL_QUANTIZE_FP4 = 16,  /* a matrix to e2m1 with group scales */
+  FLCE_KERNEL_LINEAR_FP4 = 17,    /* the head product with 4-bit weights */
+  FLCE_KERNEL_KINDS = 18
 } flce_kernel_kind;
 
 FLCE_API void flce_profile_enable(int32_t on);

@@ -779,6 +779,8 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_KERNEL_PREFERENCE_LOSS: return "preference_loss";
     case FLCE_KERNEL_QUANTIZE_FP8: return "quantize_fp8";
     case FLCE_KERNEL_LINEAR_FP8: return "linear_fp8";
+    case FLCE_KERNEL_QUANTIZE_FP4: return "quantize_fp4";
+    case FLCE_KERNEL_LINEAR_FP4: return "linear_fp4";
     default: return "unknown";
   }
 }

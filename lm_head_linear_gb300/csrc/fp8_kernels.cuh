@@ -50,10 +50,9 @@ constexpr int kBlockK = 128;                  // bytes of a K block: one swizzle
 constexpr int kRowsCta = 128;                 // vocabulary rows of one CTA: one row block of W's scales
 constexpr int kABytes = kRowsCta * kBlockK;   // 16 KB
 constexpr int kMaxN = 224;
+constexpr int kMaxN4 = 192;                   // with 4-bit weights
 constexpr int kMaxStages = 12;
 constexpr int kScaleStages = 4;
-constexpr int kScaleCols = 16;                // columns of a scale stage: A's at +0 (4), B's at +8 (8)
-constexpr int kScaleBase = 2 * kMaxN;         // 448
 constexpr int kEpiWarps = 8;   // two for each quarter of the TMEM lanes, on alternate columns
 constexpr int kScaleWarps = 4;
 constexpr int kThreads = 32 * (2 + kEpiWarps + kScaleWarps);
@@ -71,14 +70,47 @@ constexpr int kSmemLimit = 232448;
 constexpr int kStatusTimeout = 7;
 constexpr uint64_t kDrainNs = 200000000ull;   // for copies and MMAs in flight when a kernel gives up
 constexpr uint64_t kSettleNs = 200000ull;
-static_assert(kScaleBase + kScaleStages * kScaleCols <= static_cast<int>(kTmemCols), "TMEM columns");
+
+// What the kinds of weights and the two orientations differ in.
+//
+// K blocks of a stage of operands: two where 4-bit weights are on M.  A K block of them is 8 KB
+// a CTA, and the producer's and the MMA issuer's waits and commits took longer than its bytes.
+//
+// The columns of TMEM: two accumulators, then kStages stages of scale words, each of four K
+// blocks.  A word holds four bytes of a row: the scales of four K blocks (a token's, and
+// 8-bit weights', one per 128 channels), or the four of one K block (4-bit weights', one per
+// 32): A's words of K block 4 g + j at a(j), B's at b(j).
+template <bool TOKENS_M, bool W4>
+struct Form {
+  static constexpr int kStep = W4 && !TOKENS_M ? 2 : 1;
+  static constexpr int kAcc = W4 ? kMaxN4 : kMaxN;  // columns of an accumulator
+  static constexpr int kBase = 2 * kAcc;
+  static constexpr int kCols = !W4 ? 16 : TOKENS_M ? 40 : 32;
+  static constexpr int kStages = W4 && TOKENS_M ? 3 : kScaleStages;
+  __host__ __device__ static constexpr uint32_t a(uint32_t j) { return W4 && !TOKENS_M ? 4 * j : 0; }
+  __host__ __device__ static constexpr uint32_t b(uint32_t j) { return !W4 ? 8 : TOKENS_M ? 8 + 8 * j : 16; }
+  static_assert(kBase + kStages * kCols <= static_cast<int>(kTmemCols), "TMEM columns");
+};
+
+// Scale words of 4-bit weights on their way to TMEM: a ring in shared memory, kDepth stages of
+// four K blocks ahead: kWRows words of W for each K block, then kTRows of the tokens.
+template <bool TOKENS_M>
+struct Ring4 {
+  static constexpr int kWRows = TOKENS_M ? kMaxN4 : kRowsCta;
+  static constexpr int kTRows = TOKENS_M ? kRowsCta : kMaxN4;
+  static constexpr int kBytes = 4 * (4 * kWRows + kTRows);
+  static constexpr int kDepth = TOKENS_M ? 3 : 4;
+};
+constexpr int kRing4Bytes = 11264;
+static_assert(Ring4<true>::kBytes * Ring4<true>::kDepth <= kRing4Bytes && Ring4<false>::kBytes * Ring4<false>::kDepth <= kRing4Bytes,
+              "scale ring");
 
 struct Params {
   CUtensorMap tmA;   // the M side, [rows, K] bytes, box 128 x 128 rows (one token tile: x 32 rows)
   CUtensorMap tmB;   // the N side, box 128 x N / 2 rows
   CUtensorMap tmY;   // [T, v_tma] logits, box 32 logits x 32 tokens (y_tma)
   const uint8_t* sx; // [T, kb]
-  const uint8_t* sw; // [ceil(V / 128), kb]
+  const uint8_t* sw; // [ceil(V / 128), kb]; 4-bit weights: words [kb, V]
   void* y;
   int64_t ldy;
   int32_t* status;
@@ -97,6 +129,7 @@ struct Params {
 struct Smem {
   uint8_t* stages;
   uint8_t* staging;
+  uint8_t* ring;  // 4-bit weights' scales
   uint64_t* bars;
   uint32_t* tmem_slot;
   volatile int* abort_flag;
@@ -186,33 +219,42 @@ __device__ __forceinline__ void arrive_even(uint32_t bar) {
 }
 
 // Both CTAs: this CTA's 128 rows of the M side and its half of the N side.
-template <bool TOKENS_M>
+template <bool TOKENS_M, bool W4>
 __device__ __forceinline__ void producer(const Params& p, const Smem& s, const Work& w, uint32_t rank) {
   Slot at;
   uint32_t used = 0;
   bool ok = true;
   const bool small = !TOKENS_M && p.n_tiles == 1;
-  const int b_bytes = p.stage_bytes - kABytes;
+  constexpr int kStep = Form<TOKENS_M, W4>::kStep;
+  const int step_bytes = p.stage_bytes / kStep;  // of a K block
+  // The barriers count bytes as they lie in memory: a row of 128 4-bit numbers is 64.
+  constexpr int kARow = W4 && !TOKENS_M ? kBlockK / 2 : kBlockK, kBRow = W4 && TOKENS_M ? kBlockK / 2 : kBlockK;
   for (int u = w.first; u < w.count && ok; u += w.step) {
     const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
     const int n_row = un.n0 + static_cast<int>(rank) * (p.n / 2);
-    const uint32_t tx = 2u * static_cast<uint32_t>(un.boxes * 32 * kBlockK + b_bytes);
-    for (int kb = 0; kb < p.kb; ++kb) {
+    const uint32_t tx = 2u * static_cast<uint32_t>(un.boxes * 32 * kARow + p.n / 2 * kBRow);
+    for (int kb = 0; kb < p.kb; kb += kStep) {
       if (!ptx::wait_bounded_cluster(s.empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
         give_up(p, s);
         ok = false;
         break;
       }
-      if (rank == 0) ptx::mbar_arrive_expect_tx(s.full(at.i), tx);
+      const int blocks = min(kStep, p.kb - kb);
+      if (rank == 0) ptx::mbar_arrive_expect_tx(s.full(at.i), tx * blocks);
       const uint32_t full = ptx::mapa(s.full(at.i), 0);
-      const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes);
-      if (small) {
-        for (int b = 0; b < un.boxes; ++b)
-          ptx::tma_load_2d_pair(a + b * 32 * kBlockK, &p.tmA, kb * kBlockK, un.row + 32 * b, full);
-      } else {
-        ptx::tma_load_2d_pair(a, &p.tmA, kb * kBlockK, un.row, full);
+#pragma unroll
+      for (int j = 0; j < kStep; ++j) {
+        if (j >= blocks) break;
+        const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes) + j * step_bytes;
+        const int c = (kb + j) * kBlockK;
+        if (small) {
+          for (int b = 0; b < un.boxes; ++b)
+            ptx::tma_load_2d_pair(a + b * 32 * kBlockK, &p.tmA, c, un.row + 32 * b, full);
+        } else {
+          ptx::tma_load_2d_pair(a, &p.tmA, c, un.row, full);
+        }
+        ptx::tma_load_2d_pair(a + kABytes, &p.tmB, c, n_row, full);
       }
-      ptx::tma_load_2d_pair(a + kABytes, &p.tmB, kb * kBlockK, n_row, full);
       used |= 1u << at.i;
       at.next(p.stages);
     }
@@ -226,16 +268,20 @@ __device__ __forceinline__ void producer(const Params& p, const Smem& s, const W
 }
 
 // Even CTA only.
+template <bool TOKENS_M, bool W4>
 __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const Work& w, uint32_t tmem) {
+  using F = Form<TOKENS_M, W4>;
   Slot at, sc, acc;
   bool ok = true;
-  const uint32_t idesc0 = ptx::idesc_mxf8(2 * kRowsCta, static_cast<uint32_t>(p.n), 0);
+  const int step_bytes = p.stage_bytes / F::kStep;
+  const uint32_t idesc0 = ptx::idesc_mxf8(2 * kRowsCta, static_cast<uint32_t>(p.n), 0) |
+                          (!W4 ? 0u : TOKENS_M ? ptx::kIdescB2M1 : ptx::kIdescA2M1);
   for (int u = w.first; u < w.count && ok; u += w.step) {
     ok = ptx::wait_bounded_cluster(s.acc_empty(acc.i), acc.phase ^ 1u, p.timeout_ns, s.abort_flag);
     if (!ok) break;
     ptx::tc_fence_after();
-    const uint32_t d = tmem + acc.i * kMaxN;
-    for (int kb = 0; kb < p.kb; ++kb) {
+    const uint32_t d = tmem + acc.i * F::kAcc;
+    for (int kb = 0; kb < p.kb; kb += F::kStep) {
       if ((kb & 3) == 0) {
         ok = ptx::wait_bounded_cluster(s.scale_full(sc.i), sc.phase, p.timeout_ns, s.abort_flag);
         if (!ok) break;
@@ -243,20 +289,26 @@ __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const
       ok = ptx::wait_bounded(s.full(at.i), at.phase, p.timeout_ns, s.abort_flag);
       if (!ok) break;
       ptx::tc_fence_after();
-      const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes);
-      const uint32_t sf = static_cast<uint32_t>(kb & 3);
-      const uint32_t idesc = idesc0 | (sf << 4) | (sf << 29);
-      const uint32_t sfa = tmem + kScaleBase + sc.i * kScaleCols;
+      const uint32_t scales = tmem + F::kBase + sc.i * F::kCols;
 #pragma unroll
-      for (int k = 0; k < kBlockK / 32; ++k)
-        ptx::mma_mxf8_pair(d, ptx::smem_desc_sw128(a + k * 32, 16, 1024),
-                           ptx::smem_desc_sw128(a + kABytes + k * 32, 16, 1024), idesc, sfa, sfa + 8,
-                           (kb | k) != 0 ? 1u : 0u);
+      for (int j = 0; j < F::kStep; ++j) {
+        if (kb + j >= p.kb) break;
+        const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes) + j * step_bytes;
+        const uint32_t sf = static_cast<uint32_t>((kb + j) & 3);
+#pragma unroll
+        for (uint32_t k = 0; k < kBlockK / 32; ++k) {
+          // the byte of A's and of B's words
+          const uint32_t idesc = idesc0 | ((W4 && TOKENS_M ? k : sf) << 4) | ((W4 && !TOKENS_M ? k : sf) << 29);
+          ptx::mma_mxf8_pair(d, ptx::smem_desc_sw128(a + k * 32, 16, 1024),
+                             ptx::smem_desc_sw128(a + kABytes + k * 32, 16, 1024), idesc, scales + F::a(sf),
+                             scales + F::b(sf), (static_cast<uint32_t>(kb + j) | k) != 0 ? 1u : 0u);
+        }
+      }
       ptx::mma_commit_pair(s.empty(at.i), 0x3);
       at.next(p.stages);
-      if ((kb & 3) == 3 || kb == p.kb - 1) {
+      if (((kb + F::kStep) & 3) == 0 || kb + F::kStep >= p.kb) {
         ptx::mma_commit_pair(s.scale_empty(sc.i), 0x3);
-        sc.next(kScaleStages);
+        sc.next(F::kStages);
       }
     }
     if (!ok) break;
@@ -359,7 +411,7 @@ __device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, con
     };
     ptx::tc_fence_after();
     __syncwarp();
-    const uint32_t col = tmem + lanes + kScaleBase + at.i * kScaleCols;
+    const uint32_t col = tmem + lanes + Form<TOKENS_M, false>::kBase + at.i * Form<TOKENS_M, false>::kCols;
     if constexpr (TOKENS_M) {
       ptx::tmem_st4(col, tw[0], tw[1], tw[2], tw[3]);
       const uint32_t b[8] = {block_word(0), block_word(1), block_word(2), block_word(3),
@@ -385,6 +437,142 @@ __device__ __forceinline__ void scale_writer(const Params& p, const Smem& s, con
     if (!more_y || !put(y)) return;
     more_y = next(y);
   }
+}
+
+// All scale warps of the CTA: a barrier, and whether any thread passed true.
+__device__ __forceinline__ bool scale_any(bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\t"
+      "setp.ne.u32 a, %2, 0;\n\t"
+      "bar.red.or.pred b, 5, %1, a;\n\t"
+      "selp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "n"(32 * kScaleWarps), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+
+// The scale words of 4-bit weights, 16 bytes a row and stage.  They come from memory, where
+// the operands ahead of them keep every load waiting for microseconds, so they are copied
+// Ring4::kDepth stages ahead into shared memory, a quarter by each warp (W's words of K
+// block j by warp j, the tokens' by columns), and every warp then writes all of them to its
+// lanes (1 x 2048 x 124,160: 50 us with the words loaded into registers two stages ahead).
+template <bool TOKENS_M>
+__device__ __forceinline__ void scale_writer4(const Params& p, const Smem& s, const Work& w, uint32_t tmem,
+                                              uint32_t rank, int warp, int lane) {
+  using F = Form<TOKENS_M, true>;
+  using R = Ring4<TOKENS_M>;
+  constexpr int kMyTokens = (R::kTRows / 32 + kScaleWarps - 1) / kScaleWarps;
+  const int part = warp & 3;
+  const uint32_t lanes = static_cast<uint32_t>(part * 32) << 16;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(p.sw);
+  const int groups = (p.kb + 3) / 4;
+  const int64_t x_bytes = static_cast<int64_t>(p.T) * p.kb;
+  const int w_cols = TOKENS_M ? p.n / 32 : kRowsCta / 32, t_cols = TOKENS_M ? kRowsCta / 32 : p.n / 32;
+  uint32_t* ring = reinterpret_cast<uint32_t*>(s.ring);
+  constexpr int kSlotWords = R::kBytes / 4;
+
+  struct Next {
+    TwoWords t[kMyTokens];
+    int t0, g, slot;
+    bool live = false;
+  } held;
+  int u = w.first, g = 0, slot = 0;  // of the next stage to copy, and the slot it goes to
+  // W's words into the next slot; the tokens' into registers
+  const auto copy = [&]() {
+    held.live = u < w.count;
+    if (held.live) {
+      const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
+      held.t0 = TOKENS_M ? un.row : un.n0;
+      held.g = g;
+      held.slot = slot;
+      const int r0 = TOKENS_M ? un.n0 : un.row, b = 4 * g + part;
+      const uint32_t to = ptx::smem_u32(ring + slot * kSlotWords + part * R::kWRows + lane);
+#pragma unroll
+      for (int c = 0; c < R::kWRows / 32; ++c) {
+        const int row = r0 + 32 * c + lane;
+        const bool in = row < p.V && b < p.kb && c < w_cols;
+        const uint32_t* from = words + (in ? static_cast<int64_t>(b) * p.V + row : 0);
+        // past V and K: zero bytes, a scale like any other
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 128 * c), "l"(from), "r"(in ? 4 : 0) : "memory");
+      }
+#pragma unroll
+      for (int i = 0; i < kMyTokens; ++i) {
+        const int c = part + kScaleWarps * i, t = held.t0 + 32 * c + lane;
+        if (c < t_cols && t < p.T) held.t[i] = load_words(p.sx, x_bytes, static_cast<int64_t>(t) * p.kb + 4 * g);
+      }
+      if (++g == groups) g = 0, u += w.step;
+      if (++slot == R::kDepth) slot = 0;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const auto put_tokens = [&]() {  // what copy() loaded, into its slot
+    if (held.live) {
+#pragma unroll
+      for (int i = 0; i < kMyTokens; ++i) {
+        const int c = part + kScaleWarps * i, t = held.t0 + 32 * c + lane;
+        if (c < t_cols)  // rows past T meet zeros: any scale but NaN will do
+          ring[held.slot * kSlotWords + 4 * R::kWRows + 32 * c + lane] =
+              t < p.T ? bytes_of(held.t[i], p.sx, static_cast<int64_t>(t) * p.kb + 4 * held.g) : 0x7f7f7f7fu;
+      }
+      held.live = false;
+    }
+  };
+  for (int i = 0; i < R::kDepth - 1; ++i) {
+    copy();
+    put_tokens();
+  }
+
+  // One stage a turn.  At its barrier every warp's part of the stage is in its slot, and the
+  // slot of the turn before has been read by all: the stage kDepth - 1 turns on goes there.
+  // Its tokens' words follow a turn later, when they have come (kDepth >= 3).
+  static_assert(R::kDepth >= 3, "ring depth");
+  Slot at;
+  int from = 0, left = 0;
+  for (int v = w.first; v < w.count; v += w.step) left += groups;
+  for (; left > 0; --left) {
+    const bool ok = ptx::wait_bounded_cluster(s.scale_empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag);
+    asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 2) : "memory");
+    if (scale_any(!ok)) {
+      give_up(p, s);
+      break;
+    }
+    put_tokens();
+    copy();
+    const uint32_t* have = ring + from * kSlotWords + lane;
+    uint32_t ww[4][R::kWRows / 32], tw[8] = {};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int c = 0; c < R::kWRows / 32; ++c) ww[j][c] = have[j * R::kWRows + 32 * c];
+#pragma unroll
+    for (int c = 0; c < R::kTRows / 32; ++c)
+      if (c < t_cols) tw[c] = have[4 * R::kWRows + 32 * c];
+    ptx::tc_fence_after();
+    __syncwarp();
+    const uint32_t col = tmem + lanes + F::kBase + at.i * F::kCols;
+    if constexpr (TOKENS_M) {
+      ptx::tmem_st4(col + F::a(0), tw[0], tw[1], tw[2], tw[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t b[8] = {ww[j][0], ww[j][1], ww[j][2], ww[j][3], ww[j][4], ww[j][5], ww[j][5], ww[j][5]};
+        ptx::tmem_st8(col + F::b(j), b);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ptx::tmem_st4(col + F::a(j), ww[j][0], ww[j][1], ww[j][2], ww[j][3]);
+      ptx::tmem_st8(col + F::b(0), tw);
+    }
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_even(s.scale_full(at.i));
+    at.next(F::kStages);
+    if (++from == R::kDepth) from = 0;
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Staging of 32 logits of 32 tokens: token rows of 64 (fp32: 128) bytes in the TMA's
@@ -621,7 +809,7 @@ __device__ __forceinline__ void store_images(const Params& p, uint32_t image, co
 }
 
 // A warp's 32 lanes x 32 columns at a time.
-template <typename E, bool TOKENS_M>
+template <typename E, bool TOKENS_M, bool W4>
 __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const Work& w, uint32_t tmem, uint32_t rank,
                                          int warp, int lane) {
   const int q = warp & 3, part = (warp - 2) >> 2;
@@ -640,7 +828,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
     }
     __syncwarp();
     ptx::tc_fence_after();
-    const uint32_t col = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.i * kMaxN;
+    const uint32_t col = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc.i * Form<TOKENS_M, W4>::kAcc;
     const int m0 = un.row + q * 32;
     const int m_end = TOKENS_M ? p.T : p.V, n_end = TOKENS_M ? p.V : p.T;
     if (images) {
@@ -692,14 +880,16 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
   __syncwarp();
 }
 
-template <bool TOKENS_M>
+// W4: the weights are 4-bit numbers.
+template <bool TOKENS_M, bool W4>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    linear_fp8_kernel(const __grid_constant__ Params p) {
+    linear_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   Smem s;
   s.stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   s.staging = s.stages + p.stages * p.stage_bytes;
-  uint8_t* tail = s.staging + p.staging_bytes;
+  s.ring = s.staging + p.staging_bytes;
+  uint8_t* tail = s.ring + (W4 ? kRing4Bytes : 0);
   s.bars = reinterpret_cast<uint64_t*>(tail);
   s.tmem_slot = reinterpret_cast<uint32_t*>(tail + kBars * 8);
   s.abort_flag = reinterpret_cast<volatile int*>(tail + kBars * 8 + 4);
@@ -748,19 +938,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
   if (warp == 0) {
-    if (ptx::elect_one()) producer<TOKENS_M>(p, s, w, rank);
+    if (ptx::elect_one()) producer<TOKENS_M, W4>(p, s, w, rank);
     __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && ptx::elect_one()) mma_issuer(p, s, w, tmem);
+    if (rank == 0 && ptx::elect_one()) mma_issuer<TOKENS_M, W4>(p, s, w, tmem);
     __syncwarp();
   } else if (warp < 2 + kEpiWarps) {
     if (p.y_f32)
-      epilogue<float, TOKENS_M>(p, s, w, tmem, rank, warp, lane);
+      epilogue<float, TOKENS_M, W4>(p, s, w, tmem, rank, warp, lane);
     else
-      epilogue<__nv_bfloat16, TOKENS_M>(p, s, w, tmem, rank, warp, lane);
+      epilogue<__nv_bfloat16, TOKENS_M, W4>(p, s, w, tmem, rank, warp, lane);
     __syncwarp();
   } else {
-    scale_writer<TOKENS_M>(p, s, w, tmem, rank, warp, lane);
+    if constexpr (W4)
+      scale_writer4<TOKENS_M>(p, s, w, tmem, rank, warp, lane);
+    else
+      scale_writer<TOKENS_M>(p, s, w, tmem, rank, warp, lane);
     __syncwarp();
   }
 
@@ -839,6 +1032,77 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const E* a, int
       unpack8<E>(raw[i], v);
       *reinterpret_cast<uint2*>(q + r * K + c) = to_e4m3x8(v, inv_scale(e));
       if (!SQUARE && (threadIdx.x & 15) == 0) qs[r * nb + kb] = static_cast<uint8_t>(e);
+    }
+  }
+}
+
+// a [R, K] -> packed e2m1 numbers [R, 64 kb], kb = ceil(K / 128), and one E8M0 byte per row
+// and group of 32: the smallest 2^e with amax / 2^e <= 6 = 1.5 * 2^2, -126 <= e <= 125 (above,
+// 6 * 2^e is no fp32 number: it saturates).  A group with a NaN in it gets the scale NaN,
+// since e2m1 has none.  Rows are filled up to whole K blocks with zeros.
+//
+// Four threads to a group, 16 to a row's K block: the scales (q_scale [kb, R, 4]) of a
+// warp's two rows are 8 consecutive bytes.  Bound by reading a.
+__device__ __forceinline__ uint32_t e8m0_of_e2m1(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int e = static_cast<int>(bits >> 23) - 2 + ((bits & 0x7fffffu) > 0x400000u ? 1 : 0);
+  return static_cast<uint32_t>(min(max(e, 1), 252));
+}
+
+// Eight floats to e2m1, round to nearest even, the first in the low bits.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&v)[kVec], float inv) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t b;
+    asm("{\n\t.reg .b8 t;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
+        "cvt.u32.u8 %0, t;\n\t}"
+        : "=r"(b)
+        : "f"(v[2 * i + 1] * inv), "f"(v[2 * i] * inv));
+    r |= b << (8 * i);
+  }
+  return r;
+}
+
+constexpr int kQuant4Rows = kQuantThreads / 16;  // rows of a step
+constexpr int kQuant4Steps = 8;
+
+template <typename E>
+__global__ void __launch_bounds__(kQuantThreads) quantize_fp4_kernel(const E* a, int64_t lda, int64_t R, int K, uint32_t* q,
+                                                                     uint8_t* qs) {
+  const int kb = (K + 127) / 128;
+  const int64_t rb = blockIdx.x / kb;
+  const int b = static_cast<int>(blockIdx.x - rb * kb);
+  const int piece = threadIdx.x & 15, c = b * 128 + piece * kVec;
+  const int64_t r0 = rb * (kQuant4Rows * kQuant4Steps) + (threadIdx.x >> 4);
+  Raw8 raw[kQuant4Steps];
+#pragma unroll
+  for (int i = 0; i < kQuant4Steps; ++i) {
+    const int64_t r = r0 + i * kQuant4Rows;
+    if (r < R && c < K) raw[i] = load8(a + r * lda + c);
+  }
+#pragma unroll
+  for (int i = 0; i < kQuant4Steps; ++i) {
+    const int64_t r = r0 + i * kQuant4Rows;
+    float v[kVec] = {};
+    if (r < R && c < K) unpack8<E>(raw[i], v);
+    float amax = 0.0f;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      amax = fmaxf(amax, fabsf(v[j]));
+      nan = nan || v[j] != v[j];
+    }
+    uint32_t bits = nan ? 0x7fffffffu : __float_as_uint(amax);  // the largest bits of all
+    bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
+    bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
+    nan = bits > 0x7f800000u;
+    const uint32_t e = e8m0_of_e2m1(__uint_as_float(nan ? 0u : bits));
+    const uint32_t codes = nan ? 0u : to_e2m1x8(v, inv_scale(e));
+    if (r < R) {
+      q[(r * kb + b) * 16 + piece] = codes;
+      if ((piece & 3) == 0) qs[(static_cast<int64_t>(b) * R + r) * 4 + (piece >> 2)] = static_cast<uint8_t>(nan ? 255u : e);
     }
   }
 }

@@ -355,6 +355,55 @@ PyObject* linear_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------------ 4 bits
+// a, stream, out -> q, q_scale
+PyObject* quantize_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arguments(n, 3);
+    const Tensor& m = tensor(a[0], "a");
+    matrix(m, "a");
+    const OnDevice on(m.device());
+    const int64_t rows = m.size(0), K = m.size(1), kb = (K + 127) / 128;
+    const int32_t type = dtype_of(m, "a");
+    const int64_t ld = rows_of(m, "a", rows, K, m.device());
+    const Tensor q = output(a[2], "q", {rows, 64 * kb}, ScalarType::Byte, m);
+    const Tensor qs = output(a[2], "q_scale", {kb, rows, 4}, ScalarType::Float8_e8m0fnu, m);
+    check(flce_quantize_fp4(ptr(m), type, ld, rows, K, ptr(q), ptr<uint8_t>(qs), stream_of(a[1], m)));
+    return tuple_of(q, qs);
+  });
+}
+
+// x, x_scale, W, W_scale, fp32, workspace, stream, out -> y, workspace
+PyObject* linear_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arguments(n, 8);
+    const Tensor& x = tensor(a[0], "x");
+    const Tensor& xs = tensor(a[1], "x_scale");
+    const Tensor& W = tensor(a[2], "W");
+    const Tensor& Ws = tensor(a[3], "W_scale");
+    matrix(x, "x");
+    matrix(W, "W");
+    const at::Device dev = x.device();
+    const OnDevice on(dev);
+    const int64_t T = x.size(0), K = x.size(1), V = W.size(0), kb = (K + 127) / 128;
+    blocks(x, xs, "x", 1, dev);
+    if (W.scalar_type() != ScalarType::Byte || W.size(1) != 64 * kb || W.device() != dev || !W.is_contiguous())
+      bad("W must be a contiguous uint8 [V, %lld] matrix on %s, got %s", (long long)(64 * kb), dev.str().c_str(),
+          text_of(W).c_str());
+    if ((Ws.scalar_type() != ScalarType::Float8_e8m0fnu && Ws.scalar_type() != ScalarType::Byte) || Ws.dim() != 3 ||
+        Ws.size(0) != kb || Ws.size(1) != V || Ws.size(2) != 4 || Ws.device() != dev || !Ws.is_contiguous())
+      bad("W's scales must be a contiguous float8_e8m0fnu or uint8 [%lld, %lld, 4] tensor on %s, got %s", (long long)kb,
+          (long long)V, dev.str().c_str(), text_of(Ws).c_str());
+    const bool f32 = truth(a[4]);
+    int64_t ldy = 0;
+    const Tensor y = output_rows(a[7], "y", T, V, f32 ? ScalarType::Float : ScalarType::BFloat16, x, &ldy);
+    const Tensor ws = workspace_of(a[5], flce_linear_fp4_workspace_size(T, K, V), x);
+    check(flce_linear_fp4(ptr(x), ptr<uint8_t>(xs), ptr(W), ptr<uint8_t>(Ws), T, K, V, ptr(y),
+                          f32 ? FLCE_DTYPE_F32 : FLCE_DTYPE_BF16, ldy, ptr(ws), ws.numel(), stream_of(a[6], x)));
+    return tuple_of(y, ws);
+  });
+}
+
 // ------------------------------------------------------------------ losses
 const Tensor& logp_of(PyObject* o) {
   const Tensor& t = tensor(o, "logp");
@@ -464,6 +513,8 @@ PyMethodDef methods[] = {FAST(add_rms_norm),
                          FAST(add_rms_norm_backward),
                          FAST(quantize_fp8),
                          FAST(linear_fp8),
+                         FAST(quantize_fp4),
+                         FAST(linear_fp4),
                          FAST(policy_loss),
                          FAST(preference_loss),
                          {"set_check", set_check, METH_O, nullptr},

@@ -333,6 +333,9 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(uint32_t M, uint32_t N, uint32
   return (sf << 4) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24) | (sf << 29);
 }
 
+// The same with e2m1 numbers (format 5) for A or B: 16 of them in the low half of each 16 bytes.
+constexpr uint32_t kIdescA2M1 = 5u << 7, kIdescB2M1 = 5u << 10;
+
 // ---------------------------------------------------------------- math
 // 2^x on the special-function unit (the PTX ex2.approx instruction).
 __device__ __forceinline__ float ex2(float x) {

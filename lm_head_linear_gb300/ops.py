@@ -138,6 +138,32 @@ def flce_linear_fp8(x: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, W_s
     return (_OPS or load_operators()).linear_fp8(x, x_scale, W, W_scale, dtype is torch.float32, workspace, stream, out)
 
 
+def flce_quantize_fp4(a: torch.Tensor, stream=None, out: Optional[dict] = None):
+    """Run ``flce_quantize_fp4``; returns ``(q uint8 [rows, 64 kb], q_scale float8_e8m0fnu [kb, rows, 4])``,
+    kb = ceil(K / 128): two e2m1 numbers to a byte, the first of two channels in its low bits, and one scale per
+    row and 32 channels.  ``out`` may hold preallocated ``q`` and ``q_scale`` tensors."""
+    return (_OPS or load_operators()).quantize_fp4(a, stream, out)
+
+
+def flce_linear_fp4_workspace_size(T: int, K: int, V: int) -> int:
+    return int(load_library().flce_linear_fp4_workspace_size(T, K, V))
+
+
+def flce_linear_fp4(x: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, W_scale: torch.Tensor,
+                    dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None, stream=None,
+                    out: Optional[dict] = None):
+    """Run ``flce_linear_fp4``; returns ``(y [T, V], workspace)`` in ``dtype`` (bfloat16 or float32).
+
+    ``x`` and ``x_scale`` as :func:`flce_linear_fp8` takes them; ``W`` [V, 64 kb] uint8 and ``W_scale`` [kb, V, 4]
+    (float8_e8m0fnu, or its bytes as uint8) as :func:`flce_quantize_fp4` writes them.  Packed weights that come
+    with scales [V, 4 kb] need those laid out once: ``W_scale.view(V, kb, 4).transpose(0, 1).contiguous()``.
+    ``out`` may hold a preallocated ``y``, whose rows may be longer than V.
+    """
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError("dtype must be bfloat16 or float32")
+    return (_OPS or load_operators()).linear_fp4(x, x_scale, W, W_scale, dtype is torch.float32, workspace, stream, out)
+
+
 POLICY_REDUCTIONS = {"none": 0, "mean": 1, "sum": 2, "sequence_mean": 3}
 KL_KINDS = {"k1": 1, "k2": 2, "k3": 3}
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}

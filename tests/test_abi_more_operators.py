@@ -1,0 +1,31 @@
+"""Argument checks, without a device, of the 4-bit product and its quantiser: as test_abi_operators.py."""
+
+import pytest
+
+import lm_head_linear_gb300 as flce
+from test_abi_operators import LIN, OK, QUANT, call, lib  # noqa: F401 (lib is a fixture)
+
+QUANT4 = {k: v for k, v in QUANT.items() if k != "block"}
+
+CASES = [
+    ("flce_quantize_fp4", QUANT4, [
+        (1, dict(rows=-1)), (1, dict(rows=1 << 30)), (1, dict(K=0)), (1, dict(K=1 << 24)), (2, dict(K=40, lda=40)), (1, dict(dtype=2)),
+        (1, dict(A=None)), (1, dict(Q=None)), (1, dict(QS=None)), (3, dict(lda=130)), (3, dict(lda=112)), (3, dict(A=OK + 2)),
+        (3, dict(Q=OK + 8))]),
+    ("flce_linear_fp4", LIN, [
+        (1, dict(T=-1)), (1, dict(T=1 << 30)), (1, dict(V=0)), (1, dict(V=1 << 30)), (1, dict(K=0)), (1, dict(K=1 << 24)), (2, dict(K=24)),
+        (1, dict(y_dtype=2)), (1, dict(X=None)), (1, dict(XS=None)), (1, dict(W=None)), (1, dict(WS_=None)), (1, dict(Y=None)),
+        (1, dict(ldy=99)), (3, dict(X=OK + 8)), (3, dict(W=OK + 1)), (3, dict(W=OK + 16)), (3, dict(WS_=OK + 2)), (3, dict(Y=OK + 1)),
+        (4, dict(WS=None)), (4, dict(bytes=255)), (3, dict(WS=OK + 128))]),
+]
+
+
+@pytest.mark.parametrize("name,defaults,status,change", [(n, d, st, ch) for n, d, cases in CASES for st, ch in cases])
+def test_refused_on_the_host(lib, name, defaults, status, change):  # noqa: F811
+    assert call(getattr(lib, name), defaults, **change) == status
+    assert len(lib.flce_last_error()) > 0
+
+
+def test_workspace_sizes(lib):  # noqa: F811
+    assert flce.flce_linear_fp4_workspace_size(1, 2048, 124160) >= 256
+    assert flce.flce_linear_fp4_workspace_size(-1, 2048, 124160) == 0
