@@ -377,6 +377,31 @@ FLCE_API flce_status flce_linear_fp4(const void* x, const uint8_t* x_scale, cons
                                      int64_t T, int64_t K, int64_t V, void* y, int32_t y_dtype, int64_t ldy,
                                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- drawing tokens ------------------------------------------------------------
+ * One token for each row of logits, from a random number u in [0, 1) of its own, and the
+ * logarithm of the probability it was drawn with (a rollout's old_logp).  With the row's logits
+ * in descending order, equal ones by their index, and w_i = e^((l_i - max) / temperature):
+ *   top-k  keeps the first k                                           (k <= 0: all)
+ *   top-p  of those the shortest prefix whose w reach p times their sum (rounded to 53 bits),
+ *          at least one                                                (p >= 1: all)
+ *   min-p  those with w_i >= min_p w_max                               (min_p <= 0: all)
+ * and the token is the first in vocabulary order whose cumulative kept w exceeds u times
+ * the kept sum.  A temperature of 0 or less, or NaN, draws the largest logit of the lowest
+ * index (logp 0).
+ *   logits [T, V] bf16 or fp32, row stride ldl >= V elements, any alignment of their type.
+ *          -inf and NaN are never drawn (a mask); where a row has +inf those alone are.  A row
+ *          with nothing to draw gives the token ignore_index and logp 0.
+ *   u      [T] fp32; below 0 and NaN count as 0, 1 and more as the number before 1
+ *   temperature, top_k (int32), top_p, min_p: [T] of a setting for each row, or NULL: the
+ *          number behind it for all (refused where negative, NaN or above 1, other than top_k)
+ *   tokens [T] int64;  logp [T] fp32 or NULL
+ * Weights are whole multiples of 2^-44 of the largest and their sums exact, so the result does
+ * not depend on the order of summation.  V up to 393,216.  ignore_index lies outside [0, V). */
+FLCE_API flce_status flce_sample(const void* logits, int32_t dtype, int64_t ldl, const float* u, int64_t T, int64_t V,
+                                 const float* temperature, double temperature_all, const int32_t* top_k,
+                                 int64_t top_k_all, const float* top_p, double top_p_all, const float* min_p,
+                                 double min_p_all, int64_t ignore_index, int64_t* tokens, float* logp, void* stream);
+
 /* ---- objectives on logp ------------------------------------------------------
  * Both take the per-token log-probabilities that the forward returns and give
  * the gradient that flce_backward_logp takes as dlogp: forward, loss, backward
@@ -512,7 +537,8 @@ typedef enum flce_kernel_kind {
   FLCE_KERNEL_LINEAR_FP8 = 15,    /* the 8-bit head product */
   FLCE_KERNEL_QUANTIZE_FP4 = 16,  /* a matrix to e2m1 with group scales */
   FLCE_KERNEL_LINEAR_FP4 = 17,    /* the head product with 4-bit weights */
-  FLCE_KERNEL_KINDS = 18
+  FLCE_KERNEL_SAMPLE = 18,        /* tokens drawn from logits */
+  FLCE_KERNEL_KINDS = 19
 } flce_kernel_kind;
 
 FLCE_API void flce_profile_enable(int32_t on);

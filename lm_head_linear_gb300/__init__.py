@@ -52,6 +52,7 @@ from .ops import (  # noqa: F401
     flce_preference_loss_workspace_size,
     flce_quantize_fp4,
     flce_quantize_fp8,
+    flce_sample,
     load_operators,
     policy_loss,
     preference_loss,

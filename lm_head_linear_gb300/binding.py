@@ -24,7 +24,7 @@ STATUS_NAMES = {
     4: "FLCE_ERR_WORKSPACE", 5: "FLCE_ERR_CUDA", 6: "FLCE_ERR_TARGET_RANGE", 7: "FLCE_ERR_TIMEOUT",
     8: "FLCE_ERR_SEQUENCES",
 }
-KERNEL_KINDS = 18
+KERNEL_KINDS = 19
 ABI_VERSION = 2  # FLCE_ABI_VERSION of include/flce.h
 
 # Every symbol the header declares: name -> (restype, argtypes).
@@ -32,6 +32,7 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _F32 = ctypes.c_float
+_F64 = ctypes.c_double
 _SZ = ctypes.c_size_t
 SIGNATURES = {
     "flce_forward_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
@@ -66,6 +67,7 @@ SIGNATURES = {
     "flce_quantize_fp4": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _P]),
     "flce_linear_fp4_workspace_size": (_SZ, [_I64, _I64, _I64]),
     "flce_linear_fp4": (_I32, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _I32, _I64, _P, _SZ, _P]),
+    "flce_sample": (_I32, [_P, _I32, _I64, _P, _I64, _I64, _P, _F64, _P, _I64, _P, _F64, _P, _F64, _I64, _P, _P, _P]),
     "flce_policy_loss_workspace_size": (_SZ, [_I64, _I64]),
     "flce_policy_loss": (_I32, [_P, _P, _P, _P, _P, _I32, _P, _P, _I64, _I64, _I64, _I32, _F32, _F32, _F32, _F32, _I32,
                                 _P, _P, _P, _P, _P, _SZ, _P]),

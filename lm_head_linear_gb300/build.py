@@ -24,9 +24,9 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libflce.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("flce_api.cu", "flce_norm.cu", "flce_fp8.cu", "flce_losses.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("flce_api.cu", "flce_norm.cu", "flce_fp8.cu", "flce_sample.cu", "flce_losses.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
-    "flce_host.cuh", "flce_kernels.cuh", "fp8_kernels.cuh", "loss_kernels.cuh", "norm_kernels.cuh", "ptx.cuh",
+    "flce_host.cuh", "flce_kernels.cuh", "fp8_kernels.cuh", "loss_kernels.cuh", "norm_kernels.cuh", "sample_kernels.cuh", "ptx.cuh",
     "vec8.cuh")] + [
     os.path.join(INCLUDE, "flce.h")]
 

@@ -781,6 +781,7 @@ const char* flce_kernel_name(int32_t kind) {
     case FLCE_KERNEL_LINEAR_FP8: return "linear_fp8";
     case FLCE_KERNEL_QUANTIZE_FP4: return "quantize_fp4";
     case FLCE_KERNEL_LINEAR_FP4: return "linear_fp4";
+    case FLCE_KERNEL_SAMPLE: return "sample";
     default: return "unknown";
   }
 }

@@ -404,6 +404,51 @@ PyObject* linear_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------------ sampling
+// A setting of flce_sample: a tensor [T], or a number for all rows.
+template <typename E>
+const E* setting(PyObject* o, const char* name, int64_t T, ScalarType type, at::Device dev, double* all) {
+  *all = 0.0;
+  if (!THPVariable_Check(o)) {
+    *all = number(o);
+    return nullptr;
+  }
+  const Tensor& t = THPVariable_Unpack(o);
+  vector(t, name, T, type, dev);
+  return ptr<E>(t);
+}
+
+// logits, u, temperature, top_k, top_p, min_p, ignore_index, stream, out -> tokens, logp
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arguments(n, 9);
+    const Tensor& l = tensor(a[0], "logits");
+    const Tensor& u = tensor(a[1], "u");
+    matrix(l, "logits");
+    const at::Device dev = l.device();
+    const OnDevice on(dev);
+    const int64_t T = l.size(0), V = l.size(1);
+    const int32_t type = dtype_of(l, "logits");
+    const int64_t ld = rows_of(l, "logits", T, V, dev);
+    vector(u, "u", T, ScalarType::Float, dev);
+    double temperature, top_p, min_p, unused;
+    const float* ts = setting<float>(a[2], "temperature", T, ScalarType::Float, dev, &temperature);
+    int64_t top_k = 0;
+    const int32_t* ks = nullptr;
+    if (THPVariable_Check(a[3]))
+      ks = setting<int32_t>(a[3], "top_k", T, ScalarType::Int, dev, &unused);
+    else
+      top_k = integer(a[3]);
+    const float* ps = setting<float>(a[4], "top_p", T, ScalarType::Float, dev, &top_p);
+    const float* ms = setting<float>(a[5], "min_p", T, ScalarType::Float, dev, &min_p);
+    const Tensor tokens = output(a[8], "tokens", {T}, ScalarType::Long, l);
+    const Tensor logp = output(a[8], "logp", {T}, ScalarType::Float, l);
+    check(flce_sample(ptr(l), type, ld, ptr<float>(u), T, V, ts, temperature, ks, top_k, ps, top_p, ms, min_p, integer(a[6]),
+                      ptr<int64_t>(tokens), ptr<float>(logp), stream_of(a[7], l)));
+    return tuple_of(tokens, logp);
+  });
+}
+
 // ------------------------------------------------------------------ losses
 const Tensor& logp_of(PyObject* o) {
   const Tensor& t = tensor(o, "logp");
@@ -515,6 +560,7 @@ PyMethodDef methods[] = {FAST(add_rms_norm),
                          FAST(linear_fp8),
                          FAST(quantize_fp4),
                          FAST(linear_fp4),
+                         FAST(sample),
                          FAST(policy_loss),
                          FAST(preference_loss),
                          {"set_check", set_check, METH_O, nullptr},

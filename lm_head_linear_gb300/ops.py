@@ -164,6 +164,20 @@ def flce_linear_fp4(x: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, W_s
     return (_OPS or load_operators()).linear_fp4(x, x_scale, W, W_scale, dtype is torch.float32, workspace, stream, out)
 
 
+def flce_sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, ignore_index: int = -100,
+                stream=None, out: Optional[dict] = None):
+    """Run ``flce_sample``; returns ``(tokens int64 [T], logp fp32 [T])``: one token drawn for each row of
+    ``logits`` [T, V] (bfloat16 or float32, rows at any distance) with the random numbers ``u`` [T] (float32 in
+    [0, 1)), and the log of the probability it was drawn with.
+
+    ``temperature``, ``top_p``, ``min_p`` (float32) and ``top_k`` (int32) are numbers for all rows or tensors [T].
+    Temperature 0 draws the largest logit of the lowest index; top_k 0, top_p 1 and min_p 0 keep every word.  Logits
+    of -inf are never drawn; a row of nothing else gets the token ``ignore_index``, which the losses leave out.  ``out``
+    may hold preallocated ``tokens`` and ``logp`` tensors.
+    """
+    return (_OPS or load_operators()).sample(logits, u, temperature, top_k, top_p, min_p, ignore_index, stream, out)
+
+
 POLICY_REDUCTIONS = {"none": 0, "mean": 1, "sum": 2, "sequence_mean": 3}
 KL_KINDS = {"k1": 1, "k2": 2, "k3": 3}
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}

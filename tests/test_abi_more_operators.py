@@ -1,4 +1,4 @@
-"""Argument checks, without a device, of the 4-bit product and its quantiser: as test_abi_operators.py."""
+"""Argument checks, without a device, of the 4-bit product, its quantiser and the sampler: as test_abi_operators.py."""
 
 import pytest
 
@@ -6,6 +6,10 @@ import lm_head_linear_gb300 as flce
 from test_abi_operators import LIN, OK, QUANT, call, lib  # noqa: F401 (lib is a fixture)
 
 QUANT4 = {k: v for k, v in QUANT.items() if k != "block"}
+
+SAMPLE = dict(L=OK, dtype=0, ldl=100, U=OK, T=4, V=100, TEMP=None, temp=1.0, TOPK=None, k=0, TOPP=None, p=1.0, MINP=None, mp=0.0, ign=-100,
+              TOKENS=OK, LOGP=OK, STREAM=None)
+NAN = float("nan")
 
 CASES = [
     ("flce_quantize_fp4", QUANT4, [
@@ -17,6 +21,13 @@ CASES = [
         (1, dict(y_dtype=2)), (1, dict(X=None)), (1, dict(XS=None)), (1, dict(W=None)), (1, dict(WS_=None)), (1, dict(Y=None)),
         (1, dict(ldy=99)), (3, dict(X=OK + 8)), (3, dict(W=OK + 1)), (3, dict(W=OK + 16)), (3, dict(WS_=OK + 2)), (3, dict(Y=OK + 1)),
         (4, dict(WS=None)), (4, dict(bytes=255)), (3, dict(WS=OK + 128))]),
+    ("flce_sample", SAMPLE, [
+        (1, dict(T=-1)), (1, dict(T=1 << 30)), (1, dict(V=0)), (2, dict(V=393217, ldl=400000)), (1, dict(dtype=2)), (1, dict(ldl=99)),
+        (1, dict(ign=0)), (1, dict(ign=99)), (1, dict(temp=-0.1)), (1, dict(temp=NAN)), (1, dict(temp=float("inf"))), (1, dict(p=1.01)),
+        (1, dict(p=-0.01)), (1, dict(p=NAN)), (1, dict(mp=1.01)), (1, dict(mp=-0.01)), (1, dict(mp=NAN)), (1, dict(L=None)),
+        (1, dict(U=None)), (1, dict(TOKENS=None)), (3, dict(L=OK + 1)), (3, dict(L=OK + 2, dtype=1)), (3, dict(U=OK + 2)),
+        (3, dict(TEMP=OK + 2)), (3, dict(TOPK=OK + 1)), (3, dict(TOPP=OK + 3)), (3, dict(MINP=OK + 2)), (3, dict(TOKENS=OK + 4)),
+        (3, dict(LOGP=OK + 2))]),
 ]
 
 
