@@ -325,6 +325,31 @@ FLCE_API flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype
                                                 int64_t T, int64_t Hd, void* dx, float* dweight, void* workspace,
                                                 size_t workspace_bytes, void* stream);
 
+/* The norm for training with what its backward needs of h kept in 8 bits: the checkpoint takes
+ * 1 + 1/128 bytes a channel instead of h's 2 or 4, and the backward reads as much.
+ *   hq        [T, Hd] e4m3          h in 8 bits, rounded once, to nearest even
+ *   hq_scale  [T, ceil(Hd/128)]     its E8M0 bytes, by q_scale's rule
+ * h, y and rstd come from h itself and are bit-identical to flce_add_rms_norm's; y, rstd, hq and
+ * hq_scale must all be given. */
+FLCE_API flce_status flce_add_rms_norm_checkpoint(const void* x, int32_t x_dtype, int64_t ldx, const void* residual,
+                                                  int32_t residual_dtype, int64_t ldr, const void* weight,
+                                                  int32_t weight_dtype, int64_t T, int64_t Hd, float eps, void* h,
+                                                  int64_t ldh, void* y, float* rstd, void* hq, uint8_t* hq_scale,
+                                                  void* stream);
+
+/* Its backward: flce_add_rms_norm_backward with h^ = hq 2^(hq_scale - 127) in the place of h
+ * (rstd stays the forward's):
+ *   u = dy w,  dx = rstd (u - h^ rstd^2 mean_c(u h^)) + dh,  dweight = sum_t dy h^ rstd
+ * dh and dx have the type h_dtype.  An h^ is off by up to 2^-4 of h (and by 2^-10 of its scale);
+ * dx and dweight are linear in such errors to first order and their mean is 0.
+ *   workspace, workspace_bytes  >= flce_add_rms_norm_backward_workspace_size(T, Hd) */
+FLCE_API flce_status flce_add_rms_norm_checkpoint_backward(const void* dy, int32_t dy_dtype, int64_t lddy,
+                                                           const void* hq, const uint8_t* hq_scale, int32_t h_dtype,
+                                                           const void* weight, int32_t weight_dtype, const float* rstd,
+                                                           const void* dh, int64_t lddh, int64_t T, int64_t Hd, void* dx,
+                                                           float* dweight, void* workspace, size_t workspace_bytes,
+                                                           void* stream);
+
 /* ---- the head's product in 8 bits ---------------------------------------------
  * For decoding (rollouts), and where logits are wanted as such (scores of given tokens
  * without [T x V] logits are flce_score's): logits from e4m3 operands with one

@@ -42,6 +42,8 @@ from .ops import (  # noqa: F401
     flce_add_rms_norm,
     flce_add_rms_norm_backward,
     flce_add_rms_norm_backward_workspace_size,
+    flce_add_rms_norm_checkpoint,
+    flce_add_rms_norm_checkpoint_backward,
     flce_linear_fp4,
     flce_linear_fp4_workspace_size,
     flce_linear_fp8,

@@ -61,6 +61,10 @@ SIGNATURES = {
     "flce_add_rms_norm_backward_workspace_size": (_SZ, [_I64, _I64]),
     "flce_add_rms_norm_backward": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _P, _I32, _P, _P, _I64, _I64, _I64, _P, _P,
                                           _P, _SZ, _P]),
+    "flce_add_rms_norm_checkpoint": (_I32, [_P, _I32, _I64, _P, _I32, _I64, _P, _I32, _I64, _I64, _F32, _P, _I64, _P, _P, _P,
+                                            _P, _P]),
+    "flce_add_rms_norm_checkpoint_backward": (_I32, [_P, _I32, _I64, _P, _P, _I32, _P, _I32, _P, _P, _I64, _I64, _I64, _P, _P,
+                                                     _P, _SZ, _P]),
     "flce_quantize_fp8": (_I32, [_P, _I32, _I64, _I64, _I64, _I32, _P, _P, _P]),
     "flce_linear_fp8_workspace_size": (_SZ, [_I64, _I64, _I64]),
     "flce_linear_fp8": (_I32, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _I32, _I64, _P, _SZ, _P]),

@@ -38,13 +38,13 @@ Shape pick_shape(int64_t T, int64_t Hd, int sms) {
   s.threads = T > sms ? std::max(s.group, 128 / s.group * s.group) : s.group;
   return s;
 }
-template <typename TX, typename TR, bool EXACT>
+template <typename TX, typename TR, bool EXACT, bool KEEP = false>
 flce_status launch_fwd(const norm::FwdParams& p, const Shape& s, cudaStream_t st) {
   const int rows = s.threads / s.group;
   const dim3 grid(static_cast<unsigned>(cdiv(p.T, rows))), block(s.group, rows);
-  if (s.vecs == 1) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 1, 1, EXACT>, grid, block, 0, st, p);
-  if (s.vecs == 2) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 2, 1, EXACT>, grid, block, 0, st, p);
-  return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 2, 2, EXACT>, grid, block, 0, st, p);
+  if (s.vecs == 1) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 1, 1, EXACT, KEEP>, grid, block, 0, st, p);
+  if (s.vecs == 2) return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 2, 1, EXACT, KEEP>, grid, block, 0, st, p);
+  return launch_overlapped(norm::add_rms_norm_kernel<TX, TR, 2, 2, EXACT, KEEP>, grid, block, 0, st, p);
 }
 
 // The backward: four vectors per thread (two or one where they cover a row), and as many
@@ -77,7 +77,7 @@ BwdShape pick_bwd_shape(int64_t T, int64_t Hd, int64_t row_bytes, bool w_f32, in
   return s;
 }
 
-template <typename TY, typename TH, int NV, bool W32>
+template <typename TY, typename TH, int NV, bool W32, bool H8>
 flce_status launch_bwd(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, cudaStream_t st) {
   static std::mutex mu;
   static bool set[64] = {};
@@ -86,25 +86,33 @@ flce_status launch_bwd(const norm::BwdParams& p, const BwdShape& s, int64_t bloc
   {
     std::lock_guard<std::mutex> lk(mu);
     if (dev >= 0 && dev < 64 && !set[dev]) {
-      CUDA_TRY(cudaFuncSetAttribute(norm::norm_backward_kernel<TY, TH, NV, W32>,
+      CUDA_TRY(cudaFuncSetAttribute(norm::norm_backward_kernel<TY, TH, NV, W32, H8>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem));
       set[dev] = true;
     }
   }
-  return launch_overlapped(norm::norm_backward_kernel<TY, TH, NV, W32>, dim3(static_cast<unsigned>(blocks)),
+  return launch_overlapped(norm::norm_backward_kernel<TY, TH, NV, W32, H8>, dim3(static_cast<unsigned>(blocks)),
                            s.threads, s.smem, st, p);
 }
 
-template <typename TY, typename TH, bool W32>
+template <typename TY, typename TH, bool W32, bool H8>
 flce_status launch_bwd_nv(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, cudaStream_t st) {
-  if (s.nv == 1) return launch_bwd<TY, TH, 1, W32>(p, s, blocks, st);
-  if (s.nv == 2) return launch_bwd<TY, TH, 2, W32>(p, s, blocks, st);
-  return launch_bwd<TY, TH, 4, W32>(p, s, blocks, st);
+  if (s.nv == 1) return launch_bwd<TY, TH, 1, W32, H8>(p, s, blocks, st);
+  if (s.nv == 2) return launch_bwd<TY, TH, 2, W32, H8>(p, s, blocks, st);
+  return launch_bwd<TY, TH, 4, W32, H8>(p, s, blocks, st);
 }
 
-template <typename TY, typename TH>
-flce_status launch_bwd_types(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, bool w_f32, cudaStream_t st) {
-  return w_f32 ? launch_bwd_nv<TY, TH, true>(p, s, blocks, st) : launch_bwd_nv<TY, TH, false>(p, s, blocks, st);
+template <bool H8>
+flce_status launch_bwd_types(const norm::BwdParams& p, const BwdShape& s, int64_t blocks, bool y_f32, bool h_f32, bool w_f32,
+                             cudaStream_t st) {
+  const auto weights = [&](auto y, auto h) {
+    using TY = decltype(y);
+    using TH = decltype(h);
+    return w_f32 ? launch_bwd_nv<TY, TH, true, H8>(p, s, blocks, st) : launch_bwd_nv<TY, TH, false, H8>(p, s, blocks, st);
+  };
+  const float f = 0.0f;
+  const uint16_t b = 0;
+  return y_f32 ? (h_f32 ? weights(f, f) : weights(f, b)) : (h_f32 ? weights(b, f) : weights(b, b));
 }
 
 flce_status check_sizes(int64_t T, int64_t Hd) {
@@ -116,14 +124,10 @@ flce_status check_sizes(int64_t T, int64_t Hd) {
   return FLCE_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const void* residual,
-                              int32_t residual_dtype, int64_t ldr, const void* weight, int32_t weight_dtype,
-                              int64_t T, int64_t Hd, float eps, void* h, int64_t ldh, void* y, float* rstd, void* q,
-                              uint8_t* q_scale, void* stream) {
+// keep: q and q_scale are h in 8 bits, and y, rstd, q and q_scale are all wanted.
+flce_status forward(const void* x, int32_t x_dtype, int64_t ldx, const void* residual, int32_t residual_dtype,
+                    int64_t ldr, const void* weight, int32_t weight_dtype, int64_t T, int64_t Hd, float eps, void* h,
+                    int64_t ldh, void* y, float* rstd, void* q, uint8_t* q_scale, bool keep, void* stream) {
   flce_status st = check_sizes(T, Hd);
   if (st != FLCE_OK) return st;
   if (!known_dtype(x_dtype) || !known_dtype(weight_dtype) || (residual && !known_dtype(residual_dtype)))
@@ -134,6 +138,7 @@ flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const
     return fail(FLCE_ERR_INVALID_ARG, "residual and h are given together or not at all");
   if ((q != nullptr) != (q_scale != nullptr)) return fail(FLCE_ERR_INVALID_ARG, "q and q_scale are given together");
   if (T > 0 && !y && !q) return fail(FLCE_ERR_INVALID_ARG, "neither y nor q is given");
+  if (keep && T > 0 && (!y || !rstd || !q)) return fail(FLCE_ERR_INVALID_ARG, "y, rstd, hq or hq_scale is NULL");
   if (bad_ld(ldx, Hd, x_dtype) || (residual && (bad_ld(ldr, Hd, residual_dtype) || bad_ld(ldh, Hd, residual_dtype))))
     return fail(FLCE_ERR_ALIGNMENT, "row strides must be at least Hd and whole multiples of 16 bytes");
   if (off16(x) || off16(residual) || off16(weight) || off16(h) || off16(y) || off16(q))
@@ -156,7 +161,10 @@ flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const
                  n * (size_of(x_dtype) + (residual ? 2.0 * size_of(residual_dtype) : 0.0) + (y ? 2.0 : 0.0) +
                       (q ? 1.0 + 1.0 / 128 : 0.0)));
   const bool xf = x_dtype == FLCE_DTYPE_F32, rf = residual ? residual_dtype == FLCE_DTYPE_F32 : xf;
-  if (rf)  // h in fp32
+  if (keep)
+    st = rf ? (xf ? launch_fwd<float, float, false, true>(p, s, cs) : launch_fwd<uint16_t, float, false, true>(p, s, cs))
+            : (xf ? launch_fwd<float, uint16_t, false, true>(p, s, cs) : launch_fwd<uint16_t, uint16_t, false, true>(p, s, cs));
+  else if (rf)  // h in fp32
     st = xf ? launch_fwd<float, float, false>(p, s, cs) : launch_fwd<uint16_t, float, false>(p, s, cs);
   else if (p.w_f32)
     st = xf ? launch_fwd<float, uint16_t, false>(p, s, cs) : launch_fwd<uint16_t, uint16_t, false>(p, s, cs);
@@ -167,23 +175,20 @@ flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const
   return check_launch("add_rms_norm");
 }
 
-size_t flce_add_rms_norm_backward_workspace_size(int64_t T, int64_t Hd) {
-  if (T < 0 || Hd < 1) return 0;
-  return kHeaderBytes + sizeof(float) * static_cast<size_t>(std::min<int64_t>(std::max<int64_t>(T, 1), kMaxNormBlocks)) *
-                            static_cast<size_t>(Hd);
-}
-
-flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const void* h, int32_t h_dtype,
-                                       int64_t ldh, const void* weight, int32_t weight_dtype, const float* rstd,
-                                       const void* dh, int64_t lddh, int64_t T, int64_t Hd, void* dx, float* dweight,
-                                       void* workspace, size_t workspace_bytes, void* stream) {
+// H8: h is e4m3 with the scales hs (h_dtype is dh's and dx's type).
+template <bool H8>
+flce_status backward(const void* dy, int32_t dy_dtype, int64_t lddy, const void* h, const uint8_t* hs, int32_t h_dtype,
+                     int64_t ldh, const void* weight, int32_t weight_dtype, const float* rstd, const void* dh,
+                     int64_t lddh, int64_t T, int64_t Hd, void* dx, float* dweight, void* workspace,
+                     size_t workspace_bytes, void* stream) {
   flce_status st = check_sizes(T, Hd);
   if (st != FLCE_OK) return st;
   if (!known_dtype(dy_dtype) || !known_dtype(h_dtype) || !known_dtype(weight_dtype))
     return fail(FLCE_ERR_INVALID_ARG, "unknown element type");
   if (!weight || !dweight || (T > 0 && (!dy || !h || !rstd || !dx)))
     return fail(FLCE_ERR_INVALID_ARG, "dy, h, weight, rstd, dx or dweight is NULL");
-  if (bad_ld(lddy, Hd, dy_dtype) || bad_ld(ldh, Hd, h_dtype) || (dh && bad_ld(lddh, Hd, h_dtype)))
+  if (H8 && T > 0 && !hs) return fail(FLCE_ERR_INVALID_ARG, "hq_scale is NULL");
+  if (bad_ld(lddy, Hd, dy_dtype) || (!H8 && bad_ld(ldh, Hd, h_dtype)) || (dh && bad_ld(lddh, Hd, h_dtype)))
     return fail(FLCE_ERR_ALIGNMENT, "row strides must be at least Hd and whole multiples of 16 bytes");
   if (off16(dy) || off16(h) || off16(weight) || off16(dh) || off16(dx))
     return fail(FLCE_ERR_ALIGNMENT, "dy, h, weight, dh and dx must be 16-byte aligned");
@@ -203,25 +208,23 @@ flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t
     return FLCE_OK;
   }
   norm::BwdParams p{};
-  p.dy = dy, p.h = h, p.w = weight, p.rstd = rstd, p.dh = dh, p.dx = dx;
+  p.dy = dy, p.h = h, p.hs = hs, p.w = weight, p.rstd = rstd, p.dh = dh, p.dx = dx;
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kHeaderBytes);
   p.lddy = lddy, p.ldh = ldh, p.lddh = lddh, p.T = T, p.Hd = static_cast<int32_t>(Hd);
   p.inv_hd = 1.0f / static_cast<float>(Hd);
   p.status = static_cast<int32_t*>(workspace);
   p.timeout_ns = wait_limit_ns(0);
-  const BwdShape s = pick_bwd_shape(T, Hd, Hd * (size_of(dy_dtype) + (dh ? 2 : 1) * size_of(h_dtype)),
+  const BwdShape s = pick_bwd_shape(T, Hd, Hd * (size_of(dy_dtype) + (H8 ? 1 : size_of(h_dtype)) + (dh ? size_of(h_dtype) : 0)),
                                     weight_dtype == FLCE_DTYPE_F32, sms);
   p.group = s.group, p.stages = s.stages, p.w_shared = s.w_shared;
   const int64_t blocks = std::min<int64_t>(std::min<int64_t>(cdiv(T, s.threads / s.group), sms), kMaxNormBlocks);
   const double n = static_cast<double>(T) * Hd;
   {
     KernelScope ks(FLCE_KERNEL_NORM_BWD, cs, 10.0 * n,
-                   n * (size_of(dy_dtype) + (dh ? 3.0 : 2.0) * size_of(h_dtype)) + 4.0 * Hd);
-    const bool yf = dy_dtype == FLCE_DTYPE_F32, hf = h_dtype == FLCE_DTYPE_F32, wf = weight_dtype == FLCE_DTYPE_F32;
-    st = yf && hf ? launch_bwd_types<float, float>(p, s, blocks, wf, cs)
-         : yf     ? launch_bwd_types<float, uint16_t>(p, s, blocks, wf, cs)
-         : hf     ? launch_bwd_types<uint16_t, float>(p, s, blocks, wf, cs)
-                  : launch_bwd_types<uint16_t, uint16_t>(p, s, blocks, wf, cs);
+                   n * (size_of(dy_dtype) + (H8 ? 1.0 + 1.0 / 128 : size_of(h_dtype)) + (dh ? 2.0 : 1.0) * size_of(h_dtype)) +
+                       4.0 * Hd);
+    st = launch_bwd_types<H8>(p, s, blocks, dy_dtype == FLCE_DTYPE_F32, h_dtype == FLCE_DTYPE_F32,
+                              weight_dtype == FLCE_DTYPE_F32, cs);
     if (st != FLCE_OK) return st;
     ks.done();
     if ((st = check_launch("norm_bwd")) != FLCE_OK) return st;
@@ -232,6 +235,49 @@ flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t
   if (st != FLCE_OK) return st;
   ks.done();
   return check_launch("norm_dw");
+}
+
+}  // namespace
+
+extern "C" {
+
+flce_status flce_add_rms_norm(const void* x, int32_t x_dtype, int64_t ldx, const void* residual,
+                              int32_t residual_dtype, int64_t ldr, const void* weight, int32_t weight_dtype,
+                              int64_t T, int64_t Hd, float eps, void* h, int64_t ldh, void* y, float* rstd, void* q,
+                              uint8_t* q_scale, void* stream) {
+  return forward(x, x_dtype, ldx, residual, residual_dtype, ldr, weight, weight_dtype, T, Hd, eps, h, ldh, y, rstd, q,
+                 q_scale, false, stream);
+}
+
+flce_status flce_add_rms_norm_checkpoint(const void* x, int32_t x_dtype, int64_t ldx, const void* residual,
+                                         int32_t residual_dtype, int64_t ldr, const void* weight, int32_t weight_dtype,
+                                         int64_t T, int64_t Hd, float eps, void* h, int64_t ldh, void* y, float* rstd,
+                                         void* hq, uint8_t* hq_scale, void* stream) {
+  return forward(x, x_dtype, ldx, residual, residual_dtype, ldr, weight, weight_dtype, T, Hd, eps, h, ldh, y, rstd, hq,
+                 hq_scale, true, stream);
+}
+
+size_t flce_add_rms_norm_backward_workspace_size(int64_t T, int64_t Hd) {
+  if (T < 0 || Hd < 1) return 0;
+  return kHeaderBytes + sizeof(float) * static_cast<size_t>(std::min<int64_t>(std::max<int64_t>(T, 1), kMaxNormBlocks)) *
+                            static_cast<size_t>(Hd);
+}
+
+flce_status flce_add_rms_norm_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const void* h, int32_t h_dtype,
+                                       int64_t ldh, const void* weight, int32_t weight_dtype, const float* rstd,
+                                       const void* dh, int64_t lddh, int64_t T, int64_t Hd, void* dx, float* dweight,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  return backward<false>(dy, dy_dtype, lddy, h, nullptr, h_dtype, ldh, weight, weight_dtype, rstd, dh, lddh, T, Hd, dx,
+                         dweight, workspace, workspace_bytes, stream);
+}
+
+flce_status flce_add_rms_norm_checkpoint_backward(const void* dy, int32_t dy_dtype, int64_t lddy, const void* hq,
+                                                  const uint8_t* hq_scale, int32_t h_dtype, const void* weight,
+                                                  int32_t weight_dtype, const float* rstd, const void* dh, int64_t lddh,
+                                                  int64_t T, int64_t Hd, void* dx, float* dweight, void* workspace,
+                                                  size_t workspace_bytes, void* stream) {
+  return backward<true>(dy, dy_dtype, lddy, hq, hq_scale, h_dtype, Hd, weight, weight_dtype, rstd, dh, lddh, T, Hd, dx,
+                        dweight, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -65,7 +65,7 @@ struct FwdParams {
   void* h;         // residual output, or nullptr
   uint16_t* y;     // bf16 [T, Hd], or nullptr
   float* rstd;     // [T], or nullptr
-  uint8_t* q;      // e4m3 [T, Hd], or nullptr
+  uint8_t* q;      // e4m3 [T, Hd], or nullptr; KEEP: h's
   uint8_t* qs;     // E8M0 [T, ceil(Hd / 128)]
   int64_t ldx, ldr, ldh;
   int64_t T;
@@ -91,7 +91,10 @@ struct FwdParams {
 // channels go through one instruction.  Rounding to odd by both directed roundings and a
 // choice took 10 us more, and exact squares from the first on another 25: the issue
 // slots ran out.
-template <typename TX, typename TR, int NV, int B, bool EXACT>
+//
+// KEEP: q and qs are h itself in 8 bits, for the backward, and y has bf16 only.  Dividing by a
+// power of two is exact, so h is rounded once.
+template <typename TX, typename TR, int NV, int B, bool EXACT, bool KEEP>
 __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const FwdParams p) {
   constexpr int kRun = B * kVec, kRunPairs = B * kPairs, kBlockRuns = 128 / kRun;
   __shared__ Twofold red[32];
@@ -176,12 +179,36 @@ __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const
   // h w rounds off, nothing where that is exact, so what is exact stays exact.
   const uint32_t odd_bit = lo != 0.0f ? 1u : 0u;
   const int nblk = (p.Hd + 127) / 128;
+  const auto store_q = [&](const float* y, float amax, int run, bool mine) {  // all threads of the warp
+#pragma unroll
+    for (int d = kBlockRuns / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    if (mine) {
+      const uint32_t e = e8m0_of(amax);  // the odd bit of a zero is below the least scale
+      uint8_t* q = p.q + row * p.Hd + run * kRun;
+      const uint2 a = to_e4m3x8(y, inv_scale(e));
+      if constexpr (B == 2) {
+        const uint2 b = to_e4m3x8(y + kVec, inv_scale(e));
+        *reinterpret_cast<uint4*>(q) = make_uint4(a.x, a.y, b.x, b.y);
+      } else {
+        *reinterpret_cast<uint2*>(q) = a;
+      }
+      if ((i & (kBlockRuns - 1)) == 0) p.qs[row * nblk + run / kBlockRuns] = static_cast<uint8_t>(e);
+    }
+  };
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int run = i + k * group, c = run * kRun;
     const bool mine = live && c < p.Hd;
     float y[kRun];
     float amax = 0.0f;
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int j = 0; j < kRunPairs; ++j) {
+        split(v[k][j], y[2 * j], y[2 * j + 1]);
+        amax = fmaxf(amax, fmaxf(fabsf(y[2 * j]), fabsf(y[2 * j + 1])));
+      }
+      store_q(y, amax, run, mine);
+    }
     if (mine) {
       F2 rest[kRunPairs];
 #pragma unroll
@@ -204,7 +231,7 @@ __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const
           store8(p.y + row * p.Hd + c + b * kVec, pack_pairs<uint16_t>(s));
         }
       }
-      if (p.q) {  // rounded to odd; fmaxf drops NaN: the scale comes from the block's numbers, a NaN stays NaN in q
+      if (!KEEP && p.q) {  // rounded to odd; fmaxf drops NaN: the scale comes from the block's numbers, a NaN stays NaN in q
 #pragma unroll
         for (int j = 0; j < kRunPairs; ++j) split(fma2_zero(v[k][j], hi2, rest[j]), y[2 * j], y[2 * j + 1]);
         if constexpr (!EXACT) {
@@ -226,22 +253,7 @@ __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const
         }
       }
     }
-    if (p.q) {  // the same for every thread of the launch
-#pragma unroll
-      for (int d = kBlockRuns / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-      if (mine) {
-        const uint32_t e = e8m0_of(amax);  // the odd bit of a zero is below the least scale
-        uint8_t* q = p.q + row * p.Hd + c;
-        const uint2 a = to_e4m3x8(y, inv_scale(e));
-        if constexpr (B == 2) {
-          const uint2 b = to_e4m3x8(y + kVec, inv_scale(e));
-          *reinterpret_cast<uint4*>(q) = make_uint4(a.x, a.y, b.x, b.y);
-        } else {
-          *reinterpret_cast<uint2*>(q) = a;
-        }
-        if ((i & (kBlockRuns - 1)) == 0) p.qs[row * nblk + run / kBlockRuns] = static_cast<uint8_t>(e);
-      }
-    }
+    if (!KEEP && p.q) store_q(y, amax, run, mine);  // the same for every thread of the launch
   }
 }
 
@@ -270,6 +282,7 @@ constexpr int kStatusTimeout = 7;  // FLCE_ERR_TIMEOUT
 struct BwdParams {
   const void* dy;
   const void* h;
+  const uint8_t* hs;  // H8: h is e4m3 [T, Hd] with these scales
   const void* w;
   const float* rstd;
   const void* dh;     // gradient that reaches h directly, or nullptr
@@ -314,8 +327,27 @@ __device__ __forceinline__ bool group_any(int g, int threads, bool v) {
   return r != 0;
 }
 
-// W32: fp32 weights (bf16 ones always fit beside the stages).
-template <typename TY, typename TH, int NV, bool W32>
+// Eight e4m3 numbers times 2^(e8m0 - 127).
+__device__ __forceinline__ void unpack_e4m3(const uint2& q, uint32_t e8m0, F2 (&v)[kPairs]) {
+  const F2 by = both(__uint_as_float(e8m0 ? e8m0 << 23 : 1u << 22));  // (2^-127 is subnormal)
+  const uint32_t w[2] = {q.x, q.y};
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    float lo, hi;
+    asm("{\n\t.reg .b32 h;\n\t.reg .b16 a, b;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h, %2;\n\t"
+        "mov.b32 {a, b}, h;\n\t"
+        "cvt.f32.f16 %0, a;\n\t"
+        "cvt.f32.f16 %1, b;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "h"(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)))));
+    v[i] = mul2(pair(__float_as_uint(lo), __float_as_uint(hi)), by);
+  }
+}
+
+// W32: fp32 weights (bf16 ones always fit beside the stages).  H8: h in 8 bits; TH is then the
+// type of dh and dx alone.
+template <typename TY, typename TH, int NV, bool W32, bool H8>
 __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdParams p) {
   // groups x stages x (dy, h, dh rows), weights; afterwards the CTA's dw
   extern __shared__ __align__(16) uint8_t ring[];
@@ -327,7 +359,8 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
   const int warps = p.group >> 5;
   const int nvec = p.Hd / kVec;
   const uint32_t y_bytes = p.Hd * static_cast<uint32_t>(sizeof(TY)), h_bytes = p.Hd * static_cast<uint32_t>(sizeof(TH));
-  const uint32_t row_bytes = y_bytes + h_bytes + (p.dh ? h_bytes : 0u);
+  const uint32_t kept_bytes = H8 ? p.Hd : h_bytes;
+  const uint32_t row_bytes = y_bytes + kept_bytes + (p.dh ? h_bytes : 0u);
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups + g;
   uint8_t* mine = ring + static_cast<size_t>(g) * p.stages * row_bytes;
@@ -339,8 +372,11 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
     const uint32_t to = ptx::smem_u32(mine + static_cast<size_t>(slot) * row_bytes);
     ptx::mbar_arrive_expect_tx(bar, row_bytes);
     bulk_load(to, static_cast<const TY*>(p.dy) + row * p.lddy, y_bytes, bar);
-    bulk_load(to + y_bytes, static_cast<const TH*>(p.h) + row * p.ldh, h_bytes, bar);
-    if (p.dh) bulk_load(to + y_bytes + h_bytes, static_cast<const TH*>(p.dh) + row * p.lddh, h_bytes, bar);
+    if constexpr (H8)
+      bulk_load(to + y_bytes, static_cast<const uint8_t*>(p.h) + row * p.Hd, kept_bytes, bar);
+    else
+      bulk_load(to + y_bytes, static_cast<const TH*>(p.h) + row * p.ldh, h_bytes, bar);
+    if (p.dh) bulk_load(to + y_bytes + kept_bytes, static_cast<const TH*>(p.dh) + row * p.lddh, h_bytes, bar);
   };
   if (threadIdx.x == 0) {
     for (int k = 0; k < groups; ++k)
@@ -377,12 +413,27 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) acc[k][j] = 0;
   float rstd_next = row0 < p.T ? p.rstd[row0] : 0.0f;
+  const int nblk = (p.Hd + 127) / 128;
+  uint32_t scale_next[NV] = {}, scale[NV];  // H8: of this thread's vectors, a row ahead
+  const auto load_scales = [&](int64_t row) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int c = i + k * p.group;
+      if (row < p.T && c < nvec) scale_next[k] = __ldg(p.hs + row * nblk + c / (128 / kVec));
+    }
+  };
+  if constexpr (H8) load_scales(row0);
   int slot = 0;
   uint32_t phase = 0;
   bool ok = true;
   for (int64_t row = row0; row < p.T; row += step) {
     const float rstd = rstd_next;
     rstd_next = row + step < p.T ? p.rstd[row + step] : 0.0f;
+    if constexpr (H8) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) scale[k] = scale_next[k];
+      load_scales(row + step);
+    }
     ok = ptx::wait_bounded(ptx::smem_u32(bars + slot), phase, p.timeout_ns, nullptr);
     if (group_any(g, p.group, !ok)) {
       ok = false;
@@ -390,8 +441,13 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
     }
     const uint8_t* stage = mine + static_cast<size_t>(slot) * row_bytes;
     const TY* dy = reinterpret_cast<const TY*>(stage);
-    const TH* h = reinterpret_cast<const TH*>(stage + y_bytes);
-    const TH* dh = reinterpret_cast<const TH*>(stage + y_bytes + h_bytes);
+    const TH* dh = reinterpret_cast<const TH*>(stage + y_bytes + kept_bytes);
+    const auto h_pairs = [&](int c, int k, F2 (&v)[kPairs]) {
+      if constexpr (H8)
+        unpack_e4m3(*reinterpret_cast<const uint2*>(stage + y_bytes + c * kVec), scale[k], v);
+      else
+        unpack_pairs<TH>(load8(reinterpret_cast<const TH*>(stage + y_bytes) + c * kVec), v);
+    };
     // with q = dy h:  c = sum q w,  dw += q rstd
     const F2 rstd2 = both(rstd);
     F2 s2[2] = {0, 0};  // two chains
@@ -401,7 +457,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
       if (c < nvec) {
         F2 y[kPairs], hv[kPairs], w[kPairs];
         unpack_pairs<TY>(load8(dy + c * kVec), y);
-        unpack_pairs<TH>(load8(h + c * kVec), hv);
+        h_pairs(c, k, hv);
         weight_pairs(c, w);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
@@ -431,7 +487,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
       if (c < nvec) {
         F2 y[kPairs], hv[kPairs], w[kPairs], d[kPairs];
         unpack_pairs<TY>(load8(dy + c * kVec), y);
-        unpack_pairs<TH>(load8(h + c * kVec), hv);
+        h_pairs(c, k, hv);
         weight_pairs(c, w);
         if (p.dh) {
           unpack_pairs<TH>(load8(dh + c * kVec), d);

@@ -297,6 +297,79 @@ PyObject* add_rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// x, weight, residual, eps, stream, out -> y, h, rstd, hq, hq_scale
+PyObject* add_rms_norm_checkpoint(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arguments(n, 6);
+    const Tensor& x = tensor(a[0], "x");
+    const Tensor& w = tensor(a[1], "weight");
+    const Tensor* r = optional_tensor(a[2], "residual");
+    matrix(x, "x");
+    const at::Device dev = x.device();
+    const OnDevice on(dev);
+    const int64_t T = x.size(0), Hd = x.size(1);
+    const int32_t x_type = dtype_of(x, "x");
+    const int64_t ldx = rows_of(x, "x", T, Hd, dev);
+    const int32_t w_type = weight_of(w, Hd, dev);
+    PyObject* out = a[5];
+    Tensor h = x;
+    int64_t ldr = 0, ldh = 0;
+    int32_t r_type = 0;
+    if (r) {
+      r_type = dtype_of(*r, "residual");
+      ldr = rows_of(*r, "residual", T, Hd, dev);
+      h = output_rows(out, "h", T, Hd, r->scalar_type(), x, &ldh);
+    }
+    const Tensor y = output(out, "y", {T, Hd}, ScalarType::BFloat16, x);
+    const Tensor rstd = output(out, "rstd", {T}, ScalarType::Float, x);
+    const Tensor q = output(out, "hq", {T, Hd}, ScalarType::Float8_e4m3fn, x);
+    const Tensor qs = output(out, "hq_scale", {T, (Hd + 127) / 128}, ScalarType::Float8_e8m0fnu, x);
+    check(flce_add_rms_norm_checkpoint(ptr(x), x_type, ldx, ptr(r), r_type, ldr, ptr(w), w_type, T, Hd,
+                                       static_cast<float>(number(a[3])), r ? ptr(h) : nullptr, ldh, ptr(y), ptr<float>(rstd),
+                                       ptr(q), ptr<uint8_t>(qs), stream_of(a[4], x)));
+    return tuple_of(y, h, rstd, q, qs);
+  });
+}
+
+void blocks(const Tensor& q, const Tensor& s, const char* name, int64_t per, at::Device dev);
+
+// dy, hq, hq_scale, weight, rstd, dh, fp32, workspace, stream, out -> dx, dweight, workspace
+PyObject* add_rms_norm_checkpoint_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    arguments(n, 10);
+    const Tensor& dy = tensor(a[0], "dy");
+    const Tensor& q = tensor(a[1], "hq");
+    const Tensor& qs = tensor(a[2], "hq_scale");
+    const Tensor& w = tensor(a[3], "weight");
+    const Tensor& rstd = tensor(a[4], "rstd");
+    const Tensor* dh = optional_tensor(a[5], "dh");
+    matrix(q, "hq");
+    const at::Device dev = q.device();
+    const OnDevice on(dev);
+    const int64_t T = q.size(0), Hd = q.size(1);
+    blocks(q, qs, "hq", 1, dev);
+    const bool f32 = truth(a[6]);
+    const ScalarType type = f32 ? ScalarType::Float : ScalarType::BFloat16;
+    const int32_t y_type = dtype_of(dy, "dy");
+    const int64_t lddy = rows_of(dy, "dy", T, Hd, dev);
+    const int32_t w_type = weight_of(w, Hd, dev);
+    vector(rstd, "rstd", T, ScalarType::Float, dev);
+    int64_t lddh = 0;
+    if (dh) {
+      if (dh->scalar_type() != type) bad("dh must have the dtype of dx, got %s", text_of(*dh).c_str());
+      lddh = rows_of(*dh, "dh", T, Hd, dev);
+    }
+    const Tensor dx = output(a[9], "dx", {T, Hd}, type, q);
+    const Tensor dw = output(a[9], "dweight", {Hd}, ScalarType::Float, q);
+    const Tensor ws = workspace_of(a[7], flce_add_rms_norm_backward_workspace_size(T, Hd), q);
+    check(flce_add_rms_norm_checkpoint_backward(ptr(dy), y_type, lddy, ptr(q), ptr<uint8_t>(qs),
+                                                f32 ? FLCE_DTYPE_F32 : FLCE_DTYPE_BF16, ptr(w), w_type, ptr<float>(rstd),
+                                                ptr(dh), lddh, T, Hd, ptr(dx), ptr<float>(dw), ptr(ws), ws.numel(),
+                                                stream_of(a[8], q)));
+    return tuple_of(dx, dw, ws);
+  });
+}
+
 // ------------------------------------------------------------------ 8 bits
 // a, block_rows, stream, out -> q, q_scale
 PyObject* quantize_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -556,6 +629,8 @@ PyObject* set_check(PyObject*, PyObject* f) {
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(add_rms_norm),
                          FAST(add_rms_norm_backward),
+                         FAST(add_rms_norm_checkpoint),
+                         FAST(add_rms_norm_checkpoint_backward),
                          FAST(quantize_fp8),
                          FAST(linear_fp8),
                          FAST(quantize_fp4),

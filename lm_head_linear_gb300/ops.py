@@ -70,13 +70,39 @@ def flce_add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.
     return (_OPS or load_operators()).add_rms_norm_backward(dy, h, weight, rstd, dh, workspace, stream, out)
 
 
+def flce_add_rms_norm_checkpoint(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                                 eps: float = 1e-6, stream=None, out: Optional[dict] = None):
+    """Run ``flce_add_rms_norm_checkpoint``; returns ``(y, h, rstd, hq, hq_scale)``: what :func:`flce_add_rms_norm`
+    returns as y, h and rstd, and h in 8 bits for the backward (``hq`` float8_e4m3fn [T, Hd], ``hq_scale``
+    float8_e8m0fnu per 128 channels).  ``out`` may hold preallocated tensors under those names."""
+    return (_OPS or load_operators()).add_rms_norm_checkpoint(x, weight, residual, eps, stream, out)
+
+
+def flce_add_rms_norm_checkpoint_backward(dy: torch.Tensor, hq: torch.Tensor, hq_scale: torch.Tensor, weight: torch.Tensor,
+                                          rstd: torch.Tensor, dh: Optional[torch.Tensor] = None,
+                                          dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+                                          stream=None, out: Optional[dict] = None):
+    """Run ``flce_add_rms_norm_checkpoint_backward``; returns ``(dx [T, Hd] in ``dtype``, dweight [Hd] fp32, workspace)``.
+    ``dtype`` is h's (bfloat16 or float32), and ``dh``'s where that is given; the workspace has
+    :func:`flce_add_rms_norm_backward_workspace_size` bytes.  ``out`` may hold preallocated ``dx`` and ``dweight``."""
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError("dtype must be bfloat16 or float32")
+    return (_OPS or load_operators()).add_rms_norm_checkpoint_backward(dy, hq, hq_scale, weight, rstd, dh,
+                                                                       dtype is torch.float32, workspace, stream, out)
+
+
 class AddRMSNorm(torch.autograd.Function):
     """autograd wrapper of the norm: returns ``(y, h)``, both differentiable."""
 
     @staticmethod
-    def forward(ctx, x, weight, residual=None, eps: float = 1e-6):
-        y, h, rstd, _, _ = flce_add_rms_norm(x, weight, residual, eps, save_rstd=True)
-        ctx.save_for_backward(h, weight, rstd)
+    def forward(ctx, x, weight, residual=None, eps: float = 1e-6, checkpoint: bool = False):
+        if checkpoint:
+            y, h, rstd, hq, hq_scale = flce_add_rms_norm_checkpoint(x, weight, residual, eps)
+            ctx.save_for_backward(hq, hq_scale, weight, rstd)
+        else:
+            y, h, rstd, _, _ = flce_add_rms_norm(x, weight, residual, eps, save_rstd=True)
+            ctx.save_for_backward(h, weight, rstd)
+        ctx.checkpoint, ctx.h_dtype = checkpoint, h.dtype
         ctx.x_dtype = x.dtype
         ctx.has_residual = residual is not None
         ctx.set_materialize_grads(False)
@@ -89,16 +115,21 @@ class AddRMSNorm(torch.autograd.Function):
         if dy is not None:
             return AddRMSNorm._through_the_norm(ctx, dy, dh)
         if dh is None:
-            return None, None, None, None
-        return dh.to(ctx.x_dtype), None, dh if ctx.has_residual else None, None
+            return None, None, None, None, None
+        return dh.to(ctx.x_dtype), None, dh if ctx.has_residual else None, None, None
 
     @staticmethod
     @first_order
     def _through_the_norm(ctx, dy, dh):
-        h, weight, rstd = ctx.saved_tensors
-        dx, dw, _ = flce_add_rms_norm_backward(_dense_rows(dy), h, weight, rstd,
-                                               dh=None if dh is None else _dense_rows(dh.to(h.dtype)))
-        return dx.to(ctx.x_dtype), dw.to(weight.dtype), dx if ctx.has_residual else None, None
+        dh = None if dh is None else _dense_rows(dh.to(ctx.h_dtype))
+        if ctx.checkpoint:
+            hq, hq_scale, weight, rstd = ctx.saved_tensors
+            dx, dw, _ = flce_add_rms_norm_checkpoint_backward(_dense_rows(dy), hq, hq_scale, weight, rstd, dh=dh,
+                                                              dtype=ctx.h_dtype)
+        else:
+            h, weight, rstd = ctx.saved_tensors
+            dx, dw, _ = flce_add_rms_norm_backward(_dense_rows(dy), h, weight, rstd, dh=dh)
+        return dx.to(ctx.x_dtype), dw.to(weight.dtype), dx if ctx.has_residual else None, None, None
 
 
 def _dense_rows(t: torch.Tensor) -> torch.Tensor:
@@ -107,9 +138,11 @@ def _dense_rows(t: torch.Tensor) -> torch.Tensor:
         t.stride(0) * t.element_size() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
 
 
-def add_rms_norm(x, weight, residual=None, eps: float = 1e-6):
-    """``(rms_norm(x + residual) * weight, x + residual)``, differentiable in every input."""
-    return AddRMSNorm.apply(x, weight, residual, eps)
+def add_rms_norm(x, weight, residual=None, eps: float = 1e-6, checkpoint: bool = False):
+    """``(rms_norm(x + residual) * weight, x + residual)``, differentiable in every input.  With ``checkpoint`` the
+    graph holds x + residual in 8 bits (one byte a channel and a scale per 128) instead of as it is; the forward is
+    the same, and the gradients are those at the rounded values."""
+    return AddRMSNorm.apply(x, weight, residual, eps, checkpoint)
 
 
 def flce_quantize_fp8(a: torch.Tensor, block_rows: int = 128, stream=None, out: Optional[dict] = None):
