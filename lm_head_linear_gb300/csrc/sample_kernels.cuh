@@ -5,7 +5,7 @@
 //   sum, min-p those with w_i >= min_p; the token is the first in vocabulary order whose
 //   cumulative kept weight exceeds u times their sum.
 // What is kept is then all l > t and the first n, by index, of l == t: a threshold is searched
-// for, and nothing is sorted but a short list around it.
+// for, and nothing is sorted but a short list of candidates.
 //
 // The answer is a whole number that turns on comparisons of long sums, so weights are integers
 // in units of 2^-44 of the largest: their sums are exact, in whatever order they are formed, and
@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"
+#include "vec8.cuh"
 
 namespace flce {
 namespace sample {
@@ -32,12 +33,13 @@ constexpr int kMaxCtas = 16;       // of a cluster
 constexpr int kMaxThreads = 512;
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kUnit = 44;          // weights are whole multiples of 2^-44: their sum stays below 2^63
-constexpr int kBins = 2048;        // of -log2(weight), 0 .. 45
-constexpr float kLeast = -45.0f;   // weights below 2^-45 are 0
-constexpr float kBinsPerOctave = kBins / 45.0f;
+constexpr int kTable = 32;         // steps of an octave
+constexpr int kBins = 1536;        // of -32 log2(weight), rounded
+constexpr int kLive = (kUnit + 1) * kTable;  // from this bin on weights are 0
 constexpr int kList = 1024;        // candidates that are sorted
-constexpr int kTable = 32;
+constexpr int kGroups = 1024;      // whose largest logits bound the k-th largest from below
 constexpr uint32_t kAll = 0x7fffffffu;
+static_assert(kLive <= kBins && kBins % kMaxThreads == 0, "bins");
 
 struct Params {
   const void* logits;
@@ -71,48 +73,79 @@ __device__ __forceinline__ uint32_t key_of(float f) {
 __device__ __forceinline__ float float_of(uint32_t key) {
   return __uint_as_float(key ^ (key >> 31 ? 0x80000000u : 0xffffffffu));
 }
+constexpr uint32_t kMinusZero = 0x7fffffffu;  // no key: float_of() of it compares like 0, the key above it
+__device__ __forceinline__ uint32_t next_below(uint32_t key) { return key - 1 == kMinusZero ? key - 2 : key - 1; }
 
-// A row's way from a logit to its weight: w = 2^y, y = (l / 2 - max / 2) (c_hi + c_lo).  Halves:
-// the difference of two fp32 numbers need not be one.
+// A row's way from a logit to its weight: w = 2^-z, z = (l / 2 - max / 2) (-c_hi - c_lo).  Halves:
+// the difference of two fp32 numbers need not be one.  (A row whose largest logit is
+// infinite is rewritten first, so max is finite.)
 struct Scale {
   float half_max, c_hi, c_lo;
 };
+constexpr float kMagic = 393216.0f;  // 1.5 2^18: sums with it round to whole multiples of 1/32
+constexpr float kMostZ = 63.0f;      // l = -inf, and NaN where c is 0
 
-// y, not below -64; -inf (whatever l is infinitely below max) and NaN give -64.
-__device__ __forceinline__ float log2_weight(float l, const Scale& s, float& d) {
-  d = fminf(fmaf(l, 0.5f, -s.half_max), 0.0f);  // NaN where both are infinite: 0, the weight 1
-  return fmaxf(d * s.c_hi, -64.0f);
+// Two logits' weights in units of 2^-44, and their bins, n = round(32 z).
+struct Weights {
+  U64 w[2];
+  int n[2];
+};
+// `lane_table`: this lane's column of the table of powers, which is there once for every lane so
+// that no two lanes meet in a bank.
+template <typename E>
+__device__ __forceinline__ Weights weights(float l0, float l1, const Scale& s, const uint2* lane_table) {
+  const F2 l = pair(__float_as_uint(l0), __float_as_uint(l1)), minus = both(-1.0f), c = both(s.c_hi);
+  const F2 d = fma2(l, both(0.5f), both(-s.half_max));
+  const F2 z = mul2(d, both(-s.c_hi));
+  F2 lo = fma2(d, both(s.c_lo), fma2(d, c, z));
+  if constexpr (sizeof(E) == 4) {  // what d rounds off; bf16 logits lose nothing that counts
+    const F2 h = mul2(l, both(0.5f)), b = fma2(h, minus, d);
+    lo = fma2(add2(fma2(fma2(b, minus, d), minus, h), fma2(b, minus, both(-s.half_max))), c, lo);
+  }
+  float z0, z1;
+  split(z, z0, z1);
+  z0 = fminf(z0, kMostZ), z1 = fminf(z1, kMostZ);
+  const F2 zz = pair(__float_as_uint(z0), __float_as_uint(z1));
+  const F2 t = fma2(zz, minus, both(kMagic));
+  // |r| <= 1/64, exact but for lo; NaN where l is infinite
+  const F2 r = add2(fma2(zz, minus, fma2(t, minus, both(kMagic))), lo);
+  // 2^r - 1, off by less than 2^-32.8: a polynomial fitted to it (least largest error on |r| <= 1/64)
+  const F2 p = mul2(r, fma2(r, fma2(r, both(0.05550457f), both(0.24022846f)), both(0.6931472f)));
+  float t0, t1;
+  split(t, t0, t1);
+  Weights out;
+  out.n[0] = __float_as_int(kMagic) - __float_as_int(t0);
+  out.n[1] = __float_as_int(kMagic) - __float_as_int(t1);
+  const uint2 e0 = lane_table[(out.n[0] & (kTable - 1)) * 32], e1 = lane_table[(out.n[1] & (kTable - 1)) * 32];
+  float q[2];
+  split(mul2(pair(e0.y, e1.y), p), q[0], q[1]);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = (i ? e1.x : e0.x) + static_cast<uint32_t>(__float2int_rn(q[i]));  // 2^31 of the octave
+    const int shift = ((out.n[i] + kTable - 1) >> 5) + (63 - kUnit);
+    asm("shr.u64 %0, %1, %2;" : "=l"(out.w[i]) : "l"(static_cast<U64>(w) << 32), "r"(shift));  // 0 from 64 on
+  }
+  return out;
 }
-
-// The weight in units of 2^-44.  `lane_table`: this lane's column of the table, which is there
-// once for every lane so that no two lanes meet in a bank.
 template <typename E>
 __device__ __forceinline__ U64 weight(float l, const Scale& s, const uint2* lane_table) {
-  constexpr float kMagic = 393216.0f;  // 1.5 2^18: sums round to whole multiples of 1/32
-  float d;
-  const float y = log2_weight(l, s, d);
-  const float yh = d * s.c_hi;
-  float lo = fmaf(d, s.c_lo, fmaf(d, s.c_hi, -yh));
-  if constexpr (sizeof(E) == 4) {  // what l - max rounds off; bf16 logits lose nothing that counts
-    const float h = 0.5f * l, b = d - h;
-    lo = fmaf((h - (d - b)) + (-s.half_max - b), s.c_hi, lo);
-  }
-  const float t = y + kMagic;
-  const float r = (y - (t - kMagic)) + lo;  // |r| <= 1/64 (the difference is exact); NaN where l or max is infinite
-  const int bits = __float_as_int(t);
-  const uint2 entry = lane_table[(bits & (kTable - 1)) * 32];
-  // 2^r - 1, off by less than 2^-32.8: a polynomial fitted to it (least largest error on |r| <= 1/64)
-  const float p = r * fmaf(r, fmaf(r, 0.05550457f, 0.24022846f), 0.6931472f);
-  const uint32_t w = entry.x + static_cast<uint32_t>(__float2int_rn(__uint_as_float(entry.y) * p));
-  const int shift = (__float_as_int(kMagic) - bits + kTable - 1) >> 5;  // whole octaves below 1: 0 .. 64
-  return (static_cast<U64>(w) << (kUnit - 31)) >> min(shift, 63);
+  return weights<E>(l, l, s, lane_table).w[0];
 }
 
-// Its bin, kBins and more where it is 0.
+// The same bin on its own.
 __device__ __forceinline__ int bin_of(float l, const Scale& s) {
-  float d;
-  const float y = log2_weight(l, s, d);
-  return y > kLeast ? min(static_cast<int>(-y * kBinsPerOctave), kBins - 1) : kBins;
+  const float z = fminf(fmaf(l, 0.5f, -s.half_max) * -s.c_hi, kMostZ);
+  return __float_as_int(kMagic) - __float_as_int(kMagic - z);
+}
+// The lowest logit of bins up to b (bins fall as logits rise).
+__device__ __forceinline__ float lowest_in(int b, const Scale& s) {
+  uint32_t lo = 0x007fffffu, hi = key_of(2.0f * s.half_max);  // -inf, the largest logit: bin 0
+  while (lo < hi) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    if (bin_of(float_of(mid), s) <= b) hi = mid;
+    else lo = mid + 1;
+  }
+  return float_of(hi);
 }
 
 // ------------------------------------------------------------------ 16-byte pieces
@@ -142,6 +175,30 @@ __device__ __forceinline__ Piece<E> unpack(const uint4& a) {
   return r;
 }
 
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+
+// The larger of `best` and a piece's logits; `nan` if one of them is none (best is then unknown).
+template <typename E>
+__device__ __forceinline__ void largest(const uint4& a, float& best, bool& nan) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  float m;
+  if constexpr (sizeof(E) == 4) {
+    float x, y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(x) : "f"(__uint_as_float(w[0])), "f"(__uint_as_float(w[1])));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(__uint_as_float(w[2])), "f"(__uint_as_float(w[3])));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(x), "f"(y));
+  } else {
+    uint32_t x, y;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[0]), "r"(w[1]));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(w[2]), "r"(w[3]));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(y));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(__uint_as_float(x << 16)), "f"(__uint_as_float(x & 0xffff0000u)));
+  }
+  nan = nan || m != m;
+  best = fmaxf(best, m);
+}
+
 // ------------------------------------------------------------------ the cluster
 struct Two {
   U64 a, b;
@@ -167,7 +224,6 @@ struct Shared {
   double inv_t, least;
   float c_hi, c_lo;
   uint32_t listed, found[3];
-  U64 found_mass;
 };
 
 template <typename T>
@@ -251,8 +307,11 @@ __device__ __forceinline__ U64 share_up(double f, U64 m) { return __double2ull_r
 __device__ __forceinline__ U64 share_down(U64 f, U64 m) { return __umul64hi(f, m) << 1 | (f * m) >> 63; }
 
 // ------------------------------------------------------------------ the kernel
+// The pieces of a CTA's part of a row: 16 bytes as they lie in memory; what a piece holds before
+// or behind the row counts as -inf.  A warp has a stretch of its own, and its lanes read back
+// what they have copied themselves.
 template <typename E>
-__global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
+__global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) {
   constexpr int kPer = Piece<E>::kPer;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
@@ -260,23 +319,22 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
   uint2* const table = reinterpret_cast<uint2*>(smem + static_cast<size_t>(p.chunk) * 16);
   uint32_t* const bins = reinterpret_cast<uint32_t*>(table + kTable * 32);
   U64* const list = reinterpret_cast<U64*>(bins + kBins);
-  U64* const mass_of = list + kList;
+  U64* const mass_of = list + kList;                               // sums of the sorted list's weights
+  uint32_t* const group_max = reinterpret_cast<uint32_t*>(mass_of);  // before that: of every group of the row
 
   const int threads = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
   Cluster cl{p.ctas, static_cast<int>(blockIdx.x % p.ctas), &sh, 0, 0};
+  if (p.ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // for the wait below
   const int64_t row = blockIdx.x / p.ctas;
   const uint2* const lane_table = table + lane;
 
-  for (int i = tid; i < kTable * 32; i += threads) {
-    const uint32_t t = kPow2[i / 32];
+  for (int i = tid; i < kTable * 32; i += threads) {  // entry m: 2^(-m / 32) in its octave
+    const uint32_t t = kPow2[(kTable - i / 32) & (kTable - 1)];
     table[i] = make_uint2(t, __float_as_uint(static_cast<float>(t)));
   }
   ptx::launch_dependents();
   ptx::wait_prerequisites();
 
-  // This CTA's part of the row: pieces of 16 bytes as they lie in memory; what a piece holds
-  // before or behind the row counts as -inf.  A warp has a stretch of its own, and its lanes
-  // read back what they have copied themselves.
   const E* const logits = static_cast<const E*>(p.logits) + row * p.ldl;
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(logits) & 15) / static_cast<int>(sizeof(E));
   const int all_pieces = (off + p.V + kPer - 1) / kPer;
@@ -284,23 +342,21 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
   const int mine = max(0, min(p.chunk, all_pieces - first));
   const int stretch = ((p.chunk + warps - 1) / warps + 31) / 32 * 32;
   const int w0 = warp * stretch, w1 = min(w0 + stretch, mine);
-  const E* const aligned = logits - off;
   for (int i = w0 + lane; i < w1; i += 32) {
     const int64_t at = static_cast<int64_t>(first + i) * kPer - off;  // the piece's first logit
     if (at >= 0 && at + kPer <= p.V) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(pieces + i)), "l"(aligned + at + off)
-                   : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(pieces + i)), "l"(logits + at) : "memory");
     } else {
 #pragma unroll
       for (int e = 0; e < kPer; ++e)
-        reinterpret_cast<E*>(pieces + i)[e] =
-            at + e >= 0 && at + e < p.V ? logits[at + e] : lowest<E>();
+        reinterpret_cast<E*>(pieces + i)[e] = at + e >= 0 && at + e < p.V ? logits[at + e] : lowest<E>();
     }
   }
   const double temperature = p.temperature ? p.temperature[row] : p.temperature_all;
   const int64_t top_k = p.top_k ? p.top_k[row] : p.top_k_all;
   const double top_p = p.top_p ? p.top_p[row] : p.top_p_all;
   const double min_p = p.min_p ? p.min_p[row] : p.min_p_all;
+  const float u = p.u[row];
   const bool greedy = !(temperature > 0.0) || top_k == 1 || top_p <= 0.0;
   const bool by_k = top_k > 0, by_p = top_p < 1.0, by_min = min_p > 0.0;
   if (tid == 0) {
@@ -315,22 +371,35 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
   float best = -INFINITY;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const Piece<E> l = unpack<E>(pieces[i]);
-    bool nan = false;
+  bool nan = false;
+  for (int i = w0 + lane; i < w1; i += 32) largest<E>(pieces[i], best, nan);
+  if (__any_sync(0xffffffffu, nan)) {  // never drawn
+    best = -INFINITY;
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const Piece<E> l = unpack<E>(pieces[i]);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      best = fmaxf(best, l.v[e]);
-      nan = nan || l.v[e] != l.v[e];
-    }
-    if (nan) {  // never drawn
-#pragma unroll
-      for (int e = 0; e < kPer; ++e)
+      for (int e = 0; e < kPer; ++e) {
         if (l.v[e] != l.v[e]) reinterpret_cast<E*>(pieces + i)[e] = lowest<E>();
+        best = fmaxf(best, l.v[e]);
+      }
     }
   }
-  cl.sync();  // the others' shared memory is there
-  const float row_max = float_of(static_cast<uint32_t>(cl.all<MaxMin>(Two{key_of(best), ~0ull}).a));
+  if (p.ctas > 1) {  // the others' shared memory is there
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  // The largest logits of up to 1024 groups of the row, to every CTA: at least k logits are no
+  // smaller than the k-th largest of them.
+  const int groups = min(threads, kGroups / p.ctas);  // of a CTA
+  const bool short_k = !greedy && by_k && top_k <= groups * p.ctas;
+  if (short_k) {
+    float g = best;
+    const int lanes = threads / groups;  // a power of two
+    for (int d = lanes / 2; d > 0; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
+    for (int r = tid & (lanes - 1); r < p.ctas; r += lanes) peer(group_max, r)[cl.rank * groups + tid / lanes] = key_of(g);
+  }
+  float row_max = float_of(static_cast<uint32_t>(cl.all<MaxMin>(Two{key_of(best), ~0ull}).a));
+  const float real_max = row_max;
   if (row_max == -INFINITY) {  // nothing to draw
     if (cl.rank == 0 && tid == 0) {
       p.tokens[row] = p.ignore_index;
@@ -338,57 +407,95 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
     }
     return;
   }
+  if (row_max == INFINITY) {  // the infinite ones alone, as equals
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const Piece<E> l = unpack<E>(pieces[i]);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) reinterpret_cast<E*>(pieces + i)[e] = l.v[e] == INFINITY ? static_cast<E>(0) : lowest<E>();
+    }
+    row_max = 0.0f;
+  }
   const Scale sc{0.5f * row_max, sh.c_hi, sh.c_lo};
-  const auto each = [&](auto f) {  // every logit of this thread's and its piece's number
+  const float least = by_min ? fminf(__double2float_ru(static_cast<double>(row_max) + sh.least), row_max) : -INFINITY;
+  const auto each = [&](auto f) {  // every logit of this thread's and its number
     for (int i = w0 + lane; i < w1; i += 32) {
       const Piece<E> l = unpack<E>(pieces[i]);
 #pragma unroll
       for (int e = 0; e < kPer; ++e) f(l.v[e], (first + i) * kPer + e - off);
     }
   };
+  const auto each_weight = [&](auto f) {  // f(l, weight, bin)
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const Piece<E> l = unpack<E>(pieces[i]);
+#pragma unroll
+      for (int e = 0; e < kPer; e += 2) {
+        const Weights w = weights<E>(l.v[e], l.v[e + 1], sc, lane_table);
+        f(l.v[e], w.w[0], w.n[0]);
+        f(l.v[e + 1], w.w[1], w.n[1]);
+      }
+    }
+  };
+  const auto write = [&](int64_t token, U64 total) {  // one thread: the token, and log(its weight / total)
+    p.tokens[row] = token;
+    if (!p.logp) return;
+    // the weight's from the logit; of the total the exponent, the leading 24 bits, and the rest apart
+    const int top = 63 - __clzll(total);
+    const U64 bits = total << (63 - top);
+    const float lead = __ull2float_rz(bits);
+    const float rest = static_cast<float>(bits - static_cast<U64>(lead)) / lead;
+    const float drawn = as_float(logits[token]);
+    const double d = drawn == real_max ? 0.0 : static_cast<double>(drawn) - static_cast<double>(real_max);
+    const double log_total = static_cast<double>(top - kUnit) * 0.6931471805599453 + (static_cast<double>(logf(lead * 0x1p-63f)) + rest);
+    p.logp[row] = greedy ? 0.0f : static_cast<float>(d * sh.inv_t - log_total);
+  };
+  const U64 u_share = u > 0.0f ? static_cast<U64>(fminf(u, 0x1.fffffep-1f) * 0x1p63f) : 0;
 
-  // What is kept: l > t, and the first n of l == t.
-  float t = -INFINITY;
-  uint32_t n = 0;
-  if (greedy) t = row_max, n = 1;
-
-  // The candidates' list, best first, on the first CTA: the elements `in` selects, `m` of them.
-  const auto gather_list = [&](auto in) {
+  // ---- the list: logits from `low` on, unsorted, on the first CTA.  Returns how many there are.
+  const auto gather_list = [&](float low, float high) -> U64 {
+    U64 count = 0;
     each([&](float l, int index) {
-      if (in(l)) {
+      if (l >= low && l <= high) {
         const uint32_t at = atomicAdd(peer(&sh.listed, 0), 1u);
         if (at < kList) *peer(list + at, 0) = static_cast<U64>(key_of(l)) << 32 | (0xffffffffu - static_cast<uint32_t>(index));
+        ++count;
       }
     });
-    cl.sync();
+    return cl.all<Sum>(Two{count, 0}).a;
   };
-  // On the first CTA: sorts the list and gives mass_of[] the sums of its weights up to each.
-  const auto sort_list = [&]() -> int {
-    const int m = min(static_cast<int>(sh.listed), kList);
+  const auto listed = [&](U64 count) { return static_cast<int>(count < kList ? count : kList); };
+  const auto key_in_list = [&](int i) { return float_of(static_cast<uint32_t>(list[i] >> 32)); };
+  // Sorts m numbers, the largest first; all threads of a CTA.
+  const auto sort = [&](U64* a, int m) {
     int size = 32;
     while (size < m) size *= 2;
-    for (int i = m + tid; i < size; i += threads) list[i] = 0;
+    for (int i = m + tid; i < size; i += threads) a[i] = 0;
     __syncthreads();
-    for (int k = 2; k <= size; k *= 2)
-      for (int j = k / 2; j > 0; j /= 2) {
-        for (int i = tid; i < size / 2; i += threads) {
-          const int a = (i / j) * 2 * j + i % j, b = a + j;
-          const U64 x = list[a], y = list[b];
-          if ((x < y) == ((a & k) == 0)) list[a] = y, list[b] = x;
+    const bool one_warp = size <= 128;  // without block barriers
+    const int step = one_warp ? 32 : threads;
+    if (!one_warp || warp == 0) {
+      for (int k = 2; k <= size; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+          for (int i = tid; i < size / 2; i += step) {
+            const int x = 2 * i - (i & (j - 1)), y = x + j;
+            const U64 vx = a[x], vy = a[y];
+            if ((vx < vy) == ((x & k) == 0)) a[x] = vy, a[y] = vx;
+          }
+          if (one_warp) __syncwarp();
+          else __syncthreads();
         }
-        __syncthreads();
-      }
-    const int per = (m + threads - 1) / threads;
-    U64 sum = 0;
-    for (int i = tid * per; i < min((tid + 1) * per, m); ++i) sum += weight<E>(float_of(static_cast<uint32_t>(list[i] >> 32)), sc, lane_table);
-    U64 run = block_before(sum, &sh);
-    for (int i = tid * per; i < min((tid + 1) * per, m); ++i)
-      mass_of[i] = run += weight<E>(float_of(static_cast<uint32_t>(list[i] >> 32)), sc, lane_table);
-    if (tid == 0) sh.listed = 0, sh.found[0] = static_cast<uint32_t>(m);
+    }
     __syncthreads();
-    return m;
   };
-  // The shortest prefix of the first m of the list whose weights reach `need`.
+  // The sums of the sorted list's weights up to each.
+  const auto sum_list = [&](int m) {
+    const int per = (m + threads - 1) / threads, a = min(tid * per, m), b = min(a + per, m);
+    U64 sum = 0;
+    for (int i = a; i < b; ++i) sum += weight<E>(key_in_list(i), sc, lane_table);
+    U64 run = block_before(sum, &sh);
+    for (int i = a; i < b; ++i) mass_of[i] = run += weight<E>(key_in_list(i), sc, lane_table);
+    __syncthreads();
+  };
+  // How many of the first m of the list it takes for weights of `need`.
   const auto prefix_of = [&](int m, U64 need) -> int {
     __syncthreads();
     if (tid == 0) sh.found[0] = static_cast<uint32_t>(m);
@@ -398,30 +505,92 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
     __syncthreads();
     return static_cast<int>(sh.found[0]);
   };
-  // The first `m` of the list as a threshold: every thread of the first CTA has it.
-  const auto plan_of = [&](int m, U64 mass) {
-    const uint32_t last = static_cast<uint32_t>(list[m - 1] >> 32);
+  // The first CTA: top-k (k > 0), top-p (need > 0: the weights wanted; all of top_p otherwise) and
+  // min-p on the list of m, which holds all of them, and the draw.
+  const auto draw_from_list = [&](int m, int64_t k, U64 need) {
+    sort(list, m);
+    sum_list(m);
+    if (k > 0 && k < m) m = static_cast<int>(k);
+    if (by_p) m = prefix_of(m, need ? need : share_up(top_p, mass_of[m - 1]));
+    if (by_min) {  // a prefix as well
+      __syncthreads();
+      if (tid == 0) sh.found[0] = static_cast<uint32_t>(m);
+      __syncthreads();
+      for (int i = tid; i < m; i += threads)
+        if (key_in_list(i) < least && (i == 0 || key_in_list(i - 1) >= least)) sh.found[0] = static_cast<uint32_t>(i);
+      __syncthreads();
+      m = static_cast<int>(sh.found[0]);
+    }
+    const U64 total = mass_of[m - 1], target = share_down(u_share, total);
+    // by index, the first first, each with its weight behind it: 19 and 45 bits
     __syncthreads();
-    if (tid == 0) sh.found[1] = 0;
-    __syncthreads();
-    uint32_t equal = 0;
-    for (int i = tid; i < m; i += threads) equal += static_cast<uint32_t>(list[i] >> 32) == last ? 1u : 0u;
-    if (equal) atomicAdd(&sh.found[1], equal);
-    __syncthreads();
-    return Plan{mass, last, sh.found[1], 0};
+    for (int i = tid; i < m; i += threads) {
+      const U64 w = mass_of[i] - (i ? mass_of[i - 1] : 0);
+      list[i] = list[i] << 45 | w;  // of ~index
+    }
+    sort(list, m);
+    const int per = (m + threads - 1) / threads, a = min(tid * per, m), b = min(a + per, m);
+    constexpr U64 kWeight = (1ull << 45) - 1;
+    U64 sum = 0;
+    for (int i = a; i < b; ++i) sum += list[i] & kWeight;
+    U64 run = block_before(sum, &sh);
+    for (int i = a; i < b; ++i) {
+      const U64 next = run + (list[i] & kWeight);
+      if (run <= target && target < next) write(static_cast<int64_t>(~(list[i] >> 45) & 0x7ffffu), total);
+      run = next;
+    }
   };
 
+  // ---- what is kept: l > t, and the first n of l == t.  `own`: this thread's weights of l > sure,
+  // known already (sure: +inf if none).
+  float t = -INFINITY, sure = INFINITY;
+  uint32_t n = 0;
+  Two own{0, 0};
+  if (greedy) t = row_max, n = 1;
+
   if (!greedy && (by_k || by_p)) {
-    // How many logits fall into each of 2048 bins of log2(weight), and the sum of weights.
+    if (short_k && row_max == real_max) {
+      // Every CTA finds the same bound.
+      for (int i = tid; i < kBins; i += threads) bins[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < groups * p.ctas; i += threads) {
+        const int b = bin_of(float_of(group_max[i]), sc);
+        if (static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u);
+      }
+      const int per = kBins / threads;
+      __syncthreads();
+      U64 count = 0;
+      for (int i = tid * per; i < (tid + 1) * per; ++i) count += bins[i];
+      U64 run = block_before(count, &sh);
+      if (tid == 0) sh.found[0] = kBins;
+      __syncthreads();
+      if (run < static_cast<U64>(top_k) && run + count >= static_cast<U64>(top_k))
+        for (int i = tid * per; i < (tid + 1) * per; ++i) {
+          if (run < static_cast<U64>(top_k) && run + bins[i] >= static_cast<U64>(top_k)) sh.found[0] = i;
+          run += bins[i];
+        }
+      __syncthreads();
+      const int b = static_cast<int>(sh.found[0]);
+      if (b < kBins) {
+        const U64 m = gather_list(lowest_in(b, sc), INFINITY);
+        if (m <= kList) {
+          if (cl.rank == 0) draw_from_list(listed(m), top_k, 0);
+          return;
+        }
+        __syncthreads();
+        if (tid == 0) sh.listed = 0;  // seen by the others after the next barrier
+      }
+    }
+    // How many logits fall into each bin, and the sum of weights.
+    __syncthreads();
     for (int i = tid; i < kBins; i += threads) bins[i] = 0;
     __syncthreads();
     U64 sum = 0;
-    each([&](float l, int) {
-      const int b = bin_of(l, sc);
-      if (b < kBins) atomicAdd(bins + b, 1u);
-      if (!by_k) sum += weight<E>(l, sc, lane_table);
+    each_weight([&](float, U64 w, int b) {
+      if (static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u);
+      sum += w;
     });
-    U64 total = cl.all<Sum>(Two{sum, 0}).a;  // everything that has a weight; with top-k: of the first k, later
+    U64 total = cl.all<Sum>(Two{sum, 0}).a;  // with top-k: of the first k, later
     // The first CTA adds up the bins of all: bins[b] = how many lie in bins up to b.
     const int per = kBins / threads;
     if (cl.rank == 0) {
@@ -436,12 +605,13 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
       for (int i = tid * per; i < (tid + 1) * per; ++i) bins[i] = run += bins[i];
       __syncthreads();
     }
-    // Bins [a, b] that hold the end of the shortest prefix with `need` logits, or weights, and
-    // how many lie up to b.
+    // Bins [a, b] that hold the end of the shortest prefix with `need` logits, or weights; how
+    // many lie up to b, and in all.
     const auto bracket = [&](bool mass, U64 need) {
       Plan plan{0, 0, 0, 0};
       if (cl.rank == 0) {
-        if (tid == 0) sh.found[0] = sh.found[1] = kBins - 1;
+        __syncthreads();
+        if (tid == 0) sh.found[0] = sh.found[1] = kLive - 1;  // not behind: nothing has been counted there
         __syncthreads();
         if (!mass) {
           for (int i = tid; i < kBins; i += threads)
@@ -450,9 +620,9 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
           for (int side = 0; side < 2; ++side) {
             const auto bound = [&](int i) -> U64 {
               const uint32_t c = bins[i] - (i ? bins[i - 1] : 0u);
-              const float w = ptx::ex2(static_cast<float>(-i - side) * (1.0f / kBinsPerOctave)) * (side ? 1.0f - 0x1p-15f : 1.0f + 0x1p-15f);
-              const U64 each_one = static_cast<U64>(w * 0x1p44f);
-              return c * (side ? (each_one ? each_one - 1 : 0) : each_one + 2);
+              const float w = ptx::ex2((static_cast<float>(-i - side) + 0.5f) * (1.0f / kTable)) * (side ? 1.0f - 0x1p-15f : 1.0f + 0x1p-15f);
+              const U64 one = static_cast<U64>(w * 0x1p44f);
+              return c * (side ? (one ? one - 1 : 0) : one + 2);
             };
             U64 here = 0;
             for (int i = tid * per; i < (tid + 1) * per; ++i) here += bound(i);
@@ -473,117 +643,139 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
     // The end of that prefix, where more logits share its bins than can be sorted: bisection of
     // their values.  Returns the threshold, how many of its equals, and the prefix's weight.
     const auto bisect = [&](bool by_mass, U64 need, const Plan& in) {
-      const int b1 = static_cast<int>(in.a), b2 = static_cast<int>(in.b);
-      Two above{0, 0}, range{0, ~0ull};
+      const float low = lowest_in(static_cast<int>(in.b), sc);
+      const uint32_t top_key = in.a ? key_of(lowest_in(static_cast<int>(in.a) - 1, sc)) : 0xffffffffu;  // above the bracket
+      sure = in.a ? float_of(next_below(top_key)) : INFINITY;
+      own = Two{0, 0};
       U64 count = 0;
-      each([&](float l, int) {
-        const int b = bin_of(l, sc);
-        if (b < b1) {
-          above.a += weight<E>(l, sc, lane_table), ++above.b;
-        } else if (b <= b2) {
-          ++count;
-          const U64 k = key_of(l);
-          range = MaxMin::of(range, Two{k, k});
+      Two range{0, ~0ull};
+      const float over = sure;
+      for (int i = w0 + lane; i < w1; i += 32) {
+        const Piece<E> l = unpack<E>(pieces[i]);
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          any = any || l.v[e] > over;
+          if (l.v[e] >= low && l.v[e] <= over) {
+            ++count;
+            const U64 k = key_of(l.v[e]);
+            range = MaxMin::of(range, Two{k, k});
+          }
         }
-      });
-      above = cl.all<Sum>(above);
+        if (any) {
+#pragma unroll
+          for (int e = 0; e < kPer; e += 2) {
+            const Weights w = weights<E>(l.v[e], l.v[e + 1], sc, lane_table);
+            if (l.v[e] > over) own.a += w.w[0], ++own.b;
+            if (l.v[e + 1] > over) own.a += w.w[1], ++own.b;
+          }
+        }
+      }
+      Two above = cl.all<Sum>(own);
       count = cl.all<Sum>(Two{count, 0}).a;
       range = cl.all<MaxMin>(range);
       uint32_t hi = static_cast<uint32_t>(range.a), lo = static_cast<uint32_t>(range.b);
       while (count > kList && lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;  // (mid, hi] or [lo, mid]
-        Two top{0, 0};
+        uint32_t mid = lo + (hi - lo) / 2;  // (mid, hi] or [lo, mid]
+        if (mid == kMinusZero) --mid;
+        const float a = float_of(mid), b = float_of(hi);
+        Two here{0, 0};
         each([&](float l, int) {
-          const uint32_t k = key_of(l);
-          if (k > mid && k <= hi) top.a += weight<E>(l, sc, lane_table), ++top.b;
+          if (l > a && l <= b) here.a += weight<E>(l, sc, lane_table), ++here.b;
         });
-        top = cl.all<Sum>(top);
-        if ((by_mass ? above.a + top.a : above.b + top.b) >= need)
+        const Two top = cl.all<Sum>(here);
+        if ((by_mass ? above.a + top.a : above.b + top.b) >= need) {
           lo = mid + 1, count = top.b;
-        else
+          if (lo == kMinusZero) ++lo;
+        } else {
           hi = mid, count -= top.b, above = Sum::of(above, top);
+          own = Sum::of(own, here), sure = a;
+        }
       }
-      Plan plan{0, 0, 0, 0};
       if (lo >= hi) {  // equal ones
         const U64 w = weight<E>(float_of(hi), sc, lane_table);
         U64 equal = by_mass ? (w ? (need - above.a + w - 1) / w : 1) : need - above.b;
         equal = equal < 1 ? 1 : equal > count ? count : equal;
         return Plan{above.a + equal * w, hi, static_cast<uint32_t>(equal), 0};
       }
-      gather_list([&](float l) {
-        const uint32_t k = key_of(l);
-        return k >= lo && k <= hi;
-      });
+      const int m = listed(gather_list(float_of(lo), float_of(hi)));
+      Plan plan{0, 0, 0, 0};
       if (cl.rank == 0) {
-        const int m = sort_list();
+        sort(list, m);
+        sum_list(m);
         const int end = by_mass ? prefix_of(m, need - above.a) : min(m, static_cast<int>(need - above.b));
-        plan = plan_of(end, above.a + mass_of[end - 1]);
+        const uint32_t last = static_cast<uint32_t>(list[end - 1] >> 32);
+        if (tid == 0) sh.found[1] = 0, sh.listed = 0;
+        __syncthreads();
+        uint32_t equal = 0;
+        for (int i = tid; i < end; i += threads) equal += static_cast<uint32_t>(list[i] >> 32) == last ? 1u : 0u;
+        if (equal) atomicAdd(&sh.found[1], equal);
+        __syncthreads();
+        plan = Plan{above.a + mass_of[end - 1], last, sh.found[1], 0};
       }
       return cl.tell(plan);
     };
 
     Plan end{0, 0, 0, 0};
-    bool found = false, done = !by_p;
+    bool found = false;
     if (by_k) {
       const Plan in = bracket(false, static_cast<U64>(top_k));
-      if (static_cast<U64>(top_k) >= in.mass) {  // all that have a weight
-        if (by_p) {
-          sum = 0;
-          each([&](float l, int) { sum += weight<E>(l, sc, lane_table); });
-          total = cl.all<Sum>(Two{sum, 0}).a;
+      if (static_cast<U64>(top_k) < in.mass) {  // else all that have a weight
+        if (in.c <= kList) {
+          const U64 m = gather_list(lowest_in(static_cast<int>(in.b), sc), INFINITY);
+          if (cl.rank == 0) draw_from_list(listed(m), top_k, 0);
+          return;
         }
-      } else if (in.c <= kList) {  // top-p with it
-        gather_list([&](float l) { return bin_of(l, sc) <= static_cast<int>(in.b); });
-        Plan plan{0, 0, 0, 0};
-        if (cl.rank == 0) {
-          sort_list();
-          int m = static_cast<int>(top_k);
-          if (by_p) m = prefix_of(m, share_up(top_p, mass_of[m - 1]));
-          plan = plan_of(m, mass_of[m - 1]);
-        }
-        end = cl.tell(plan);
-        found = done = true;
-      } else {
         end = bisect(false, static_cast<U64>(top_k), in);
         total = end.mass;
         found = true;
       }
     }
-    if (!done) {
+    if (by_p) {
       const U64 need = share_up(top_p, total);
       const Plan in = bracket(true, need);
       if (in.c <= kList) {
-        gather_list([&](float l) { return bin_of(l, sc) <= static_cast<int>(in.b); });
-        Plan plan{0, 0, 0, 0};
-        if (cl.rank == 0) {
-          const int m = prefix_of(sort_list(), need);
-          plan = plan_of(m, mass_of[m - 1]);
-        }
-        end = cl.tell(plan);
-      } else {
-        end = bisect(true, need, in);
+        const U64 m = gather_list(lowest_in(static_cast<int>(in.b), sc), INFINITY);
+        if (cl.rank == 0) draw_from_list(listed(m), 0, need);
+        return;
       }
+      end = bisect(true, need, in);
       found = true;
     }
     if (found) t = float_of(end.a), n = end.b;
   }
-  if (!greedy && by_min) {
-    const float least = fminf(__double2float_ru(static_cast<double>(row_max) + sh.least), row_max);
-    if (least > t) t = least, n = kAll;
-  }
+  if (!greedy && by_min && least > t) t = least, n = kAll;
 
-  // The kept weights of every warp's stretch, and the draw.
-  Two own{0, 0};
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const Piece<E> l = unpack<E>(pieces[i]);
+  // The kept weights of a piece, but those of l > sure.
+  const auto kept_of = [&](const Piece<E>& l, float known) {
+    Two v{0, 0};
+    if (t == -INFINITY && known == INFINITY) {
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (l.v[e] > t)
-        own.a += weight<E>(l.v[e], sc, lane_table);
-      else if (l.v[e] == t)
-        ++own.b;
+      for (int e = 0; e < kPer; e += 2) {
+        const Weights w = weights<E>(l.v[e], l.v[e + 1], sc, lane_table);
+        v.a += w.w[0] + w.w[1];
+      }
+    } else {
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        any = any || (l.v[e] > t && l.v[e] <= known);
+        if (l.v[e] == t) ++v.b;
+      }
+      if (any) {
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          const Weights w = weights<E>(l.v[e], l.v[e + 1], sc, lane_table);
+          if (l.v[e] > t && l.v[e] <= known) v.a += w.w[0];
+          if (l.v[e + 1] > t && l.v[e + 1] <= known) v.a += w.w[1];
+        }
+      }
     }
-  }
+    return v;
+  };
+  if (t > sure) sure = INFINITY, own = Two{0, 0};  // min-p cut into what was known
+  own.b = 0;
+  for (int i = w0 + lane; i < w1; i += 32) own = Sum::of(own, kept_of(unpack<E>(pieces[i]), sure));
   const Two* from = cl.gather<Sum>(own);
   const U64 w_t = n ? weight<E>(t, sc, lane_table) : 0;
   const auto kept = [&](const Two& s) { return s.a + (s.b < n ? s.b : static_cast<U64>(n)) * w_t; };
@@ -592,9 +784,7 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
     if (i == cl.rank) before = all;
     all = Sum::of(all, from[i]);
   }
-  const U64 total = kept(all);
-  const float u = p.u[row];
-  const U64 target = share_down(u > 0.0f ? static_cast<U64>(fminf(u, 0x1.fffffep-1f) * 0x1p63f) : 0, total);
+  const U64 total = kept(all), target = share_down(u_share, total);
   for (int i = 0; i < warp; ++i) before = Sum::of(before, sh.part[i]);
   const Two here = Sum::of(before, sh.part[warp]);
   if (!(kept(before) <= target && target < kept(here))) return;  // another warp's stretch
@@ -602,16 +792,7 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
     const int i = i0 + lane;
     Two v{0, 0};
     Piece<E> l;
-    if (i < w1) {
-      l = unpack<E>(pieces[i]);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        if (l.v[e] > t)
-          v.a += weight<E>(l.v[e], sc, lane_table);
-        else if (l.v[e] == t)
-          ++v.b;
-      }
-    }
+    if (i < w1) l = unpack<E>(pieces[i]), v = kept_of(l, INFINITY);
     Two incl = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -622,28 +803,14 @@ __global__ void __launch_bounds__(kMaxThreads) sample_kernel(const Params p) {
     if (past) {
       if (lane == __ffs(past) - 1) {
         Two run{before.a + incl.a - v.a, before.b + incl.b - v.b};
-        float drawn = 0.0f;
         int e_drawn = -1;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-          if (l.v[e] > t)
-            run.a += weight<E>(l.v[e], sc, lane_table);
-          else if (l.v[e] == t)
-            ++run.b;
-          if (e_drawn < 0 && kept(run) > target) e_drawn = e, drawn = l.v[e];
+          if (l.v[e] > t) run.a += weight<E>(l.v[e], sc, lane_table);
+          else if (l.v[e] == t) ++run.b;
+          if (e_drawn < 0 && kept(run) > target) e_drawn = e;
         }
-        p.tokens[row] = static_cast<int64_t>(first + i) * kPer + e_drawn - off;
-        if (p.logp) {
-          // log(weight / total): of the total the exponent, the leading 24 bits, and the rest apart
-          const int top = 63 - __clzll(total);
-          const U64 bits = total << (63 - top);
-          const float lead = __ull2float_rz(bits);
-          const float rest = static_cast<float>(bits - static_cast<U64>(lead)) / lead;
-          const double d = drawn == row_max ? 0.0 : static_cast<double>(drawn) - static_cast<double>(row_max);
-          const double log_total =
-              static_cast<double>(top - kUnit) * 0.6931471805599453 + (static_cast<double>(logf(lead * 0x1p-63f)) + rest);
-          p.logp[row] = greedy ? 0.0f : static_cast<float>(d * sh.inv_t - log_total);
-        }
+        write(static_cast<int64_t>(first + i) * kPer + e_drawn - off, total);
       }
       return;
     }

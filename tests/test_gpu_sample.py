@@ -148,6 +148,21 @@ def test_masks_infinities_and_nan(cuda_device, dtype):
     assert tokens[0] == -1 and tokens[1] == -1 and logp[0] == 0 and tokens[2] == 4321
 
 
+@pytest.mark.parametrize("V", [4097, 40000, 250000])
+@pytest.mark.parametrize("octaves", [44.2, 45.1, 46.5, 47.9, 60.0])
+def test_words_without_a_weight(cuda_device, V, octaves):
+    """Few words with a weight and thousands just below the least one."""
+    l = torch.full((4, V), -octaves * math.log(2.0), device=cuda_device)
+    l[:, 17] = 0.0
+    l[1, 1000:1400] = -1.0
+    l[2, ::5] = -octaves * math.log(2.0) + 0.01
+    l[3, 1::3] = float("-inf")
+    u = torch.tensor([0.3, 0.9, 0.5, 0.999], device=cuda_device)
+    for s in (dict(p=0.995), dict(k=2000, p=0.995), dict(k=700, p=0.999), dict(k=2000), dict(k=30), dict(p=0.5)):
+        check(l, u, **s)
+        check(l * 0.3, u, temp=0.3, **s)
+
+
 def test_random_numbers_out_of_range(cuda_device):
     l, _ = rows_of(8, 1000, cuda_device, F32, seed=3)
     l = l[:1].expand(8, 1000).contiguous()
