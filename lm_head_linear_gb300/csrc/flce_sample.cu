@@ -105,6 +105,9 @@ flce_status flce_sample(const void* logits, int32_t dtype, int64_t ldl, const fl
   sample::Params p{};
   p.logits = logits, p.u = u, p.temperature = temperature, p.top_k = top_k, p.top_p = top_p, p.min_p = min_p;
   p.temperature_all = temperature_all, p.top_k_all = top_k_all, p.top_p_all = top_p_all, p.min_p_all = min_p_all;
+  p.temperature_like = temperature_all > 0.0 ? 1.0f : 0.0f;
+  p.top_p_like = top_p_all <= 0.0 ? 0.0f : top_p_all < 1.0 ? 0.5f : 1.0f;
+  p.min_p_like = min_p_all > 0.0 ? 0.5f : 0.0f;
   p.ldl = ldl, p.ignore_index = ignore_index, p.tokens = tokens, p.logp = logp, p.V = static_cast<int32_t>(V);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   KernelScope ks(FLCE_KERNEL_SAMPLE, s, 4.0 * T * V, T * (V * (dtype == FLCE_DTYPE_F32 ? 4.0 : 2.0) + 16.0));

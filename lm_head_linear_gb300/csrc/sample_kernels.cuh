@@ -10,7 +10,7 @@
 // The answer is a whole number that turns on comparisons of long sums, so weights are integers
 // in units of 2^-44 of the largest: their sums are exact, in whatever order they are formed, and
 // the sum that the search compares is the one that the drawing walks through.  A weight itself
-// is good to 2^-31 (table-driven exponential after Tang, 1989): a draw among 250,000
+// is good to 2^-31 of it and 2^-44 (table-driven exponential after Tang, 1989): a draw among 250,000
 // equally likely words then falls on the other side of a border about once in a million.
 //
 // A row belongs to a cluster of CTAs, each with its part in shared memory: the logits are
@@ -22,7 +22,6 @@
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"
-#include "vec8.cuh"
 
 namespace flce {
 namespace sample {
@@ -35,7 +34,7 @@ constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kUnit = 44;          // weights are whole multiples of 2^-44: their sum stays below 2^63
 constexpr int kTable = 32;         // steps of an octave
 constexpr int kBins = 1536;        // of -32 log2(weight), rounded
-constexpr int kLive = (kUnit + 1) * kTable;  // from this bin on weights are 0
+constexpr int kLive = (kUnit + 1) * kTable + 1;  // from this bin on weights are 0
 constexpr int kList = 1024;        // candidates that are sorted
 constexpr int kGroups = 1024;      // whose largest logits bound the k-th largest from below
 constexpr uint32_t kAll = 0x7fffffffu;
@@ -49,6 +48,7 @@ struct Params {
   const float* top_p;
   const float* min_p;
   double temperature_all, top_p_all, min_p_all;
+  float temperature_like, top_p_like, min_p_like;  // numbers that compare as those do with 0 and 1
   int64_t top_k_all;
   int64_t ldl, ignore_index;
   int64_t* tokens;
@@ -78,68 +78,61 @@ __device__ __forceinline__ uint32_t next_below(uint32_t key) { return key - 1 ==
 
 // A row's way from a logit to its weight: w = 2^-z, z = (l / 2 - max / 2) (-c_hi - c_lo).  Halves:
 // the difference of two fp32 numbers need not be one.  (A row whose largest logit is
-// infinite is rewritten first, so max is finite.)
+// infinite is rewritten first, so max is finite.)  Differences below `least` count as that: z = 64,
+// the weight 0, also of l = -inf.  Where c is so small that no finite difference gets there,
+// the row is flat(), and -inf has to be told from the others by its value.
 struct Scale {
-  float half_max, c_hi, c_lo;
+  float half_max, c_hi, c_lo, least;
+  __device__ __forceinline__ bool flat() const { return c_hi < 2.0e-37f; }
 };
 constexpr float kMagic = 393216.0f;  // 1.5 2^18: sums with it round to whole multiples of 1/32
-constexpr float kMostZ = 63.0f;      // l = -inf, and NaN where c is 0
 
-// Two logits' weights in units of 2^-44, and their bins, n = round(32 z).
-struct Weights {
-  U64 w[2];
-  int n[2];
+// A logit's weight in units of 2^-44, and its bin, n = round(32 z).  `lane_table`: this lane's
+// column of the table of powers, which is there once for every lane so that no two lanes meet
+// in a bank.
+//
+// 30 cycles of a lane for bf16, 40 for fp32 (1.9 GHz, two logits' worth of registers in flight).  Packed
+// pairs of fp32 with the sum kept as two fp32 numbers, which saves the 64-bit shift and
+// addition, took 33 and 42: their constants need two registers each.
+struct Weight {
+  U64 w;
+  int n;
 };
-// `lane_table`: this lane's column of the table of powers, which is there once for every lane so
-// that no two lanes meet in a bank.
 template <typename E>
-__device__ __forceinline__ Weights weights(float l0, float l1, const Scale& s, const uint2* lane_table) {
-  const F2 l = pair(__float_as_uint(l0), __float_as_uint(l1)), minus = both(-1.0f), c = both(s.c_hi);
-  const F2 d = fma2(l, both(0.5f), both(-s.half_max));
-  const F2 z = mul2(d, both(-s.c_hi));
-  F2 lo = fma2(d, both(s.c_lo), fma2(d, c, z));
+__device__ __forceinline__ Weight weigh(float l, const Scale& s, const uint2* lane_table) {
+  const float d = fmaf(l, 0.5f, -s.half_max), dd = fmaxf(d, s.least);
+  const float z = dd * -s.c_hi;
+  float rest = fmaf(dd, s.c_lo, fmaf(dd, s.c_hi, z));
   if constexpr (sizeof(E) == 4) {  // what d rounds off; bf16 logits lose nothing that counts
-    const F2 h = mul2(l, both(0.5f)), b = fma2(h, minus, d);
-    lo = fma2(add2(fma2(fma2(b, minus, d), minus, h), fma2(b, minus, both(-s.half_max))), c, lo);
+    const float h = 0.5f * l, b = d - h;
+    const float off = ((h - (d - b)) + (-s.half_max - b)) * s.c_hi;
+    rest += fmaxf(off, -1.0f);  // far below 1; NaN where l is infinite
   }
-  float z0, z1;
-  split(z, z0, z1);
-  z0 = fminf(z0, kMostZ), z1 = fminf(z1, kMostZ);
-  const F2 zz = pair(__float_as_uint(z0), __float_as_uint(z1));
-  const F2 t = fma2(zz, minus, both(kMagic));
-  // |r| <= 1/64, exact but for lo; NaN where l is infinite
-  const F2 r = add2(fma2(zz, minus, fma2(t, minus, both(kMagic))), lo);
+  const float t = kMagic - z;
+  const float r = ((kMagic - t) - z) + rest;  // |r| <= 1/64, exact but for the rest
   // 2^r - 1, off by less than 2^-32.8: a polynomial fitted to it (least largest error on |r| <= 1/64)
-  const F2 p = mul2(r, fma2(r, fma2(r, both(0.05550457f), both(0.24022846f)), both(0.6931472f)));
-  float t0, t1;
-  split(t, t0, t1);
-  Weights out;
-  out.n[0] = __float_as_int(kMagic) - __float_as_int(t0);
-  out.n[1] = __float_as_int(kMagic) - __float_as_int(t1);
-  const uint2 e0 = lane_table[(out.n[0] & (kTable - 1)) * 32], e1 = lane_table[(out.n[1] & (kTable - 1)) * 32];
-  float q[2];
-  split(mul2(pair(e0.y, e1.y), p), q[0], q[1]);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t w = (i ? e1.x : e0.x) + static_cast<uint32_t>(__float2int_rn(q[i]));  // 2^31 of the octave
-    const int shift = ((out.n[i] + kTable - 1) >> 5) + (63 - kUnit);
-    asm("shr.u64 %0, %1, %2;" : "=l"(out.w[i]) : "l"(static_cast<U64>(w) << 32), "r"(shift));  // 0 from 64 on
-  }
+  const float p = r * fmaf(r, fmaf(r, 0.05550457f, 0.24022846f), 0.6931472f);
+  const int up = __float_as_int(kMagic) + (kTable - 1) - __float_as_int(t);  // n + 31
+  const uint2 power = lane_table[(up & (kTable - 1)) * 32];
+  const uint32_t w = power.x + static_cast<uint32_t>(__float2int_rn(__uint_as_float(power.y) * p));  // 2^31 of its octave
+  Weight out;
+  out.n = up - (kTable - 1);
+  asm("shr.u64 %0, %1, %2;" : "=l"(out.w) : "l"(static_cast<U64>(w) << 32), "r"((up >> 5) + (63 - kUnit)));  // 0 from 64 on
   return out;
 }
 template <typename E>
 __device__ __forceinline__ U64 weight(float l, const Scale& s, const uint2* lane_table) {
-  return weights<E>(l, l, s, lane_table).w[0];
+  return weigh<E>(l, s, lane_table).w;
 }
 
 // The same bin on its own.
 __device__ __forceinline__ int bin_of(float l, const Scale& s) {
-  const float z = fminf(fmaf(l, 0.5f, -s.half_max) * -s.c_hi, kMostZ);
+  const float z = fmaxf(fmaf(l, 0.5f, -s.half_max), s.least) * -s.c_hi;
   return __float_as_int(kMagic) - __float_as_int(kMagic - z);
 }
-// The lowest logit of bins up to b (bins fall as logits rise).
+// The lowest logit of bins up to b (bins fall as logits rise), not -inf.
 __device__ __forceinline__ float lowest_in(int b, const Scale& s) {
-  uint32_t lo = 0x007fffffu, hi = key_of(2.0f * s.half_max);  // -inf, the largest logit: bin 0
+  uint32_t lo = 0x00800000u, hi = key_of(2.0f * s.half_max);  // the lowest number, the largest logit: bin 0
   while (lo < hi) {
     const uint32_t mid = lo + (hi - lo) / 2;
     if (bin_of(float_of(mid), s) <= b) hi = mid;
@@ -221,8 +214,9 @@ struct Shared {
   Two part[kMaxWarps];
   Two from[2][kMaxCtas];
   Plan plan[2];
-  double inv_t, least;
-  float c_hi, c_lo;
+  double inv_t, log_min;
+  U64 need;
+  float c_hi, c_lo, least, min_logit;
   uint32_t listed, found[3];
 };
 
@@ -328,8 +322,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   const int64_t row = blockIdx.x / p.ctas;
   const uint2* const lane_table = table + lane;
 
-  for (int i = tid; i < kTable * 32; i += threads) {  // entry m: 2^(-m / 32) in its octave
-    const uint32_t t = kPow2[(kTable - i / 32) & (kTable - 1)];
+  for (int i = tid; i < kTable * 32; i += threads) {  // entry m: 2^((31 - m) / 32), for n + 31 = m modulo 32
+    const uint32_t t = kPow2[kTable - 1 - i / 32];
     table[i] = make_uint2(t, __float_as_uint(static_cast<float>(t)));
   }
   ptx::launch_dependents();
@@ -352,20 +346,24 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
         reinterpret_cast<E*>(pieces + i)[e] = at + e >= 0 && at + e < p.V ? logits[at + e] : lowest<E>();
     }
   }
-  const double temperature = p.temperature ? p.temperature[row] : p.temperature_all;
+  // In 32 bits what every thread needs; 64-bit arithmetic, of which an SM does two a cycle, is
+  // one thread's (256 x 124,160 fp32: 20 us less).
+  const float temperature = p.temperature ? p.temperature[row] : p.temperature_like;
   const int64_t top_k = p.top_k ? p.top_k[row] : p.top_k_all;
-  const double top_p = p.top_p ? p.top_p[row] : p.top_p_all;
-  const double min_p = p.min_p ? p.min_p[row] : p.min_p_all;
+  const float top_p = p.top_p ? p.top_p[row] : p.top_p_like;
+  const float min_p = p.min_p ? p.min_p[row] : p.min_p_like;
   const float u = p.u[row];
-  const bool greedy = !(temperature > 0.0) || top_k == 1 || top_p <= 0.0;
-  const bool by_k = top_k > 0, by_p = top_p < 1.0, by_min = min_p > 0.0;
+  const bool greedy = !(temperature > 0.0f) || top_k == 1 || top_p <= 0.0f;
+  const bool by_k = top_k > 0, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
   if (tid == 0) {
-    const double inv = temperature > 0.0 ? fmin(1.0 / temperature, 1e37) : 1.0;
+    const double t = p.temperature ? static_cast<double>(temperature) : p.temperature_all;
+    const double inv = greedy ? 1.0 : fmin(1.0 / t, 1e37);
     const double c = inv * (2.0 * 1.4426950408889634);
     sh.inv_t = inv;
     sh.c_hi = static_cast<float>(c);
     sh.c_lo = static_cast<float>(c - static_cast<double>(sh.c_hi));
-    sh.least = by_min && !greedy ? temperature * log(min_p) : 0.0;
+    sh.least = fmaxf(-64.0f / sh.c_hi, -3.4028234e38f);
+    sh.log_min = by_min && !greedy ? t * log(p.min_p ? static_cast<double>(min_p) : p.min_p_all) : 0.0;
     sh.listed = 0;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -415,8 +413,13 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
     }
     row_max = 0.0f;
   }
-  const Scale sc{0.5f * row_max, sh.c_hi, sh.c_lo};
-  const float least = by_min ? fminf(__double2float_ru(static_cast<double>(row_max) + sh.least), row_max) : -INFINITY;
+  const Scale sc{0.5f * row_max, sh.c_hi, sh.c_lo, sh.least};
+  float least = -INFINITY;  // of min-p
+  if (by_min) {
+    if (tid == 0) sh.min_logit = fminf(__double2float_ru(static_cast<double>(row_max) + sh.log_min), row_max);
+    __syncthreads();
+    least = sh.min_logit;
+  }
   const auto each = [&](auto f) {  // every logit of this thread's and its number
     for (int i = w0 + lane; i < w1; i += 32) {
       const Piece<E> l = unpack<E>(pieces[i]);
@@ -424,16 +427,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       for (int e = 0; e < kPer; ++e) f(l.v[e], (first + i) * kPer + e - off);
     }
   };
-  const auto each_weight = [&](auto f) {  // f(l, weight, bin)
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const Piece<E> l = unpack<E>(pieces[i]);
-#pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        const Weights w = weights<E>(l.v[e], l.v[e + 1], sc, lane_table);
-        f(l.v[e], w.w[0], w.n[0]);
-        f(l.v[e + 1], w.w[1], w.n[1]);
-      }
-    }
+  const auto each_piece = [&](auto f) {
+    for (int i = w0 + lane; i < w1; i += 32) f(unpack<E>(pieces[i]));
   };
   const auto write = [&](int64_t token, U64 total) {  // one thread: the token, and log(its weight / total)
     p.tokens[row] = token;
@@ -496,10 +491,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
     __syncthreads();
   };
   // How many of the first m of the list it takes for weights of `need`.
-  const auto prefix_of = [&](int m, U64 need) -> int {
+  const auto share_of = [&](U64 total) {  // p of it; one thread
+    return share_up(p.top_p ? static_cast<double>(top_p) : p.top_p_all, total);
+  };
+  const auto prefix_of = [&](int m, U64 wanted) -> int {  // 0: p of their sum
     __syncthreads();
-    if (tid == 0) sh.found[0] = static_cast<uint32_t>(m);
+    if (tid == 0) sh.found[0] = static_cast<uint32_t>(m), sh.need = wanted ? wanted : share_of(mass_of[m - 1]);
     __syncthreads();
+    const U64 need = sh.need;
     for (int i = tid; i < m; i += threads)
       if (mass_of[i] >= need && (i == 0 || mass_of[i - 1] < need)) sh.found[0] = static_cast<uint32_t>(i) + 1;
     __syncthreads();
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
     sort(list, m);
     sum_list(m);
     if (k > 0 && k < m) m = static_cast<int>(k);
-    if (by_p) m = prefix_of(m, need ? need : share_up(top_p, mass_of[m - 1]));
+    if (by_p) m = prefix_of(m, need);
     if (by_min) {  // a prefix as well
       __syncthreads();
       if (tid == 0) sh.found[0] = static_cast<uint32_t>(m);
@@ -554,8 +553,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       for (int i = tid; i < kBins; i += threads) bins[i] = 0;
       __syncthreads();
       for (int i = tid; i < groups * p.ctas; i += threads) {
-        const int b = bin_of(float_of(group_max[i]), sc);
-        if (static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u);
+        const float l = float_of(group_max[i]);
+        const int b = bin_of(l, sc);
+        if (l > -INFINITY && static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u);
       }
       const int per = kBins / threads;
       __syncthreads();
@@ -586,10 +586,21 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
     for (int i = tid; i < kBins; i += threads) bins[i] = 0;
     __syncthreads();
     U64 sum = 0;
-    each_weight([&](float, U64 w, int b) {
-      if (static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u);
-      sum += w;
-    });
+    if (!sc.flat()) {
+      each_piece([&](const Piece<E>& l) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          const Weight w = weigh<E>(l.v[e], sc, lane_table);
+          if (static_cast<uint32_t>(w.n) < kLive) atomicAdd(bins + w.n, 1u);
+          sum += w.w;
+        }
+      });
+    } else {
+      each([&](float l, int) {
+        const int b = bin_of(l, sc);
+        if (l > -INFINITY && static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u), sum += weight<E>(l, sc, lane_table);
+      });
+    }
     U64 total = cl.all<Sum>(Two{sum, 0}).a;  // with top-k: of the first k, later
     // The first CTA adds up the bins of all: bins[b] = how many lie in bins up to b.
     const int per = kBins / threads;
@@ -605,14 +616,18 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       for (int i = tid * per; i < (tid + 1) * per; ++i) bins[i] = run += bins[i];
       __syncthreads();
     }
-    // Bins [a, b] that hold the end of the shortest prefix with `need` logits, or weights; how
-    // many lie up to b, and in all.
-    const auto bracket = [&](bool mass, U64 need) {
+    // Bins [a, b] that hold the end of the shortest prefix with `of` logits, or with p of the
+    // weights `of`; how many lie up to b; and in all, or what p of the weights is.
+    const auto bracket = [&](bool mass, U64 of) {
       Plan plan{0, 0, 0, 0};
       if (cl.rank == 0) {
         __syncthreads();
-        if (tid == 0) sh.found[0] = sh.found[1] = kLive - 1;  // not behind: nothing has been counted there
+        if (tid == 0) {
+          sh.found[0] = sh.found[1] = kLive - 1;  // not behind: nothing has been counted there
+          sh.need = mass ? share_of(of) : of;
+        }
         __syncthreads();
+        const U64 need = sh.need;
         if (!mass) {
           for (int i = tid; i < kBins; i += threads)
             if (bins[i] >= need && (i == 0 || bins[i - 1] < need)) sh.found[0] = sh.found[1] = i;
@@ -636,7 +651,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
           }
         }
         __syncthreads();
-        plan = Plan{bins[kBins - 1], sh.found[0], sh.found[1], bins[sh.found[1]]};
+        plan = Plan{mass ? need : bins[kBins - 1], sh.found[0], sh.found[1], bins[sh.found[1]]};
       }
       return cl.tell(plan);
     };
@@ -650,8 +665,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       U64 count = 0;
       Two range{0, ~0ull};
       const float over = sure;
-      for (int i = w0 + lane; i < w1; i += 32) {
-        const Piece<E> l = unpack<E>(pieces[i]);
+      each_piece([&](const Piece<E>& l) {
         bool any = false;
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
@@ -664,13 +678,12 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
         }
         if (any) {
 #pragma unroll
-          for (int e = 0; e < kPer; e += 2) {
-            const Weights w = weights<E>(l.v[e], l.v[e + 1], sc, lane_table);
-            if (l.v[e] > over) own.a += w.w[0], ++own.b;
-            if (l.v[e + 1] > over) own.a += w.w[1], ++own.b;
+          for (int e = 0; e < kPer; ++e) {
+            const U64 w = weight<E>(l.v[e], sc, lane_table);
+            if (l.v[e] > over) own.a += w, ++own.b;
           }
         }
-      }
+      });
       Two above = cl.all<Sum>(own);
       count = cl.all<Sum>(Two{count, 0}).a;
       range = cl.all<MaxMin>(range);
@@ -732,8 +745,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       }
     }
     if (by_p) {
-      const U64 need = share_up(top_p, total);
-      const Plan in = bracket(true, need);
+      const Plan in = bracket(true, total);
+      const U64 need = in.mass;
       if (in.c <= kList) {
         const U64 m = gather_list(lowest_in(static_cast<int>(in.b), sc), INFINITY);
         if (cl.rank == 0) draw_from_list(listed(m), 0, need);
@@ -746,28 +759,25 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   }
   if (!greedy && by_min && least > t) t = least, n = kAll;
 
-  // The kept weights of a piece, but those of l > sure.
+  // The kept weights of a piece, but those of l > sure, and how many are equal to t.
+  const bool everything = t == -INFINITY && sure == INFINITY && !sc.flat();
   const auto kept_of = [&](const Piece<E>& l, float known) {
     Two v{0, 0};
-    if (t == -INFINITY && known == INFINITY) {
+    if (everything) {
 #pragma unroll
-      for (int e = 0; e < kPer; e += 2) {
-        const Weights w = weights<E>(l.v[e], l.v[e + 1], sc, lane_table);
-        v.a += w.w[0] + w.w[1];
-      }
+      for (int e = 0; e < kPer; ++e) v.a += weight<E>(l.v[e], sc, lane_table);
     } else {
       bool any = false;
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
         any = any || (l.v[e] > t && l.v[e] <= known);
-        if (l.v[e] == t) ++v.b;
+        v.b += l.v[e] == t ? 1 : 0;
       }
       if (any) {
 #pragma unroll
-        for (int e = 0; e < kPer; e += 2) {
-          const Weights w = weights<E>(l.v[e], l.v[e + 1], sc, lane_table);
-          if (l.v[e] > t && l.v[e] <= known) v.a += w.w[0];
-          if (l.v[e + 1] > t && l.v[e + 1] <= known) v.a += w.w[1];
+        for (int e = 0; e < kPer; ++e) {
+          const U64 w = weight<E>(l.v[e], sc, lane_table);
+          if (l.v[e] > t && l.v[e] <= known) v.a += w;
         }
       }
     }
@@ -775,7 +785,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   };
   if (t > sure) sure = INFINITY, own = Two{0, 0};  // min-p cut into what was known
   own.b = 0;
-  for (int i = w0 + lane; i < w1; i += 32) own = Sum::of(own, kept_of(unpack<E>(pieces[i]), sure));
+  each_piece([&](const Piece<E>& l) { own = Sum::of(own, kept_of(l, sure)); });
   const Two* from = cl.gather<Sum>(own);
   const U64 w_t = n ? weight<E>(t, sc, lane_table) : 0;
   const auto kept = [&](const Two& s) { return s.a + (s.b < n ? s.b : static_cast<U64>(n)) * w_t; };
@@ -792,7 +802,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
     const int i = i0 + lane;
     Two v{0, 0};
     Piece<E> l;
-    if (i < w1) l = unpack<E>(pieces[i]), v = kept_of(l, INFINITY);
+    if (i < w1) {
+      l = unpack<E>(pieces[i]);
+      v = kept_of(l, INFINITY);
+    }
     Two incl = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -807,7 +820,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
           if (l.v[e] > t) run.a += weight<E>(l.v[e], sc, lane_table);
-          else if (l.v[e] == t) ++run.b;
+          else if (l.v[e] == t) ++run.b;  // (t = -inf: n is 0)
           if (e_drawn < 0 && kept(run) > target) e_drawn = e;
         }
         write(static_cast<int64_t>(first + i) * kPer + e_drawn - off, total);
