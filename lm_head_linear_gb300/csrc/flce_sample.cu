@@ -10,9 +10,9 @@ using namespace flce::host;
 
 namespace {
 
-constexpr int64_t kMaxVocab = 393216;      // fp32: 196,608 bytes of a row on each CTA of a cluster of 8
-constexpr int64_t kChunkBytes = 65536;     // of a row on a CTA, where a cluster can be larger: two CTAs on an SM
-constexpr int kMaxSmem = 232448 - 2048;    // less the static part
+constexpr int64_t kMaxVocab = 393216;      // an index has 19 bits, a sum of weights 63
+constexpr int64_t kChunkBytes = 65024;     // of a row on a CTA, where a cluster can be larger: two CTAs on an SM
+constexpr int kMaxSmem = 232448 - 4096;    // less the static part
 
 // The largest cluster of this kernel: 16 CTAs where the device schedules it (queried once), else 8.
 template <typename E>
@@ -52,7 +52,12 @@ flce_status launch(sample::Params& p, int64_t T, int dev, int sms, cudaStream_t 
   int ctas = 1;
   while (ctas < 8 && cdiv(pieces, ctas) * 16 > kChunkBytes) ctas *= 2;
   while (ctas < most && T * ctas * 2 <= sms && cdiv(pieces, ctas) > 256) ctas *= 2;
+  while (ctas < most && sample::shared_bytes(static_cast<int>(cdiv(pieces, ctas))) > kMaxSmem) ctas *= 2;
+  if (sample::shared_bytes(static_cast<int>(cdiv(pieces, ctas))) > kMaxSmem)
+    return fail(FLCE_ERR_UNSUPPORTED, "V = %d does not fit into a cluster of %d CTAs on this device", p.V, ctas);
   p.ctas = ctas;
+  p.unit = sample::kMostUnit;
+  while ((static_cast<int64_t>(p.V) >> (63 - p.unit)) != 0) --p.unit;
   p.chunk = static_cast<int32_t>(cdiv(pieces, ctas));
   const int threads = static_cast<int>(std::min<int64_t>(sample::kMaxThreads, std::max<int64_t>(128, cdiv(p.chunk, 256) * 128)));
   const size_t smem = sample::shared_bytes(p.chunk);

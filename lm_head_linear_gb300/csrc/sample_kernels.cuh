@@ -8,10 +8,10 @@
 // for, and nothing is sorted but a short list of candidates.
 //
 // The answer is a whole number that turns on comparisons of long sums, so weights are integers
-// in units of 2^-44 of the largest: their sums are exact, in whatever order they are formed, and
+// in units of 2^-44 or less of the largest: their sums are exact, in whatever order they are formed, and
 // the sum that the search compares is the one that the drawing walks through.  A weight itself
-// is good to 2^-31 of it and 2^-44 (table-driven exponential after Tang, 1989): a draw among 250,000
-// equally likely words then falls on the other side of a border about once in a million.
+// is good to 2^-31 of it and half a unit (table-driven exponential after Tang, 1989): a draw among
+// 250,000 equally likely words then falls on the other side of a border about once in a million.
 //
 // A row belongs to a cluster of CTAs, each with its part in shared memory: the logits are
 // read once.  The CTAs agree on maximum, sums and thresholds by pushing a few words into each
@@ -31,12 +31,12 @@ using U64 = unsigned long long;
 constexpr int kMaxCtas = 16;       // of a cluster
 constexpr int kMaxThreads = 512;
 constexpr int kMaxWarps = kMaxThreads / 32;
-constexpr int kUnit = 44;          // weights are whole multiples of 2^-44: their sum stays below 2^63
+constexpr int kMostUnit = 46;      // weights are whole multiples of 2^-unit
 constexpr int kTable = 32;         // steps of an octave
 constexpr int kBins = 1536;        // of -32 log2(weight), rounded
-constexpr int kLive = (kUnit + 1) * kTable + 1;  // from this bin on weights are 0
-constexpr int kList = 1024;        // candidates that are sorted
-constexpr int kGroups = 1024;      // whose largest logits bound the k-th largest from below
+constexpr int kLive = kMostUnit * kTable + kTable + 1;  // from this bin on weights are 0
+constexpr int kList = 2048;        // candidates that are sorted
+constexpr int kGroups = 2048;      // whose largest logits bound the k-th largest from below
 constexpr uint32_t kAll = 0x7fffffffu;
 static_assert(kLive <= kBins && kBins % kMaxThreads == 0, "bins");
 
@@ -56,14 +56,15 @@ struct Params {
   int32_t V;
   int32_t ctas;    // of a cluster
   int32_t chunk;   // 16-byte pieces of a CTA
+  int32_t unit;    // weights are multiples of 2^-unit: V 2^unit < 2^63
 };
 
-// round(2^(31 + j / 32))
+// round(2^(30 + j / 32))
 __device__ constexpr uint32_t kPow2[kTable] = {
-    2147483648u, 2194507417u, 2242560872u, 2291666561u, 2341847524u, 2393127307u, 2445529972u, 2499080105u,
-    2553802834u, 2609723834u, 2666869345u, 2725266179u, 2784941738u, 2845924021u, 2908241642u, 2971923842u,
-    3037000500u, 3103502151u, 3171459999u, 3240905930u, 3311872529u, 3384393094u, 3458501653u, 3534232978u,
-    3611622603u, 3690706840u, 3771522796u, 3854108391u, 3938502376u, 4024744348u, 4112874773u, 4202935003u};
+    1073741824u, 1097253708u, 1121280436u, 1145833280u, 1170923762u, 1196563654u, 1222764986u, 1249540052u,
+    1276901417u, 1304861917u, 1333434672u, 1362633090u, 1392470869u, 1422962010u, 1454120821u, 1485961921u,
+    1518500250u, 1551751076u, 1585730000u, 1620452965u, 1655936265u, 1692196547u, 1729250827u, 1767116489u,
+    1805811301u, 1845353420u, 1885761398u, 1927054196u, 1969251188u, 2012372174u, 2056437387u, 2101467502u};
 
 // Floats in an order of unsigned numbers (-0 and 0 the same).
 __device__ __forceinline__ uint32_t key_of(float f) {
@@ -76,63 +77,71 @@ __device__ __forceinline__ float float_of(uint32_t key) {
 constexpr uint32_t kMinusZero = 0x7fffffffu;  // no key: float_of() of it compares like 0, the key above it
 __device__ __forceinline__ uint32_t next_below(uint32_t key) { return key - 1 == kMinusZero ? key - 2 : key - 1; }
 
-// A row's way from a logit to its weight: w = 2^-z, z = (l / 2 - max / 2) (-c_hi - c_lo).  Halves:
-// the difference of two fp32 numbers need not be one.  (A row whose largest logit is
-// infinite is rewritten first, so max is finite.)  Differences below `least` count as that: z = 64,
-// the weight 0, also of l = -inf.  Where c is so small that no finite difference gets there,
-// the row is flat(), and -inf has to be told from the others by its value.
+// A row's way from a logit to its weight: w = 2^-z, z = top - (l - zero) (c_hi + c_lo), the product
+// with what it rounds off.  `zero` is 0 and `top` the largest logit's product, rounded up to
+// whole 1/32.  Where that passes 2^13 (a tiny temperature), `zero` is the largest
+// logit and `top` 0: logits that have a weight are then so close to it that the difference is
+// exact.  (A row whose largest logit is infinite is rewritten first.)
 struct Scale {
-  float half_max, c_hi, c_lo, least;
-  __device__ __forceinline__ bool flat() const { return c_hi < 2.0e-37f; }
+  float zero, c_hi, c_lo;
+  float magic;   // kMagic - top
+  float least;   // top - 64: products below count as that, the weight 0; NaN (of -inf) as well
+  int unit;
 };
 constexpr float kMagic = 393216.0f;  // 1.5 2^18: sums with it round to whole multiples of 1/32
+constexpr float kMostTop = 8192.0f;
 
-// A logit's weight in units of 2^-44, and its bin, n = round(32 z).  `lane_table`: this lane's
-// column of the table of powers, which is there once for every lane so that no two lanes meet
-// in a bank.
+__device__ __forceinline__ Scale scale_of(float max, float c_hi, float c_lo, int unit, float* top) {
+  const float y = max * c_hi;
+  const bool far = !(fabsf(y) <= kMostTop);
+  float up = (y + kMagic) - kMagic;
+  if (up < y) up += 1.0f / kTable;
+  if (far) up = 0.0f;
+  *top = up;
+  return Scale{far ? max : 0.0f, c_hi, c_lo, kMagic - up, up - 64.0f, unit};
+}
+
+// A logit's weight in units (at most 2^unit and a little), rounded to nearest, and its bin, n = round(32 z).
+// `lane_table`: this lane's column of the table of powers, which is there once for every
+// lane so that no two lanes meet in a bank.
 //
-// 30 cycles of a lane for bf16, 40 for fp32 (1.9 GHz, two logits' worth of registers in flight).  Packed
-// pairs of fp32 with the sum kept as two fp32 numbers, which saves the 64-bit shift and
-// addition, took 33 and 42: their constants need two registers each.
+// Packed pairs of fp32 with the sum kept as two fp32 numbers, which saves the 64-bit shift and
+// addition, took a tenth longer: their constants need two registers each.
 struct Weight {
   U64 w;
   int n;
 };
-template <typename E>
 __device__ __forceinline__ Weight weigh(float l, const Scale& s, const uint2* lane_table) {
-  const float d = fmaf(l, 0.5f, -s.half_max), dd = fmaxf(d, s.least);
-  const float z = dd * -s.c_hi;
-  float rest = fmaf(dd, s.c_lo, fmaf(dd, s.c_hi, z));
-  if constexpr (sizeof(E) == 4) {  // what d rounds off; bf16 logits lose nothing that counts
-    const float h = 0.5f * l, b = d - h;
-    const float off = ((h - (d - b)) + (-s.half_max - b)) * s.c_hi;
-    rest += fmaxf(off, -1.0f);  // far below 1; NaN where l is infinite
-  }
-  const float t = kMagic - z;
-  const float r = ((kMagic - t) - z) + rest;  // |r| <= 1/64, exact but for the rest
+  const float a = l - s.zero;
+  const float y = a * s.c_hi;
+  const float rest = fmaf(a, s.c_lo, fmaf(a, s.c_hi, -y));
+  const float yy = fmaxf(y, s.least);
+  const float t = yy + s.magic;
+  const float r = (yy - (t - s.magic)) + rest;  // |r| <= 1/64, exact but for the rest; NaN where l is infinite
   // 2^r - 1, off by less than 2^-32.8: a polynomial fitted to it (least largest error on |r| <= 1/64)
   const float p = r * fmaf(r, fmaf(r, 0.05550457f, 0.24022846f), 0.6931472f);
   const int up = __float_as_int(kMagic) + (kTable - 1) - __float_as_int(t);  // n + 31
   const uint2 power = lane_table[(up & (kTable - 1)) * 32];
-  const uint32_t w = power.x + static_cast<uint32_t>(__float2int_rn(__uint_as_float(power.y) * p));  // 2^31 of its octave
+  // 2^30 of its octave, below 2^31, and half a unit where units are cut off
+  const int drop = (up >> 5) + 30 - s.unit;
+  uint32_t half;
+  asm("shl.b32 %0, 1, %1;" : "=r"(half) : "r"(drop - 1));  // 0 for amounts that are negative or 32 and more
+  const uint32_t w = power.x + static_cast<uint32_t>(__float2int_rn(__uint_as_float(power.y) * p)) + half;
   Weight out;
   out.n = up - (kTable - 1);
-  asm("shr.u64 %0, %1, %2;" : "=l"(out.w) : "l"(static_cast<U64>(w) << 32), "r"((up >> 5) + (63 - kUnit)));  // 0 from 64 on
+  asm("shr.u64 %0, %1, %2;" : "=l"(out.w) : "l"(static_cast<U64>(w) << 32), "r"(drop + 32));  // 0 from 64 on
   return out;
 }
-template <typename E>
-__device__ __forceinline__ U64 weight(float l, const Scale& s, const uint2* lane_table) {
-  return weigh<E>(l, s, lane_table).w;
-}
+__device__ __forceinline__ U64 weight(float l, const Scale& s, const uint2* lane_table) { return weigh(l, s, lane_table).w; }
 
 // The same bin on its own.
 __device__ __forceinline__ int bin_of(float l, const Scale& s) {
-  const float z = fmaxf(fmaf(l, 0.5f, -s.half_max), s.least) * -s.c_hi;
-  return __float_as_int(kMagic) - __float_as_int(kMagic - z);
+  const float t = fmaxf((l - s.zero) * s.c_hi, s.least) + s.magic;
+  return __float_as_int(kMagic) - __float_as_int(t);
 }
 // The lowest logit of bins up to b (bins fall as logits rise), not -inf.
-__device__ __forceinline__ float lowest_in(int b, const Scale& s) {
-  uint32_t lo = 0x00800000u, hi = key_of(2.0f * s.half_max);  // the lowest number, the largest logit: bin 0
+__device__ __forceinline__ float lowest_in(int b, float max, const Scale& s) {
+  uint32_t lo = 0x00800000u, hi = key_of(max);  // the lowest number; b is the largest's bin or one behind it
   while (lo < hi) {
     const uint32_t mid = lo + (hi - lo) / 2;
     if (bin_of(float_of(mid), s) <= b) hi = mid;
@@ -168,6 +177,12 @@ __device__ __forceinline__ Piece<E> unpack(const uint4& a) {
   return r;
 }
 
+// The one value of a key's leading 16 bits (bf16), or of a key.
+template <typename E>
+__device__ __forceinline__ float value_of(uint32_t k) {
+  if constexpr (sizeof(E) == 4) return float_of(k);
+  else return float_of(k << 16 | (k & 0x8000u ? 0u : 0xffffu));
+}
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 
@@ -206,17 +221,17 @@ struct MaxMin {
 };
 
 struct Plan {  // what the first CTA finds out and tells the others
-  U64 mass;          // of a prefix; of a bracket: how many logits have a weight
-  uint32_t a, b, c;  // threshold's key, its equals; of a bracket: bins a .. b, logits up to b
+  U64 mass;
+  uint32_t a, b, c, d;
 };
 
 struct Shared {
   Two part[kMaxWarps];
   Two from[2][kMaxCtas];
   Plan plan[2];
-  double inv_t, log_min;
+  double c, log_min;
   U64 need;
-  float c_hi, c_lo, least, min_logit;
+  float c_hi, c_lo, min_logit;
   uint32_t listed, found[3];
 };
 
@@ -277,22 +292,23 @@ struct Cluster {
   }
 };
 
-// Exclusive prefix sum over the block's threads.
-__device__ __forceinline__ U64 block_before(U64 v, Shared* s) {
+// Exclusive prefix sums over the block's threads.
+__device__ __forceinline__ Two block_before(Two v, Shared* s) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  U64 incl = v;
+  Two incl = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const U64 o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl += o;
+    const Two o{__shfl_up_sync(0xffffffffu, incl.a, d), __shfl_up_sync(0xffffffffu, incl.b, d)};
+    if (lane >= d) incl = Sum::of(incl, o);
   }
   __syncthreads();
-  if (lane == 31) s->part[warp].a = incl;
+  if (lane == 31) s->part[warp] = incl;
   __syncthreads();
-  U64 before = incl - v;
-  for (int i = 0; i < warp; ++i) before += s->part[i].a;
+  Two before{incl.a - v.a, incl.b - v.b};
+  for (int i = 0; i < warp; ++i) before = Sum::of(before, s->part[i]);
   return before;
 }
+__device__ __forceinline__ U64 block_before(U64 v, Shared* s) { return block_before(Two{v, 0}, s).a; }
 
 // The least whole number that is f m or more, the product rounded to 53 bits: 0.9 of 4000 equal
 // weights are 3600 of them, although the number nearest to 0.9 is a little more.
@@ -302,15 +318,19 @@ __device__ __forceinline__ U64 share_down(U64 f, U64 m) { return __umul64hi(f, m
 
 // ------------------------------------------------------------------ the kernel
 // The pieces of a CTA's part of a row: 16 bytes as they lie in memory; what a piece holds before
-// or behind the row counts as -inf.  A warp has a stretch of its own, and its lanes read back
-// what they have copied themselves.
+// or behind the row counts as -inf.  A warp has a stretch of its own and a lane a stretch of
+// that, so that sums of lanes are sums of the vocabulary's order; pieces are swizzled (place_of)
+// so that the lanes of a load meet few banks twice.
+__device__ __forceinline__ int place_of(int piece) { return piece ^ ((piece >> 3) & 7); }
+__host__ __device__ constexpr size_t piece_bytes(int chunk) { return static_cast<size_t>((chunk + 7) / 8 * 8) * 16; }  // whole eights
+
 template <typename E>
 __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) {
   constexpr int kPer = Piece<E>::kPer;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
   uint4* const pieces = reinterpret_cast<uint4*>(smem);
-  uint2* const table = reinterpret_cast<uint2*>(smem + static_cast<size_t>(p.chunk) * 16);
+  uint2* const table = reinterpret_cast<uint2*>(smem + piece_bytes(p.chunk));
   uint32_t* const bins = reinterpret_cast<uint32_t*>(table + kTable * 32);
   U64* const list = reinterpret_cast<U64*>(bins + kBins);
   U64* const mass_of = list + kList;                               // sums of the sorted list's weights
@@ -331,19 +351,25 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
 
   const E* const logits = static_cast<const E*>(p.logits) + row * p.ldl;
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(logits) & 15) / static_cast<int>(sizeof(E));
-  const int all_pieces = (off + p.V + kPer - 1) / kPer;
   const int first = cl.rank * p.chunk;
-  const int mine = max(0, min(p.chunk, all_pieces - first));
-  const int stretch = ((p.chunk + warps - 1) / warps + 31) / 32 * 32;
-  const int w0 = warp * stretch, w1 = min(w0 + stretch, mine);
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const int64_t at = static_cast<int64_t>(first + i) * kPer - off;  // the piece's first logit
-    if (at >= 0 && at + kPer <= p.V) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(pieces + i)), "l"(logits + at) : "memory");
-    } else {
+  const int mine = max(0, min(p.chunk, (off + p.V + kPer - 1) / kPer - first));
+  const int whole0 = first == 0 && off ? 1 : 0, whole1 = min(mine, (off + p.V) / kPer - first);  // pieces that the row fills
+  const int run = (p.chunk + threads - 1) / threads;  // of a lane
+  const int w0 = warp * 32 * run, w1 = min(w0 + 32 * run, mine);
+  const int l0 = min(w0 + lane * run, w1), l1 = min(l0 + run, w1);
+  {
+    const uint8_t* from = reinterpret_cast<const uint8_t*>(logits - off) + 16 * static_cast<int64_t>(first + w0 + lane);
+    const uint32_t to = ptx::smem_u32(pieces);
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32, from += 512) {
+      if (i >= whole0 && i < whole1) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16 * place_of(i)), "l"(from) : "memory");
+      } else {
+        const int at = (first + i) * kPer - off;  // the piece's first logit
 #pragma unroll
-      for (int e = 0; e < kPer; ++e)
-        reinterpret_cast<E*>(pieces + i)[e] = at + e >= 0 && at + e < p.V ? logits[at + e] : lowest<E>();
+        for (int e = 0; e < kPer; ++e)
+          reinterpret_cast<E*>(pieces + place_of(i))[e] = at + e >= 0 && at + e < p.V ? logits[at + e] : lowest<E>();
+      }
     }
   }
   // In 32 bits what every thread needs; 64-bit arithmetic, of which an SM does two a cycle, is
@@ -357,44 +383,64 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   const bool by_k = top_k > 0, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
   if (tid == 0) {
     const double t = p.temperature ? static_cast<double>(temperature) : p.temperature_all;
-    const double inv = greedy ? 1.0 : fmin(1.0 / t, 1e37);
-    const double c = inv * (2.0 * 1.4426950408889634);
-    sh.inv_t = inv;
-    sh.c_hi = static_cast<float>(c);
-    sh.c_lo = static_cast<float>(c - static_cast<double>(sh.c_hi));
-    sh.least = fmaxf(-64.0f / sh.c_hi, -3.4028234e38f);
+    sh.c = greedy ? 1.0 : fmin(1.4426950408889634 / t, 1e37);
+    sh.c_hi = static_cast<float>(sh.c);
+    sh.c_lo = static_cast<float>(sh.c - static_cast<double>(sh.c_hi));
     sh.log_min = by_min && !greedy ? t * log(p.min_p ? static_cast<double>(min_p) : p.min_p_all) : 0.0;
     sh.listed = 0;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
-  float best = -INFINITY;
+  float quarter[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // the largest of every fourth piece
   bool nan = false;
-  for (int i = w0 + lane; i < w1; i += 32) largest<E>(pieces[i], best, nan);
-  if (__any_sync(0xffffffffu, nan)) {  // never drawn
-    best = -INFINITY;
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const Piece<E> l = unpack<E>(pieces[i]);
+  for (int i = l0; i < l1; i += 4) {
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        if (l.v[e] != l.v[e]) reinterpret_cast<E*>(pieces + i)[e] = lowest<E>();
-        best = fmaxf(best, l.v[e]);
+    for (int j = 0; j < 4; ++j)
+      if (i + j < l1) largest<E>(pieces[place_of(i + j)], quarter[j], nan);
+  }
+  if (__any_sync(0xffffffffu, nan)) {  // never drawn
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      quarter[j] = -INFINITY;
+      for (int i = l0 + j; i < l1; i += 4) {
+        const Piece<E> l = unpack<E>(pieces[place_of(i)]);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+          if (l.v[e] != l.v[e]) reinterpret_cast<E*>(pieces + place_of(i))[e] = lowest<E>();
+          quarter[j] = fmaxf(quarter[j], l.v[e]);
+        }
       }
     }
   }
+  const float best = fmaxf(fmaxf(quarter[0], quarter[1]), fmaxf(quarter[2], quarter[3]));
   if (p.ctas > 1) {  // the others' shared memory is there
     __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   }
-  // The largest logits of up to 1024 groups of the row, to every CTA: at least k logits are no
-  // smaller than the k-th largest of them.
-  const int groups = min(threads, kGroups / p.ctas);  // of a CTA
-  const bool short_k = !greedy && by_k && top_k <= groups * p.ctas;
+  // The largest logits of up to 2048 groups of the row, to every CTA: at least k logits are no
+  // smaller than the k-th largest of them.  With k above half of the groups that bound lets too many pass.
+  const int groups = min(4 * threads, kGroups / p.ctas);  // of a CTA
+  const bool short_k = !greedy && by_k && 2 * top_k <= groups * p.ctas + 256;
   if (short_k) {
-    float g = best;
-    const int lanes = threads / groups;  // a power of two
-    for (int d = lanes / 2; d > 0; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
-    for (int r = tid & (lanes - 1); r < p.ctas; r += lanes) peer(group_max, r)[cl.rank * groups + tid / lanes] = key_of(g);
+    if (groups >= threads) {  // 1, 2 or 4 to a thread
+      const int each_thread = groups / threads;
+      for (int r = 0; r < p.ctas; ++r) {
+        uint32_t* to = peer(group_max, r) + cl.rank * groups + tid;
+        if (each_thread == 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) to[j * threads] = key_of(quarter[j]);
+        } else if (each_thread == 2) {
+          to[0] = key_of(fmaxf(quarter[0], quarter[1])), to[threads] = key_of(fmaxf(quarter[2], quarter[3]));
+        } else {
+          to[0] = key_of(best);
+        }
+      }
+    } else {
+      float g = best;
+      const int lanes = threads / groups;  // a power of two
+      for (int d = lanes / 2; d > 0; d >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, d));
+      for (int r = tid & (lanes - 1); r < p.ctas; r += lanes) peer(group_max, r)[cl.rank * groups + tid / lanes] = key_of(g);
+    }
   }
   float row_max = float_of(static_cast<uint32_t>(cl.all<MaxMin>(Two{key_of(best), ~0ull}).a));
   const float real_max = row_max;
@@ -406,88 +452,108 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
     return;
   }
   if (row_max == INFINITY) {  // the infinite ones alone, as equals
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const Piece<E> l = unpack<E>(pieces[i]);
+    for (int i = l0; i < l1; ++i) {
+      const Piece<E> l = unpack<E>(pieces[place_of(i)]);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) reinterpret_cast<E*>(pieces + i)[e] = l.v[e] == INFINITY ? static_cast<E>(0) : lowest<E>();
+      for (int e = 0; e < kPer; ++e) reinterpret_cast<E*>(pieces + place_of(i))[e] = l.v[e] == INFINITY ? static_cast<E>(0) : lowest<E>();
     }
     row_max = 0.0f;
   }
-  const Scale sc{0.5f * row_max, sh.c_hi, sh.c_lo, sh.least};
+  float top;
+  const Scale sc = scale_of(row_max, sh.c_hi, sh.c_lo, p.unit, &top);
   float least = -INFINITY;  // of min-p
   if (by_min) {
     if (tid == 0) sh.min_logit = fminf(__double2float_ru(static_cast<double>(row_max) + sh.log_min), row_max);
     __syncthreads();
     least = sh.min_logit;
   }
-  const auto each = [&](auto f) {  // every logit of this thread's and its number
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const Piece<E> l = unpack<E>(pieces[i]);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) f(l.v[e], (first + i) * kPer + e - off);
-    }
-  };
   const auto each_piece = [&](auto f) {
-    for (int i = w0 + lane; i < w1; i += 32) f(unpack<E>(pieces[i]));
+    for (int i = l0; i < l1; ++i) f(unpack<E>(pieces[place_of(i)]));
   };
   const auto write = [&](int64_t token, U64 total) {  // one thread: the token, and log(its weight / total)
     p.tokens[row] = token;
     if (!p.logp) return;
     // the weight's from the logit; of the total the exponent, the leading 24 bits, and the rest apart
-    const int top = 63 - __clzll(total);
-    const U64 bits = total << (63 - top);
+    const int exponent = 63 - __clzll(total);
+    const U64 bits = total << (63 - exponent);
     const float lead = __ull2float_rz(bits);
     const float rest = static_cast<float>(bits - static_cast<U64>(lead)) / lead;
     const float drawn = as_float(logits[token]);
-    const double d = drawn == real_max ? 0.0 : static_cast<double>(drawn) - static_cast<double>(real_max);
-    const double log_total = static_cast<double>(top - kUnit) * 0.6931471805599453 + (static_cast<double>(logf(lead * 0x1p-63f)) + rest);
-    p.logp[row] = greedy ? 0.0f : static_cast<float>(d * sh.inv_t - log_total);
+    const double y = (drawn == INFINITY ? 0.0 : static_cast<double>(drawn) - static_cast<double>(sc.zero)) * sh.c - static_cast<double>(top);
+    p.logp[row] = greedy ? 0.0f
+                         : static_cast<float>((y - static_cast<double>(exponent - p.unit)) * 0.6931471805599453 -
+                                              (static_cast<double>(logf(lead * 0x1p-63f)) + rest));
   };
   const U64 u_share = u > 0.0f ? static_cast<U64>(fminf(u, 0x1.fffffep-1f) * 0x1p63f) : 0;
 
-  // ---- the list: logits from `low` on, unsorted, on the first CTA.  Returns how many there are.
+  // ---- the list: logits from `low` to `high`, unsorted, on the first CTA.  Returns how many there are.
   const auto gather_list = [&](float low, float high) -> U64 {
     U64 count = 0;
-    each([&](float l, int index) {
-      if (l >= low && l <= high) {
-        const uint32_t at = atomicAdd(peer(&sh.listed, 0), 1u);
-        if (at < kList) *peer(list + at, 0) = static_cast<U64>(key_of(l)) << 32 | (0xffffffffu - static_cast<uint32_t>(index));
-        ++count;
+    for (int j = 0; j < run; ++j) {
+      const int i = l0 + j;
+      Piece<E> l;
+      uint32_t hits = 0;
+      if (i < l1) {
+        l = unpack<E>(pieces[place_of(i)]);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) hits |= l.v[e] >= low && l.v[e] <= high ? 1u << e : 0u;
       }
-    });
+      if (!__any_sync(0xffffffffu, hits != 0)) continue;
+      const int here = __popc(hits);
+      int incl = here;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      uint32_t at = lane == 31 ? atomicAdd(peer(&sh.listed, 0), static_cast<uint32_t>(incl)) : 0u;
+      at = __shfl_sync(0xffffffffu, at, 31) + incl - here;
+      count += here;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e)
+        if (hits >> e & 1u) {
+          if (at < kList)
+            *peer(list + at, 0) =
+                static_cast<U64>(key_of(l.v[e])) << 32 | (0xffffffffu - static_cast<uint32_t>((first + i) * kPer + e - off));
+          ++at;
+        }
+    }
     return cl.all<Sum>(Two{count, 0}).a;
   };
   const auto listed = [&](U64 count) { return static_cast<int>(count < kList ? count : kList); };
   const auto key_in_list = [&](int i) { return float_of(static_cast<uint32_t>(list[i] >> 32)); };
-  // Sorts m numbers, the largest first; all threads of a CTA.
+  // Sorts m numbers, the largest first; all threads of a CTA.  A warp has a stretch of its own:
+  // only steps between stretches need the block's barrier.
   const auto sort = [&](U64* a, int m) {
     int size = 32;
     while (size < m) size *= 2;
     for (int i = m + tid; i < size; i += threads) a[i] = 0;
     __syncthreads();
-    const bool one_warp = size <= 128;  // without block barriers
-    const int step = one_warp ? 32 : threads;
-    if (!one_warp || warp == 0) {
-      for (int k = 2; k <= size; k *= 2)
-        for (int j = k / 2; j > 0; j /= 2) {
-          for (int i = tid; i < size / 2; i += step) {
+    const int used = min(warps, max(size / 64, 1));  // two numbers and more to a lane
+    const int stretch_of = size / used, pairs = stretch_of / 2;
+    for (int k = 2; k <= size; k *= 2)
+      for (int j = k / 2; j > 0; j /= 2) {
+        if (warp < used)
+          for (int q = lane; q < pairs; q += 32) {
+            const int i = warp * pairs + q;
             const int x = 2 * i - (i & (j - 1)), y = x + j;
             const U64 vx = a[x], vy = a[y];
             if ((vx < vy) == ((x & k) == 0)) a[x] = vy, a[y] = vx;
           }
-          if (one_warp) __syncwarp();
-          else __syncthreads();
-        }
-    }
+        // the next step's pairs: within the stretches, or not
+        const int next = j > 1 ? j / 2 : k;
+        if (j >= stretch_of || next >= stretch_of) __syncthreads();
+        else __syncwarp();
+      }
     __syncthreads();
   };
   // The sums of the sorted list's weights up to each.
   const auto sum_list = [&](int m) {
     const int per = (m + threads - 1) / threads, a = min(tid * per, m), b = min(a + per, m);
     U64 sum = 0;
-    for (int i = a; i < b; ++i) sum += weight<E>(key_in_list(i), sc, lane_table);
+    for (int i = a; i < b; ++i) sum += weight(key_in_list(i), sc, lane_table);
     U64 run = block_before(sum, &sh);
-    for (int i = a; i < b; ++i) mass_of[i] = run += weight<E>(key_in_list(i), sc, lane_table);
+    for (int i = a; i < b; ++i) mass_of[i] = run += weight(key_in_list(i), sc, lane_table);
     __syncthreads();
   };
   // How many of the first m of the list it takes for weights of `need`.
@@ -521,21 +587,22 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       m = static_cast<int>(sh.found[0]);
     }
     const U64 total = mass_of[m - 1], target = share_down(u_share, total);
-    // by index, the first first, each with its weight behind it: 19 and 45 bits
+    // by index, the first first, each with its weight behind it: 63 - unit and unit + 1 bits
+    const int weight_bits = p.unit + 1;
     __syncthreads();
     for (int i = tid; i < m; i += threads) {
       const U64 w = mass_of[i] - (i ? mass_of[i - 1] : 0);
-      list[i] = list[i] << 45 | w;  // of ~index
+      list[i] = list[i] << weight_bits | w;  // of ~index
     }
     sort(list, m);
     const int per = (m + threads - 1) / threads, a = min(tid * per, m), b = min(a + per, m);
-    constexpr U64 kWeight = (1ull << 45) - 1;
+    const U64 weights_only = (1ull << weight_bits) - 1;
     U64 sum = 0;
-    for (int i = a; i < b; ++i) sum += list[i] & kWeight;
+    for (int i = a; i < b; ++i) sum += list[i] & weights_only;
     U64 run = block_before(sum, &sh);
     for (int i = a; i < b; ++i) {
-      const U64 next = run + (list[i] & kWeight);
-      if (run <= target && target < next) write(static_cast<int64_t>(~(list[i] >> 45) & 0x7ffffu), total);
+      const U64 next = run + (list[i] & weights_only);
+      if (run <= target && target < next) write(static_cast<int64_t>(~(list[i] >> weight_bits) & ((1ull << (64 - weight_bits)) - 1)), total);
       run = next;
     }
   };
@@ -548,14 +615,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   if (greedy) t = row_max, n = 1;
 
   if (!greedy && (by_k || by_p)) {
-    if (short_k && row_max == real_max) {
+    if (short_k && real_max < INFINITY) {
       // Every CTA finds the same bound.
       for (int i = tid; i < kBins; i += threads) bins[i] = 0;
       __syncthreads();
       for (int i = tid; i < groups * p.ctas; i += threads) {
         const float l = float_of(group_max[i]);
         const int b = bin_of(l, sc);
-        if (l > -INFINITY && static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u);
+        if (static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u);
       }
       const int per = kBins / threads;
       __syncthreads();
@@ -572,7 +639,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       __syncthreads();
       const int b = static_cast<int>(sh.found[0]);
       if (b < kBins) {
-        const U64 m = gather_list(lowest_in(b, sc), INFINITY);
+        const U64 m = gather_list(lowest_in(b, row_max, sc), INFINITY);
         if (m <= kList) {
           if (cl.rank == 0) draw_from_list(listed(m), top_k, 0);
           return;
@@ -586,21 +653,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
     for (int i = tid; i < kBins; i += threads) bins[i] = 0;
     __syncthreads();
     U64 sum = 0;
-    if (!sc.flat()) {
-      each_piece([&](const Piece<E>& l) {
+    each_piece([&](const Piece<E>& l) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const Weight w = weigh<E>(l.v[e], sc, lane_table);
-          if (static_cast<uint32_t>(w.n) < kLive) atomicAdd(bins + w.n, 1u);
-          sum += w.w;
-        }
-      });
-    } else {
-      each([&](float l, int) {
-        const int b = bin_of(l, sc);
-        if (l > -INFINITY && static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u), sum += weight<E>(l, sc, lane_table);
-      });
-    }
+      for (int e = 0; e < kPer; ++e) {
+        const Weight w = weigh(l.v[e], sc, lane_table);
+        if (static_cast<uint32_t>(w.n) < kLive) atomicAdd(bins + w.n, 1u);
+        sum += w.w;
+      }
+    });
     U64 total = cl.all<Sum>(Two{sum, 0}).a;  // with top-k: of the first k, later
     // The first CTA adds up the bins of all: bins[b] = how many lie in bins up to b.
     const int per = kBins / threads;
@@ -617,9 +677,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       __syncthreads();
     }
     // Bins [a, b] that hold the end of the shortest prefix with `of` logits, or with p of the
-    // weights `of`; how many lie up to b; and in all, or what p of the weights is.
+    // weights `of`; how many lie up to b (c) and above a (d); and in all, or what p of the weights is.
     const auto bracket = [&](bool mass, U64 of) {
-      Plan plan{0, 0, 0, 0};
+      Plan plan{};
       if (cl.rank == 0) {
         __syncthreads();
         if (tid == 0) {
@@ -632,114 +692,207 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
           for (int i = tid; i < kBins; i += threads)
             if (bins[i] >= need && (i == 0 || bins[i - 1] < need)) sh.found[0] = sh.found[1] = i;
         } else {  // between the bounds of their weights
-          for (int side = 0; side < 2; ++side) {
-            const auto bound = [&](int i) -> U64 {
-              const uint32_t c = bins[i] - (i ? bins[i - 1] : 0u);
-              const float w = ptx::ex2((static_cast<float>(-i - side) + 0.5f) * (1.0f / kTable)) * (side ? 1.0f - 0x1p-15f : 1.0f + 0x1p-15f);
-              const U64 one = static_cast<U64>(w * 0x1p44f);
-              return c * (side ? (one ? one - 1 : 0) : one + 2);
-            };
-            U64 here = 0;
-            for (int i = tid * per; i < (tid + 1) * per; ++i) here += bound(i);
-            U64 run = block_before(here, &sh);
-            if (run < need && run + here >= need)
-              for (int i = tid * per; i < (tid + 1) * per; ++i) {
-                const U64 next = run + bound(i);
-                if (run < need && next >= need) sh.found[side] = i;
-                run = next;
-              }
+          const float unit_f = __uint_as_float(static_cast<uint32_t>(127 + p.unit) << 23);
+          const auto bounds = [&](int i) {
+            const U64 c = bins[i] - (i ? bins[i - 1] : 0u);
+            const float y = static_cast<float>(-i) * (1.0f / kTable), half = 0.5f / kTable;
+            const U64 lower = static_cast<U64>(ptx::ex2(y - half) * (1.0f - 0x1p-15f) * unit_f);
+            return Two{c * (static_cast<U64>(ptx::ex2(y + half) * (1.0f + 0x1p-15f) * unit_f) + 2), c * (lower ? lower - 1 : 0)};
+          };
+          Two here{0, 0};
+          for (int i = tid * per; i < (tid + 1) * per; ++i) here = Sum::of(here, bounds(i));
+          Two run = block_before(here, &sh);
+          for (int i = tid * per; i < (tid + 1) * per; ++i) {
+            const Two next = Sum::of(run, bounds(i));
+            if (run.a < need && next.a >= need) sh.found[0] = i;
+            if (run.b < need && next.b >= need) sh.found[1] = i;
+            run = next;
           }
         }
         __syncthreads();
-        plan = Plan{mass ? need : bins[kBins - 1], sh.found[0], sh.found[1], bins[sh.found[1]]};
+        plan = Plan{mass ? need : bins[kBins - 1], sh.found[0], sh.found[1], bins[sh.found[1]], sh.found[0] ? bins[sh.found[0] - 1] : 0u};
       }
       return cl.tell(plan);
     };
-    // The end of that prefix, where more logits share its bins than can be sorted: bisection of
-    // their values.  Returns the threshold, how many of its equals, and the prefix's weight.
-    const auto bisect = [&](bool by_mass, U64 need, const Plan& in) {
-      const float low = lowest_in(static_cast<int>(in.b), sc);
-      const uint32_t top_key = in.a ? key_of(lowest_in(static_cast<int>(in.a) - 1, sc)) : 0xffffffffu;  // above the bracket
-      sure = in.a ? float_of(next_below(top_key)) : INFINITY;
-      own = Two{0, 0};
-      U64 count = 0;
-      Two range{0, ~0ull};
-      const float over = sure;
-      each_piece([&](const Piece<E>& l) {
-        bool any = false;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          any = any || l.v[e] > over;
-          if (l.v[e] >= low && l.v[e] <= over) {
-            ++count;
-            const U64 k = key_of(l.v[e]);
-            range = MaxMin::of(range, Two{k, k});
-          }
-        }
-        if (any) {
+    // The end of that prefix, where more logits share its bins than can be sorted: they are counted
+    // again by their values, in steps as fine as the bins allow, until a step holds one value (bf16:
+    // nearly always at once) or few enough logits to sort.  Returns the threshold, how many of
+    // its equals (b), and the prefix's weight.
+    const auto narrow = [&](bool by_mass, U64 need, const Plan& in) {
+      uint32_t* const steps = group_max;  // kBins of them
+      uint32_t lo = key_of(lowest_in(static_cast<int>(in.b), row_max, sc));
+      uint32_t hi = in.d ? next_below(key_of(lowest_in(static_cast<int>(in.a) - 1, row_max, sc))) : key_of(row_max);
+      U64 above = 0, above_n = in.d;  // weights and number of logits above hi
+      sure = INFINITY, own = Two{0, 0};
+      Plan plan{};
+      while (true) {
+        int shift = sizeof(E) == 2 ? 16 : 0;
+        while ((hi >> shift) - (lo >> shift) >= kBins) ++shift;
+        const bool single = shift == (sizeof(E) == 2 ? 16 : 0);  // a step is one value
+        for (int i = tid; i < kBins; i += threads) steps[i] = 0;
+        __syncthreads();
+        const float low = float_of(lo), high = float_of(hi), known = sure;
+        const uint32_t last = hi >> shift;
+        U64 sum = 0;
+        each_piece([&](const Piece<E>& l) {
+          bool any = false;
+          uint32_t inside = 0;
 #pragma unroll
           for (int e = 0; e < kPer; ++e) {
-            const U64 w = weight<E>(l.v[e], sc, lane_table);
-            if (l.v[e] > over) own.a += w, ++own.b;
+            any = any || (l.v[e] > high && l.v[e] <= known);
+            inside |= l.v[e] >= low && l.v[e] <= high ? 1u << e : 0u;
+          }
+          if (any) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+              const U64 w = weight(l.v[e], sc, lane_table);
+              sum += l.v[e] > high && l.v[e] <= known ? w : 0;
+            }
+          }
+          if (inside) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+              if (inside >> e & 1u) atomicAdd(steps + (last - (key_of(l.v[e]) >> shift)), 1u);
+          }
+        });
+        own.a += sum, sure = high;
+        above += cl.all<Sum>(Two{sum, 0}).a;
+        if (cl.rank == 0) {
+          // The sums up to a step, least and most: weights (or numbers).
+          const auto bounds = [&](int i) {
+            const U64 c = steps[i];
+            if (!by_mass) return Two{c, c};
+            if (!c) return Two{0, 0};
+            const uint32_t k = last - i;
+            if (single) {
+              const U64 w = weight(value_of<E>(k), sc, lane_table);
+              return Two{c * w, c * w};
+            }
+            const uint32_t k0 = max(k << shift, lo), k1 = min((k << shift) | ((1u << shift) - 1u), hi);
+            const U64 w0 = weight(float_of(k0), sc, lane_table), w1 = weight(float_of(k1), sc, lane_table);
+            return Two{c * (w1 + (w1 >> 28) + 2), c * (w0 - min(w0, (w0 >> 28) + 2))};
+          };
+          uint32_t count = 0;
+          for (int i = tid * per; i < (tid + 1) * per; ++i) {
+            for (int r = 1; r < p.ctas; ++r) steps[i] += *peer(steps + i, r);
+            count += steps[i];
+          }
+          Two here{0, 0};
+          for (int i = tid * per; i < (tid + 1) * per; ++i) here = Sum::of(here, bounds(i));
+          if (tid == 0) sh.found[0] = 0, sh.found[1] = last - (lo >> shift);
+          Two run = block_before(here, &sh);
+          const U64 so_far = by_mass ? above : above_n;
+          run.a += so_far, run.b += so_far;
+          uint32_t run_n = static_cast<uint32_t>(block_before(static_cast<U64>(count), &sh));
+          for (int i = tid * per; i < (tid + 1) * per; ++i) {
+            const Two next = Sum::of(run, bounds(i));
+            if (run.a < need && next.a >= need) {
+              sh.found[0] = i, sh.found[2] = run_n;
+              sh.need = run.a;  // single: the prefix without this step
+            }
+            if (run.b < need && next.b >= need) sh.found[1] = i;
+            run = next, run_n += steps[i];
+          }
+          __syncthreads();
+          const uint32_t j0 = sh.found[0], j1 = max(sh.found[1], j0);
+          if (single) {
+            const uint32_t k = key_of(value_of<E>(last - j0));
+            const U64 w = weight(float_of(k), sc, lane_table), before = sh.need;
+            U64 equal = by_mass ? (w ? (need - before + w - 1) / w : 1) : need - before;
+            equal = equal < 1 ? 1 : equal > steps[j0] ? steps[j0] : equal;
+            U64 mass = before + equal * w;
+            if (!by_mass) {  // of the steps before
+              U64 part = 0;
+              for (int i = tid; i < static_cast<int>(j0); i += threads)
+                if (steps[i]) part += steps[i] * weight(value_of<E>(last - i), sc, lane_table);
+              const U64 sum_before = block_before(part, &sh) + part;
+              if (tid == threads - 1) sh.need = above + sum_before + equal * w;
+              __syncthreads();
+              mass = sh.need;
+            }
+            plan = Plan{mass, k, static_cast<uint32_t>(equal), 0, 0};
+          } else {
+            uint32_t c = 0;
+            for (int i = static_cast<int>(j0) + tid; i <= static_cast<int>(j1); i += threads) c += steps[i];
+            const U64 n_before = block_before(static_cast<U64>(c), &sh) + c;
+            if (tid == threads - 1) sh.found[0] = static_cast<uint32_t>(n_before);
+            __syncthreads();
+            // the steps' keys, how many they are, and how many lie above them here
+            plan = Plan{0, max((last - j1) << shift, lo), min(((last - j0) << shift) | ((1u << shift) - 1u), hi), sh.found[0], sh.found[2]};
           }
         }
-      });
-      Two above = cl.all<Sum>(own);
-      count = cl.all<Sum>(Two{count, 0}).a;
-      range = cl.all<MaxMin>(range);
-      uint32_t hi = static_cast<uint32_t>(range.a), lo = static_cast<uint32_t>(range.b);
-      while (count > kList && lo < hi) {
-        uint32_t mid = lo + (hi - lo) / 2;  // (mid, hi] or [lo, mid]
-        if (mid == kMinusZero) --mid;
-        const float a = float_of(mid), b = float_of(hi);
-        Two here{0, 0};
-        each([&](float l, int) {
-          if (l > a && l <= b) here.a += weight<E>(l, sc, lane_table), ++here.b;
-        });
-        const Two top = cl.all<Sum>(here);
-        if ((by_mass ? above.a + top.a : above.b + top.b) >= need) {
-          lo = mid + 1, count = top.b;
-          if (lo == kMinusZero) ++lo;
-        } else {
-          hi = mid, count -= top.b, above = Sum::of(above, top);
-          own = Sum::of(own, here), sure = a;
+        plan = cl.tell(plan);
+        if (single) return plan;
+        const uint32_t before = hi - lo;
+        lo = plan.a, hi = plan.b, above_n += plan.d;
+        if (lo == kMinusZero) ++lo;
+        if (hi == kMinusZero) --hi;
+        if (plan.c <= kList) break;
+        if (hi - lo > before / 2) {  // weights of nearly 0, which the bounds do not tell apart: halves, by exact sums
+          uint32_t mid = lo + (hi - lo) / 2;  // (mid, hi] or [lo, mid]
+          if (mid == kMinusZero) --mid;
+          const float f_hi = float_of(hi), f_mid = float_of(mid), f_sure = sure;
+          U64 over = 0;
+          Two top{0, 0};
+          each_piece([&](const Piece<E>& l) {
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+              if (l.v[e] > f_mid && l.v[e] <= f_sure) {
+                const U64 w = weight(l.v[e], sc, lane_table);
+                if (l.v[e] > f_hi) over += w;
+                else top.a += w, ++top.b;
+              }
+          });
+          own.a += over, sure = f_hi;
+          above += cl.all<Sum>(Two{over, 0}).a;
+          const Two all_top = cl.all<Sum>(top);
+          if ((by_mass ? above + all_top.a : above_n + all_top.b) >= need) {
+            lo = mid + 1;
+            if (lo == kMinusZero) ++lo;
+          } else {
+            above += all_top.a, above_n += all_top.b, own.a += top.a, sure = f_mid;
+            hi = mid;
+          }
         }
       }
-      if (lo >= hi) {  // equal ones
-        const U64 w = weight<E>(float_of(hi), sc, lane_table);
-        U64 equal = by_mass ? (w ? (need - above.a + w - 1) / w : 1) : need - above.b;
-        equal = equal < 1 ? 1 : equal > count ? count : equal;
-        return Plan{above.a + equal * w, hi, static_cast<uint32_t>(equal), 0};
-      }
-      const int m = listed(gather_list(float_of(lo), float_of(hi)));
-      Plan plan{0, 0, 0, 0};
+      // The few: sorted, with the weights of those above.
+      const float high = float_of(hi), known = sure;
+      U64 sum = 0;
+      each_piece([&](const Piece<E>& l) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (l.v[e] > high && l.v[e] <= known) sum += weight(l.v[e], sc, lane_table);
+      });
+      own.a += sum, sure = high;
+      above += cl.all<Sum>(Two{sum, 0}).a;
+      const int m = listed(gather_list(float_of(lo), high));
       if (cl.rank == 0) {
         sort(list, m);
         sum_list(m);
-        const int end = by_mass ? prefix_of(m, need - above.a) : min(m, static_cast<int>(need - above.b));
-        const uint32_t last = static_cast<uint32_t>(list[end - 1] >> 32);
+        const int end = by_mass ? prefix_of(m, need - above) : min(m, static_cast<int>(need - above_n));
+        const uint32_t key = static_cast<uint32_t>(list[end - 1] >> 32);
         if (tid == 0) sh.found[1] = 0, sh.listed = 0;
         __syncthreads();
         uint32_t equal = 0;
-        for (int i = tid; i < end; i += threads) equal += static_cast<uint32_t>(list[i] >> 32) == last ? 1u : 0u;
+        for (int i = tid; i < end; i += threads) equal += static_cast<uint32_t>(list[i] >> 32) == key ? 1u : 0u;
         if (equal) atomicAdd(&sh.found[1], equal);
         __syncthreads();
-        plan = Plan{above.a + mass_of[end - 1], last, sh.found[1], 0};
+        plan = Plan{above + mass_of[end - 1], key, sh.found[1], 0, 0};
       }
       return cl.tell(plan);
     };
 
-    Plan end{0, 0, 0, 0};
+    Plan end{};
     bool found = false;
     if (by_k) {
       const Plan in = bracket(false, static_cast<U64>(top_k));
       if (static_cast<U64>(top_k) < in.mass) {  // else all that have a weight
         if (in.c <= kList) {
-          const U64 m = gather_list(lowest_in(static_cast<int>(in.b), sc), INFINITY);
+          const U64 m = gather_list(lowest_in(static_cast<int>(in.b), row_max, sc), INFINITY);
           if (cl.rank == 0) draw_from_list(listed(m), top_k, 0);
           return;
         }
-        end = bisect(false, static_cast<U64>(top_k), in);
+        end = narrow(false, static_cast<U64>(top_k), in);
         total = end.mass;
         found = true;
       }
@@ -748,11 +901,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       const Plan in = bracket(true, total);
       const U64 need = in.mass;
       if (in.c <= kList) {
-        const U64 m = gather_list(lowest_in(static_cast<int>(in.b), sc), INFINITY);
+        const U64 m = gather_list(lowest_in(static_cast<int>(in.b), row_max, sc), INFINITY);
         if (cl.rank == 0) draw_from_list(listed(m), 0, need);
         return;
       }
-      end = bisect(true, need, in);
+      end = narrow(true, need, in);
       found = true;
     }
     if (found) t = float_of(end.a), n = end.b;
@@ -760,12 +913,12 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   if (!greedy && by_min && least > t) t = least, n = kAll;
 
   // The kept weights of a piece, but those of l > sure, and how many are equal to t.
-  const bool everything = t == -INFINITY && sure == INFINITY && !sc.flat();
+  const bool everything = t == -INFINITY && sure == INFINITY;
   const auto kept_of = [&](const Piece<E>& l, float known) {
     Two v{0, 0};
     if (everything) {
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) v.a += weight<E>(l.v[e], sc, lane_table);
+      for (int e = 0; e < kPer; ++e) v.a += weight(l.v[e], sc, lane_table);
     } else {
       bool any = false;
 #pragma unroll
@@ -776,7 +929,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       if (any) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-          const U64 w = weight<E>(l.v[e], sc, lane_table);
+          const U64 w = weight(l.v[e], sc, lane_table);
           if (l.v[e] > t && l.v[e] <= known) v.a += w;
         }
       }
@@ -785,9 +938,18 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   };
   if (t > sure) sure = INFINITY, own = Two{0, 0};  // min-p cut into what was known
   own.b = 0;
-  each_piece([&](const Piece<E>& l) { own = Sum::of(own, kept_of(l, sure)); });
+  if (everything) {
+    U64 sum = 0;
+    each_piece([&](const Piece<E>& l) {
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) sum += weight(l.v[e], sc, lane_table);
+    });
+    own.a = sum;
+  } else {
+    each_piece([&](const Piece<E>& l) { own = Sum::of(own, kept_of(l, sure)); });
+  }
   const Two* from = cl.gather<Sum>(own);
-  const U64 w_t = n ? weight<E>(t, sc, lane_table) : 0;
+  const U64 w_t = n ? weight(t, sc, lane_table) : 0;
   const auto kept = [&](const Two& s) { return s.a + (s.b < n ? s.b : static_cast<U64>(n)) * w_t; };
   Two before{0, 0}, all{0, 0};
   for (int i = 0; i < p.ctas; ++i) {
@@ -798,41 +960,42 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   for (int i = 0; i < warp; ++i) before = Sum::of(before, sh.part[i]);
   const Two here = Sum::of(before, sh.part[warp]);
   if (!(kept(before) <= target && target < kept(here))) return;  // another warp's stretch
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
+  // the lane's, from the sums that it has
+  Two incl = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Two o{__shfl_up_sync(0xffffffffu, incl.a, d), __shfl_up_sync(0xffffffffu, incl.b, d)};
+    if (lane >= d) incl = Sum::of(incl, o);
+  }
+  const int owner = __ffs(__ballot_sync(0xffffffffu, kept(Sum::of(before, incl)) > target)) - 1;
+  before = Sum::of(before, Two{__shfl_sync(0xffffffffu, incl.a - own.a, owner), __shfl_sync(0xffffffffu, incl.b - own.b, owner)});
+  // and that lane's logits, one to each lane at a time
+  const int from_piece = min(w0 + owner * run, w1), count = (min(from_piece + run, w1) - from_piece) * kPer;
+  for (int q0 = 0; q0 < count; q0 += 32) {
+    const int q = q0 + lane;
     Two v{0, 0};
-    Piece<E> l;
-    if (i < w1) {
-      l = unpack<E>(pieces[i]);
-      v = kept_of(l, INFINITY);
+    if (q < count) {
+      const float l = as_float(reinterpret_cast<const E*>(pieces + place_of(from_piece + q / kPer))[q % kPer]);
+      if (l > t) v.a = weight(l, sc, lane_table);
+      else if (l == t) v.b = 1;  // (t = -inf: n is 0)
     }
-    Two incl = v;
+    Two sums = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const Two o{__shfl_up_sync(0xffffffffu, incl.a, d), __shfl_up_sync(0xffffffffu, incl.b, d)};
-      if (lane >= d) incl = Sum::of(incl, o);
+      const Two o{__shfl_up_sync(0xffffffffu, sums.a, d), __shfl_up_sync(0xffffffffu, sums.b, d)};
+      if (lane >= d) sums = Sum::of(sums, o);
     }
-    const unsigned past = __ballot_sync(0xffffffffu, kept(Sum::of(before, incl)) > target);
+    const unsigned past = __ballot_sync(0xffffffffu, kept(Sum::of(before, sums)) > target);
     if (past) {
-      if (lane == __ffs(past) - 1) {
-        Two run{before.a + incl.a - v.a, before.b + incl.b - v.b};
-        int e_drawn = -1;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          if (l.v[e] > t) run.a += weight<E>(l.v[e], sc, lane_table);
-          else if (l.v[e] == t) ++run.b;  // (t = -inf: n is 0)
-          if (e_drawn < 0 && kept(run) > target) e_drawn = e;
-        }
-        write(static_cast<int64_t>(first + i) * kPer + e_drawn - off, total);
-      }
+      if (lane == __ffs(past) - 1) write(static_cast<int64_t>(first + from_piece) * kPer + q - off, total);
       return;
     }
-    before = Sum::of(before, Two{__shfl_sync(0xffffffffu, incl.a, 31), __shfl_sync(0xffffffffu, incl.b, 31)});
+    before = Sum::of(before, Two{__shfl_sync(0xffffffffu, sums.a, 31), __shfl_sync(0xffffffffu, sums.b, 31)});
   }
 }
 
 inline size_t shared_bytes(int chunk) {
-  return static_cast<size_t>(chunk) * 16 + sizeof(uint2) * kTable * 32 + sizeof(uint32_t) * kBins + 2 * sizeof(U64) * kList;
+  return piece_bytes(chunk) + sizeof(uint2) * kTable * 32 + sizeof(uint32_t) * kBins + 2 * sizeof(U64) * kList;
 }
 
 }  // namespace sample
