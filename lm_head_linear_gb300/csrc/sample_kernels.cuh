@@ -139,15 +139,19 @@ __device__ __forceinline__ int bin_of(float l, const Scale& s) {
   const float t = fmaxf((l - s.zero) * s.c_hi, s.least) + s.magic;
   return __float_as_int(kMagic) - __float_as_int(t);
 }
-// The lowest logit of bins up to b (bins fall as logits rise), not -inf.
+// The lowest logit of bins up to b (bins fall as logits rise), not -inf; all lanes of a warp, 32 keys
+// at a time.
 __device__ __forceinline__ float lowest_in(int b, float max, const Scale& s) {
-  uint32_t lo = 0x00800000u, hi = key_of(max);  // the lowest number; b is the largest's bin or one behind it
-  while (lo < hi) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    if (bin_of(float_of(mid), s) <= b) hi = mid;
-    else lo = mid + 1;
+  uint32_t lo = 0x00800000u;                 // the lowest number
+  const uint32_t hi = key_of(max);           // b is its bin or one behind it
+#pragma unroll 1
+  for (int digit = 27; digit >= 0; digit -= digit == 2 ? 2 : 5) {
+    const U64 last = static_cast<U64>(lo) + (static_cast<U64>((threadIdx.x & 31) + 1) << digit) - 1;  // of this lane's share
+    const bool reaches = last >= hi || bin_of(float_of(static_cast<uint32_t>(last)), s) <= b;
+    lo += static_cast<uint32_t>(__ffs(__ballot_sync(0xffffffffu, reaches)) - 1) << digit;
+    if (digit == 0) break;
   }
-  return float_of(hi);
+  return float_of(lo);
 }
 
 // ------------------------------------------------------------------ 16-byte pieces
@@ -233,6 +237,7 @@ struct Shared {
   U64 need;
   float c_hi, c_lo, min_logit;
   uint32_t listed, found[3];
+  U64 before;
 };
 
 template <typename T>
@@ -487,8 +492,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   const U64 u_share = u > 0.0f ? static_cast<U64>(fminf(u, 0x1.fffffep-1f) * 0x1p63f) : 0;
 
   // ---- the list: logits from `low` to `high`, unsorted, on the first CTA.  Returns how many there are.
-  const auto gather_list = [&](float low, float high) -> U64 {
-    U64 count = 0;
+  // With `sums` also the weights of all.
+  const auto gather_list = [&](float low, float high, bool sums = false, U64* total = nullptr) -> U64 {
+    U64 count = 0, sum = 0;
     for (int j = 0; j < run; ++j) {
       const int i = l0 + j;
       Piece<E> l;
@@ -497,6 +503,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
         l = unpack<E>(pieces[place_of(i)]);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) hits |= l.v[e] >= low && l.v[e] <= high ? 1u << e : 0u;
+        if (sums) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) sum += weight(l.v[e], sc, lane_table);
+        }
       }
       if (!__any_sync(0xffffffffu, hits != 0)) continue;
       const int here = __popc(hits);
@@ -518,7 +528,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
           ++at;
         }
     }
-    return cl.all<Sum>(Two{count, 0}).a;
+    const Two all = cl.all<Sum>(Two{count, sum});
+    if (sums) *total = all.b;
+    return all.a;
   };
   const auto listed = [&](U64 count) { return static_cast<int>(count < kList ? count : kList); };
   const auto key_in_list = [&](int i) { return float_of(static_cast<uint32_t>(list[i] >> 32)); };
@@ -612,6 +624,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   float t = -INFINITY, sure = INFINITY;
   uint32_t n = 0;
   Two own{0, 0};
+  uint32_t last_step = 0;  // not 0: list[i] is the weight of the value of key (bf16: of leading 16 bits) last_step - i
   if (greedy) t = row_max, n = 1;
 
   if (!greedy && (by_k || by_p)) {
@@ -648,20 +661,18 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
         if (tid == 0) sh.listed = 0;  // seen by the others after the next barrier
       }
     }
-    // How many logits fall into each bin, and the sum of weights.
+    // How many logits fall into each bin.
     __syncthreads();
     for (int i = tid; i < kBins; i += threads) bins[i] = 0;
     __syncthreads();
-    U64 sum = 0;
     each_piece([&](const Piece<E>& l) {
 #pragma unroll
       for (int e = 0; e < kPer; ++e) {
-        const Weight w = weigh(l.v[e], sc, lane_table);
-        if (static_cast<uint32_t>(w.n) < kLive) atomicAdd(bins + w.n, 1u);
-        sum += w.w;
+        const int b = bin_of(l.v[e], sc);
+        if (static_cast<uint32_t>(b) < kLive) atomicAdd(bins + b, 1u);
       }
     });
-    U64 total = cl.all<Sum>(Two{sum, 0}).a;  // with top-k: of the first k, later
+    cl.sync();
     // The first CTA adds up the bins of all: bins[b] = how many lie in bins up to b.
     const int per = kBins / threads;
     if (cl.rank == 0) {
@@ -677,17 +688,18 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
       __syncthreads();
     }
     // Bins [a, b] that hold the end of the shortest prefix with `of` logits, or with p of the
-    // weights `of`; how many lie up to b (c) and above a (d); and in all, or what p of the weights is.
+    // weights `of` (0: of all, which the bins bound); how many lie up to b (c) and above a (d); and
+    // in all, or what p of the weights `of` is.
     const auto bracket = [&](bool mass, U64 of) {
       Plan plan{};
       if (cl.rank == 0) {
         __syncthreads();
         if (tid == 0) {
           sh.found[0] = sh.found[1] = kLive - 1;  // not behind: nothing has been counted there
-          sh.need = mass ? share_of(of) : of;
+          sh.need = mass && of ? share_of(of) : of;
         }
         __syncthreads();
-        const U64 need = sh.need;
+        U64 need = sh.need;
         if (!mass) {
           for (int i = tid; i < kBins; i += threads)
             if (bins[i] >= need && (i == 0 || bins[i - 1] < need)) sh.found[0] = sh.found[1] = i;
@@ -702,15 +714,22 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
           Two here{0, 0};
           for (int i = tid * per; i < (tid + 1) * per; ++i) here = Sum::of(here, bounds(i));
           Two run = block_before(here, &sh);
+          U64 most = need;
+          if (!of) {  // p of the least and of the most that all may weigh
+            __syncthreads();
+            if (tid == threads - 1) sh.need = share_of(run.b + here.b), sh.before = share_of(run.a + here.a);
+            __syncthreads();
+            need = sh.need, most = sh.before;
+          }
           for (int i = tid * per; i < (tid + 1) * per; ++i) {
             const Two next = Sum::of(run, bounds(i));
             if (run.a < need && next.a >= need) sh.found[0] = i;
-            if (run.b < need && next.b >= need) sh.found[1] = i;
+            if (run.b < most && next.b >= most) sh.found[1] = i;
             run = next;
           }
         }
         __syncthreads();
-        plan = Plan{mass ? need : bins[kBins - 1], sh.found[0], sh.found[1], bins[sh.found[1]], sh.found[0] ? bins[sh.found[0] - 1] : 0u};
+        plan = Plan{mass ? sh.need : bins[kBins - 1], sh.found[0], sh.found[1], bins[sh.found[1]], sh.found[0] ? bins[sh.found[0] - 1] : 0u};
       }
       return cl.tell(plan);
     };
@@ -718,7 +737,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
     // again by their values, in steps as fine as the bins allow, until a step holds one value (bf16:
     // nearly always at once) or few enough logits to sort.  Returns the threshold, how many of
     // its equals (b), and the prefix's weight.
-    const auto narrow = [&](bool by_mass, U64 need, const Plan& in) {
+    const auto narrow = [&](bool by_mass, U64 need, const Plan& in) {  // need 0: p of all weights
       uint32_t* const steps = group_max;  // kBins of them
       uint32_t lo = key_of(lowest_in(static_cast<int>(in.b), row_max, sc));
       uint32_t hi = in.d ? next_below(key_of(lowest_in(static_cast<int>(in.a) - 1, row_max, sc))) : key_of(row_max);
@@ -733,30 +752,35 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
         __syncthreads();
         const float low = float_of(lo), high = float_of(hi), known = sure;
         const uint32_t last = hi >> shift;
-        U64 sum = 0;
-        each_piece([&](const Piece<E>& l) {
-          bool any = false;
-          uint32_t inside = 0;
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            any = any || (l.v[e] > high && l.v[e] <= known);
-            inside |= l.v[e] >= low && l.v[e] <= high ? 1u << e : 0u;
-          }
-          if (any) {
+        U64 sum = 0, total = 0;
+        const bool want_total = by_mass && !need;
+        if (known == INFINITY) {  // the first round: most of the row
+          each_piece([&](const Piece<E>& l) {
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
               const U64 w = weight(l.v[e], sc, lane_table);
-              sum += l.v[e] > high && l.v[e] <= known ? w : 0;
+              total += w;
+              if (l.v[e] > high) sum += w;
+              else if (l.v[e] >= low) atomicAdd(steps + (last - (key_of(l.v[e]) >> shift)), 1u);
             }
-          }
-          if (inside) {
+          });
+        } else {
+          each_piece([&](const Piece<E>& l) {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e)
-              if (inside >> e & 1u) atomicAdd(steps + (last - (key_of(l.v[e]) >> shift)), 1u);
-          }
-        });
+            for (int e = 0; e < kPer; ++e) {
+              if (l.v[e] > high && l.v[e] <= known) sum += weight(l.v[e], sc, lane_table);
+              else if (l.v[e] >= low && l.v[e] <= high) atomicAdd(steps + (last - (key_of(l.v[e]) >> shift)), 1u);
+            }
+          });
+        }
         own.a += sum, sure = high;
-        above += cl.all<Sum>(Two{sum, 0}).a;
+        const Two sums = cl.all<Sum>(Two{sum, total});
+        above += sums.a;
+        if (want_total && cl.rank == 0) {
+          if (tid == 0) sh.need = share_of(sums.b);
+          __syncthreads();
+          need = sh.need;
+        }
         if (cl.rank == 0) {
           // The sums up to a step, least and most: weights (or numbers).
           const auto bounds = [&](int i) {
@@ -788,7 +812,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
             const Two next = Sum::of(run, bounds(i));
             if (run.a < need && next.a >= need) {
               sh.found[0] = i, sh.found[2] = run_n;
-              sh.need = run.a;  // single: the prefix without this step
+              sh.before = run.a;  // single: the prefix without this step
             }
             if (run.b < need && next.b >= need) sh.found[1] = i;
             run = next, run_n += steps[i];
@@ -797,7 +821,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
           const uint32_t j0 = sh.found[0], j1 = max(sh.found[1], j0);
           if (single) {
             const uint32_t k = key_of(value_of<E>(last - j0));
-            const U64 w = weight(float_of(k), sc, lane_table), before = sh.need;
+            const U64 w = weight(float_of(k), sc, lane_table), before = sh.before;
             U64 equal = by_mass ? (w ? (need - before + w - 1) / w : 1) : need - before;
             equal = equal < 1 ? 1 : equal > steps[j0] ? steps[j0] : equal;
             U64 mass = before + equal * w;
@@ -806,9 +830,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
               for (int i = tid; i < static_cast<int>(j0); i += threads)
                 if (steps[i]) part += steps[i] * weight(value_of<E>(last - i), sc, lane_table);
               const U64 sum_before = block_before(part, &sh) + part;
-              if (tid == threads - 1) sh.need = above + sum_before + equal * w;
+              if (tid == threads - 1) sh.before = above + sum_before + equal * w;
               __syncthreads();
-              mass = sh.need;
+              mass = sh.before;
             }
             plan = Plan{mass, k, static_cast<uint32_t>(equal), 0, 0};
           } else {
@@ -818,11 +842,18 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
             if (tid == threads - 1) sh.found[0] = static_cast<uint32_t>(n_before);
             __syncthreads();
             // the steps' keys, how many they are, and how many lie above them here
-            plan = Plan{0, max((last - j1) << shift, lo), min(((last - j0) << shift) | ((1u << shift) - 1u), hi), sh.found[0], sh.found[2]};
+            plan = Plan{need, max((last - j1) << shift, lo), min(((last - j0) << shift) | ((1u << shift) - 1u), hi), sh.found[0], sh.found[2]};
           }
         }
         plan = cl.tell(plan);
-        if (single) return plan;
+        if (single) {
+          // The draw needs the weights of the steps above the threshold: by value, once.
+          for (int i = tid; i <= static_cast<int>(last - (plan.a >> shift)); i += threads) list[i] = weight(value_of<E>(last - i), sc, lane_table);
+          last_step = last;
+          __syncthreads();
+          return plan;
+        }
+        need = plan.mass;
         const uint32_t before = hi - lo;
         lo = plan.a, hi = plan.b, above_n += plan.d;
         if (lo == kMinusZero) ++lo;
@@ -856,6 +887,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
         }
       }
       // The few: sorted, with the weights of those above.
+      last_step = 0;
       const float high = float_of(hi), known = sure;
       U64 sum = 0;
       each_piece([&](const Piece<E>& l) {
@@ -884,6 +916,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
 
     Plan end{};
     bool found = false;
+    U64 total = 0;  // the weights that top-p is of; 0: all
     if (by_k) {
       const Plan in = bracket(false, static_cast<U64>(top_k));
       if (static_cast<U64>(top_k) < in.mass) {  // else all that have a weight
@@ -899,13 +932,18 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
     }
     if (by_p) {
       const Plan in = bracket(true, total);
-      const U64 need = in.mass;
       if (in.c <= kList) {
-        const U64 m = gather_list(lowest_in(static_cast<int>(in.b), row_max, sc), INFINITY);
-        if (cl.rank == 0) draw_from_list(listed(m), 0, need);
+        U64 all = 0;
+        const U64 m = gather_list(lowest_in(static_cast<int>(in.b), row_max, sc), INFINITY, total == 0, &all);
+        if (cl.rank == 0) {
+          __syncthreads();
+          if (tid == 0) sh.need = total ? in.mass : share_of(all);
+          __syncthreads();
+          draw_from_list(listed(m), 0, sh.need);
+        }
         return;
       }
-      end = narrow(true, need, in);
+      end = narrow(true, total ? in.mass : 0, in);
       found = true;
     }
     if (found) t = float_of(end.a), n = end.b;
@@ -926,7 +964,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
         any = any || (l.v[e] > t && l.v[e] <= known);
         v.b += l.v[e] == t ? 1 : 0;
       }
-      if (any) {
+      if (any && known < INFINITY && last_step) {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (l.v[e] > t && l.v[e] <= known) v.a += list[last_step - (key_of(l.v[e]) >> (sizeof(E) == 2 ? 16 : 0))];
+      } else if (any) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
           const U64 w = weight(l.v[e], sc, lane_table);
