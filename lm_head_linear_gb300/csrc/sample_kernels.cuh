@@ -36,6 +36,7 @@ constexpr int kTable = 32;         // steps of an octave
 constexpr int kBins = 1536;        // of -32 log2(weight), rounded
 constexpr int kLive = kMostUnit * kTable + kTable + 1;  // from this bin on weights are 0
 constexpr int kList = 2048;        // candidates that are sorted
+constexpr int kFewer = 128;        // up to which they are compared each with each
 constexpr int kGroups = 2048;      // whose largest logits bound the k-th largest from below
 constexpr uint32_t kAll = 0x7fffffffu;
 static_assert(kLive <= kBins && kBins % kMaxThreads == 0, "bins");
@@ -494,41 +495,46 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   // ---- the list: logits from `low` to `high`, unsorted, on the first CTA.  Returns how many there are.
   // With `sums` also the weights of all.
   const auto gather_list = [&](float low, float high, bool sums = false, U64* total = nullptr) -> U64 {
-    U64 count = 0, sum = 0;
-    for (int j = 0; j < run; ++j) {
-      const int i = l0 + j;
-      Piece<E> l;
+    const auto hits_of = [&](const Piece<E>& l) {
       uint32_t hits = 0;
-      if (i < l1) {
-        l = unpack<E>(pieces[place_of(i)]);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) hits |= l.v[e] >= low && l.v[e] <= high ? 1u << e : 0u;
-        if (sums) {
+      for (int e = 0; e < kPer; ++e) hits |= l.v[e] >= low && l.v[e] <= high ? 1u << e : 0u;
+      return hits;
+    };
+    U64 sum = 0;
+    int count = 0;  // of this lane; then one addition for the warp finds them their places
+    each_piece([&](const Piece<E>& l) {
+      count += __popc(hits_of(l));
+      if (sums) {
 #pragma unroll
-          for (int e = 0; e < kPer; ++e) sum += weight(l.v[e], sc, lane_table);
-        }
+        for (int e = 0; e < kPer; ++e) sum += weight(l.v[e], sc, lane_table);
       }
-      if (!__any_sync(0xffffffffu, hits != 0)) continue;
-      const int here = __popc(hits);
-      int incl = here;
+    });
+    int incl = count;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
-      }
-      uint32_t at = lane == 31 ? atomicAdd(peer(&sh.listed, 0), static_cast<uint32_t>(incl)) : 0u;
-      at = __shfl_sync(0xffffffffu, at, 31) + incl - here;
-      count += here;
-#pragma unroll
-      for (int e = 0; e < kPer; ++e)
-        if (hits >> e & 1u) {
-          if (at < kList)
-            *peer(list + at, 0) =
-                static_cast<U64>(key_of(l.v[e])) << 32 | (0xffffffffu - static_cast<uint32_t>((first + i) * kPer + e - off));
-          ++at;
-        }
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
     }
-    const Two all = cl.all<Sum>(Two{count, sum});
+    uint32_t at = 0;
+    if (lane == 31 && incl) at = atomicAdd(peer(&sh.listed, 0), static_cast<uint32_t>(incl));
+    at = __shfl_sync(0xffffffffu, at, 31) + incl - count;
+    if (count) {
+      U64* const to = peer(list, 0);
+      for (int i = l0; i < l1; ++i) {
+        const Piece<E> l = unpack<E>(pieces[place_of(i)]);
+        const uint32_t hits = hits_of(l);
+        if (!hits) continue;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (hits >> e & 1u) {
+            if (at < kList)
+              to[at] = static_cast<U64>(key_of(l.v[e])) << 32 | (0xffffffffu - static_cast<uint32_t>((first + i) * kPer + e - off));
+            ++at;
+          }
+      }
+    }
+    const Two all = cl.all<Sum>(Two{static_cast<U64>(count), sum});
     if (sums) *total = all.b;
     return all.a;
   };
@@ -585,6 +591,42 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   // The first CTA: top-k (k > 0), top-p (need > 0: the weights wanted; all of top_p otherwise) and
   // min-p on the list of m, which holds all of them, and the draw.
   const auto draw_from_list = [&](int m, int64_t k, U64 need) {
+    if (m <= kFewer) {
+      // Every one against every other, `share` threads to one: its place and the weights up to it,
+      // and then the kept weights up to it in the vocabulary.  Four barriers instead of two sorts'.
+      const int share = m <= threads / 16 ? 16 : m <= threads / 8 ? 8 : m <= threads / 4 ? 4 : m <= threads / 2 ? 2 : 1;
+      const int mine_at = tid / share, part = tid % share;
+      const bool live = mine_at < m;
+      __syncthreads();
+      for (int i = tid; i < m; i += threads) mass_of[i] = weight(key_in_list(i), sc, lane_table);
+      __syncthreads();
+      const U64 self = live ? list[mine_at] : 0, w = live ? mass_of[mine_at] : 0;
+      U64 up_to = 0;
+      int place = 0;
+      for (int j = part; j < m; j += share) {
+        const U64 other = list[j], w_j = mass_of[j];
+        up_to += other >= self ? w_j : 0;
+        place += other > self ? 1 : 0;
+      }
+      for (int d = share / 2; d > 0; d >>= 1) up_to += __shfl_xor_sync(0xffffffffu, up_to, d), place += __shfl_xor_sync(0xffffffffu, place, d);
+      const int many = k > 0 && k < m ? static_cast<int>(k) : m;
+      if (live && part == 0 && place == many - 1) sh.need = !by_p ? ~0ull : need ? need : share_of(up_to);
+      __syncthreads();
+      const bool keep = live && place < many && up_to - w < sh.need && float_of(static_cast<uint32_t>(self >> 32)) >= least;
+      if (live && part == 0) mass_of[mine_at] = keep ? w : 0;
+      __syncthreads();
+      U64 total = 0, before = 0;
+      const uint32_t self_index = static_cast<uint32_t>(self);  // ~index
+      for (int j = part; j < m; j += share) {
+        const U64 w_j = mass_of[j];
+        total += w_j;
+        before += static_cast<uint32_t>(list[j]) > self_index ? w_j : 0;
+      }
+      for (int d = share / 2; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d), before += __shfl_xor_sync(0xffffffffu, before, d);
+      const U64 target = share_down(u_share, total);
+      if (keep && part == 0 && before <= target && target < before + w) write(static_cast<int64_t>(0xffffffffu - self_index), total);
+      return;
+    }
     sort(list, m);
     sum_list(m);
     if (k > 0 && k < m) m = static_cast<int>(k);
