@@ -322,6 +322,62 @@ __device__ __forceinline__ U64 share_up(double f, U64 m) { return __double2ull_r
 // floor(f m) for f in [0, 1) as a whole multiple of 2^-63.
 __device__ __forceinline__ U64 share_down(U64 f, U64 m) { return __umul64hi(f, m) << 1 | (f * m) >> 63; }
 
+// ------------------------------------------------------------------ sorting
+// A bitonic sort of `size` numbers (a power of two, R * 32 and more), the largest first; all
+// threads of a CTA.  Steps within stretches of R * 32 are a warp's, in registers (R numbers to a
+// lane); only steps between stretches go through shared memory and the block's barrier.
+template <int R>
+__device__ __forceinline__ void merge_stretch(U64 (&v)[R], int base, int k, int j0, int lane) {
+  for (int j = j0; j > 0; j /= 2) {
+    if (j >= 32) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int step = 1; step < R; step *= 2)
+          if (step * 32 == j && !(r & step)) {
+            const bool first_largest = ((base + r * 32) & k) == 0;
+            const U64 x = v[r], y = v[r | step];
+            if ((x < y) == first_largest) v[r] = y, v[r | step] = x;
+          }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const U64 other = __shfl_xor_sync(0xffffffffu, v[r], j);
+        const bool largest = ((lane & j) == 0) == (((base + r * 32 + lane) & k) == 0);
+        if ((other > v[r]) == largest) v[r] = other;
+      }
+    }
+  }
+}
+template <int R>
+__device__ __forceinline__ void sort_stretches(U64* a, int size) {
+  constexpr int kStretch = R * 32;
+  const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+  for (int k = kStretch; k <= size; k *= 2) {
+    for (int j = k / 2; j >= kStretch; j /= 2) {
+      for (int i = tid; i < size / 2; i += blockDim.x) {
+        const int x = 2 * i - (i & (j - 1)), y = x + j;
+        const U64 vx = a[x], vy = a[y];
+        if ((vx < vy) == ((x & k) == 0)) a[x] = vy, a[y] = vx;
+      }
+      __syncthreads();
+    }
+    for (int base = (tid >> 5) * kStretch; base < size; base += warps * kStretch) {
+      U64 v[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) v[r] = a[base + r * 32 + lane];
+      if (k == kStretch) {
+        for (int kk = 2; kk < kStretch; kk *= 2) merge_stretch(v, base, kk, kk / 2, lane);
+      }
+      merge_stretch(v, base, k, kStretch / 2, lane);
+#pragma unroll
+      for (int r = 0; r < R; ++r) a[base + r * 32 + lane] = v[r];
+    }
+    __syncthreads();
+  }
+}
+
 // ------------------------------------------------------------------ the kernel
 // The pieces of a CTA's part of a row: 16 bytes as they lie in memory; what a piece holds before
 // or behind the row counts as -inf.  A warp has a stretch of its own and a lane a stretch of
@@ -540,30 +596,14 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   };
   const auto listed = [&](U64 count) { return static_cast<int>(count < kList ? count : kList); };
   const auto key_in_list = [&](int i) { return float_of(static_cast<uint32_t>(list[i] >> 32)); };
-  // Sorts m numbers, the largest first; all threads of a CTA.  A warp has a stretch of its own:
-  // only steps between stretches need the block's barrier.
+  // Sorts m numbers, the largest first; all threads of a CTA.
   const auto sort = [&](U64* a, int m) {
-    int size = 32;
+    int size = 64;
     while (size < m) size *= 2;
     for (int i = m + tid; i < size; i += threads) a[i] = 0;
     __syncthreads();
-    const int used = min(warps, max(size / 64, 1));  // two numbers and more to a lane
-    const int stretch_of = size / used, pairs = stretch_of / 2;
-    for (int k = 2; k <= size; k *= 2)
-      for (int j = k / 2; j > 0; j /= 2) {
-        if (warp < used)
-          for (int q = lane; q < pairs; q += 32) {
-            const int i = warp * pairs + q;
-            const int x = 2 * i - (i & (j - 1)), y = x + j;
-            const U64 vx = a[x], vy = a[y];
-            if ((vx < vy) == ((x & k) == 0)) a[x] = vy, a[y] = vx;
-          }
-        // the next step's pairs: within the stretches, or not
-        const int next = j > 1 ? j / 2 : k;
-        if (j >= stretch_of || next >= stretch_of) __syncthreads();
-        else __syncwarp();
-      }
-    __syncthreads();
+    if (size == 64) sort_stretches<2>(a, size);
+    else sort_stretches<4>(a, size);
   };
   // The sums of the sorted list's weights up to each.
   const auto sum_list = [&](int m) {
