@@ -30,20 +30,20 @@ flce_status matrix_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwiz
 }
 
 // Co-resident CTA pairs per device, queried once.
-template <bool TOKENS_M, bool W4>
+template <bool TOKENS_M, bool W4, int STEP>
 flce_status resident_pairs(int dev, int sms, int* pairs) {
   static std::mutex mu;
   static int known[64] = {};
   std::lock_guard<std::mutex> lk(mu);
   if (known[dev] == 0) {
-    CUDA_TRY(cudaFuncSetAttribute(fp8::linear_kernel<TOKENS_M, W4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    CUDA_TRY(cudaFuncSetAttribute(fp8::linear_kernel<TOKENS_M, W4, STEP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   fp8::kSmemLimit));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * std::max(sms / 2, 1));
     cfg.blockDim = dim3(fp8::kThreads);
     cfg.dynamicSmemBytes = fp8::kSmemLimit;
     int n = 0;
-    CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, fp8::linear_kernel<TOKENS_M, W4>, &cfg));
+    CUDA_TRY(cudaOccupancyMaxActiveClusters(&n, fp8::linear_kernel<TOKENS_M, W4, STEP>, &cfg));
     known[dev] = std::max(1, std::min(n, sms / 2));
   }
   *pairs = known[dev];
@@ -88,7 +88,14 @@ flce_status linear(const void* x, const uint8_t* x_scale, const void* W, const u
   const int64_t es = y_dtype == FLCE_DTYPE_F32 ? 4 : 2;
   p.v_tma = static_cast<int32_t>(V & ~(16 / es - 1));
   p.y_tma = !off16(y) && (ldy * es) % 16 == 0 && p.v_tma > 0;
-  if ((st = resident_pairs<true, W4>(dev, sms, &pairs)) != FLCE_OK || (st = resident_pairs<false, W4>(dev, sms, &pairs)) != FLCE_OK)
+  // K blocks of a stage of operands.  One of 4-bit weights on M is 8 KB a CTA, and the producer's
+  // and the MMA issuer's waits and commits take longer than its bytes: two, or four where tiles
+  // are narrow (1 x 2048 x 124,160: 40 us by one, 32.6 by two, 30.5 by four; 93 x 4096 x 248,320: 109 us
+  // by two, 111 by four, of which only two stages fit).
+  constexpr int kWide = W4 ? 2 : 1, kNarrow = W4 ? 4 : 1;
+  if ((st = resident_pairs<true, W4, 1>(dev, sms, &pairs)) != FLCE_OK ||
+      (st = resident_pairs<false, W4, kWide>(dev, sms, &pairs)) != FLCE_OK ||
+      (st = resident_pairs<false, W4, kNarrow>(dev, sms, &pairs)) != FLCE_OK)
     return st;
   // One token tile: the vocabulary on M.  More: the side and the width of the tiles that
   // take the fewest rounds times what a round costs, which is about its operands' rows (128 and
@@ -112,8 +119,9 @@ flce_status linear(const void* x, const uint8_t* x_scale, const void* W, const u
   if (units >= (int64_t(1) << 31) - 1024) return fail(FLCE_ERR_INVALID_ARG, "T x V is too large");
   p.n = static_cast<int32_t>(n), p.n_tiles = static_cast<int32_t>(n_tiles), p.m_tiles = static_cast<int32_t>(m_tiles);
   p.units = static_cast<int32_t>(units);
-  p.stage_bytes = (tokens_m ? fp8::Form<true, W4>::kStep : fp8::Form<false, W4>::kStep) *
-                  (fp8::kABytes + p.n / 2 * fp8::kBlockK);
+  const bool narrow = W4 && !tokens_m && n <= 32;
+  const int step = tokens_m ? 1 : narrow ? kNarrow : kWide;
+  p.stage_bytes = step * (fp8::kABytes + p.n / 2 * fp8::kBlockK);
   p.staging_bytes = tokens_m && es == 2 && !p.y_tma ? fp8::kImageBytes : fp8::kStagingBytes;
   constexpr int kRing = W4 ? fp8::kRing4Bytes : 0;
   p.stages = std::min((fp8::kSmemLimit - 1024 - p.staging_bytes - kRing - fp8::kSmemTail) / p.stage_bytes, fp8::kMaxStages);
@@ -143,7 +151,8 @@ flce_status linear(const void* x, const uint8_t* x_scale, const void* W, const u
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + p.staging_bytes + kRing + fp8::kSmemTail;
   KernelScope ks(W4 ? FLCE_KERNEL_LINEAR_FP4 : FLCE_KERNEL_LINEAR_FP8, s, 2.0 * T * K * V,
                  1.0 * T * K + (W4 ? 17.0 / 32 : 1.0) * V * K + (p.y_f32 ? 4.0 : 2.0) * T * V);
-  st = launch_overlapped(tokens_m ? fp8::linear_kernel<true, W4> : fp8::linear_kernel<false, W4>, dim3(grid),
+  st = launch_overlapped(tokens_m ? fp8::linear_kernel<true, W4, 1>
+                         : narrow ? fp8::linear_kernel<false, W4, kNarrow> : fp8::linear_kernel<false, W4, kWide>, dim3(grid),
                          fp8::kThreads, smem, s, p);
   if (st != FLCE_OK) return st;
   ks.done();

@@ -73,16 +73,12 @@ constexpr uint64_t kSettleNs = 200000ull;
 
 // What the kinds of weights and the two orientations differ in.
 //
-// K blocks of a stage of operands: two where 4-bit weights are on M.  A K block of them is 8 KB
-// a CTA, and the producer's and the MMA issuer's waits and commits took longer than its bytes.
-//
 // The columns of TMEM: two accumulators, then kStages stages of scale words, each of four K
 // blocks.  A word holds four bytes of a row: the scales of four K blocks (a token's, and
 // 8-bit weights', one per 128 channels), or the four of one K block (4-bit weights', one per
 // 32): A's words of K block 4 g + j at a(j), B's at b(j).
 template <bool TOKENS_M, bool W4>
 struct Form {
-  static constexpr int kStep = W4 && !TOKENS_M ? 2 : 1;
   static constexpr int kAcc = W4 ? kMaxN4 : kMaxN;  // columns of an accumulator
   static constexpr int kBase = 2 * kAcc;
   static constexpr int kCols = !W4 ? 16 : TOKENS_M ? 40 : 32;
@@ -219,31 +215,31 @@ __device__ __forceinline__ void arrive_even(uint32_t bar) {
 }
 
 // Both CTAs: this CTA's 128 rows of the M side and its half of the N side.
-template <bool TOKENS_M, bool W4>
+// STEP: K blocks of a stage of operands.
+template <bool TOKENS_M, bool W4, int STEP>
 __device__ __forceinline__ void producer(const Params& p, const Smem& s, const Work& w, uint32_t rank) {
   Slot at;
   uint32_t used = 0;
   bool ok = true;
   const bool small = !TOKENS_M && p.n_tiles == 1;
-  constexpr int kStep = Form<TOKENS_M, W4>::kStep;
-  const int step_bytes = p.stage_bytes / kStep;  // of a K block
+  const int step_bytes = kABytes + p.n / 2 * kBlockK;  // of a K block
   // The barriers count bytes as they lie in memory: a row of 128 4-bit numbers is 64.
   constexpr int kARow = W4 && !TOKENS_M ? kBlockK / 2 : kBlockK, kBRow = W4 && TOKENS_M ? kBlockK / 2 : kBlockK;
   for (int u = w.first; u < w.count && ok; u += w.step) {
     const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
     const int n_row = un.n0 + static_cast<int>(rank) * (p.n / 2);
     const uint32_t tx = 2u * static_cast<uint32_t>(un.boxes * 32 * kARow + p.n / 2 * kBRow);
-    for (int kb = 0; kb < p.kb; kb += kStep) {
+    for (int kb = 0; kb < p.kb; kb += STEP) {
       if (!ptx::wait_bounded_cluster(s.empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
         give_up(p, s);
         ok = false;
         break;
       }
-      const int blocks = min(kStep, p.kb - kb);
+      const int blocks = min(STEP, p.kb - kb);
       if (rank == 0) ptx::mbar_arrive_expect_tx(s.full(at.i), tx * blocks);
       const uint32_t full = ptx::mapa(s.full(at.i), 0);
 #pragma unroll
-      for (int j = 0; j < kStep; ++j) {
+      for (int j = 0; j < STEP; ++j) {
         if (j >= blocks) break;
         const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes) + j * step_bytes;
         const int c = (kb + j) * kBlockK;
@@ -268,12 +264,13 @@ __device__ __forceinline__ void producer(const Params& p, const Smem& s, const W
 }
 
 // Even CTA only.
-template <bool TOKENS_M, bool W4>
+template <bool TOKENS_M, bool W4, int STEP>
 __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const Work& w, uint32_t tmem) {
   using F = Form<TOKENS_M, W4>;
   Slot at, sc, acc;
   bool ok = true;
-  const int step_bytes = p.stage_bytes / F::kStep;
+  static_assert(4 % STEP == 0, "a stage of scales is whole stages of operands");
+  const int step_bytes = kABytes + p.n / 2 * kBlockK;
   const uint32_t idesc0 = ptx::idesc_mxf8(2 * kRowsCta, static_cast<uint32_t>(p.n), 0) |
                           (!W4 ? 0u : TOKENS_M ? ptx::kIdescB2M1 : ptx::kIdescA2M1);
   for (int u = w.first; u < w.count && ok; u += w.step) {
@@ -281,7 +278,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const
     if (!ok) break;
     ptx::tc_fence_after();
     const uint32_t d = tmem + acc.i * F::kAcc;
-    for (int kb = 0; kb < p.kb; kb += F::kStep) {
+    for (int kb = 0; kb < p.kb; kb += STEP) {
       if ((kb & 3) == 0) {
         ok = ptx::wait_bounded_cluster(s.scale_full(sc.i), sc.phase, p.timeout_ns, s.abort_flag);
         if (!ok) break;
@@ -291,7 +288,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const
       ptx::tc_fence_after();
       const uint32_t scales = tmem + F::kBase + sc.i * F::kCols;
 #pragma unroll
-      for (int j = 0; j < F::kStep; ++j) {
+      for (int j = 0; j < STEP; ++j) {
         if (kb + j >= p.kb) break;
         const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes) + j * step_bytes;
         const uint32_t sf = static_cast<uint32_t>((kb + j) & 3);
@@ -306,7 +303,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const
       }
       ptx::mma_commit_pair(s.empty(at.i), 0x3);
       at.next(p.stages);
-      if (((kb + F::kStep) & 3) == 0 || kb + F::kStep >= p.kb) {
+      if (((kb + STEP) & 3) == 0 || kb + STEP >= p.kb) {
         ptx::mma_commit_pair(s.scale_empty(sc.i), 0x3);
         sc.next(F::kStages);
       }
@@ -456,9 +453,10 @@ __device__ __forceinline__ bool scale_any(bool v) {
 
 // The scale words of 4-bit weights, 16 bytes a row and stage.  They come from memory, where
 // the operands ahead of them keep every load waiting for microseconds, so they are copied
-// Ring4::kDepth stages ahead into shared memory, a quarter by each warp (W's words of K
+// Ring4::kDepth - 1 stages ahead into shared memory, a quarter by each warp (W's words of K
 // block j by warp j, the tokens' by columns), and every warp then writes all of them to its
-// lanes (1 x 2048 x 124,160: 50 us with the words loaded into registers two stages ahead).
+// lanes; four stages before that they are fetched into L2 (1 x 2048 x 124,160: 50 us with the words
+// loaded into registers two stages ahead; 93 x 4096 x 248,320: 121 us without the fetch, 109 with).
 template <bool TOKENS_M>
 __device__ __forceinline__ void scale_writer4(const Params& p, const Smem& s, const Work& w, uint32_t tmem,
                                               uint32_t rank, int warp, int lane) {
@@ -480,8 +478,18 @@ __device__ __forceinline__ void scale_writer4(const Params& p, const Smem& s, co
     bool live = false;
   } held;
   int u = w.first, g = 0, slot = 0;  // of the next stage to copy, and the slot it goes to
+  int ahead_u = w.first, ahead_g = 0;  // of the next stage to fetch into L2, four stages ahead of the copies
+  for (int i = 0; i < 4 && ahead_u < w.count; ++i)
+    if (++ahead_g == groups) ahead_g = 0, ahead_u += w.step;
   // W's words into the next slot; the tokens' into registers
   const auto copy = [&]() {
+    if (ahead_u < w.count) {  // into L2, further ahead
+      const Unit un = unit_of<TOKENS_M>(p, w, ahead_u, rank);
+      const int row = (TOKENS_M ? un.n0 : un.row) + 32 * lane, b = 4 * ahead_g + part;
+      if (lane < w_cols && row < p.V && b < p.kb)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(words + static_cast<int64_t>(b) * p.V + row));
+      if (++ahead_g == groups) ahead_g = 0, ahead_u += w.step;
+    }
     held.live = u < w.count;
     if (held.live) {
       const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
@@ -881,7 +889,7 @@ __device__ __forceinline__ void epilogue(const Params& p, const Smem& s, const W
 }
 
 // W4: the weights are 4-bit numbers.
-template <bool TOKENS_M, bool W4>
+template <bool TOKENS_M, bool W4, int STEP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
@@ -938,10 +946,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
   if (warp == 0) {
-    if (ptx::elect_one()) producer<TOKENS_M, W4>(p, s, w, rank);
+    if (ptx::elect_one()) producer<TOKENS_M, W4, STEP>(p, s, w, rank);
     __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0 && ptx::elect_one()) mma_issuer<TOKENS_M, W4>(p, s, w, tmem);
+    if (rank == 0 && ptx::elect_one()) mma_issuer<TOKENS_M, W4, STEP>(p, s, w, tmem);
     __syncwarp();
   } else if (warp < 2 + kEpiWarps) {
     if (p.y_f32)
