@@ -1,5 +1,6 @@
 // Host side of flce_sample of include/flce.h.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 
 #include "flce_host.cuh"
@@ -109,7 +110,11 @@ flce_status flce_sample(const void* logits, int32_t dtype, int64_t ldl, const fl
   if (T == 0) return FLCE_OK;
   sample::Params p{};
   p.logits = logits, p.u = u, p.temperature = temperature, p.top_k = top_k, p.top_p = top_p, p.min_p = min_p;
-  p.temperature_all = temperature_all, p.top_k_all = top_k_all, p.top_p_all = top_p_all, p.min_p_all = min_p_all;
+  p.temperature_all = temperature_all, p.top_k_all = top_k_all, p.top_p_all = top_p_all;
+  p.log_min_p_all = min_p_all > 0.0 ? std::log(min_p_all) : 0.0;
+  const double c = temperature_all > 0.0 ? std::min(1.4426950408889634 / temperature_all, 1e37) : 1.0;
+  p.c_hi_all = static_cast<float>(c);
+  p.c_lo_all = static_cast<float>(c - static_cast<double>(p.c_hi_all));
   p.temperature_like = temperature_all > 0.0 ? 1.0f : 0.0f;
   p.top_p_like = top_p_all <= 0.0 ? 0.0f : top_p_all < 1.0 ? 0.5f : 1.0f;
   p.min_p_like = min_p_all > 0.0 ? 0.5f : 0.0f;

@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include "ptx.cuh"
+#include "vec8.cuh"
 
 namespace flce {
 namespace sample {
@@ -48,7 +49,8 @@ struct Params {
   const int32_t* top_k;
   const float* top_p;
   const float* min_p;
-  double temperature_all, top_p_all, min_p_all;
+  double temperature_all, top_p_all, log_min_p_all;
+  float c_hi_all, c_lo_all;  // log2(e) / temperature_all
   float temperature_like, top_p_like, min_p_like;  // numbers that compare as those do with 0 and 1
   int64_t top_k_all;
   int64_t ldl, ignore_index;
@@ -234,7 +236,7 @@ struct Shared {
   Two part[kMaxWarps];
   Two from[2][kMaxCtas];
   Plan plan[2];
-  double c, log_min;
+  double log_min;
   U64 need;
   float c_hi, c_lo, min_logit;
   uint32_t listed, found[3];
@@ -353,7 +355,7 @@ __device__ __forceinline__ void merge_stretch(U64 (&v)[R], int base, int k, int 
 template <int R>
 __device__ __forceinline__ void sort_stretches(U64* a, int size) {
   constexpr int kStretch = R * 32;
-  const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   for (int k = kStretch; k <= size; k *= 2) {
     for (int j = k / 2; j >= kStretch; j /= 2) {
       for (int i = tid; i < size / 2; i += blockDim.x) {
@@ -363,7 +365,7 @@ __device__ __forceinline__ void sort_stretches(U64* a, int size) {
       }
       __syncthreads();
     }
-    for (int base = (tid >> 5) * kStretch; base < size; base += warps * kStretch) {
+    for (int base = (tid >> 5) * kStretch; base < size; base += static_cast<int>(blockDim.x >> 5) * kStretch) {
       U64 v[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) v[r] = a[base + r * 32 + lane];
@@ -444,11 +446,20 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   const bool greedy = !(temperature > 0.0f) || top_k == 1 || top_p <= 0.0f;
   const bool by_k = top_k > 0, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
   if (tid == 0) {
-    const double t = p.temperature ? static_cast<double>(temperature) : p.temperature_all;
-    sh.c = greedy ? 1.0 : fmin(1.4426950408889634 / t, 1e37);
-    sh.c_hi = static_cast<float>(sh.c);
-    sh.c_lo = static_cast<float>(sh.c - static_cast<double>(sh.c_hi));
-    sh.log_min = by_min && !greedy ? t * log(p.min_p ? static_cast<double>(min_p) : p.min_p_all) : 0.0;
+    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;  // log2(e)
+    if (greedy) {
+      sh.c_hi = 1.0f, sh.c_lo = 0.0f;
+    } else if (!p.temperature) {
+      sh.c_hi = p.c_hi_all, sh.c_lo = p.c_lo_all;
+    } else {
+      const float c = fminf(kHi / temperature, 1e37f);
+      sh.c_hi = c;
+      sh.c_lo = c < 1e37f && temperature < INFINITY ? (fmaf(-c, temperature, kHi) + kLo) / temperature : 0.0f;
+    }
+    sh.log_min = 0.0;
+    if (by_min && !greedy)
+      sh.log_min = (p.temperature ? static_cast<double>(temperature) : p.temperature_all) *
+                   (p.min_p ? log(static_cast<double>(min_p)) : p.log_min_p_all);
     sh.listed = 0;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -482,7 +493,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   // The largest logits of up to 2048 groups of the row, to every CTA: at least k logits are no
   // smaller than the k-th largest of them.  With k above half of the groups that bound lets too many pass.
   const int groups = min(4 * threads, kGroups / p.ctas);  // of a CTA
-  const bool short_k = !greedy && by_k && 2 * top_k <= groups * p.ctas + 256;
+  const bool short_k = !greedy && by_k && top_k <= groups * p.ctas / 2 + 128;
   if (short_k) {
     if (groups >= threads) {  // 1, 2 or 4 to a thread
       const int each_thread = groups / threads;
@@ -535,16 +546,31 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   const auto write = [&](int64_t token, U64 total) {  // one thread: the token, and log(its weight / total)
     p.tokens[row] = token;
     if (!p.logp) return;
-    // the weight's from the logit; of the total the exponent, the leading 24 bits, and the rest apart
-    const int exponent = 63 - __clzll(total);
-    const U64 bits = total << (63 - exponent);
-    const float lead = __ull2float_rz(bits);
-    const float rest = static_cast<float>(bits - static_cast<U64>(lead)) / lead;
-    const float drawn = as_float(logits[token]);
-    const double y = (drawn == INFINITY ? 0.0 : static_cast<double>(drawn) - static_cast<double>(sc.zero)) * sh.c - static_cast<double>(top);
-    p.logp[row] = greedy ? 0.0f
-                         : static_cast<float>((y - static_cast<double>(exponent - p.unit)) * 0.6931471805599453 -
-                                              (static_cast<double>(logf(lead * 0x1p-63f)) + rest));
+    const float drawn = as_float(logits[token]), l = drawn == INFINITY ? 0.0f : drawn;
+    const U64 w = weight(l, sc, lane_table);
+    // Pairs of fp32 numbers: 64-bit arithmetic took 5 us longer for each row.
+    const auto pair_of = [](U64 v) {
+      const float hi = __ull2float_rz(v);
+      return Twofold{hi, static_cast<float>(v - static_cast<U64>(hi))};
+    };
+    float log_p;
+    if (w > total - w) {  // -log1p(others / this one): keeps its digits near 0
+      const Twofold a = pair_of(total - w), b = pair_of(w);
+      const float q = a.hi / b.hi, rest = (fmaf(-q, b.hi, a.hi) + (a.lo - q * b.lo)) / b.hi;
+      log_p = -(log1pf(q) + rest / (1.0f + q));
+    } else {  // log 2 (y - top - the total's exponent) - log(its leading digits), y from the logit
+      constexpr float kHi = 0.693147182f, kLo = -1.90465421e-9f;  // log 2
+      const int exponent = 63 - __clzll(total);
+      const Twofold lead = pair_of(total << (63 - exponent));
+      const float a = l - sc.zero, y = a * sc.c_hi;
+      const Twofold v = Twofold{y, fmaf(a, sc.c_lo, fmaf(a, sc.c_hi, -y))} + Twofold{-top, 0.0f} +
+                        Twofold{static_cast<float>(p.unit - exponent), 0.0f};
+      const float m = v.hi * kHi;
+      const Twofold sum = Twofold{m, fmaf(v.hi, kHi, -m) + fmaf(v.hi, kLo, v.lo * kHi)} +
+                          Twofold{-logf(lead.hi * 0x1p-63f), -lead.lo / lead.hi};
+      log_p = sum.hi + sum.lo;
+    }
+    p.logp[row] = greedy ? 0.0f : log_p;
   };
   const U64 u_share = u > 0.0f ? static_cast<U64>(fminf(u, 0x1.fffffep-1f) * 0x1p63f) : 0;
 

@@ -163,6 +163,26 @@ def test_words_without_a_weight(cuda_device, V, octaves):
         check(l * 0.3, u, temp=0.3, **s)
 
 
+def test_logp_of_words_that_are_nearly_certain(cuda_device):
+    """One word far ahead: its logp is the others' weight to 2^-21 of itself (sums good to 2^-29, fp32 logarithm) and
+    half a unit of 2^-46 for each of the 199 others (over this one's weight, at least 2^(-1/32)); 0 where it is alone."""
+    gaps = torch.tensor([2.0, 5.0, 9.0, 14.0, 18.0], dtype=F32, device=cuda_device)
+    l = torch.zeros(5, 3000, device=cuda_device)
+    l[:, 100:200] = torch.linspace(-1, 0, 100, device=cuda_device)
+    l[:, 200:] = float("-inf")
+    l[:, 7] = gaps + 3
+    tokens, logp = flce.flce_sample(l, torch.full((5,), 0.5, device=cuda_device), temperature=0.7)
+    assert torch.equal(tokens[1:], torch.full_like(tokens[1:], 7))
+    z = l.double() / 0.7
+    others = torch.where(torch.arange(3000, device=cuda_device) == 7, -math.inf, z)
+    want = -torch.log1p(torch.exp(torch.logsumexp(others, 1) - z[:, 7]))
+    assert bool(((logp.double() - want).abs() <= 2.0 ** -21 * want.abs() + 199 * 2.0 ** -47 * 1.03)[1:].all())
+    _, alone = flce.flce_sample(l, torch.full((5,), 0.5, device=cuda_device), top_k=2, top_p=0.5)
+    assert bool((alone[1:] == 0).all())
+    for s in (dict(top_k=1), dict(top_p=1e-9), dict(min_p=1.0)):
+        assert bool((flce.flce_sample(l, torch.full((5,), 0.9, device=cuda_device), **s)[1] == 0).all())
+
+
 def test_random_numbers_out_of_range(cuda_device):
     l, _ = rows_of(8, 1000, cuda_device, F32, seed=3)
     l = l[:1].expand(8, 1000).contiguous()
