@@ -16,13 +16,13 @@ constexpr int64_t kChunkBytes = 65024;     // of a row on a CTA, where a cluster
 constexpr int kMaxSmem = 232448 - 4096;    // less the static part
 
 // The largest cluster of this kernel: 16 CTAs where the device schedules it (queried once), else 8.
-template <typename E>
+template <typename E, bool SEARCH>
 flce_status set_up(int dev, int* most) {
   static std::mutex mu;
   static int known[64] = {};
   std::lock_guard<std::mutex> lk(mu);
   if (known[dev] == 0) {
-    const void* k = reinterpret_cast<const void*>(sample::sample_kernel<E>);
+    const void* k = reinterpret_cast<const void*>(sample::sample_kernel<E, SEARCH>);
     CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem));
     CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     cudaLaunchAttribute at{};
@@ -43,25 +43,25 @@ flce_status set_up(int dev, int* most) {
 }
 
 // CTAs of a row, pieces of 16 bytes on each, and threads.
-template <typename E>
+template <typename E, bool SEARCH>
 flce_status launch(sample::Params& p, int64_t T, int dev, int sms, cudaStream_t s) {
   int most = 8;
-  flce_status st = set_up<E>(dev, &most);
+  flce_status st = set_up<E, SEARCH>(dev, &most);
   if (st != FLCE_OK) return st;
   constexpr int64_t kPer = 16 / sizeof(E);
   const int64_t pieces = cdiv(p.V + kPer - 1, kPer);  // a row that starts on the last element of a piece
   int ctas = 1;
   while (ctas < 8 && cdiv(pieces, ctas) * 16 > kChunkBytes) ctas *= 2;
   while (ctas < most && T * ctas * 2 <= sms && cdiv(pieces, ctas) > 256) ctas *= 2;
-  while (ctas < most && sample::shared_bytes(static_cast<int>(cdiv(pieces, ctas))) > kMaxSmem) ctas *= 2;
-  if (sample::shared_bytes(static_cast<int>(cdiv(pieces, ctas))) > kMaxSmem)
+  while (ctas < most && sample::shared_bytes(static_cast<int>(cdiv(pieces, ctas)), SEARCH) > kMaxSmem) ctas *= 2;
+  if (sample::shared_bytes(static_cast<int>(cdiv(pieces, ctas)), SEARCH) > kMaxSmem)
     return fail(FLCE_ERR_UNSUPPORTED, "V = %d does not fit into a cluster of %d CTAs on this device", p.V, ctas);
   p.ctas = ctas;
   p.unit = sample::kMostUnit;
   while ((static_cast<int64_t>(p.V) >> (63 - p.unit)) != 0) --p.unit;
   p.chunk = static_cast<int32_t>(cdiv(pieces, ctas));
   const int threads = static_cast<int>(std::min<int64_t>(sample::kMaxThreads, std::max<int64_t>(128, cdiv(p.chunk, 256) * 128)));
-  const size_t smem = sample::shared_bytes(p.chunk);
+  const size_t smem = sample::shared_bytes(p.chunk, SEARCH);
   if (T * ctas >= (int64_t(1) << 31)) return fail(FLCE_ERR_INVALID_ARG, "T = %lld is too large", (long long)T);
   int pow2 = 128;
   while (pow2 < threads) pow2 *= 2;  // a whole share of the bins for each thread
@@ -76,7 +76,7 @@ flce_status launch(sample::Params& p, int64_t T, int dev, int sms, cudaStream_t 
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = at, cfg.numAttrs = 2;
-  CUDA_TRY(cudaLaunchKernelEx(&cfg, sample::sample_kernel<E>, p));
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, sample::sample_kernel<E, SEARCH>, p));
   return FLCE_OK;
 }
 
@@ -121,7 +121,10 @@ flce_status flce_sample(const void* logits, int32_t dtype, int64_t ldl, const fl
   p.ldl = ldl, p.ignore_index = ignore_index, p.tokens = tokens, p.logp = logp, p.V = static_cast<int32_t>(V);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   KernelScope ks(FLCE_KERNEL_SAMPLE, s, 4.0 * T * V, T * (V * (dtype == FLCE_DTYPE_F32 ? 4.0 : 2.0) + 16.0));
-  st = dtype == FLCE_DTYPE_F32 ? launch<float>(p, T, dev, sms, s) : launch<uint16_t>(p, T, dev, sms, s);
+  if (top_k || top_k_all > 0 || top_p || top_p_all < 1.0)
+    st = dtype == FLCE_DTYPE_F32 ? launch<float, true>(p, T, dev, sms, s) : launch<uint16_t, true>(p, T, dev, sms, s);
+  else
+    st = dtype == FLCE_DTYPE_F32 ? launch<float, false>(p, T, dev, sms, s) : launch<uint16_t, false>(p, T, dev, sms, s);
   if (st != FLCE_OK) return st;
   ks.done();
   return check_launch("sample");

@@ -15,7 +15,23 @@
 //
 // A row belongs to a cluster of CTAs, each with its part in shared memory: the logits are
 // read once.  The CTAs agree on maximum, sums and thresholds by pushing a few words into each
-// other's shared memory and a cluster barrier.
+// other's shared memory and a cluster barrier.  The ways through the kernel:
+//   no filter, min-p alone   maximum; weights of every lane's stretch; the draw
+//   top-k up to about 1000   the k-th largest of 2048 groups' maxima bounds the k-th logit from
+//                            below; what is above it is listed on one CTA, which does the rest
+//   top-p, larger k          logits counted in steps of 1/32 octave of their weight; a prefix
+//                            that surely ends within 2048 logits is listed; a longer one ends
+//                            within a few steps: these are counted again by value, and everything
+//                            is weighed once
+//
+// Bound: not by memory (the floor is 18.7 us for the 127 MB of 256 x 124,160 fp32).  A long
+// prefix costs 25 to 35 instructions a logit for its weight (the issue slots are 50 to 60 % taken)
+// and every step that the CTAs agree on 2 to 3 us of barrier and skew, which two or three CTAs on an SM hide
+// in part.  One row of 248,320 bf16 logits with top-k 50 and top-p: 12.1 us, of which the load takes
+// 2.4, the maximum 2, bound and list 6, the rest 2.  256 x 124,160 fp32 as they are: 86 us.  93 x 248,320
+// top-p: 173 us, 55 a row (the maximum 5, counting 8, bracketing 7, weighing 19, thresholds 8, the draw 10).
+// 777 x 32,001 with settings for each row: 122 us.  Clusters of 16 with less of a row on each
+// took half as long again, 4 with twice as much 5 to 10 % longer.
 #pragma once
 
 #include <cstdint>
@@ -388,8 +404,11 @@ __device__ __forceinline__ void sort_stretches(U64* a, int size) {
 __device__ __forceinline__ int place_of(int piece) { return piece ^ ((piece >> 3) & 7); }
 __host__ __device__ constexpr size_t piece_bytes(int chunk) { return static_cast<size_t>((chunk + 7) / 8 * 8) * 16; }  // whole eights
 
-template <typename E>
-__global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) {
+//
+// SEARCH: some row may have top-k or top-p.  Without, nothing is counted or listed, and three CTAs fit on
+// an SM instead of two (256 x 124,160 fp32: 86 us, 97 in the other form).
+template <typename E, bool SEARCH>
+__global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(const Params p) {
   constexpr int kPer = Piece<E>::kPer;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
@@ -400,7 +419,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   U64* const mass_of = list + kList;                               // sums of the sorted list's weights
   uint32_t* const group_max = reinterpret_cast<uint32_t*>(mass_of);  // before that: of every group of the row
 
-  const int threads = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
+  const int threads = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Cluster cl{p.ctas, static_cast<int>(blockIdx.x % p.ctas), &sh, 0, 0};
   if (p.ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // for the wait below
   const int64_t row = blockIdx.x / p.ctas;
@@ -444,7 +463,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   const float min_p = p.min_p ? p.min_p[row] : p.min_p_like;
   const float u = p.u[row];
   const bool greedy = !(temperature > 0.0f) || top_k == 1 || top_p <= 0.0f;
-  const bool by_k = top_k > 0, by_p = top_p < 1.0f, by_min = min_p > 0.0f;
+  const bool by_k = SEARCH && top_k > 0, by_p = SEARCH && top_p < 1.0f, by_min = min_p > 0.0f;
   if (tid == 0) {
     constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;  // log2(e)
     if (greedy) {
@@ -1144,8 +1163,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) sample_kernel(const Params p) 
   }
 }
 
-inline size_t shared_bytes(int chunk) {
-  return piece_bytes(chunk) + sizeof(uint2) * kTable * 32 + sizeof(uint32_t) * kBins + 2 * sizeof(U64) * kList;
+inline size_t shared_bytes(int chunk, bool search) {
+  return piece_bytes(chunk) + sizeof(uint2) * kTable * 32 + (search ? sizeof(uint32_t) * kBins + 2 * sizeof(U64) * kList : 0);
 }
 
 }  // namespace sample
