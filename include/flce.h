@@ -418,10 +418,12 @@ FLCE_API flce_status flce_linear_fp4(const void* x, const uint8_t* x_scale, cons
  *          with nothing to draw gives the token ignore_index and logp 0.
  *   u      [T] fp32; below 0 and NaN count as 0, 1 and more as the number before 1
  *   temperature, top_k (int32), top_p, min_p: [T] of a setting for each row, or NULL: the
- *          number behind it for all (refused where negative, NaN or above 1, other than top_k)
+ *          number behind it for all (refused where negative or NaN, and top_p and min_p above
+ *          1; any top_k will do).  At a temperature of +inf (a row's) every w is 1
  *   tokens [T] int64;  logp [T] fp32 or NULL
- * Weights are whole multiples of 2^-44 of the largest and their sums exact, so the result does
- * not depend on the order of summation.  V up to 393,216.  ignore_index lies outside [0, V). */
+ * Weights are rounded to whole multiples of a unit, the largest being 2^44 of them or more (2^46 up
+ * to 131,071 words, 2^45 up to 262,143), and their sums are exact, so the result does not depend on
+ * the order of summation.  V up to 393,216.  ignore_index lies outside [0, V). */
 FLCE_API flce_status flce_sample(const void* logits, int32_t dtype, int64_t ldl, const float* u, int64_t T, int64_t V,
                                  const float* temperature, double temperature_all, const int32_t* top_k,
                                  int64_t top_k_all, const float* top_p, double top_p_all, const float* min_p,

@@ -8,7 +8,7 @@
 // for, and nothing is sorted but a short list of candidates.
 //
 // The answer is a whole number that turns on comparisons of long sums, so weights are integers
-// in units of 2^-44 or less of the largest: their sums are exact, in whatever order they are formed, and
+// in units of 2^-44 or less (2^-46 up to 131,071 words): their sums are exact, in whatever order they are formed, and
 // the sum that the search compares is the one that the drawing walks through.  A weight itself
 // is good to 2^-31 of it and half a unit (table-driven exponential after Tang, 1989): a draw among
 // 250,000 equally likely words then falls on the other side of a border about once in a million.
@@ -30,8 +30,8 @@
 // in part.  One row of 248,320 bf16 logits with top-k 50 and top-p: 12.1 us, of which the load takes
 // 2.4, the maximum 2, bound and list 6, the rest 2.  256 x 124,160 fp32 as they are: 86 us.  93 x 248,320
 // top-p: 173 us, 55 a row (the maximum 5, counting 8, bracketing 7, weighing 19, thresholds 8, the draw 10).
-// 777 x 32,001 with settings for each row: 122 us.  Clusters of 16 with less of a row on each
-// took half as long again, 4 with twice as much 5 to 10 % longer.
+// 777 x 32,001 with settings for each row: 122 us.  At least 44 KB instead of 64 of a row on
+// each CTA, in clusters up to 16: 143 instead of 86 us and 317 instead of 173.
 #pragma once
 
 #include <cstdint>
@@ -476,8 +476,8 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
       sh.c_lo = c < 1e37f && temperature < INFINITY ? (fmaf(-c, temperature, kHi) + kLo) / temperature : 0.0f;
     }
     sh.log_min = 0.0;
-    if (by_min && !greedy)
-      sh.log_min = (p.temperature ? static_cast<double>(temperature) : p.temperature_all) *
+    if (by_min && !greedy)  // at an infinite temperature every weight is 1, which none of up to 1 cuts off
+      sh.log_min = temperature == INFINITY && min_p <= 1.0f ? -INFINITY : (p.temperature ? static_cast<double>(temperature) : p.temperature_all) *
                    (p.min_p ? log(static_cast<double>(min_p)) : p.log_min_p_all);
     sh.listed = 0;
   }

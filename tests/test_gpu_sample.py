@@ -211,6 +211,22 @@ def test_settings_of_each_row(cuda_device):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_infinite_temperature(cuda_device, dtype):
+    """Every word that is not masked weighs 1, whatever its logit and whatever min_p up to 1."""
+    l, _ = rows_of(16, 4097, cuda_device, dtype, seed=41)
+    l = l.clone()
+    l[3, ::2] = float("-inf")
+    u = (torch.arange(16, device=cuda_device) + 0.5) / 16
+    temp = torch.full((16,), float("inf"), device=cuda_device)
+    for mp in (0.0, 0.5, 1.0, torch.linspace(0, 1, 16, device=cuda_device)):
+        check(l, u, temp=temp, mp=mp)
+        check(l, u, temp=temp, mp=mp, k=1000)
+    _, logp = flce.flce_sample(l, u, temperature=temp, min_p=1.0)
+    assert abs(logp[0].item() + math.log(4097)) <= 1e-6
+
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("V,pad,offset", [(33, 1, 1), (1000, 3, 5), (4097, 0, 3), (4096, 7, 0), (50257, 2, 7), (13, 0, 2)])
 def test_rows_of_any_alignment_and_guards(cuda_device, dtype, V, pad, offset):
     """Rows that start anywhere and lie V + pad apart; what is between them (NaN) counts for nothing; nothing but the
