@@ -3,6 +3,10 @@
 //
 //   Y[t, v] = sum_b sx[t, b] sw[v / 128, b] sum_{k in block b} X[t, k] W[v, k]
 //
+// And the same with 4-bit weights (W4): W of e2m1 numbers with one scale per row and 32 channels,
+//
+//   Y[t, v] = sum_g sx[t, g / 4] sw[g / 4, v, g % 4] sum_{k in group g} X[t, k] W[v, k]
+//
 // The scales are E8M0 bytes, which the tensor cores apply themselves
 // (kind::mxf8f6f4 with block scaling): the products of a block are scaled on
 // their way into the fp32 accumulator, and no partial sum leaves TMEM before the
@@ -26,6 +30,10 @@
 // 224, not 256, tokens per tile: two accumulators (448 columns) and four stages
 // of scales (64 columns) fill the 512 columns of TMEM.
 //
+// 4-bit weights: TMA unpacks them, 16 numbers (8 bytes) to 16 bytes of shared memory, which is
+// how the tensor cores read them beside e4m3; nothing is converted.  Every row has a word of scales
+// for each K block: 32 to 40 columns a stage of four K blocks instead of 16, so tiles end at N = 192.
+//
 // Bound: few tokens by reading W (1 x 2048 x 124,160: 43 us for 254 MB, of which a
 // kernel that only reads takes 37.1; 93 x 4096 x 248,320: 157 to 160 us, 6.7 TB/s); a prompt by
 // shared memory and the clock.  A K block of a 256 x 224 tile keeps the tensor pipe busy
@@ -33,6 +41,13 @@
 // for 56 more of the epilogue's transposes; it measures 535 cycles at K = 2048 and 503 at
 // K = 4096.  8192 x 2048 x 124,160: 1360 to 1470 us, 2.8 to 3.1 PFLOP/s, at the 1.4 to
 // 1.6 GHz that the power cap leaves.
+//   4-bit weights, few tokens: 1 x 2048 x 124,160 30.4 us for 135 MB, 93 x 4096 x 248,320 109 to 110 us
+// for 587 MB (5.4 TB/s).  The former with the tokens' copies, the scales' copies and stores
+// and three of four MMAs left out takes 24.9 us; the rest is scales and the chain of barriers between
+// their warps, the MMA issuer and the producer, which has half as long for a K block as
+// with 8-bit weights.  W fetched into L2 ahead by TMA took 47 us: the copy engine needs 1.4 ns
+// for a row of 64 bytes, wherever it goes.  A prompt runs at the 8-bit rate (2048 x 2048 x 124,160: 343 to
+// 351 us, 337 with 8-bit weights).
 #pragma once
 
 #include <cstdint>
@@ -1050,7 +1065,8 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const E* a, int
 // since e2m1 has none.  Rows are filled up to whole K blocks with zeros.
 //
 // Four threads to a group, 16 to a row's K block: the scales (q_scale [kb, R, 4]) of a
-// warp's two rows are 8 consecutive bytes.  Bound by reading a.
+// warp's two rows are 8 consecutive bytes.  124,160 x 2048 bf16: 131 us for 643 MB, 72 % of the issue
+// slots taken (weights are laid out once).
 __device__ __forceinline__ uint32_t e8m0_of_e2m1(float amax) {
   const uint32_t bits = __float_as_uint(amax);
   const int e = static_cast<int>(bits >> 23) - 2 + ((bits & 0x7fffffu) > 0x400000u ? 1 : 0);

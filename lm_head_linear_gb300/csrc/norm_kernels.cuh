@@ -93,7 +93,8 @@ struct FwdParams {
 // slots ran out.
 //
 // KEEP: q and qs are h itself in 8 bits, for the backward, and y has bf16 only.  Dividing by a
-// power of two is exact, so h is rounded once.
+// power of two is exact, so h is rounded once.  Bound by memory: 32,768 x 2048 with residual (605 MB)
+// and the backward that reads q (470 MB) take 162 to 164 us together, 6.6 TB/s.
 template <typename TX, typename TR, int NV, int B, bool EXACT, bool KEEP>
 __global__ void __launch_bounds__(max_threads(NV * B)) add_rms_norm_kernel(const FwdParams p) {
   constexpr int kRun = B * kVec, kRunPairs = B * kPairs, kBlockRuns = 128 / kRun;
@@ -346,7 +347,8 @@ __device__ __forceinline__ void unpack_e4m3(const uint2& q, uint32_t e8m0, F2 (&
 }
 
 // W32: fp32 weights (bf16 ones always fit beside the stages).  H8: h in 8 bits; TH is then the
-// type of dh and dx alone.
+// type of dh and dx alone.  A row's numbers are converted twice, before and after its mean: 67 % of
+// the issue slots at 75 % of DRAM's rate.
 template <typename TY, typename TH, int NV, bool W32, bool H8>
 __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdParams p) {
   // groups x stages x (dy, h, dh rows), weights; afterwards the CTA's dw

@@ -1,5 +1,6 @@
-"""The operators around the LM head: the norm in front of it, its
-product in 8 bits, and the policy and preference losses on the log-probabilities
+"""The operators around the LM head: the norm in front of it (and with its input
+kept in 8 bits for the backward), its product with 8-bit and with 4-bit weights, drawing
+tokens from logits, and the policy and preference losses on the log-probabilities
 it returns.
 
 As in :mod:`.binding`, arguments are checked, outputs and workspaces allocated
