@@ -46,8 +46,8 @@
 // and three of four MMAs left out takes 24.9 us; the rest is scales and the chain of barriers between
 // their warps, the MMA issuer and the producer, which has half as long for a K block as
 // with 8-bit weights.  W fetched into L2 ahead by TMA took 47 us: the copy engine needs 1.4 ns
-// for a row of 64 bytes, wherever it goes.  A prompt runs at the 8-bit rate (2048 x 2048 x 124,160: 343 to
-// 351 us, 337 with 8-bit weights).
+// for a row of 64 bytes, wherever it goes.  A prompt runs at the 8-bit rate (2048 x 2048 x 124,160 under
+// the power cap: 359 us, 358 with 8-bit weights).
 #pragma once
 
 #include <cstdint>
@@ -237,20 +237,20 @@ __device__ __forceinline__ void producer(const Params& p, const Smem& s, const W
   uint32_t used = 0;
   bool ok = true;
   const bool small = !TOKENS_M && p.n_tiles == 1;
-  const int step_bytes = kABytes + p.n / 2 * kBlockK;  // of a K block
+  const int step_bytes = STEP == 1 ? p.stage_bytes : kABytes + p.n / 2 * kBlockK;  // of a K block
   // The barriers count bytes as they lie in memory: a row of 128 4-bit numbers is 64.
   constexpr int kARow = W4 && !TOKENS_M ? kBlockK / 2 : kBlockK, kBRow = W4 && TOKENS_M ? kBlockK / 2 : kBlockK;
   for (int u = w.first; u < w.count && ok; u += w.step) {
     const Unit un = unit_of<TOKENS_M>(p, w, u, rank);
     const int n_row = un.n0 + static_cast<int>(rank) * (p.n / 2);
-    const uint32_t tx = 2u * static_cast<uint32_t>(un.boxes * 32 * kARow + p.n / 2 * kBRow);
+    const uint32_t tx = 2u * static_cast<uint32_t>(un.boxes * 32 * kARow + (step_bytes - kABytes) / (kBlockK / kBRow));
     for (int kb = 0; kb < p.kb; kb += STEP) {
       if (!ptx::wait_bounded_cluster(s.empty(at.i), at.phase ^ 1u, p.timeout_ns, s.abort_flag)) {
         give_up(p, s);
         ok = false;
         break;
       }
-      const int blocks = min(STEP, p.kb - kb);
+      const int blocks = STEP == 1 ? 1 : min(STEP, p.kb - kb);
       if (rank == 0) ptx::mbar_arrive_expect_tx(s.full(at.i), tx * blocks);
       const uint32_t full = ptx::mapa(s.full(at.i), 0);
 #pragma unroll
@@ -278,7 +278,9 @@ __device__ __forceinline__ void producer(const Params& p, const Smem& s, const W
         break;  // the odd CTA gave up before its half: what it did issue has landed by now
 }
 
-// Even CTA only.
+// Even CTA only.  One thread issues everything, and what it works out between two MMAs counts: the
+// test for the end of K in stages of one K block, where the loop has made it, took the 8-bit
+// 8192 x 2048 x 124,160 from 1374 to 1484 us.
 template <bool TOKENS_M, bool W4, int STEP>
 __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const Work& w, uint32_t tmem) {
   using F = Form<TOKENS_M, W4>;
@@ -304,7 +306,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const
       const uint32_t scales = tmem + F::kBase + sc.i * F::kCols;
 #pragma unroll
       for (int j = 0; j < STEP; ++j) {
-        if (kb + j >= p.kb) break;
+        if (STEP > 1 && kb + j >= p.kb) break;
         const uint32_t a = ptx::smem_u32(s.stages + at.i * p.stage_bytes) + j * step_bytes;
         const uint32_t sf = static_cast<uint32_t>((kb + j) & 3);
 #pragma unroll
@@ -318,7 +320,7 @@ __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const
       }
       ptx::mma_commit_pair(s.empty(at.i), 0x3);
       at.next(p.stages);
-      if (((kb + STEP) & 3) == 0 || kb + STEP >= p.kb) {
+      if (STEP == 1 ? (kb & 3) == 3 || kb == p.kb - 1 : ((kb + STEP) & 3) == 0 || kb + STEP >= p.kb) {
         ptx::mma_commit_pair(s.scale_empty(sc.i), 0x3);
         sc.next(F::kStages);
       }
