@@ -56,6 +56,8 @@ constexpr int kList = 2048;        // candidates that are sorted
 constexpr int kFewer = 128;        // up to which they are compared each with each
 constexpr int kGroups = 2048;      // whose largest logits bound the k-th largest from below
 constexpr uint32_t kAll = 0x7fffffffu;
+constexpr int kValues = 4096;      // bf16 values that have a weight, for a row to be counted by value
+constexpr uint32_t kPositive = 0xbb80u, kNegative = 0x447fu;  // leading 16 bits of the keys of 2^-8 and -2^-8
 static_assert(kLive <= kBins && kBins % kMaxThreads == 0, "bins");
 
 struct Params {
@@ -751,10 +753,82 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
   float t = -INFINITY, sure = INFINITY;
   uint32_t n = 0;
   Two own{0, 0};
-  uint32_t last_step = 0;  // not 0: list[i] is the weight of the value of key (bf16: of leading 16 bits) last_step - i
+  uint32_t last_step = 0;  // not 0: list[i] is the weight of the value of key (bf16: of leading 16 bits) last_step - i,
+  uint32_t skipped = 0;    // or for keys up to kNegative last_step - skipped - i, and none is there between them and kPositive
   if (greedy) t = row_max, n = 1;
 
-  if (!greedy && (by_k || by_p)) {
+  // top-p of bf16 logits, by value.  Few thousand values have a weight (128 to an octave of the logit;
+  // those within 2^-8 of 0, of which there are endless octaves, are weighed where they are met): the
+  // logits of each are counted, each CTA adds up and weighs its share of the values, and where p of the sum
+  // is reached among them is the end.  A row is counted so if it is several times as
+  // long as there are values.
+  bool counted = false;
+  if constexpr (sizeof(E) == 2) {
+    if (!greedy && by_p && !by_k) {
+      const uint32_t top_key = key_of(row_max) >> 16, low_key = key_of(lowest_in(kLive - 1, row_max, sc)) >> 16;
+      const uint32_t gap = top_key >= kPositive ? kPositive - kNegative - 1 : 0;
+      const auto middle = [&](uint32_t k) { return k < kPositive && k > kNegative; };
+      const auto index_of = [&](uint32_t k) { return top_key - k - (k <= kNegative ? gap : 0); };
+      const int above = gap ? static_cast<int>(top_key - kPositive) + 1 : 0;  // values before the middle
+      const int values = middle(low_key) ? above : static_cast<int>(index_of(low_key)) + 1;
+      const auto key_at = [&](int i) { return top_key - i - (i >= above ? gap : 0); };
+      if (!middle(top_key) && values <= kValues && 4 * values <= p.V) {
+        uint32_t* const counts = reinterpret_cast<uint32_t*>(mass_of);
+        __syncthreads();
+        for (int i = tid; i < values; i += threads) counts[i] = 0;
+        __syncthreads();
+        U64 mid = 0;
+        each_piece([&](const Piece<E>& l) {
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const uint32_t k = key_of(l.v[e]) >> 16;
+            const uint32_t i = index_of(k);
+            if (middle(k)) mid += weight(l.v[e], sc, lane_table);
+            else if (i < static_cast<uint32_t>(values)) atomicAdd(counts + i, 1u);
+          }
+        });
+        cl.sync();
+        const int each = (values + p.ctas - 1) / p.ctas, v0 = min(cl.rank * each, values), v1 = min(v0 + each, values);
+        const int per = (each + threads - 1) / threads, a = min(v0 + tid * per, v1), b = min(a + per, v1);
+        U64 here = 0;
+        for (int i = a; i < b; ++i) {
+          uint32_t c = 0;
+          for (int r = 0; r < p.ctas; ++r) c += *peer(counts + i, r);
+          counts[i] = c;  // of the whole row; nobody else reads it
+          here += c * weight(value_of<E>(key_at(i)), sc, lane_table);
+        }
+        const Two* from = cl.gather<Sum>(Two{here, mid});
+        U64 run = 0, sum = 0, mids = 0;
+        for (int r = 0; r < p.ctas; ++r) {
+          if (r == cl.rank) run = sum;
+          sum += from[r].a, mids += from[r].b;
+        }
+        __syncthreads();
+        if (tid == 0) sh.need = share_up(p.top_p ? static_cast<double>(top_p) : p.top_p_all, sum + mids);
+        run += block_before(here, &sh);
+        const U64 need = sh.need;
+        Two end{0, 0};
+        for (int i = a; i < b; ++i) {
+          const U64 w = weight(value_of<E>(key_at(i)), sc, lane_table), before = run + (i >= above && gap ? mids : 0);
+          if (before < need && before + counts[i] * w >= need)
+            end = Two{(need - before + w - 1) / w, static_cast<U64>(key_at(i)) + 1};
+          run += counts[i] * w;
+        }
+        __syncthreads();  // the sums before are read
+        end = cl.all<Sum>(end);
+        counted = end.b != 0;  // else it ends in the middle
+        if (counted) {
+          const uint32_t key = static_cast<uint32_t>(end.b) - 1;
+          t = value_of<E>(key), n = static_cast<uint32_t>(end.a);
+          sure = row_max, last_step = top_key, skipped = key <= kNegative ? gap : 0;
+          for (int i = tid; i < static_cast<int>(index_of(key)); i += threads) list[i] = weight(value_of<E>(key_at(i)), sc, lane_table);
+          __syncthreads();
+        }
+      }
+    }
+  }
+
+  if (!counted && !greedy && (by_k || by_p)) {
     if (short_k && real_max < INFINITY) {
       // Every CTA finds the same bound.
       for (int i = tid; i < kBins; i += threads) bins[i] = 0;
@@ -1094,7 +1168,11 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
       if (any && known < INFINITY && last_step) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e)
-          if (l.v[e] > t && l.v[e] <= known) v.a += list[last_step - (key_of(l.v[e]) >> (sizeof(E) == 2 ? 16 : 0))];
+          if (l.v[e] > t && l.v[e] <= known) {
+            const uint32_t k = key_of(l.v[e]) >> (sizeof(E) == 2 ? 16 : 0);
+            if (skipped && k > kNegative && k < kPositive) v.a += weight(l.v[e], sc, lane_table);
+            else v.a += list[last_step - k - (k <= kNegative ? skipped : 0)];
+          }
       } else if (any) {
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {

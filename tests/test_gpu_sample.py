@@ -210,6 +210,22 @@ def test_settings_of_each_row(cuda_device):
     check(l, u, 0.9, k, 0.95, mp)
 
 
+@pytest.mark.parametrize("V", [12345, 32001, 248320, 393216])
+@pytest.mark.parametrize("shift", [-40.0, -3.0, -0.25, 0.0, 0.25, 3.0, 40.0])
+def test_nuclei_of_rows_with_few_values(cuda_device, V, shift):
+    """bf16 rows have some thousand values: nuclei that end at positive ones, at negative ones, close to 0 (where values
+    have no end) and with min-p, and rows with masks, infinities, or more values than are counted."""
+    for i, s in enumerate([dict(p=0.5), dict(p=0.95), dict(p=0.9999, mp=1e-4), dict(p=0.99, temp=4.0, mp=0.01), dict(p=0.1, temp=0.3),
+                           dict(p=0.9, temp=100.0)]):
+        for spread in (0.02, 2.0):
+            l, u = rows_of(4, V, cuda_device, BF, seed=V + i, spread=spread, peaks=0)
+            l = (l.float() + shift).to(BF)
+            l[1, ::3] = float("-inf")
+            l[2, 1::2] = float("nan")
+            l[3, 1:4000] *= 2.0 ** -12  # many close to 0
+            check(l, u, **s)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_infinite_temperature(cuda_device, dtype):
     """Every word that is not masked weighs 1, whatever its logit and whatever min_p up to 1."""
