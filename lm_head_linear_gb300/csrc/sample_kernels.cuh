@@ -279,14 +279,19 @@ struct Cluster {
     else
       ptx::cluster_sync();
   }
+  // Every warp's value, in part[] after a barrier.
+  template <typename Op>
+  __device__ __forceinline__ void sum_warps(Two v) const {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+      v = Op::of(v, Two{__shfl_xor_sync(0xffffffffu, v.a, d), __shfl_xor_sync(0xffffffffu, v.b, d)});
+    if ((threadIdx.x & 31) == 0) s->part[threadIdx.x >> 5] = v;
+  }
   // Every CTA's value, in from[], for all threads of all CTAs.
   template <typename Op>
   __device__ __forceinline__ const Two* gather(Two v) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-      v = Op::of(v, Two{__shfl_xor_sync(0xffffffffu, v.a, d), __shfl_xor_sync(0xffffffffu, v.b, d)});
-    if (lane == 0) s->part[warp] = v;
+    sum_warps<Op>(v);
     __syncthreads();
     if (warp == 0) {
       v = lane < warps ? s->part[lane] : Op::kNone;
@@ -301,6 +306,7 @@ struct Cluster {
     turn ^= 1;  // the next one but one writes here: every thread has read it by the barrier between
     return r;
   }
+  __device__ __forceinline__ const Two* last() const { return s->from[turn ^ 1]; }  // what it returned
   template <typename Op>
   __device__ __forceinline__ Two all(Two v) {
     const Two* f = gather<Op>(v);
@@ -762,7 +768,7 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
   // logits of each are counted, each CTA adds up and weighs its share of the values, and where p of the sum
   // is reached among them is the end.  A row is counted so if it is several times as
   // long as there are values.
-  bool counted = false;
+  bool counted = false, alone = false;
   if constexpr (sizeof(E) == 2) {
     if (!greedy && by_p && !by_k) {
       const uint32_t top_key = key_of(row_max) >> 16, low_key = key_of(lowest_in(kLive - 1, row_max, sc)) >> 16;
@@ -773,7 +779,8 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
       const int values = middle(low_key) ? above : static_cast<int>(index_of(low_key)) + 1;
       const auto key_at = [&](int i) { return top_key - i - (i >= above ? gap : 0); };
       if (!middle(top_key) && values <= kValues && 4 * values <= p.V) {
-        uint32_t* const counts = reinterpret_cast<uint32_t*>(mass_of);
+        uint32_t* const counts = reinterpret_cast<uint32_t*>(mass_of);      // of this CTA
+        uint32_t* const row_counts = reinterpret_cast<uint32_t*>(list);     // of the row, its share
         __syncthreads();
         for (int i = tid; i < values; i += threads) counts[i] = 0;
         __syncthreads();
@@ -794,7 +801,7 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
         for (int i = a; i < b; ++i) {
           uint32_t c = 0;
           for (int r = 0; r < p.ctas; ++r) c += *peer(counts + i, r);
-          counts[i] = c;  // of the whole row; nobody else reads it
+          row_counts[i] = c;
           here += c * weight(value_of<E>(key_at(i)), sc, lane_table);
         }
         const Two* from = cl.gather<Sum>(Two{here, mid});
@@ -810,9 +817,9 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
         Two end{0, 0};
         for (int i = a; i < b; ++i) {
           const U64 w = weight(value_of<E>(key_at(i)), sc, lane_table), before = run + (i >= above && gap ? mids : 0);
-          if (before < need && before + counts[i] * w >= need)
+          if (before < need && before + row_counts[i] * w >= need)
             end = Two{(need - before + w - 1) / w, static_cast<U64>(key_at(i)) + 1};
-          run += counts[i] * w;
+          run += row_counts[i] * w;
         }
         __syncthreads();  // the sums before are read
         end = cl.all<Sum>(end);
@@ -821,6 +828,23 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
           const uint32_t key = static_cast<uint32_t>(end.b) - 1;
           t = value_of<E>(key), n = static_cast<uint32_t>(end.a);
           sure = row_max, last_step = top_key, skipped = key <= kNegative ? gap : 0;
+          if (p.ctas > 1 && !by_min) {  // the CTA that the draw falls to goes on alone
+            const int last = static_cast<int>(index_of(key));
+            Two own_kept{skipped ? mid : 0, tid == 0 ? counts[last] : 0u};
+            for (int i = tid; i < last; i += threads)
+              if (counts[i]) own_kept.a += counts[i] * weight(value_of<E>(key_at(i)), sc, lane_table);
+            const Two* kept_by = cl.gather<Sum>(own_kept);
+            const U64 w_t = weight(t, sc, lane_table);
+            const auto up_to = [&](const Two& v) { return v.a + (v.b < n ? v.b : static_cast<U64>(n)) * w_t; };
+            Two before{0, 0}, all{0, 0};
+            for (int r = 0; r < p.ctas; ++r) {
+              if (r == cl.rank) before = all;
+              all = Sum::of(all, kept_by[r]);
+            }
+            const U64 target = share_down(u_share, up_to(all));
+            if (!(up_to(before) <= target && target < up_to(Sum::of(before, kept_by[cl.rank])))) return;
+            alone = true;
+          }
           for (int i = tid; i < static_cast<int>(index_of(key)); i += threads) list[i] = weight(value_of<E>(key_at(i)), sc, lane_table);
           __syncthreads();
         }
@@ -1195,7 +1219,14 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
   } else {
     each_piece([&](const Piece<E>& l) { own = Sum::of(own, kept_of(l, sure)); });
   }
-  const Two* from = cl.gather<Sum>(own);
+  const Two* from;
+  if (alone) {  // the CTAs' sums were gathered last
+    cl.sum_warps<Sum>(own);
+    __syncthreads();
+    from = cl.last();
+  } else {
+    from = cl.gather<Sum>(own);
+  }
   const U64 w_t = n ? weight(t, sc, lane_table) : 0;
   const auto kept = [&](const Two& s) { return s.a + (s.b < n ? s.b : static_cast<U64>(n)) * w_t; };
   Two before{0, 0}, all{0, 0};

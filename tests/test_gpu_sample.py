@@ -226,6 +226,22 @@ def test_nuclei_of_rows_with_few_values(cuda_device, V, shift):
             check(l, u, **s)
 
 
+@pytest.mark.parametrize("V", [12345, 32001, 248320])
+@pytest.mark.parametrize("shift", [-40.0, -0.25, 0.0, 3.0])
+def test_top_k_of_rows_with_few_values(cuda_device, V, shift):
+    """The k-th logit among many equals, at positive values, negative ones and close to 0, alone and before top-p and min-p;
+    k above the number of words that are not masked."""
+    for i, s in enumerate([dict(k=100), dict(k=300), dict(k=700, p=0.9), dict(k=1000, p=0.99, mp=0.01), dict(k=3000), dict(k=V // 2, p=0.7),
+                           dict(k=V // 2 + 1, temp=9.0), dict(k=V - 1), dict(k=V - 1, p=0.99999)]):
+        for spread in (0.02, 2.0):
+            l, u = rows_of(4, V, cuda_device, BF, seed=V + i, spread=spread, peaks=0)
+            l = (l.float() + shift).to(BF)
+            l[1, ::3] = float("-inf")
+            l[2, 1::2] = float("nan")
+            l[3, 1:4000] *= 2.0 ** -12
+            check(l, u, **s)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_infinite_temperature(cuda_device, dtype):
     """Every word that is not masked weighs 1, whatever its logit and whatever min_p up to 1."""
