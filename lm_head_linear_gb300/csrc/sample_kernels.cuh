@@ -19,19 +19,22 @@
 //   no filter, min-p alone   maximum; weights of every lane's stretch; the draw
 //   top-k up to about 1000   the k-th largest of 2048 groups' maxima bounds the k-th logit from
 //                            below; what is above it is listed on one CTA, which does the rest
-//   top-p, larger k          logits counted in steps of 1/32 octave of their weight; a prefix
+//   top-p of bf16            logits counted by their value, each value weighed once; then only the CTA
+//                            that holds the drawn word goes through its part again
+//   other top-p, larger k    logits counted in steps of 1/32 octave of their weight; a prefix
 //                            that surely ends within 2048 logits is listed; a longer one ends
 //                            within a few steps: these are counted again by value, and everything
 //                            is weighed once
 //
-// Bound: not by memory (the floor is 18.7 us for the 127 MB of 256 x 124,160 fp32).  A long
-// prefix costs 25 to 35 instructions a logit for its weight (the issue slots are 50 to 60 % taken)
+// Bound: not by memory (the floor is 18.7 us for the 127 MB of 256 x 124,160 fp32).  A
+// weight costs 25 to 35 instructions (the issue slots are 54 to 66 % taken)
 // and every step that the CTAs agree on 2 to 3 us of barrier and skew, which two or three CTAs on an SM hide
 // in part.  One row of 248,320 bf16 logits with top-k 50 and top-p: 12.1 us, of which the load takes
 // 2.4, the maximum 2, bound and list 6, the rest 2.  256 x 124,160 fp32 as they are: 86 us.  93 x 248,320
-// top-p: 173 us, 55 a row (the maximum 5, counting 8, bracketing 7, weighing 19, thresholds 8, the draw 10).
-// 777 x 32,001 with settings for each row: 122 us.  At least 44 KB instead of 64 of a row on
-// each CTA, in clusters up to 16: 143 instead of 86 us and 317 instead of 173.
+// top-p: 91 us (173 by steps of 1/32 octave, of whose 55 us a row weighing every logit took 19 and thresholds
+// 15; 105 with all CTAs in the draw).  777 x 32,001 with settings for each row: 83 us (122 by steps).
+// Counted by value, top-k above 256 took 83 us there as well, and made top-p 5 us slower.  At least 44 KB instead of 64 of a row on
+// each CTA, in clusters up to 16: 143 instead of 86 us, and 317 for 173 by steps.
 #pragma once
 
 #include <cstdint>
@@ -766,8 +769,9 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
   // top-p of bf16 logits, by value.  Few thousand values have a weight (128 to an octave of the logit;
   // those within 2^-8 of 0, of which there are endless octaves, are weighed where they are met): the
   // logits of each are counted, each CTA adds up and weighs its share of the values, and where p of the sum
-  // is reached among them is the end.  A row is counted so if it is several times as
-  // long as there are values.
+  // is reached among them is the end.  Rows of much fewer words than there are values are listed instead
+  // (p = 0.95, temperature 1: 256 x 1000 35 us listed, 21 counted; 256 x 4096 50 and 19; 256 x 100 18 and 24.
+  // Nuclei of some words, temperature 0.3: 256 x 1000 17 and 19, 2000 x 1000 64 and 71.)
   bool counted = false, alone = false;
   if constexpr (sizeof(E) == 2) {
     if (!greedy && by_p && !by_k) {
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
       const int above = gap ? static_cast<int>(top_key - kPositive) + 1 : 0;  // values before the middle
       const int values = middle(low_key) ? above : static_cast<int>(index_of(low_key)) + 1;
       const auto key_at = [&](int i) { return top_key - i - (i >= above ? gap : 0); };
-      if (!middle(top_key) && values <= kValues && 4 * values <= p.V) {
+      if (!middle(top_key) && values <= kValues && values <= 4 * p.V) {
         uint32_t* const counts = reinterpret_cast<uint32_t*>(mass_of);      // of this CTA
         uint32_t* const row_counts = reinterpret_cast<uint32_t*>(list);     // of the row, its share
         __syncthreads();
