@@ -933,10 +933,13 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
           for (int i = tid; i < kBins; i += threads)
             if (bins[i] >= need && (i == 0 || bins[i - 1] < need)) sh.found[0] = sh.found[1] = i;
         } else {  // between the bounds of their weights
+          // A bin is that of the rounded product, a weight that of the product with its rest, which is below
+          // 2^-23 + 2^-26 of it (what it rounds off, and c_lo): 2^-10 where it is near 2^13.
           const float unit_f = __uint_as_float(static_cast<uint32_t>(127 + p.unit) << 23);
+          const float half = 0.5f / kTable + 0x1p-22f * fmaxf(fabsf(sc.least), fabsf(sc.least + 64.0f));
           const auto bounds = [&](int i) {
             const U64 c = bins[i] - (i ? bins[i - 1] : 0u);
-            const float y = static_cast<float>(-i) * (1.0f / kTable), half = 0.5f / kTable;
+            const float y = static_cast<float>(-i) * (1.0f / kTable);
             const U64 lower = static_cast<U64>(ptx::ex2(y - half) * (1.0f - 0x1p-15f) * unit_f);
             return Two{c * (static_cast<U64>(ptx::ex2(y + half) * (1.0f + 0x1p-15f) * unit_f) + 2), c * (lower ? lower - 1 : 0)};
           };
