@@ -337,7 +337,8 @@ __device__ __forceinline__ void mma_issuer(const Params& p, const Smem& s, const
 
 // Four scale bytes from any byte address: the two aligned words they lie in, loaded
 // here, and combined by bytes_of() when they are used, so that nothing waits for the
-// loads before.  Bytes of the pair outside the array are never touched.
+// loads before.  Bytes of the pair outside the array are never touched.  Plain loads: a kernel
+// dispatched early lives while the one before it writes the tokens' scales.
 struct TwoWords {
   uint32_t lo, hi;
 };
@@ -346,13 +347,13 @@ __device__ __forceinline__ TwoWords load_words(const uint8_t* base, int64_t byte
   const uint8_t* p = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(a) & ~uintptr_t(3));
   TwoWords w;
   if (p >= base && p + 8 <= base + bytes) {
-    w.lo = __ldg(reinterpret_cast<const uint32_t*>(p));
-    w.hi = __ldg(reinterpret_cast<const uint32_t*>(p) + 1);
+    w.lo = *reinterpret_cast<const uint32_t*>(p);
+    w.hi = *(reinterpret_cast<const uint32_t*>(p) + 1);
   } else {  // the array's first or last bytes
     w.lo = w.hi = 0;
     for (int j = 0; j < 8; ++j)
       if (p + j >= base && p + j < base + bytes) {
-        const uint32_t v = static_cast<uint32_t>(__ldg(p + j)) << (8 * (j & 3));
+        const uint32_t v = static_cast<uint32_t>(p[j]) << (8 * (j & 3));
         if (j < 4) w.lo |= v;
         else w.hi |= v;
       }

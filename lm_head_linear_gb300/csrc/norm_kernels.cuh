@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kBwdThreads) norm_backward_kernel(const BwdPar
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int c = i + k * p.group;
-      if (row < p.T && c < nvec) scale_next[k] = __ldg(p.hs + row * nblk + c / (128 / kVec));
+      if (row < p.T && c < nvec) scale_next[k] = p.hs[row * nblk + c / (128 / kVec)];
     }
   };
   if constexpr (H8) load_scales(row0);
