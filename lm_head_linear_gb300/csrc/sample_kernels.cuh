@@ -10,8 +10,11 @@
 // The answer is a whole number that turns on comparisons of long sums, so weights are integers
 // in units of 2^-44 or less (2^-46 up to 131,071 words): their sums are exact, in whatever order they are formed, and
 // the sum that the search compares is the one that the drawing walks through.  A weight itself
-// is good to 2^-31 of it and half a unit (table-driven exponential after Tang, 1989): a draw among
-// 250,000 equally likely words then falls on the other side of a border about once in a million.
+// (table-driven exponential after Tang, 1989) is good to 2^-28.6 of it, 2^-31 in the mean (root mean square
+// over all table entries), and half a unit.  A draw from 250,000 words with normal logits then falls on the other side of
+// a border once in two million at a deviation of 2, five times in a million at 3, and top-p ends a word off in
+// eight rows of a million at most (worked out from the weights on the CPU).  Words with the same logit are off by the same factor;
+// two values whose errors are opposite could shift a border by 2^-29.6 of the sum, where a word is 2^-18 of it.
 //
 // A row belongs to a cluster of CTAs, each with its part in shared memory: the logits are
 // read once.  The CTAs agree on maximum, sums and thresholds by pushing a few words into each
@@ -26,15 +29,17 @@
 //                            within a few steps: these are counted again by value, and everything
 //                            is weighed once
 //
-// Bound: not by memory (the floor is 18.7 us for the 127 MB of 256 x 124,160 fp32).  A
-// weight costs 25 to 35 instructions (the issue slots are 54 to 66 % taken)
-// and every step that the CTAs agree on 2 to 3 us of barrier and skew, which two or three CTAs on an SM hide
-// in part.  One row of 248,320 bf16 logits with top-k 50 and top-p: 12.1 us, of which the load takes
-// 2.4, the maximum 2, bound and list 6, the rest 2.  256 x 124,160 fp32 as they are: 86 us.  93 x 248,320
-// top-p: 91 us (173 by steps of 1/32 octave, of whose 55 us a row weighing every logit took 19 and thresholds
-// 15; 105 with all CTAs in the draw).  777 x 32,001 with settings for each row: 83 us (122 by steps).
-// Counted by value, top-k above 256 took 83 us there as well, and made top-p 5 us slower.  At least 44 KB instead of 64 of a row on
-// each CTA, in clusters up to 16: 143 instead of 86 us, and 317 for 173 by steps.
+// Bound: not by memory (the floor is 18.7 us for the 127 MB of 256 x 124,160 fp32).  67 instructions are
+// issued for each logit there, of which a weight is 25 to 35 (what the others are was not taken apart; the issue slots
+// are 54 to 66 % taken), and every step that the CTAs agree on 2 to 3 us of barrier and skew, which two or three CTAs on an SM hide
+// in part.  One row of 248,320 bf16 logits with top-k 50 and top-p: 12.4 us, of which the load takes
+// 2.4, the maximum 2, bound and list 6, the rest 2.  256 x 124,160 as they are: fp32 86 us, bf16 55.  93 x 248,320
+// bf16 top-p: 91 us (173 by steps of 1/32 octave, of whose 55 us a row weighing every logit took 19 and thresholds
+// 15; 105 with all CTAs in the draw).  fp32 rows, and top-k of more than about 1000 words, go by steps: 93 x 248,320
+// fp32 top-p 384 us, top-k 3000 and top-p 398 (bf16 189).  777 x 32,001 with settings for each row: 83 us (122 by steps).
+// Counted by value, top-k above 256 took 83 us there as well, and made top-p 5 us slower.  44 KB instead of 64 of a row on
+// each CTA, in clusters up to 16: 256 x 124,160 fp32 145 instead of 86 us, 93 x 248,320 top-p 139 instead of 91; 127 KB:
+// 102 and 110.
 #pragma once
 
 #include <cstdint>
@@ -125,24 +130,22 @@ __device__ __forceinline__ Scale scale_of(float max, float c_hi, float c_lo, int
   return Scale{far ? max : 0.0f, c_hi, c_lo, kMagic - up, up - 64.0f, unit};
 }
 
-// A logit's weight in units (at most 2^unit and a little), rounded to nearest, and its bin, n = round(32 z).
+// A logit's weight in units (at most 2^unit and a little), rounded to nearest; n = round(32 z) below.
 // `lane_table`: this lane's column of the table of powers, which is there once for every
 // lane so that no two lanes meet in a bank.
 //
 // Packed pairs of fp32 with the sum kept as two fp32 numbers, which saves the 64-bit shift and
 // addition, took a tenth longer: their constants need two registers each.
-struct Weight {
-  U64 w;
-  int n;
-};
-__device__ __forceinline__ Weight weigh(float l, const Scale& s, const uint2* lane_table) {
+__device__ __forceinline__ U64 weight(float l, const Scale& s, const uint2* lane_table) {
   const float a = l - s.zero;
   const float y = a * s.c_hi;
   const float rest = fmaf(a, s.c_lo, fmaf(a, s.c_hi, -y));
   const float yy = fmaxf(y, s.least);
   const float t = yy + s.magic;
-  const float r = (yy - (t - s.magic)) + rest;  // |r| <= 1/64, exact but for the rest; NaN where l is infinite
-  // 2^r - 1, off by less than 2^-32.8: a polynomial fitted to it (least largest error on |r| <= 1/64)
+  // |r| <= 1/64 and the rest (below 2^-10, where products are near 2^13); exact but for that; NaN where l is infinite
+  const float r = (yy - (t - s.magic)) + rest;
+  // 2^r - 1: a polynomial fitted to it (least largest error on |r| <= 1/64: 2^-32.8, 2^-32 with the rest), off by
+  // 2^-29.7 as it is worked out here
   const float p = r * fmaf(r, fmaf(r, 0.05550457f, 0.24022846f), 0.6931472f);
   const int up = __float_as_int(kMagic) + (kTable - 1) - __float_as_int(t);  // n + 31
   const uint2 power = lane_table[(up & (kTable - 1)) * 32];
@@ -151,14 +154,12 @@ __device__ __forceinline__ Weight weigh(float l, const Scale& s, const uint2* la
   uint32_t half;
   asm("shl.b32 %0, 1, %1;" : "=r"(half) : "r"(drop - 1));  // 0 for amounts that are negative or 32 and more
   const uint32_t w = power.x + static_cast<uint32_t>(__float2int_rn(__uint_as_float(power.y) * p)) + half;
-  Weight out;
-  out.n = up - (kTable - 1);
-  asm("shr.u64 %0, %1, %2;" : "=l"(out.w) : "l"(static_cast<U64>(w) << 32), "r"(drop + 32));  // 0 from 64 on
+  U64 out;
+  asm("shr.u64 %0, %1, %2;" : "=l"(out) : "l"(static_cast<U64>(w) << 32), "r"(drop + 32));  // 0 from 64 on
   return out;
 }
-__device__ __forceinline__ U64 weight(float l, const Scale& s, const uint2* lane_table) { return weigh(l, s, lane_table).w; }
 
-// The same bin on its own.
+// A logit's bin, round(32 z) with z from the rounded product alone.
 __device__ __forceinline__ int bin_of(float l, const Scale& s) {
   const float t = fmaxf((l - s.zero) * s.c_hi, s.least) + s.magic;
   return __float_as_int(kMagic) - __float_as_int(t);
@@ -415,7 +416,6 @@ __device__ __forceinline__ void sort_stretches(U64* a, int size) {
 __device__ __forceinline__ int place_of(int piece) { return piece ^ ((piece >> 3) & 7); }
 __host__ __device__ constexpr size_t piece_bytes(int chunk) { return static_cast<size_t>((chunk + 7) / 8 * 8) * 16; }  // whole eights
 
-//
 // SEARCH: some row may have top-k or top-p.  Without, nothing is counted or listed, and three CTAs fit on
 // an SM instead of two (256 x 124,160 fp32: 86 us, 97 in the other form).
 template <typename E, bool SEARCH>
@@ -670,10 +670,10 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
     for (int i = a; i < b; ++i) mass_of[i] = run += weight(key_in_list(i), sc, lane_table);
     __syncthreads();
   };
-  // How many of the first m of the list it takes for weights of `need`.
   const auto share_of = [&](U64 total) {  // p of it; one thread
     return share_up(p.top_p ? static_cast<double>(top_p) : p.top_p_all, total);
   };
+  // How many of the first m of the list it takes for weights of `wanted`.
   const auto prefix_of = [&](int m, U64 wanted) -> int {  // 0: p of their sum
     __syncthreads();
     if (tid == 0) sh.found[0] = static_cast<uint32_t>(m), sh.need = wanted ? wanted : share_of(mass_of[m - 1]);
@@ -770,8 +770,9 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
   // those within 2^-8 of 0, of which there are endless octaves, are weighed where they are met): the
   // logits of each are counted, each CTA adds up and weighs its share of the values, and where p of the sum
   // is reached among them is the end.  Rows of much fewer words than there are values are listed instead
-  // (p = 0.95, temperature 1: 256 x 1000 35 us listed, 21 counted; 256 x 4096 50 and 19; 256 x 100 18 and 24.
-  // Nuclei of some words, temperature 0.3: 256 x 1000 17 and 19, 2000 x 1000 64 and 71.)
+  // (p = 0.95, normal logits of deviation 2, temperature 1: 256 x 1000 34 us listed, 21 counted; 256 x 4096 50 and 19;
+  // 256 x 100 18 and 24.  Temperature 0.3, nuclei of some words: 256 x 1000 17 and 19, 2000 x 1000 65 and 72;
+  // 0.1, fewer values: 17 and 10, 64 and 38.  How long the nucleus is, which would tell, is known after counting.)
   bool counted = false, alone = false;
   if constexpr (sizeof(E) == 2) {
     if (!greedy && by_p && !by_k) {
@@ -967,7 +968,8 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
     };
     // The end of that prefix, where more logits share its bins than can be sorted: they are counted
     // again by their values, in steps as fine as the bins allow, until a step holds one value (bf16:
-    // nearly always at once) or few enough logits to sort.  Returns the threshold, how many of
+    // nearly always at once) or few enough logits to sort.  The end has to lie in the bins given: weights above them
+    // are less than wanted, and with theirs enough.  Returns the threshold, how many of
     // its equals (b), and the prefix's weight.
     const auto narrow = [&](bool by_mass, U64 need, const Plan& in) {  // need 0: p of all weights
       uint32_t* const steps = group_max;  // kBins of them
@@ -1024,6 +1026,8 @@ __global__ void __launch_bounds__(kMaxThreads, SEARCH ? 2 : 3) sample_kernel(con
               const U64 w = weight(value_of<E>(k), sc, lane_table);
               return Two{c * w, c * w};
             }
+            // Weights fall back by 2^-29 of them at most where logits rise (from one table entry to the next,
+            // close to 0, where numbers lie that near to each other).
             const uint32_t k0 = max(k << shift, lo), k1 = min((k << shift) | ((1u << shift) - 1u), hi);
             const U64 w0 = weight(float_of(k0), sc, lane_table), w1 = weight(float_of(k1), sc, lane_table);
             return Two{c * (w1 + (w1 >> 28) + 2), c * (w0 - min(w0, (w0 >> 28) + 2))};
