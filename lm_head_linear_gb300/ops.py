@@ -205,7 +205,8 @@ def flce_sample(logits: torch.Tensor, u: torch.Tensor, temperature=1.0, top_k=0,
     [0, 1)), and the log of the probability it was drawn with.
 
     ``temperature``, ``top_p``, ``min_p`` (float32) and ``top_k`` (int32) are numbers for all rows or tensors [T].
-    Temperature 0 draws the largest logit of the lowest index; top_k 0, top_p 1 and min_p 0 keep every word.  Logits
+    Temperature 0 draws the largest logit of the lowest index; top_k 0, top_p 1 and min_p 0 keep every word.  Infinite
+    temperatures are taken from a tensor only.  Logits
     of -inf are never drawn; a row of nothing else gets the token ``ignore_index``, which the losses leave out.  ``out``
     may hold preallocated ``tokens`` and ``logp`` tensors.
     """
