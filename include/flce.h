@@ -420,7 +420,7 @@ FLCE_API flce_status flce_linear_fp4(const void* x, const uint8_t* x_scale, cons
  *   temperature, top_k (int32), top_p, min_p: [T] of a setting for each row, or NULL: the
  *          number behind it for all (refused where negative or NaN, a temperature above 1e300
  *          (+inf), and top_p and min_p above 1; any top_k will do).  A row's temperature may be
- *          +inf: every w is then 1
+ *          +inf: every w is then 1.  Temperatures below 1.44e-37 count as that
  *   tokens [T] int64;  logp [T] fp32 or NULL
  * Weights are rounded to whole multiples of a unit, the largest being 2^44 of them or more (2^46 up
  * to 131,071 words, 2^45 up to 262,143), and their sums are exact, so the result does not depend on
